@@ -442,6 +442,7 @@ def _exact_append(st):
                 part, page = fresh[x][lo - length + new:hi - length + new].transpose(0, 1), pages[at]    # [Hk, tokens, D]
                 amax = part.abs().amax((1, 2))
                 e = torch.ceil(torch.log2(amax / E4M3_MAX)).clamp(EXP_MIN, EXP_MAX)
+                e = (e - (amax <= E4M3_MAX * 2.0 ** (e - 1)).double()).clamp(EXP_MIN)      # where log2 came out too large
                 if lo > at * P:
                     was = exps[x][page].double()
                     e = torch.maximum(e, was)
