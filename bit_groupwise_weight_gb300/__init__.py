@@ -11,6 +11,12 @@ if the compiled library is missing.
     y = linear(x, packed, scales, zeros, bias, bits=4, group=64)
     h = linear_swiglu(x, packed_gate_up, scales, zeros, bias, bits=4, group=64)   # silu(gate) * up
     quantize_(model, bits=4, group=64)             # nn.Linear -> LowbitLinear, in place
+
+and, between a decoder's linear layers (module ``decoder``):
+
+    q = kv_append(q, k, v, *cache, page_table, lens, turns=rotary_turns(128))   # rotate, write the 8-bit cache
+    o = attention(q, *cache, page_table, lens)
+    token = sample(logits, u, temperature=0.8, top_p=0.9)
 """
 from __future__ import annotations
 
@@ -33,10 +39,19 @@ from ._abi import (  # noqa: F401
     unpack_weights,
     wait_timeouts,
 )
+from .decoder import (  # noqa: F401
+    attention,
+    attention_workspace,
+    empty_cache,
+    kv_append,
+    rotary_turns,
+    sample,
+)
 from .module import LowbitGateUp, LowbitLinear, quantize_  # noqa: F401
 
 __all__ = [
-    "LowbitError", "LowbitGateUp", "LowbitLinear", "PATH_AUTO", "PATH_QMM", "PATH_QMV", "abi", "linear", "linear_ptr",
+    "LowbitError", "LowbitGateUp", "LowbitLinear", "PATH_AUTO", "PATH_QMM", "PATH_QMV", "abi", "attention",
+    "attention_workspace", "empty_cache", "kv_append", "linear", "linear_ptr", "rotary_turns", "sample",
     "linear_swiglu", "linear_swiglu_ptr",
     "pack_weights", "packed_bytes", "quantize_weights", "select_path", "selftest_wait_timeout", "status_string", "unpack_weights",
     "quantize_", "wait_timeouts",

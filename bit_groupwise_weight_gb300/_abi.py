@@ -47,6 +47,14 @@ def _bind(lib):
     lib.lowbit_linear_swiglu.restype = ci
     lib.lowbit_select_path.argtypes = [i64, i64, i64, ci, ci]
     lib.lowbit_select_path.restype = ci
+    lib.lowbit_kv_append.argtypes = [vp, vp, vp, vp]
+    lib.lowbit_kv_append.restype = ci
+    lib.lowbit_attention.argtypes = [vp, vp, vp, vp]
+    lib.lowbit_attention.restype = ci
+    lib.lowbit_attention_workspace.argtypes = [ctypes.c_int32, vp, vp]
+    lib.lowbit_attention_workspace.restype = ctypes.c_size_t
+    lib.lowbit_sample.argtypes = [vp, vp]
+    lib.lowbit_sample.restype = ci
     lib.lowbit_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint32), ci]
     lib.lowbit_wait_timeouts.restype = ci
     lib.lowbit_selftest_wait_timeout.argtypes = [vp, vp]

@@ -88,6 +88,33 @@ lowbit_status check_linear_args(const uint16_t *x, const uint8_t *w, const uint1
     return LOWBIT_OK;
 }
 
+lowbit_status check_cache(const lowbit_cache *c, const lowbit_sequences *s, int heads) {
+    if (c == nullptr || s == nullptr) return LOWBIT_EINVAL;
+    if (s->batch < 0 || s->tokens < 0 || s->batch > kMaxDim || s->tokens > kMaxDim || s->width < 0 || s->width > kMaxDim)
+        return LOWBIT_EINVAL;
+    if (c->kv_heads <= 0 || c->kv_heads > 65535 || heads <= 0 || heads % c->kv_heads != 0 || c->pages < 0 ||
+        (c->head_dim != 64 && c->head_dim != 128))
+        return LOWBIT_EINVAL;
+    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) != 0) return LOWBIT_EINVAL;
+    // Rows (tokens times heads of a group) and lengths stay inside int32.
+    if ((int64_t)s->tokens * (heads / c->kv_heads) > kMaxDim || (int64_t)s->width * c->page > kMaxDim) return LOWBIT_EINVAL;
+    if (s->batch == 0 || s->tokens == 0) return LOWBIT_OK;
+    if (s->cu_q == nullptr ? s->tokens % s->batch != 0 : s->max_q <= 0) return LOWBIT_EINVAL;
+    if (c->pages == 0 || s->width == 0 || s->table_stride < s->width) return LOWBIT_EINVAL;
+    if (!c->k || !c->v || !c->k_exp || !c->v_exp || !s->page_table || !s->lens) return LOWBIT_EINVAL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(s->page_table, 4) || !aligned(s->lens, 4) ||
+        (s->cu_q != nullptr && !aligned(s->cu_q, 4)))
+        return LOWBIT_EINVAL;
+    const int64_t tile = (int64_t)c->page * c->head_dim;
+    if (c->head_stride < tile || c->page_stride < tile || c->head_stride % 16 != 0 || c->page_stride % 16 != 0 ||
+        c->head_stride >= ((int64_t)1 << 40) || c->page_stride >= ((int64_t)1 << 40))
+        return LOWBIT_EINVAL;
+    return LOWBIT_OK;
+}
+
+// Rows of head_dim 16-bit values that can be moved in 16-byte vectors.
+bool vector_rows(const void *p, int64_t token, int64_t head) { return aligned(p, 16) && token % 8 == 0 && head % 8 == 0; }
+
 // Crossover between the decode kernels and the batched tensor-core kernel
 // (qmm), measured on GB300 in-stream at b = 4 for the Llama-3.1-8B shapes and
 // the 3B gate+up and down, g = 32 / 64 / 128, M = 2..16.  The tensor-core
@@ -227,13 +254,100 @@ lowbit_status lowbit_linear_swiglu(const uint16_t *x, const uint8_t *packed_w, c
                                               (cudaStream_t)stream));
 }
 
+lowbit_status lowbit_kv_append(const lowbit_kv_append_args *a, const lowbit_cache *c, const lowbit_sequences *s,
+                               lowbit_stream_t stream) {
+    if (a == nullptr) return LOWBIT_EINVAL;
+    lowbit_status st = check_cache(c, s, a->heads);
+    if (st != LOWBIT_OK) return st;
+    if (a->rotary_dim < 0 || a->rotary_dim > c->head_dim || a->rotary_dim % 2 != 0) return LOWBIT_EINVAL;
+    if (s->batch == 0 || s->tokens == 0) return LOWBIT_OK;
+    if (!a->q || !a->k || !a->v || !a->q_out || !aligned(a->q, 2) || !aligned(a->k, 2) || !aligned(a->v, 2) ||
+        !aligned(a->q_out, 2))
+        return LOWBIT_EINVAL;
+    if (a->rotary_dim > 0 && (a->turns == nullptr || !aligned(a->turns, 8))) return LOWBIT_EINVAL;
+    if ((st = check_device()) != LOWBIT_OK) return st;
+    lowbit::AppendArgs p{};
+    p.q = a->q, p.k = a->k, p.v = a->v, p.q_out = a->q_out;
+    p.k_cache = c->k, p.v_cache = c->v, p.k_exp = c->k_exp, p.v_exp = c->v_exp;
+    p.page_table = s->page_table, p.lens = s->lens, p.cu_q = s->cu_q, p.turns = a->turns;
+    p.q_token = a->q_token, p.q_head = a->q_head, p.k_token = a->k_token, p.k_head = a->k_head;
+    p.v_token = a->v_token, p.v_head = a->v_head, p.o_token = a->o_token, p.o_head = a->o_head;
+    p.page_stride = c->page_stride, p.head_stride = c->head_stride, p.table_stride = s->table_stride;
+    p.factor = a->factor;
+    p.T = s->tokens, p.B = s->batch, p.max_q = s->max_q, p.Hq = a->heads, p.Hk = c->kv_heads;
+    p.D = c->head_dim, p.P = c->page, p.pages = c->pages, p.width = s->width, p.R = a->rotary_dim;
+    p.interleaved = a->interleaved != 0;
+    p.qvec = vector_rows(a->q, a->q_token, a->q_head);
+    p.kvec = vector_rows(a->k, a->k_token, a->k_head);
+    p.vvec = vector_rows(a->v, a->v_token, a->v_head);
+    p.ovec = vector_rows(a->q_out, a->o_token, a->o_head);
+    return from_cuda(lowbit::launch_kv_append(p, (cudaStream_t)stream));
+}
+
+size_t lowbit_attention_workspace(int32_t heads, const lowbit_cache *c, const lowbit_sequences *s) {
+    if (c == nullptr || s == nullptr || s->batch <= 0 || s->tokens <= 0 || c->kv_heads <= 0 || heads <= 0 ||
+        heads % c->kv_heads != 0 || (s->cu_q != nullptr && s->max_q <= 0))
+        return 0;
+    const bool uniform = s->cu_q == nullptr;
+    return lowbit::attention_workspace_bytes(s->tokens, s->batch, uniform ? s->tokens / s->batch : s->max_q, uniform,
+                                             heads, c->kv_heads, c->head_dim);
+}
+
+lowbit_status lowbit_attention(const lowbit_attention_args *a, const lowbit_cache *c, const lowbit_sequences *s,
+                               lowbit_stream_t stream) {
+    if (a == nullptr) return LOWBIT_EINVAL;
+    lowbit_status st = check_cache(c, s, a->heads);
+    if (st != LOWBIT_OK) return st;
+    if (a->window < 0 || !(a->scale > -1e30f && a->scale < 1e30f)) return LOWBIT_EINVAL;
+    if (s->batch == 0 || s->tokens == 0) return LOWBIT_OK;
+    if (!a->q || !a->out || !aligned(a->q, 8) || !aligned(a->out, 8) || (a->lse != nullptr && !aligned(a->lse, 4)))
+        return LOWBIT_EINVAL;
+    if (a->q_token % 4 != 0 || a->q_head % 4 != 0 || a->o_token % 4 != 0 || a->o_head % 4 != 0) return LOWBIT_EINVAL;
+    if (a->workspace == nullptr || !aligned(a->workspace, 16) ||
+        a->workspace_bytes < lowbit_attention_workspace(a->heads, c, s))
+        return LOWBIT_EINVAL;
+    if ((st = check_device()) != LOWBIT_OK) return st;
+    lowbit::AttentionArgs p{};
+    p.q = a->q, p.out = a->out, p.lse = a->lse;
+    p.k_cache = c->k, p.v_cache = c->v, p.k_exp = c->k_exp, p.v_exp = c->v_exp;
+    p.page_table = s->page_table, p.lens = s->lens, p.cu_q = s->cu_q;
+    p.workspace = static_cast<float *>(a->workspace);
+    p.q_token = a->q_token, p.q_head = a->q_head, p.o_token = a->o_token, p.o_head = a->o_head;
+    p.lse_token = a->lse_token;
+    p.page_stride = c->page_stride, p.head_stride = c->head_stride, p.table_stride = s->table_stride;
+    p.scale_log2 = a->scale * 1.4426950408889634f;
+    p.T = s->tokens, p.B = s->batch, p.max_q = s->max_q, p.Hq = a->heads, p.Hk = c->kv_heads;
+    p.D = c->head_dim, p.P = c->page, p.pages = c->pages, p.width = s->width, p.window = a->window;
+    return from_cuda(lowbit::launch_attention(p, (cudaStream_t)stream));
+}
+
+lowbit_status lowbit_sample(const lowbit_sample_args *a, lowbit_stream_t stream) {
+    if (a == nullptr || a->rows < 0 || a->rows > kMaxDim / 8 || a->vocab <= 0) return LOWBIT_EINVAL;
+    if (a->dtype != LOWBIT_DTYPE_F32 && a->dtype != LOWBIT_DTYPE_BF16 && a->dtype != LOWBIT_DTYPE_F16)
+        return LOWBIT_EINVAL;
+    if (a->rows == 0) return LOWBIT_OK;
+    if (!a->logits || !a->u || !a->token || !aligned(a->logits, a->dtype == LOWBIT_DTYPE_F32 ? 4 : 2) ||
+        !aligned(a->u, 4) || !aligned(a->token, 8) || (a->logprob && !aligned(a->logprob, 4)) ||
+        (a->temperature && !aligned(a->temperature, 4)) || (a->top_p && !aligned(a->top_p, 4)) ||
+        (a->min_p && !aligned(a->min_p, 4)) || (a->top_k && !aligned(a->top_k, 4)))
+        return LOWBIT_EINVAL;
+    lowbit_status st = check_device();
+    if (st != LOWBIT_OK) return st;
+    lowbit::SampleArgs p{};
+    p.logits = a->logits, p.u = a->u, p.temperature = a->temperature, p.top_p = a->top_p, p.min_p = a->min_p;
+    p.top_k = a->top_k, p.token = a->token, p.logprob = a->logprob, p.row_stride = a->row_stride;
+    p.temperature_all = a->temperature_all, p.top_p_all = a->top_p_all, p.min_p_all = a->min_p_all;
+    p.top_k_all = a->top_k_all, p.B = a->rows, p.V = a->vocab, p.dtype = (int)a->dtype;
+    return from_cuda(lowbit::launch_sample(p, (cudaStream_t)stream));
+}
+
 lowbit_status lowbit_wait_timeouts(uint32_t *count, int reset) {
     if (count == nullptr) return LOWBIT_EINVAL;
     lowbit_status st = check_device();
     if (st != LOWBIT_OK) return st;
     if (cudaDeviceSynchronize() != cudaSuccess) return LOWBIT_ECUDA;
     *count = lowbit::qmv_timeouts(reset != 0) + lowbit::mma_timeouts(reset != 0) + lowbit::qmm_timeouts(reset != 0) +
-             selftest_timeouts(reset != 0);
+             lowbit::attention_timeouts(reset != 0) + selftest_timeouts(reset != 0);
     return cudaGetLastError() == cudaSuccess ? LOWBIT_OK : LOWBIT_ECUDA;
 }
 

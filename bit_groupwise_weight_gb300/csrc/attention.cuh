@@ -1,0 +1,47 @@
+// attention.cuh -- shared by the attention kernels over the 8-bit paged cache
+// (attention.cu).
+#pragma once
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "ptx.cuh"
+
+namespace lowbit {
+
+namespace attn {
+
+constexpr int kSms = 152;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Where a sequence's new tokens lie, and its length with them.
+struct Span { int start, n, len; };
+
+__device__ __forceinline__ Span span(const AttentionArgs &p, int b) {
+    Span s;
+    if (p.cu_q == nullptr) {
+        s.n = p.T / p.B;
+        s.start = b * s.n;
+    } else {
+        s.start = min(max(p.cu_q[b], 0), p.T);
+        s.n = min(max(min(p.cu_q[b + 1], p.T) - s.start, 0), p.max_q);
+    }
+    s.len = min(max(p.lens[b], 0), p.width * p.P);
+    return s;
+}
+
+// Power of two that brings a row of q whose largest finite magnitude is amax into
+// [2^10, 2^11): bf16's 8 bits are then exact in fp16 down to 2^-35 of it.
+__device__ __forceinline__ int query_shift(float amax) { return min(10 + 127 - (int)(__float_as_uint(amax) >> 23), 100); }
+
+}  // namespace attn
+}  // namespace lowbit

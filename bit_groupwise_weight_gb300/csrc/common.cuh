@@ -170,4 +170,52 @@ bool qmm_supported(int64_t K, const void *x, const void *w);
 cudaError_t launch_qmm(const uint16_t *x, const uint8_t *w, const uint16_t *scales,
                        const uint16_t *zeros, const uint16_t *bias, uint16_t *y, int64_t M,
                        int64_t K, int64_t N, int bits, int group, cudaStream_t stream);
+// Rotary positions and the write into the 8-bit paged cache (cache.cu).  Strides
+// of q, k, v and q_out in elements, of the caches in bytes; *vec: rows may be
+// read or written in 16-byte vectors.
+struct AppendArgs {
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out;
+    uint8_t *k_cache, *v_cache;
+    int8_t *k_exp, *v_exp;
+    const int32_t *page_table, *lens, *cu_q;
+    const int64_t *turns;
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+    int64_t page_stride, head_stride, table_stride;
+    float factor;
+    int T, B, max_q, Hq, Hk, D, P, pages, width, R, units;
+    bool interleaved, qvec, kvec, vvec, ovec;
+};
+cudaError_t launch_kv_append(const AppendArgs &args, cudaStream_t stream);
+// Attention over that cache (attention.cu).
+struct AttentionArgs {
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;                          // may be null
+    const uint8_t *k_cache, *v_cache;
+    const int8_t *k_exp, *v_exp;
+    const int32_t *page_table, *lens, *cu_q;
+    float *workspace;
+    int64_t q_token, q_head, o_token, o_head, lse_token;
+    int64_t page_stride, head_stride, table_stride;
+    float scale_log2;                    // softmax scale * log2(e)
+    int T, B, max_q, Hq, Hk, D, P, pages, width, window;
+    int few_rows;                        // more query rows than this: a sequence for the prompt kernel
+};
+size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D);
+cudaError_t launch_attention(const AttentionArgs &args, cudaStream_t stream);
+uint32_t attention_timeouts(bool reset);
+// A token for each row of logits (sample.cu).  Per-row settings may be null:
+// the scalars beside them then hold for every row.
+struct SampleArgs {
+    const void *logits;
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    int64_t *token;
+    float *logprob;                      // may be null
+    int64_t row_stride;
+    float temperature_all, top_p_all, min_p_all;
+    int top_k_all, B, V, dtype;
+};
+cudaError_t launch_sample(const SampleArgs &args, cudaStream_t stream);
 }  // namespace lowbit

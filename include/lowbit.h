@@ -37,7 +37,8 @@
  *     weights, scales and zeros of a linear call must not be written by the
  *     kernel immediately before it in the stream if that kernel is one of
  *     this library's linear kernels (which write only y) or another kernel
- *     that allows early launch.  Ordinary kernels and copies, and this
+ *     that allows early launch (the cache, attention and sampling kernels do,
+ *     and write no weights).  Ordinary kernels and copies, and this
  *     library's packing and quantising kernels, do not allow it: weights they
  *     produce are always seen complete.
  *   - 16-bit floats are passed as their bit patterns (uint16_t): bf16 for x and
@@ -210,6 +211,146 @@ LOWBIT_API lowbit_status lowbit_linear_swiglu(const uint16_t *x, const uint8_t *
                                    const uint16_t *bias, uint16_t *y,
                                    int64_t M, int64_t K, int64_t F, int bits, int group,
                                    lowbit_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Between the linear layers of a decoder: rotary positions and the write into an
+ * 8-bit key-value cache, attention over that cache, and sampling.
+ *
+ * The cache holds keys and values in pages of `page` tokens, as e4m3 codes with
+ * one exponent for each page and key-value head: value = code * 2^exp.  (A power
+ * of two, so that scaling is exact, and a page whose exponent grows keeps its
+ * older codes but for those that become subnormal.)  Sequence b's token at
+ * position i is slot i % page of page page_table[b][i / page].
+ *
+ * Both calls take sequences of any lengths in one batch: the new tokens of all
+ * sequences stand one after another in q, k and v (`tokens` rows), sequence b's
+ * at rows [cu_q[b], cu_q[b+1]), or tokens / batch of them each when cu_q is NULL.
+ * lens[b] counts the sequence with its new tokens, so new token i of n stands at
+ * position lens[b] - n + i.  Lengths, offsets and pages are read on the device:
+ * nothing waits for the host, and a captured call follows their values.
+ */
+typedef struct {
+    uint8_t *k, *v;          /* [pages, kv_heads, page, head_dim] e4m3, 16-byte aligned  */
+    int8_t *k_exp, *v_exp;   /* [pages, kv_heads], each in [-64, 64]                      */
+    int64_t page_stride;     /* bytes from a page to the next, of k and of v               */
+    int64_t head_stride;     /* bytes from a head to the next; a head's page is contiguous;
+                                both multiples of 16                                      */
+    int32_t pages, kv_heads;
+    int32_t head_dim;        /* 64 or 128                                                  */
+    int32_t page;            /* tokens of a page: 16, 32, 64, 128 or 256                   */
+} lowbit_cache;
+
+typedef struct {
+    const int32_t *page_table;  /* [batch, width], rows table_stride apart.  Entries past a
+                                   sequence's end are not read; one outside the cache is
+                                   not written, and reads as zeros                         */
+    const int32_t *lens;        /* [batch]                                                 */
+    const int32_t *cu_q;        /* [batch + 1], rising from 0 to `tokens`, or NULL          */
+    int64_t table_stride;       /* elements                                                */
+    int32_t width;              /* columns of page_table: lengths are at most width * page  */
+    int32_t batch, tokens;
+    int32_t max_q;              /* bound of a sequence's new tokens (cu_q given); tokens past
+                                   it are left out                                         */
+} lowbit_sequences;
+
+/* Rotary positions on q and k, and k and v into the cache, in one launch.
+ * Pair j of a head's first rotary_dim values turns by 2 pi frac(pos turns[j] / 2^64)
+ * (turns[j]: the pair's frequency in turns per position times 2^64; the product
+ * wraps exactly, so positions of any size are as exact as small ones):
+ *     (a, b) -> factor * (a cos - b sin, a sin + b cos),
+ * a pair being values (j, j + rotary_dim/2), or (2j, 2j+1) when `interleaved`.  The
+ * rest of the head passes unchanged.  Computed in fp32; q_out is rounded to bf16, the
+ * codes to e4m3 (nearest even; infinities and values past 448 * 2^64 stored as 448).
+ * A page's exponent is the smallest e >= -64 with every finite new value of that
+ * page and head within 448 * 2^e, and at least its present one if the page holds
+ * older tokens of the sequence, whose codes are then rounded to the new one.
+ *   q, q_out [tokens, heads, head_dim], k, v [tokens, kv_heads, head_dim] bf16, with
+ *            strides in elements for tokens and heads, head_dim contiguous, 2-byte
+ *            aligned (16-byte aligned rows are read in vectors).  q_out may be q;
+ *            otherwise the outputs overlap nothing.
+ *   turns    [rotary_dim / 2] int64, device; NULL with rotary_dim == 0.
+ *   heads a multiple of kv_heads; rotary_dim even, 0 .. head_dim.
+ * New tokens before position 0 or past width * page are rotated but not stored.
+ * tokens == 0 or batch == 0 is a valid empty call.
+ * Errors: LOWBIT_EINVAL for a bad size, null or misaligned pointer or stride;
+ * LOWBIT_EUNSUPPORTED on a device that is not sm_103; LOWBIT_ECUDA when the launch
+ * fails. */
+typedef struct {
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out;
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+    const int64_t *turns;
+    float factor;
+    int32_t heads, rotary_dim, interleaved;
+} lowbit_kv_append_args;
+LOWBIT_API lowbit_status lowbit_kv_append(const lowbit_kv_append_args *args, const lowbit_cache *cache,
+                                          const lowbit_sequences *seqs, lowbit_stream_t stream);
+
+/* Softmax attention of the new tokens over the cache: for query row (token, head)
+ * at position pos, over the keys t <= pos (and t > pos - window when window > 0)
+ *     out = sum_t softmax_t(scale q.k_t) v_t,   lse = ln sum_t e^(scale q.k_t),
+ * with k and v the cached values (code * 2^exp), head h reading key-value head
+ * h / (heads / kv_heads).  Scores, softmax and sums in fp32; out rounded once to
+ * bf16.  A row that sees no key gives out 0 and lse -infinity.  What the cache holds
+ * at keys that a row does not see (NaN codes among it) does not reach that row.
+ *   q, out   [tokens, heads, head_dim] bf16, strides in elements (multiples of 4),
+ *            head_dim contiguous, 8-byte aligned.
+ *   lse      [tokens, heads] fp32 or NULL, heads contiguous, rows lse_token apart.
+ *   workspace  device memory of at least lowbit_attention_workspace bytes, 16-byte
+ *            aligned, for this call alone until it has run.
+ * tokens == 0 or batch == 0 is a valid empty call.
+ * Errors: as for lowbit_kv_append, and LOWBIT_EINVAL for a workspace that is too small. */
+typedef struct {
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    int64_t q_token, q_head, o_token, o_head, lse_token;
+    void *workspace;
+    size_t workspace_bytes;
+    float scale;
+    int32_t heads, window;
+} lowbit_attention_args;
+LOWBIT_API lowbit_status lowbit_attention(const lowbit_attention_args *args, const lowbit_cache *cache,
+                                          const lowbit_sequences *seqs, lowbit_stream_t stream);
+
+/* Bytes of workspace that lowbit_attention needs for these sizes (of the cache,
+ * head counts and dim; of the sequences, batch, tokens, width, max_q and whether
+ * cu_q is NULL).  Host-only.  0 for sizes that lowbit_attention rejects. */
+LOWBIT_API size_t lowbit_attention_workspace(int32_t heads, const lowbit_cache *cache, const lowbit_sequences *seqs);
+
+/* One token for each row of logits, from a given uniform number.  With m the row's
+ * largest logit, s_i = (x_i - m) / temperature and W_i = rint(2^30 e^s_i) (weights
+ * are whole numbers, so that sums are exact and a result does not depend on how the
+ * work is split): of the tokens in the order (logit falling, index rising) are kept
+ *     those with e^s_i >= min_p,
+ *     of these the first top_k (top_k <= 0: all),
+ *     of these the ones before which less than ceil(top_p * their total W) comes
+ *     (top_p >= 1: all; at least one),
+ * and token is the first index whose running total of kept W, in index order, passes
+ * floor(u * kept total).  logprob is s - ln(kept total / 2^30): the token's
+ * log-probability in the distribution that it was drawn from.
+ * temperature <= 0: the largest logit's index (the lowest of equals), logprob 0.
+ * NaN logits count as -infinity; a row without any logit above that gives token -1
+ * and logprob -infinity.  Tokens under 2^-31 of the likeliest are never drawn.
+ *   logits   [rows, vocab] of `dtype`, rows row_stride elements apart, naturally aligned.
+ *   u        [rows] fp32 in [0, 1).
+ *   temperature, top_p, min_p [rows] fp32 and top_k [rows] int32, device; each may be
+ *            NULL: the scalar of the same name holds for every row then.
+ *   token    [rows] int64; logprob [rows] fp32 or NULL.
+ *   rows >= 0, 1 <= vocab < 2^31.  rows == 0 is a valid empty call.
+ * Errors: as for lowbit_kv_append. */
+typedef struct {
+    const void *logits;
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    int64_t *token;
+    float *logprob;
+    int64_t row_stride;
+    float temperature_all, top_p_all, min_p_all;
+    int32_t top_k_all, rows, vocab;
+    lowbit_dtype dtype;
+} lowbit_sample_args;
+LOWBIT_API lowbit_status lowbit_sample(const lowbit_sample_args *args, lowbit_stream_t stream);
 
 /* The kernel lowbit_linear runs for this problem, from crossovers measured on
  * GB300: LOWBIT_PATH_QMV when the tensor-core decode kernel takes the shape
