@@ -52,6 +52,9 @@ struct Shape {
     static constexpr int kPerSm = D == 128 ? 2 : 3;
     static constexpr int kCtas = kSms * kPerSm;
 };
+// Sequences with more query rows (new tokens times heads of a group) than this go to
+// the prompt kernel.
+constexpr int kFewRows = 64;
 
 __device__ unsigned int g_attn_timeouts;
 
@@ -603,13 +606,22 @@ cudaError_t launch(const AttentionArgs &p, cudaStream_t stream) {
 }  // namespace
 
 uint32_t attention_timeouts(bool reset) {
+    const uint32_t prompt = prompt_timeouts(reset);
     unsigned int v = 0;
     cudaMemcpyFromSymbol(&v, g_attn_timeouts, sizeof(v));
     if (reset) {
         const unsigned int zero = 0;
         cudaMemcpyToSymbol(g_attn_timeouts, &zero, sizeof(zero));
     }
-    return v;
+    return v + prompt;
+}
+
+// Which kernels a call needs: sequences are sorted by their number of query rows, on
+// the device when the host does not know it.
+struct Split { bool few, many; int few_rows; };
+static Split split_of(int max_q, bool uniform, int G) {
+    if ((int64_t)max_q * G <= kFewRows) return {true, false, kFewRows};
+    return {!uniform, true, uniform ? 0 : kFewRows};
 }
 
 static size_t few_workspace_bytes(int max_q, int G, int D) {
@@ -618,8 +630,10 @@ static size_t few_workspace_bytes(int max_q, int G, int D) {
 }
 
 size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D) {
-    (void)T, (void)B, (void)uniform;
-    return few_workspace_bytes(max_q, Hq / Hk, D);
+    const Split s = split_of(max_q, uniform, Hq / Hk);
+    size_t bytes = s.few ? few_workspace_bytes(max_q, Hq / Hk, D) : 0;
+    if (s.many) bytes += prompt_workspace_bytes(prompt_grid(T, B, max_q, uniform, Hq, Hk, D), Hk, D);
+    return std::max<size_t>(bytes, 16);
 }
 
 cudaError_t launch_attention(const AttentionArgs &args, cudaStream_t stream) {
@@ -627,7 +641,14 @@ cudaError_t launch_attention(const AttentionArgs &args, cudaStream_t stream) {
     const bool uniform = p.cu_q == nullptr;
     if (uniform) p.max_q = p.T / p.B;
     const int G = p.Hq / p.Hk;
-    p.few_rows = INT32_MAX;
+    const Split s = split_of(p.max_q, uniform, G);
+    p.few_rows = s.few_rows;
+    if (s.many) {
+        PromptGrid g = prompt_grid(p.T, p.B, p.max_q, uniform, p.Hq, p.Hk, p.D);
+        g.workspace = s.few ? (int64_t)(few_workspace_bytes(p.max_q, G, p.D) / sizeof(float)) : 0;
+        const cudaError_t e = launch_prompt(p, g, stream);
+        if (e != cudaSuccess || !s.few) return e;
+    }
     const bool half = (int64_t)p.max_q * G <= 8;
     if (p.D == 128) return half ? launch<128, 8>(p, stream) : launch<128, 16>(p, stream);
     return half ? launch<64, 8>(p, stream) : launch<64, 16>(p, stream);

@@ -1,5 +1,5 @@
 // attention.cuh -- shared by the attention kernels over the 8-bit paged cache
-// (attention.cu).
+// (attention.cu: few query rows a sequence; attention_prompt.cu: many).
 #pragma once
 
 #include "common.cuh"
@@ -7,6 +7,17 @@
 #include "ptx.cuh"
 
 namespace lowbit {
+
+// Grid of the prompt kernel: row tiles over all sequences (an upper bound when the
+// sequences are ragged), splits of the keys, and where its workspace begins (floats).
+struct PromptGrid {
+    int tiles, splits;
+    int64_t workspace;
+};
+PromptGrid prompt_grid(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D);
+size_t prompt_workspace_bytes(const PromptGrid &g, int Hk, int D);
+cudaError_t launch_prompt(const AttentionArgs &p, const PromptGrid &g, cudaStream_t stream);
+uint32_t prompt_timeouts(bool reset);
 
 namespace attn {
 

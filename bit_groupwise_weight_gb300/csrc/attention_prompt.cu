@@ -1,0 +1,594 @@
+// attention_prompt.cu -- attention over the 8-bit paged cache for many new tokens
+// (prompts), on the tcgen05 tensor cores with accumulators in tensor memory.
+//
+// Mathematics: as attention.cu (codes multiplied as fp16 numbers, page exponents
+// applied in fp32, V's exponent inside the softmax exponent).  The running maximum
+// may lag: O and l are rescaled only when a row's maximum has grown by more than
+// 2^kLag since it was last taken, so weights reach 2^kLag (fp16 holds 2^15) and the
+// rescaling of O, a round trip through tensor memory, is rare.
+//
+// Work split.  A CTA takes 256 rows (new tokens x heads of a group) of one sequence
+// and kv head, as two 128-row tiles whose softmax and products alternate: while one
+// tile's weights are computed, the other's products run.  Keys come 128 at a time.
+// When there are fewer CTAs than SMs the keys are split between several, and a
+// second launch joins their parts.  Tiles with the most keys start first.
+//
+// Tensor memory (512 columns): S of both tiles (128 fp32 columns each; the fp16
+// weights P take the place of the S they come from), O of both tiles.
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (one thread a row), 8-11 turn e4m3
+// codes into fp16 operand tiles (once per 256 rows), 12 TMA producer, 13 MMA issuer.
+// Order of the issuer, which keeps a tile's S free while its P is read:
+//     PV0(j-1) QK0(j) PV1(j-1) QK1(j) ...
+// Bound: the tensor cores, 4 D flops per row and key; at 128 x 128 x 128 a product
+// takes 512 cycles, and 256 rows x 128 keys 2048; their exponentials 32768 / 16-32
+// per cycle and SM.
+#include <algorithm>
+
+#include "attention.cuh"
+
+namespace lowbit {
+namespace {
+
+using namespace attn;
+
+constexpr int kKeys = 128;                       // keys of a step
+constexpr int kRows = 256;                       // rows of a CTA
+constexpr int kUnit = 64;                        // keys of a raw TMA unit
+constexpr int kRaw = 4;                          // raw units in flight
+constexpr int kBuf = 2;                          // fp16 K and V tiles
+constexpr int kExps = 8;                         // steps whose page exponents are kept
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
+constexpr int kProducer = 12, kIssuer = 13;
+constexpr int kThreads = 14 * 32;
+constexpr float kLag = 8.f;
+
+__device__ unsigned int g_prompt_timeouts;
+
+template <int D>
+struct Smem {
+    static constexpr int kQ = 128 * D * 2, kTile = kKeys * D * 2, kRawBytes = kUnit * D;
+    alignas(1024) uint8_t q[2][kQ];
+    alignas(1024) uint8_t k[kBuf][kTile];
+    alignas(1024) uint8_t v[kBuf][kTile];
+    alignas(1024) uint8_t raw[kRaw][kRawBytes];
+    float4 exps[kExps][kKeys / 16];              // 2^ke, ve, 2^-ve of each 16 keys
+    uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBuf], k_empty[kBuf], v_full[kBuf], v_empty[kBuf];
+    uint64_t q_full, s_full[2], p_full[2], o_full, e_full[kExps];
+    uint32_t tmem;
+    int poisoned;
+};
+
+// MN-major operand (the 64 contiguous values of an atom run along N): 128-byte
+// swizzle atoms of 8 k-rows, 1024 bytes from one to the next along K, `lead` bytes
+// to the next 64 values along N.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr, uint32_t lead) {
+    return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+        "%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// The CTA's part of the work.
+struct Work {
+    int b, h, row0, nrows, start, first, len;    // rows row0 .. of nrows; first: position of the first new token
+    int lo, n;                                   // first step of 128 keys, and how many
+    int split, unit;
+    bool live;
+};
+
+__device__ __forceinline__ Work work_of(const AttentionArgs &p, const PromptGrid &g, int id) {
+    Work w{};
+    const int G = p.Hq / p.Hk;
+    // Ids count down over the row tiles, so that tiles with the most keys start first.
+    w.split = id % g.splits;
+    w.unit = id / g.splits;
+    w.h = w.unit % p.Hk;
+    const int tile = g.tiles - 1 - w.unit / p.Hk;
+    int b, t;
+    if (p.cu_q == nullptr) {
+        const int per = g.tiles / p.B;
+        b = tile % p.B, t = tile / p.B;
+        if (t >= per) return w;
+    } else {
+        // Sequence b owns the tiles from cu_q[b] G / 256 + b on: enough for its rows.
+        auto base = [&](int i) { return (int)((int64_t)min(max(p.cu_q[i], 0), p.T) * G / kRows) + i; };
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (base(mid) <= tile) lo = mid;
+            else hi = mid - 1;
+        }
+        b = lo, t = tile - base(lo);
+    }
+    const Span s = span(p, b);
+    w.b = b, w.start = s.start, w.len = s.len, w.first = s.len - s.n;
+    w.nrows = s.n * G, w.row0 = t * kRows;
+    w.live = t >= 0 && w.row0 < w.nrows && w.nrows > p.few_rows;
+    if (!w.live) return w;
+    const int pos_lo = w.first + w.row0 / G, pos_hi = w.first + (min(w.row0 + kRows, w.nrows) - 1) / G;
+    const int lo = p.window > 0 ? max(pos_lo - p.window + 1, 0) / kKeys : 0;
+    const int n = pos_hi >= 0 ? pos_hi / kKeys + 1 - lo : 0;
+    const int a = (int)((int64_t)n * w.split / g.splits), e = (int)((int64_t)n * (w.split + 1) / g.splits);
+    w.lo = lo + a, w.n = e - a;
+    return w;
+}
+
+// Workspace of a (unit, split): 256 x D sums, then 256 (m, l) pairs.
+template <int D>
+__device__ __forceinline__ float *part_of(const AttentionArgs &p, const PromptGrid &g, int unit, int split) {
+    return p.workspace + g.workspace + ((int64_t)unit * g.splits + split) * (kRows * (D + 2));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttentionArgs p,
+                  const PromptGrid grid) {
+    extern __shared__ uint8_t raw_smem[];
+    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw_smem + ((1024 - (ptx::smem_u32(raw_smem) & 1023)) & 1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto at = [](const uint64_t &bar) { return ptx::smem_u32(&bar); };
+    if (tid == 0) {
+        for (int i = 0; i < kRaw; ++i) ptx::mbar_init(at(sm.raw_full[i]), 1), ptx::mbar_init(at(sm.raw_empty[i]), kConvertWarps);
+        for (int i = 0; i < kBuf; ++i) {
+            ptx::mbar_init(at(sm.k_full[i]), kConvertWarps), ptx::mbar_init(at(sm.k_empty[i]), 1);
+            ptx::mbar_init(at(sm.v_full[i]), kConvertWarps), ptx::mbar_init(at(sm.v_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(at(sm.s_full[i]), 1), ptx::mbar_init(at(sm.p_full[i]), 4);
+        for (int i = 0; i < kExps; ++i) ptx::mbar_init(at(sm.e_full[i]), 1);
+        ptx::mbar_init(at(sm.q_full), kSoftmaxWarps);
+        ptx::mbar_init(at(sm.o_full), 1);
+        sm.poisoned = 0;
+        ptx::fence_mbar_init();
+    }
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+    const Work w = work_of(p, grid, blockIdx.x);
+    if (!w.live || (w.n == 0 && grid.splits > 1)) return;      // the join leaves empty parts out too
+    const int G = p.Hq / p.Hk, P = p.P;
+    if (warp == kIssuer) {
+        ptx::tmem_alloc(ptx::smem_u32(&sm.tmem), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 256 + D};
+    // Steps in which some row of the CTA does not see some key.
+    const int pos_lo = w.first + w.row0 / G, pos_hi = w.first + (min(w.row0 + kRows, w.nrows) - 1) / G;
+    auto partial = [&](int key0) { return key0 + kKeys - 1 > pos_lo || (p.window > 0 && key0 <= pos_hi - p.window); };
+
+    if (warp < kSoftmaxWarps) {
+        // ------------------------------------------------ softmax: a thread owns a row.
+        const int t = warp >> 2, r = t * 128 + (warp & 3) * 32 + lane, row = w.row0 + r;
+        const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+        const bool live = row < w.nrows;
+        const int token = live ? row / G : 0, head = w.h * G + (live ? row - token * G : 0);
+        const int pos = live ? w.first + token : -1;
+        const int low = p.window > 0 ? pos - p.window : -1;    // keys low < key <= pos are seen
+        float qs;
+        {
+            // The row of q as fp16 times a power of two, into the swizzled operand tile.
+            const uint16_t *q = p.q + (int64_t)(w.start + token) * p.q_token + head * p.q_head;
+            float amax = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 4; ++c) {
+                const uint2 v = live ? *reinterpret_cast<const uint2 *>(q + 4 * c) : make_uint2(0u, 0u);
+                const float x[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) amax = fabsf(x[k]) < INFINITY ? fmaxf(amax, fabsf(x[k])) : amax;
+            }
+            const int up = query_shift(amax);
+            // A negative scale goes into q: the maximum is taken before scaling.
+            const float f = p.scale_log2 < 0.f ? -exp2_int(up) : exp2_int(up);
+            qs = exp2_int(-up) * fabsf(p.scale_log2);
+            const uint32_t base = ptx::smem_u32(sm.q[t]);
+            const int lr = r & 127;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const uint2 a = live ? *reinterpret_cast<const uint2 *>(q + 8 * c) : make_uint2(0u, 0u);
+                const uint2 b = live ? *reinterpret_cast<const uint2 *>(q + 8 * c + 4) : make_uint2(0u, 0u);
+                const uint32_t o[4] = {f32x2_to_f16x2(bf16_lo(a.x) * f, bf16_hi(a.x) * f), f32x2_to_f16x2(bf16_lo(a.y) * f, bf16_hi(a.y) * f),
+                                       f32x2_to_f16x2(bf16_lo(b.x) * f, bf16_hi(b.x) * f), f32x2_to_f16x2(bf16_lo(b.y) * f, bf16_hi(b.y) * f)};
+                sts_v4(base + (c >> 3) * 16384 + lr * 128 + (((c & 7) ^ (lr & 7)) << 4), o[0], o[1], o[2], o[3]);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(at(sm.q_full));
+        }
+        bool ok = true;
+        float m = -INFINITY, l = 0.f;
+        const uint32_t sc = s_col[t] + quarter, oc = o_col[t] + quarter;
+        for (int j = 0; j < w.n; ++j) {
+            const int key0 = (w.lo + j) * kKeys;
+            const bool mask = partial(key0);
+            if (ok) ok = ptx::mbar_wait(at(sm.e_full[j % kExps]), (j / kExps) & 1, &g_prompt_timeouts);
+            if (ok) ok = ptx::mbar_wait(at(sm.s_full[t]), j & 1, &g_prompt_timeouts);
+            ptx::tc_fence_after();
+            const float4 *ex = sm.exps[j % kExps];
+            // Pass 1: the row's maximum, by 16 keys (one page at least).
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tmem_ld32(sc + c * 32, v);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float x = -INFINITY;
+                    const float4 e = ex[2 * c + g];
+                    if (mask) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int key = key0 + c * 32 + g * 16 + k;
+                            if (key <= pos && key > low) x = fmaxf(x, __uint_as_float(v[g * 16 + k]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[g * 16 + k]));
+                    }
+                    // No key seen: stays -infinity whatever the page's exponents.
+                    mx = fmaxf(mx, x == -INFINITY ? x : fmaf(x, qs * e.x, e.y));
+                }
+            }
+            // The maximum in use follows when it lags by more than kLag.
+            const bool move = mx > m + kLag || (m == -INFINITY && mx > m);
+            if (__any_sync(~0u, move)) {
+                const float a = move ? ex2(m - mx) : 1.f;
+                if (move) m = mx;
+                l *= a;
+                if (j > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t v[16];
+                        ptx::tmem_ld16(oc + c * 16, v);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * a);
+                        ptx::tmem_st16(oc + c * 16, v);
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            // Pass 2: weights, their sum, and fp16 pairs over the scores they come from.
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32], h[16];
+                tmem_ld32(sc + c * 32, v);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float4 e = ex[2 * c + g];
+                    const float f = qs * e.x, d = e.y - ref;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        float x = ex2(fmaf(__uint_as_float(v[g * 16 + k]), f, d));
+                        float y = ex2(fmaf(__uint_as_float(v[g * 16 + k + 1]), f, d));
+                        if (mask) {
+                            const int key = key0 + c * 32 + g * 16 + k;
+                            if (!(key <= pos && key > low)) x = 0.f;
+                            if (!(key + 1 <= pos && key + 1 > low)) y = 0.f;
+                        }
+                        sum += x + y;
+                        h[g * 8 + k / 2] = f32x2_to_f16x2(x, y);
+                    }
+                    l = fmaf(sum, e.z, l);
+                }
+                ptx::tmem_st16(sc + c * 16, h);
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(at(sm.p_full[t]));
+        }
+        // ------------------------------------------------ the row's result.
+        if (w.n > 0) {
+            if (ok) ok = ptx::mbar_wait(at(sm.o_full), 0, &g_prompt_timeouts);
+            ptx::tc_fence_after();
+        }
+        // NaN among the V codes of partly seen steps was taken out of the product; a
+        // row that sees such a code takes it here.
+        uint32_t nan[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) nan[i] = 0u;
+        if (sm.poisoned && live) {
+            for (int j = 0; j < w.n; ++j) {
+                const int key0 = (w.lo + j) * kKeys;
+                if (!partial(key0)) continue;
+                for (int key = max(key0, low + 1); key <= min(key0 + kKeys - 1, pos); ++key) {
+                    const int page = p.page_table[(int64_t)w.b * p.table_stride + key / P];
+                    if ((unsigned)page >= (unsigned)p.pages) continue;
+                    const uint8_t *code = p.v_cache + page * p.page_stride + w.h * p.head_stride + (int64_t)(key % P) * D;
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i)
+                        for (int d = 0; d < 32; ++d)
+                            if ((code[i * 32 + d] & 0x7F) == 0x7F) nan[i] |= 1u << d;
+                }
+            }
+        }
+        float *part = grid.splits > 1 ? part_of<D>(p, grid, w.unit, w.split) + r * D : nullptr;
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        uint16_t *out = p.out + (int64_t)(w.start + token) * p.o_token + head * p.o_head;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
+            if (w.n > 0) {
+                ptx::tmem_ld16(oc + c * 16, v);
+                ptx::tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = 0u;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (nan[c / 2] >> ((c & 1) * 16 + k) & 1u) v[k] = 0x7FFFFFFFu;
+            if (live) {
+                if (part != nullptr) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) *reinterpret_cast<uint4 *>(part + c * 16 + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                } else {
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = f32x2_to_bf16x2(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) *reinterpret_cast<uint2 *>(out + c * 16 + 2 * k) = make_uint2(o[k], o[k + 1]);
+                }
+            }
+        }
+        if (live) {
+            if (part != nullptr)
+                *reinterpret_cast<float2 *>(part_of<D>(p, grid, w.unit, w.split) + kRows * D + 2 * r) = make_float2(m, l);
+            else if (p.lse != nullptr)
+                p.lse[(w.start + token) * p.lse_token + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+        }
+        ptx::tc_fence_before();
+    } else if (warp < kProducer) {
+        // ------------------------------------------------ codes to fp16 operand tiles.
+        const int ct = tid - kSoftmaxWarps * 32;
+        bool ok = true;
+        int unit = 0;
+        for (int j = 0; j < w.n; ++j) {
+            const int key0 = (w.lo + j) * kKeys, buf = j % kBuf;
+            const bool mask = partial(key0);
+#pragma unroll 1
+            for (int which = 0; which < 2; ++which) {
+                uint64_t &full = which ? sm.v_full[buf] : sm.k_full[buf], &empty = which ? sm.v_empty[buf] : sm.k_empty[buf];
+                const uint32_t dst = ptx::smem_u32(which ? sm.v[buf] : sm.k[buf]);
+                if (ok && j >= kBuf) ok = ptx::mbar_wait(at(empty), (j / kBuf - 1) & 1, &g_prompt_timeouts);
+#pragma unroll 1
+                for (int u = 0; u < kKeys / kUnit; ++u, ++unit) {
+                    const int st = unit % kRaw;
+                    if (ok) ok = ptx::mbar_wait(at(sm.raw_full[st]), (unit / kRaw) & 1, &g_prompt_timeouts);
+                    constexpr int kChunks = kUnit * D / 16 / (kConvertWarps * 32);     // 16-code chunks of a thread
+                    uint4 x[kChunks];
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) x[i] = *reinterpret_cast<const uint4 *>(sm.raw[st] + (ct + i * 128) * 16);
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(at(sm.raw_empty[st]));
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int chunk = ct + i * 128, key = u * kUnit + chunk / (D / 16), c = chunk % (D / 16);
+                        uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, o[8];
+                        if (mask && which) {
+                            if (key0 + key >= w.len) in[0] = in[1] = in[2] = in[3] = 0u;
+                            uint32_t any = 0u;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t hit = (((in[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+                                in[k] &= ~(hit * 0xFFu);
+                                any |= hit;
+                            }
+                            if (any) sm.poisoned = 1;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2(in[k], o[2 * k], o[2 * k + 1]);
+                        // Chunk c of 16 values: 16-byte pieces 2 (c % 4) and + 1 of half c / 4.  Halves
+                        // alternate which piece goes first: eight lanes then fill all banks.
+                        const int half = c >> 2, sw = key & 7, first = (2 * (c & 3) + half) ^ sw, second = (2 * (c & 3) + (half ^ 1)) ^ sw;
+                        const uint32_t rowat = dst + half * 16384 + key * 128;
+                        if (half == 0) {
+                            sts_v4(rowat + (first << 4), o[0], o[1], o[2], o[3]);
+                            sts_v4(rowat + (second << 4), o[4], o[5], o[6], o[7]);
+                        } else {
+                            sts_v4(rowat + (first << 4), o[4], o[5], o[6], o[7]);
+                            sts_v4(rowat + (second << 4), o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(at(full));
+            }
+        }
+    } else if (warp == kProducer) {
+        // ------------------------------------------------ TMA producer: K then V of each step, 64 keys a unit.
+        const int parts = P < kUnit ? kUnit / P : 1, box = min(P, kUnit);
+        int unit = 0;
+        bool ok = true;
+        // Lane i looks up the page of the step's i-th 16 keys, a step ahead.
+        int page = -1, next = -1, ke = 0, ve = 0, nke = 0, nve = 0;
+        auto look = [&](int j) {
+            next = -1, nke = nve = 0;
+            const int key = (w.lo + j) * kKeys + (lane & 7) * 16;
+            if (j < w.n && key < w.len) {
+                next = p.page_table[(int64_t)w.b * p.table_stride + key / P];
+                if ((unsigned)next < (unsigned)p.pages) {
+                    nke = min(max((int)p.k_exp[(int64_t)next * p.Hk + w.h], kExpMin), kExpMax);
+                    nve = min(max((int)p.v_exp[(int64_t)next * p.Hk + w.h], kExpMin), kExpMax);
+                } else {
+                    next = p.pages;                                    // outside the cache: read as zeros
+                }
+            }
+        };
+        look(0);
+        for (int j = 0; j < w.n && ok; ++j) {
+            page = next, ke = nke, ve = nve;
+            look(j + 1);
+            // Steps back to j - kExps have long been weighed: K of step j - 2 is released after them.
+            if (lane < 8) sm.exps[j % kExps][lane] = make_float4(exp2_int(ke), (float)ve, exp2_int(-ve), 0.f);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(at(sm.e_full[j % kExps]));
+            for (int i = 0; i < 2 * (kKeys / kUnit) && ok; ++i, ++unit) {
+                const int u = i % (kKeys / kUnit), st = unit % kRaw;
+                if (unit >= kRaw)
+                    ok = __all_sync(~0u, ptx::mbar_wait(at(sm.raw_empty[st]), (unit / kRaw - 1) & 1, &g_prompt_timeouts));
+                if (!ok) break;
+                const int part = lane % parts, key = u * kUnit + part * box;
+                const int id = __shfl_sync(~0u, page, (key / 16) & 7);
+                const bool mine = lane < parts && id >= 0;
+                const uint32_t bytes = __popc(__ballot_sync(~0u, mine)) * (uint32_t)(box * D);
+                const uint32_t bar = at(sm.raw_full[st]);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+                __syncwarp();
+                if (mine)
+                    ptx::tma_load_4d(ptx::smem_u32(sm.raw[st]) + part * box * D, i < kKeys / kUnit ? &kmap : &vmap, 0,
+                                     ((w.lo + j) * kKeys + key) % P, w.h, id, bar);
+                __syncwarp();
+            }
+        }
+        for (int i = max(0, unit - kRaw); i < unit; ++i)
+            if (!ptx::mbar_wait(at(sm.raw_full[i % kRaw]), (i / kRaw) & 1, &g_prompt_timeouts)) break;
+    } else if (lane == 0) {
+        // ------------------------------------------------ MMA issuer.
+        const uint32_t qk = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);             // fp16 x fp16 -> fp32, M = 128
+        const uint32_t pv = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);    // B along N
+        bool ok = w.n > 0 && ptx::mbar_wait(at(sm.q_full), 0, &g_prompt_timeouts);
+        auto weighted = [&](int t, int j) {      // O_t += P_t V(j)
+            if (ok) ok = ptx::mbar_wait(at(sm.p_full[t]), j & 1, &g_prompt_timeouts);
+            if (ok) ok = ptx::mbar_wait(at(sm.v_full[j % kBuf]), (j / kBuf) & 1, &g_prompt_timeouts);
+            if (!ok) return;
+            ptx::tc_fence_after();
+            const uint64_t vd = sw128_mn_desc(ptx::smem_u32(sm.v[j % kBuf]), 16384);
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+                ptx::mma_f16_tmem_a(o_col[t], s_col[t] + k * 8, vd + (uint64_t)(k * (2048 >> 4)), pv, j > 0 || k > 0);
+        };
+        for (int j = 0; j < w.n && ok; ++j) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (j > 0) {
+                    weighted(t, j - 1);
+                    if (ok && t == 1) ptx::mma_commit(at(sm.v_empty[(j - 1) % kBuf]));
+                }
+                if (ok) ok = ptx::mbar_wait(at(sm.k_full[j % kBuf]), (j / kBuf) & 1, &g_prompt_timeouts);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t qd = ptx::sw128_desc(ptx::smem_u32(sm.q[t])), kd = ptx::sw128_desc(ptx::smem_u32(sm.k[j % kBuf]));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t off = (uint64_t)((k >> 2) * (16384 >> 4) + (k & 3) * 2);
+                    ptx::mma_f16(s_col[t], qd + off, kd + off, qk, k > 0);
+                }
+                ptx::mma_commit(at(sm.s_full[t]));
+                if (t == 1) ptx::mma_commit(at(sm.k_empty[j % kBuf]));
+            }
+        }
+        if (ok) {
+            weighted(0, w.n - 1);
+            weighted(1, w.n - 1);
+        }
+        if (w.n > 0) {
+            ptx::mma_commit(at(sm.o_full));
+            ptx::mbar_wait(at(sm.o_full), 0, &g_prompt_timeouts);      // nothing in flight when tensor memory is freed
+        }
+    }
+    __syncthreads();
+    if (warp == kIssuer) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the splits: block (unit, r) takes 8 rows of a unit, a warp each.
+template <int D>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const AttentionArgs p, const PromptGrid grid) {
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+    const Work w = work_of(p, grid, blockIdx.x * grid.splits);
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (!w.live || w.row0 + r >= w.nrows) return;
+    const int G = p.Hq / p.Hk, token = (w.row0 + r) / G, head = w.h * G + w.row0 + r - token * G;
+    constexpr int kPer = D / 32;
+    float m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+    for (int s = 0; s < grid.splits; ++s) {
+        if (work_of(p, grid, blockIdx.x * grid.splits + s).n == 0) continue;
+        const float *part = part_of<D>(p, grid, w.unit, s);
+        const float2 ml = *reinterpret_cast<const float2 *>(part + kRows * D + 2 * r);
+        const float mx = fmaxf(m, ml.x), ref = mx == -INFINITY ? 0.f : mx;
+        const float a = ex2(m - ref), b = ex2(ml.x - ref);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] = o[i] * a + part[r * D + lane * kPer + i] * b;
+        l = l * a + ml.y * b;
+        m = mx;
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    uint16_t *out = p.out + (int64_t)(w.start + token) * p.o_token + head * p.o_head + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2)
+        *reinterpret_cast<uint32_t *>(out + i) = f32x2_to_bf16x2(o[i] * inv, o[i + 1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[(w.start + token) * p.lse_token + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+}
+
+template <int D>
+cudaError_t launch(const AttentionArgs &p, const PromptGrid &g, cudaStream_t stream) {
+    const uint32_t box[4] = {(uint32_t)D, (uint32_t)std::min(p.P, kUnit), 1, 1};
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.P, (uint64_t)p.Hk, (uint64_t)p.pages};
+    const uint64_t strides[3] = {(uint64_t)D, (uint64_t)p.head_stride, (uint64_t)p.page_stride};
+    CUtensorMap kmap, vmap;
+    if (!encode_tiled(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.k_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_tiled(&vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.v_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    const int smem = (int)sizeof(Smem<D>) + 1024;
+    cudaError_t e = raise_smem_limit((const void *)prompt_kernel<D>, current_device(), smem);
+    if (e != cudaSuccess) return e;
+    const unsigned units = (unsigned)(g.tiles * p.Hk);
+    e = launch_pdl(prompt_kernel<D>, dim3(units * (unsigned)g.splits), dim3(kThreads), smem, stream, kmap, vmap, p, g);
+    if (e != cudaSuccess || g.splits == 1) return e;
+    return launch_pdl(prompt_join_kernel<D>, dim3(units, kRows / 8), dim3(256), 0, stream, p, g);
+}
+
+}  // namespace
+
+PromptGrid prompt_grid(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D) {
+    const int G = Hq / Hk;
+    PromptGrid g{};
+    g.tiles = uniform ? B * (int)(((int64_t)max_q * G + kRows - 1) / kRows) : (int)(T * G / kRows) + B;
+    // Keys are split only while CTAs are fewer than SMs.
+    g.splits = std::max(1, kSms / std::max(1, g.tiles * Hk));
+    return g;
+}
+
+size_t prompt_workspace_bytes(const PromptGrid &g, int Hk, int D) {
+    return g.splits == 1 ? 0 : (size_t)g.tiles * Hk * g.splits * kRows * (D + 2) * sizeof(float);
+}
+
+cudaError_t launch_prompt(const AttentionArgs &p, const PromptGrid &g, cudaStream_t stream) {
+    return p.D == 128 ? launch<128>(p, g, stream) : launch<64>(p, g, stream);
+}
+
+uint32_t prompt_timeouts(bool reset) {
+    unsigned int v = 0;
+    cudaMemcpyFromSymbol(&v, g_prompt_timeouts, sizeof(v));
+    if (reset) {
+        const unsigned int zero = 0;
+        cudaMemcpyToSymbol(g_prompt_timeouts, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace lowbit
