@@ -96,8 +96,10 @@ lowbit_status check_cache(const lowbit_cache *c, const lowbit_sequences *s, int 
         (c->head_dim != 64 && c->head_dim != 128))
         return LOWBIT_EINVAL;
     if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) != 0) return LOWBIT_EINVAL;
-    // Rows (tokens times heads of a group) and lengths stay inside int32.
-    if ((int64_t)s->tokens * (heads / c->kv_heads) > kMaxDim || (int64_t)s->width * c->page > kMaxDim) return LOWBIT_EINVAL;
+    // Rows (tokens times heads of a group), lengths and a sequence's tiles stay inside int32.
+    if ((int64_t)s->tokens * (heads / c->kv_heads) > kMaxDim || (int64_t)s->width * c->page > kMaxDim ||
+        (int64_t)s->width * c->page * c->kv_heads > (int64_t)1 << 34)
+        return LOWBIT_EINVAL;
     if (s->batch == 0 || s->tokens == 0) return LOWBIT_OK;
     if (s->cu_q == nullptr ? s->tokens % s->batch != 0 : s->max_q <= 0) return LOWBIT_EINVAL;
     if (c->pages == 0 || s->width == 0 || s->table_stride < s->width) return LOWBIT_EINVAL;
@@ -290,7 +292,7 @@ size_t lowbit_attention_workspace(int32_t heads, const lowbit_cache *c, const lo
         return 0;
     const bool uniform = s->cu_q == nullptr;
     return lowbit::attention_workspace_bytes(s->tokens, s->batch, uniform ? s->tokens / s->batch : s->max_q, uniform,
-                                             heads, c->kv_heads, c->head_dim);
+                                             heads, c->kv_heads, c->head_dim, (int64_t)s->width * c->page);
 }
 
 lowbit_status lowbit_attention(const lowbit_attention_args *a, const lowbit_cache *c, const lowbit_sequences *s,

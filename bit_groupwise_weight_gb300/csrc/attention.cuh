@@ -14,7 +14,7 @@ struct PromptGrid {
     int tiles, splits;
     int64_t workspace;
 };
-PromptGrid prompt_grid(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D);
+PromptGrid prompt_grid(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int64_t max_len);
 size_t prompt_workspace_bytes(const PromptGrid &g, int Hk, int D);
 cudaError_t launch_prompt(const AttentionArgs &p, const PromptGrid &g, cudaStream_t stream);
 uint32_t prompt_timeouts(bool reset);
@@ -40,7 +40,7 @@ struct Span { int start, n, len; };
 __device__ __forceinline__ Span span(const AttentionArgs &p, int b) {
     Span s;
     if (p.cu_q == nullptr) {
-        s.n = p.T / p.B;
+        s.n = p.n;
         s.start = b * s.n;
     } else {
         s.start = min(max(p.cu_q[b], 0), p.T);

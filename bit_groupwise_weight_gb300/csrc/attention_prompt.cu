@@ -564,12 +564,13 @@ cudaError_t launch(const AttentionArgs &p, const PromptGrid &g, cudaStream_t str
 
 }  // namespace
 
-PromptGrid prompt_grid(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D) {
+PromptGrid prompt_grid(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int64_t max_len) {
     const int G = Hq / Hk;
     PromptGrid g{};
     g.tiles = uniform ? B * (int)(((int64_t)max_q * G + kRows - 1) / kRows) : (int)(T * G / kRows) + B;
-    // Keys are split only while CTAs are fewer than SMs.
-    g.splits = std::max(1, kSms / std::max(1, g.tiles * Hk));
+    // Keys are split only while CTAs are fewer than SMs, into no less than two steps each.
+    const int64_t steps = std::max<int64_t>(1, max_len / (2 * kKeys));
+    g.splits = (int)std::min<int64_t>(steps, std::max(1, kSms / std::max(1, g.tiles * Hk)));
     return g;
 }
 

@@ -200,9 +200,10 @@ struct AttentionArgs {
     int64_t page_stride, head_stride, table_stride;
     float scale_log2;                    // softmax scale * log2(e)
     int T, B, max_q, Hq, Hk, D, P, pages, width, window;
+    int G, n, pshift;                    // Hq / Hk; tokens a sequence without cu_q; log2 P (set by launch_attention)
     int few_rows;                        // more query rows than this: a sequence for the prompt kernel
 };
-size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D);
+size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D, int64_t max_len);
 cudaError_t launch_attention(const AttentionArgs &args, cudaStream_t stream);
 uint32_t attention_timeouts(bool reset);
 // A token for each row of logits (sample.cu).  Per-row settings may be null:

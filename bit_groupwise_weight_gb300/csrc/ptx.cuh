@@ -274,6 +274,10 @@ __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const void *tmap,
         ::"r"(dst), "l"(tmap), "r"(c0), "r"(c1), "r"(bar), "l"(policy) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_tensormap(const void *tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+
 // 4D box at coordinates (c0 innermost .. c3); c0 * element size a multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int c0, int c1, int c2, int c3,
                                             uint32_t bar) {
