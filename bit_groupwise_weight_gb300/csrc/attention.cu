@@ -26,7 +26,8 @@
 //
 // Work split.  An item is (sequence, kv head, tile of 8 or 16 rows), the rows being
 // the new tokens times the heads of the group; its keys come in tiles of 64.  All
-// items' tiles form one list, cut into equal ranges, one per CTA: sequences of any
+// items' tiles form one list, each item's preceded by kItemCost units that stand for
+// its other cost, and the list is cut into equal ranges, one per CTA: sequences of any
 // lengths fill the machine evenly.  An item that a cut divides leaves its parts'
 // (m, l, O) in the workspace, and a second launch joins them.
 //
@@ -49,7 +50,8 @@ using namespace attn;
 constexpr int kTile = 64;                        // keys of a stage
 constexpr int kWarps = 4;                        // consumer warps, 16 keys each
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kMinTiles = 4;                     // of a CTA's range
+constexpr int kItemCost = 6;                     // what an item costs beside its tiles, in tiles
+constexpr int kMinChunk = 7;                     // of a CTA's range
 constexpr int kCtas = kSms * 3;                  // at most
 constexpr float kLag = 8.f;
 
@@ -84,7 +86,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) { return (((v & 0x7F7F
 struct Seq : Span {
     int lo, nt;             // first key tile and number of tiles
     int rt;                 // row tiles; none for a sequence of the prompt kernel
-    __device__ long long tiles(const AttentionArgs &p) const { return (long long)nt * (rt * p.Hk); }
+    __device__ long long units(const AttentionArgs &p) const { return (long long)(kItemCost + nt) * (rt * p.Hk); }
 };
 
 template <int ROWS>
@@ -98,20 +100,20 @@ __device__ __forceinline__ Seq sequence(const AttentionArgs &p, int b) {
     return s;
 }
 
-// A place in the list: sequence b, item (h, rt) and tile t of it; `before`: tiles of
-// earlier sequences.
+// A place in the list: sequence b, item (h, rt) and tile t of it (below 0: before its
+// first tile); `before`: units of earlier sequences.
 struct Place { int b, h, rt, t; long long before; };
 
 // Moves pl forward to the place `idx`.
 template <int ROWS>
 __device__ __forceinline__ Seq locate(const AttentionArgs &p, long long idx, Place &pl) {
     Seq s = sequence<ROWS>(p, pl.b);
-    while (idx - pl.before >= s.tiles(p) && pl.b + 1 < p.B) {
-        pl.before += s.tiles(p);
+    while (idx - pl.before >= s.units(p) && pl.b + 1 < p.B) {
+        pl.before += s.units(p);
         s = sequence<ROWS>(p, ++pl.b);
     }
-    const uint32_t in = (uint32_t)(idx - pl.before), item = in / (uint32_t)s.nt;
-    pl.t = (int)(in - item * (uint32_t)s.nt);
+    const uint32_t in = (uint32_t)(idx - pl.before), each = (uint32_t)(kItemCost + s.nt), item = in / each;
+    pl.t = (int)(in - item * each) - kItemCost;
     pl.h = s.rt > 1 ? (int)item / s.rt : (int)item;
     pl.rt = (int)item - pl.h * s.rt;
     return s;
@@ -124,14 +126,14 @@ struct Plan { long long begin, end, chunk; Place pl; };
 template <int ROWS>
 __device__ __forceinline__ Plan make_plan(const AttentionArgs &p, int cta, int ctas) {
     const int lane = threadIdx.x & 31;
-    auto weight = [&](int b) { return b < p.B ? sequence<ROWS>(p, b).tiles(p) : 0ll; };
+    auto weight = [&](int b) { return b < p.B ? sequence<ROWS>(p, b).units(p) : 0ll; };
     const long long w0 = weight(lane);
     long long total = w0;
     for (int b = lane + 32; b < p.B; b += 32) total += weight(b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
     Plan r;
-    r.chunk = total <= (long long)ctas * kMinTiles ? kMinTiles : (total + ctas - 1) / ctas;
+    r.chunk = total <= (long long)ctas * kMinChunk ? kMinChunk : (total + ctas - 1) / ctas;
     r.begin = min((long long)cta * r.chunk, total);
     r.end = min(r.begin + r.chunk, total);
     r.pl = Place{0, 0, 0, 0, 0};
@@ -367,23 +369,36 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
         const int pshift = p.pshift, page_keys = 1 << pshift;
         const int parts = page_keys < kTile ? kTile >> pshift : 1;       // pages of a tile
         const int pbits = page_keys < kTile ? 6 - pshift : 0, part = lane & (parts - 1);
-        const int ahead = 32 >> pbits;                                   // tiles of a window
         const int box = min(page_keys, kTile);
         const uint32_t off = (uint32_t)(part * box * D);
-        int n_page = -1, n_row = 0, n_head = 0, n_ke = 0, n_ve = 0;
-        auto look_up = [&](long long w0) {                               // window that starts at tile w0 of the list
-            const long long idx = w0 + (lane >> pbits);
+        int n_page = -1, n_row = 0, n_head = 0, n_ke = 0, n_ve = 0, n_tiles = 0;
+        long long next = plan.begin;                                     // unit from which the next window's tiles are counted
+        auto look_up = [&] {
+            long long u = next;
+            int i = lane >> pbits;                                       // this lane's tile of the window
+            bool found = false;
             n_page = -1;                                                 // nothing to fetch
-            if (idx < plan.end) {
-                const Seq s = locate<ROWS>(p, idx, pl);
-                const int key = (s.lo + pl.t) * kTile + part * box;
-                n_head = pl.h;
-                n_row = key & (page_keys - 1);
-                if (key < s.len) {
-                    n_page = p.page_table[(int64_t)pl.b * p.table_stride + (key >> pshift)];
-                    if (n_page < 0) n_page = p.pages;                    // outside the cache: read as zeros
+            while (u < plan.end) {
+                const Seq s = locate<ROWS>(p, u, pl);
+                const int t = max(pl.t, 0), left = (int)min((long long)(s.nt - t), plan.end - u - (t - pl.t));
+                u += t - pl.t;
+                if (i < left) {
+                    u += i;
+                    found = true;
+                    const int key = (s.lo + t + i) * kTile + part * box;
+                    n_head = pl.h;
+                    n_row = key & (page_keys - 1);
+                    if (key < s.len) {
+                        n_page = p.page_table[(int64_t)pl.b * p.table_stride + (key >> pshift)];
+                        if (n_page < 0) n_page = p.pages;                // outside the cache: read as zeros
+                    }
+                    break;
                 }
+                i -= max(left, 0);
+                u += max(left, 0);
             }
+            n_tiles = __popc(__ballot_sync(~0u, found)) >> pbits;
+            next = __shfl_sync(~0u, u, 31) + 1;
         };
         auto look_up_exps = [&] {
             n_ke = n_ve = 0;
@@ -392,17 +407,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
                 n_ve = p.v_exp[(int64_t)n_page * p.Hk + n_head];
             }
         };
-        look_up(plan.begin);
+        look_up();
         look_up_exps();
         bool ok = true;
         int issued = 0, st = 0;
         uint32_t round = 1;                                              // parity of the stage's last release
-        for (long long w0 = plan.begin; w0 < plan.end && ok; w0 += ahead) {
-            const int page = n_page, row = n_row, head = n_head, ke = n_ke, ve = n_ve;
-            if (w0 + ahead < plan.end) look_up(w0 + ahead);
-            const int cnt = (int)min((long long)ahead, plan.end - w0);
-            for (int i = 0; i < cnt; ++i, ++issued) {
-                if (i == cnt / 2 && w0 + ahead < plan.end) look_up_exps();
+        while (n_tiles > 0 && ok) {
+            const int page = n_page, row = n_row, head = n_head, ke = n_ke, ve = n_ve, cnt = n_tiles;
+            n_tiles = 0;
+            if (cnt == 32 >> pbits && next < plan.end) look_up();
+            for (int i = 0; i < cnt; ++i) {
+                if (i == cnt / 2 && n_tiles > 0) look_up_exps();
                 if (issued >= S)
                     ok = __all_sync(~0u, ptx::mbar_wait(ptx::smem_u32(&sm.empty[st]), round, &g_attn_timeouts));
                 if (!ok) break;
@@ -420,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
                     sm.exps[st][lane] = make_int2(min(max(ske, kExpMin), kExpMax), min(max(sve, kExpMin), kExpMax));
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+                ++issued;
                 if (++st == S) st = 0, round ^= 1;
             }
         }
@@ -440,7 +456,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
     State<D, ROWS> a;
     for (long long idx = plan.begin; idx < plan.end;) {
         const Seq s = locate<ROWS>(p, idx, pl);
-        const int cnt = (int)min((long long)(s.nt - pl.t), plan.end - idx);
+        const int units = (int)min((long long)(s.nt - pl.t), plan.end - idx);
+        const int t0 = max(pl.t, 0), cnt = pl.t + units - t0;            // this CTA's tiles of the item
+        const long long item_end = idx + (s.nt - pl.t);
+        idx += units;
+        if (cnt <= 0) continue;
         const int nrows = s.n * p.G, row0 = pl.rt * ROWS, first = s.len - s.n;
 
         // Query fragments: fp16, each row times a power of two.
@@ -482,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
         }
         const int pos_lo = first + row0 / p.G, pos_hi = first + (min(row0 + ROWS, nrows) - 1) / p.G;
 
-        int key0 = (s.lo + pl.t) * kTile + warp * 16;
+        int key0 = (s.lo + t0) * kTile + warp * 16;
         for (int tile = 0; tile < cnt; ++tile, key0 += kTile) {
             if (ok) ok = ptx::mbar_wait(ptx::smem_u32(&sm.full[st]), round, &g_attn_timeouts);
             const uint32_t kat = ptx::smem_u32(sm.k[st]) + moff, vat = ptx::smem_u32(sm.v[st]) + moff;
@@ -496,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
         }
 
         // The warps' parts of the item are joined in shared memory, 8 rows at a time.
-        const bool continued = pl.t > 0, unfinished = pl.t + cnt < s.nt;
+        const bool continued = t0 > 0, unfinished = t0 + cnt < s.nt;
         float *slot = slot_of<D, ROWS>(p, 2 * (int)blockIdx.x + (continued ? 0 : 1));
 #pragma unroll
         for (int n = 0; n < N; ++n) {
@@ -536,14 +556,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
             }
             ptx::named_sync(1, kWarps * 32);
         }
-        idx += cnt;
         if (unfinished && !continued) {
             // The CTA that begins a divided item describes it to the join.
             cut = true;
-            if (tid == 0) {
-                const long long item_end = idx - cnt + s.nt;             // pl.t is 0 here
+            if (tid == 0)
                 *cut_of(p, blockIdx.x) = Cut{(int)((item_end - 1) / plan.chunk) - (int)blockIdx.x + 1, s.start, nrows, row0, pl.h, {}};
-            }
         }
     }
     if (!cut && tid == 0) cut_of(p, blockIdx.x)->parts = 0;
@@ -601,11 +618,11 @@ cudaError_t launch(const AttentionArgs &p, cudaStream_t stream) {
     const int smem = (int)sizeof(Smem<D, ROWS>) + 1024;
     cudaError_t e = raise_smem_limit((const void *)attention_kernel<D, ROWS>, current_device(), smem);
     if (e != cudaSuccess) return e;
-    // No more CTAs than ranges of kMinTiles that the page table allows.
+    // No more CTAs than ranges of kMinChunk that the page table allows.
     const int rows_max = (int)std::min<int64_t>((int64_t)p.max_q * p.G, p.few_rows);
     const int64_t items = (int64_t)p.B * p.Hk * ((rows_max + ROWS - 1) / ROWS);
     const int64_t tiles = ((int64_t)p.width * p.P + kTile - 1) / kTile;
-    const int ctas = (int)std::min<int64_t>(kSms * kPerSm<D, ROWS>, std::max<int64_t>(1, (items * tiles + kMinTiles - 1) / kMinTiles));
+    const int ctas = (int)std::min<int64_t>(kSms * kPerSm<D, ROWS>, std::max<int64_t>(1, (items * (kItemCost + tiles) + kMinChunk - 1) / kMinChunk));
     e = launch_pdl(attention_kernel<D, ROWS>, dim3(ctas), dim3(kThreads), smem, stream, kmap, vmap, p);
     // A tile list of one range each needs no join.
     if (e != cudaSuccess || ctas == 1) return e;

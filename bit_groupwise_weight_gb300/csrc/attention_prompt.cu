@@ -15,8 +15,9 @@
 //
 // Tensor memory (512 columns): S of both tiles (128 fp32 columns each; the fp16
 // weights P take the place of the S they come from), O of both tiles.
-// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (one thread a row), 8-11 turn e4m3
-// codes into fp16 operand tiles (once per 256 rows), 12 TMA producer, 13 MMA issuer.
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (one thread a row, which holds the
+// row's 128 scores in registers: 184 a thread, taken from the other warps), 8-11 turn
+// e4m3 codes into fp16 operand tiles (once per 256 rows), 12 TMA producer, 13 MMA issuer.
 // Order of the issuer, which keeps a tile's S free while its P is read:
 //     PV0(j-1) QK0(j) PV1(j-1) QK1(j) ...
 // Bound: the tensor cores, 4 D flops per row and key; at 128 x 128 x 128 a product
@@ -39,7 +40,8 @@ constexpr int kBuf = 2;                          // fp16 K and V tiles
 constexpr int kExps = 8;                         // steps whose page exponents are kept
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kProducer = 12, kIssuer = 13;
-constexpr int kThreads = 14 * 32;
+constexpr int kThreads = 16 * 32;              // whole warpgroups, for the register split
+constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kOtherRegs = 64;   // 2 x 184 + 80 + 64 = 4 x 128
 constexpr float kLag = 8.f;
 
 __device__ unsigned int g_prompt_timeouts;
@@ -66,16 +68,30 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr, uint32_t l
            ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
         "%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(taddr));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // The CTA's part of the work.
@@ -170,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kSoftmaxWarps) {
         // ------------------------------------------------ softmax: a thread owns a row.
+        more_registers<kSoftmaxRegs>();
         const int t = warp >> 2, r = t * 128 + (warp & 3) * 32 + lane, row = w.row0 + r;
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         const bool live = row < w.nrows;
@@ -216,30 +233,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ok = ptx::mbar_wait(at(sm.s_full[t]), j & 1, &g_prompt_timeouts);
             ptx::tc_fence_after();
             const float4 *ex = sm.exps[j % kExps];
-            // Pass 1: the row's maximum, by 16 keys (one page at least).
-            float mx = -INFINITY;
+            float v[kKeys];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                tmem_ld32(sc + c * 32, v);
-                ptx::tmem_ld_wait();
+            for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, v + c * 32);
+            ptx::tmem_ld_wait();
+            if (mask) {
+                const int hi = pos - key0, lo = low - key0;            // of the step's keys, those in (lo, hi] are seen
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float x = -INFINITY;
-                    const float4 e = ex[2 * c + g];
-                    if (mask) {
+                for (int k = 0; k < kKeys; ++k)
+                    if (k > hi || k <= lo) v[k] = -INFINITY;
+            }
+            // The row's maximum, by 16 keys (one page at least).  A factor of 0 would make
+            // masked scores NaN.
+            float mx = -INFINITY, f[kKeys / 16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int key = key0 + c * 32 + g * 16 + k;
-                            if (key <= pos && key > low) x = fmaxf(x, __uint_as_float(v[g * 16 + k]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) x = fmaxf(x, __uint_as_float(v[g * 16 + k]));
-                    }
-                    // No key seen: stays -infinity whatever the page's exponents.
-                    mx = fmaxf(mx, x == -INFINITY ? x : fmaf(x, qs * e.x, e.y));
-                }
+            for (int g = 0; g < kKeys / 16; ++g) {
+                const float *x = v + g * 16;
+                f[g] = fmaxf(qs * ex[g].x, 1.2e-38f);
+                const float a = max3(max3(x[0], x[1], x[2]), x[3], x[4]), b = max3(max3(x[5], x[6], x[7]), x[8], x[9]);
+                const float c = max3(max3(x[10], x[11], x[12]), x[13], x[14]);
+                mx = fmaxf(mx, fmaf(max3(max3(a, b, c), x[15], x[15]), f[g], ex[g].y));
             }
             // The maximum in use follows when it lags by more than kLag.
             const bool move = mx > m + kLag || (m == -INFINITY && mx > m);
@@ -260,30 +273,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            // Pass 2: weights, their sum, and fp16 pairs over the scores they come from.
+            // Weights, their sum, and fp16 pairs in the place of the scores.
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t v[32], h[16];
-                tmem_ld32(sc + c * 32, v);
-                ptx::tmem_ld_wait();
+                uint32_t h[16];
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const float4 e = ex[2 * c + g];
-                    const float f = qs * e.x, d = e.y - ref;
-                    float sum = 0.f;
+                    const float2 ff = make_float2(f[2 * c + g], f[2 * c + g]), d = make_float2(e.y - ref, e.y - ref);
+                    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
-                        float x = ex2(fmaf(__uint_as_float(v[g * 16 + k]), f, d));
-                        float y = ex2(fmaf(__uint_as_float(v[g * 16 + k + 1]), f, d));
-                        if (mask) {
-                            const int key = key0 + c * 32 + g * 16 + k;
-                            if (!(key <= pos && key > low)) x = 0.f;
-                            if (!(key + 1 <= pos && key + 1 > low)) y = 0.f;
-                        }
-                        sum += x + y;
-                        h[g * 8 + k / 2] = f32x2_to_f16x2(x, y);
+                        float2 x = make_float2(v[c * 32 + g * 16 + k], v[c * 32 + g * 16 + k + 1]);
+                        ptx::ffma2(x, x, ff, d);
+                        x.x = ex2(x.x), x.y = ex2(x.y);
+                        sum = ptx::fadd2(sum, x);
+                        h[g * 8 + k / 2] = f32x2_to_f16x2(x.x, x.y);
                     }
-                    l = fmaf(sum, e.z, l);
+                    l = fmaf(sum.x + sum.y, e.z, l);
                 }
                 ptx::tmem_st16(sc + c * 16, h);
             }
@@ -356,7 +363,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_before();
     } else if (warp < kProducer) {
         // ------------------------------------------------ codes to fp16 operand tiles.
-        const int ct = tid - kSoftmaxWarps * 32;
+        fewer_registers<kConvertRegs>();
+        // A thread's 16-code chunks of a unit: chunk c of every 128 * 16 / D-th key, so all
+        // addresses but the key's are the thread's own.  A chunk makes the 16-byte pieces
+        // 2 (c % 4) and + 1 of half c / 4 of the key's row; halves alternate which piece goes
+        // first: eight lanes then fill all banks.
+        constexpr int kChunks = kUnit * D / 16 / (kConvertWarps * 32), kStep = 128 * 16 / D;
+        const int ct = tid - kSoftmaxWarps * 32, c = ct % (D / 16), key_in = ct / (D / 16), half = c >> 2, sw = key_in & 7;
+        const uint32_t row_off = half * 16384 + key_in * 128;
+        const uint32_t first = row_off + (((2 * (c & 3) + half) ^ sw) << 4), second = row_off + (((2 * (c & 3) + (half ^ 1)) ^ sw) << 4);
         bool ok = true;
         int unit = 0;
         for (int j = 0; j < w.n; ++j) {
@@ -371,40 +386,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < kKeys / kUnit; ++u, ++unit) {
                     const int st = unit % kRaw;
                     if (ok) ok = ptx::mbar_wait(at(sm.raw_full[st]), (unit / kRaw) & 1, &g_prompt_timeouts);
-                    constexpr int kChunks = kUnit * D / 16 / (kConvertWarps * 32);     // 16-code chunks of a thread
                     uint4 x[kChunks];
 #pragma unroll
                     for (int i = 0; i < kChunks; ++i) x[i] = *reinterpret_cast<const uint4 *>(sm.raw[st] + (ct + i * 128) * 16);
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(at(sm.raw_empty[st]));
+                    if (mask && which) {
+                        // Codes past the end, and NaN that not all rows may see, are cleared.
 #pragma unroll
-                    for (int i = 0; i < kChunks; ++i) {
-                        const int chunk = ct + i * 128, key = u * kUnit + chunk / (D / 16), c = chunk % (D / 16);
-                        uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, o[8];
-                        if (mask && which) {
-                            if (key0 + key >= w.len) in[0] = in[1] = in[2] = in[3] = 0u;
-                            uint32_t any = 0u;
+                        for (int i = 0; i < kChunks; ++i) {
+                            uint32_t *in = reinterpret_cast<uint32_t *>(&x[i]), any = 0u;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
+                                if (key0 + u * kUnit + key_in + i * kStep >= w.len) in[k] = 0u;
                                 const uint32_t hit = (((in[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
                                 in[k] &= ~(hit * 0xFFu);
                                 any |= hit;
                             }
                             if (any) sm.poisoned = 1;
                         }
+                    }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2(in[k], o[2 * k], o[2 * k + 1]);
-                        // Chunk c of 16 values: 16-byte pieces 2 (c % 4) and + 1 of half c / 4.  Halves
-                        // alternate which piece goes first: eight lanes then fill all banks.
-                        const int half = c >> 2, sw = key & 7, first = (2 * (c & 3) + half) ^ sw, second = (2 * (c & 3) + (half ^ 1)) ^ sw;
-                        const uint32_t rowat = dst + half * 16384 + key * 128;
-                        if (half == 0) {
-                            sts_v4(rowat + (first << 4), o[0], o[1], o[2], o[3]);
-                            sts_v4(rowat + (second << 4), o[4], o[5], o[6], o[7]);
-                        } else {
-                            sts_v4(rowat + (first << 4), o[4], o[5], o[6], o[7]);
-                            sts_v4(rowat + (second << 4), o[0], o[1], o[2], o[3]);
-                        }
+                    for (int i = 0; i < kChunks; ++i) {
+                        uint32_t o[8];
+                        e4m3x4_to_f16x2(x[i].x, o[0], o[1]);
+                        e4m3x4_to_f16x2(x[i].y, o[2], o[3]);
+                        e4m3x4_to_f16x2(x[i].z, o[4], o[5]);
+                        e4m3x4_to_f16x2(x[i].w, o[6], o[7]);
+                        const uint32_t key_at = dst + (u * kUnit + i * kStep) * 128;
+                        const bool flip = half != 0;                     // piece `first` holds the upper 8 values
+                        sts_v4(key_at + first, flip ? o[4] : o[0], flip ? o[5] : o[1], flip ? o[6] : o[2], flip ? o[7] : o[3]);
+                        sts_v4(key_at + second, flip ? o[0] : o[4], flip ? o[1] : o[5], flip ? o[2] : o[6], flip ? o[3] : o[7]);
                     }
                 }
                 ptx::fence_proxy_async_smem();
@@ -412,32 +424,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(at(full));
             }
         }
-    } else if (warp == kProducer) {
+    } else if (warp >= kProducer) {
+        fewer_registers<kOtherRegs>();
+    }
+    if (warp == kProducer) {
         // ------------------------------------------------ TMA producer: K then V of each step, 64 keys a unit.
         const int parts = P < kUnit ? kUnit / P : 1, box = min(P, kUnit);
         int unit = 0;
         bool ok = true;
-        // Lane i looks up the page of the step's i-th 16 keys, a step ahead.
+        // Lane 8 i + k looks up the page of the k-th 16 keys of step i of four, a window ahead.
         int page = -1, next = -1, ke = 0, ve = 0, nke = 0, nve = 0;
         auto look = [&](int j) {
-            next = -1, nke = nve = 0;
-            const int key = (w.lo + j) * kKeys + (lane & 7) * 16;
-            if (j < w.n && key < w.len) {
-                next = p.page_table[(int64_t)w.b * p.table_stride + key / P];
-                if ((unsigned)next < (unsigned)p.pages) {
-                    nke = min(max((int)p.k_exp[(int64_t)next * p.Hk + w.h], kExpMin), kExpMax);
-                    nve = min(max((int)p.v_exp[(int64_t)next * p.Hk + w.h], kExpMin), kExpMax);
-                } else {
-                    next = p.pages;                                    // outside the cache: read as zeros
-                }
+            next = -1;
+            const int key = (w.lo + j + (lane >> 3)) * kKeys + (lane & 7) * 16;
+            if (j + (lane >> 3) < w.n && key < w.len) {
+                next = p.page_table[(int64_t)w.b * p.table_stride + (key >> p.pshift)];
+                if (next < 0) next = p.pages;                          // outside the cache: read as zeros
+            }
+        };
+        auto look_exps = [&] {
+            nke = nve = 0;
+            if ((unsigned)next < (unsigned)p.pages) {
+                nke = p.k_exp[(int64_t)next * p.Hk + w.h];
+                nve = p.v_exp[(int64_t)next * p.Hk + w.h];
             }
         };
         look(0);
+        look_exps();
         for (int j = 0; j < w.n && ok; ++j) {
-            page = next, ke = nke, ve = nve;
-            look(j + 1);
+            if ((j & 3) == 0) {
+                page = next, ke = min(max(nke, kExpMin), kExpMax), ve = min(max(nve, kExpMin), kExpMax);
+                look(j + 4);
+            } else if ((j & 3) == 2) {
+                look_exps();
+            }
             // Steps back to j - kExps have long been weighed: K of step j - 2 is released after them.
-            if (lane < 8) sm.exps[j % kExps][lane] = make_float4(exp2_int(ke), (float)ve, exp2_int(-ve), 0.f);
+            if ((lane >> 3) == (j & 3)) sm.exps[j % kExps][lane & 7] = make_float4(exp2_int(ke), (float)ve, exp2_int(-ve), 0.f);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(at(sm.e_full[j % kExps]));
             for (int i = 0; i < 2 * (kKeys / kUnit) && ok; ++i, ++unit) {
@@ -446,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(~0u, ptx::mbar_wait(at(sm.raw_empty[st]), (unit / kRaw - 1) & 1, &g_prompt_timeouts));
                 if (!ok) break;
                 const int part = lane % parts, key = u * kUnit + part * box;
-                const int id = __shfl_sync(~0u, page, (key / 16) & 7);
+                const int id = __shfl_sync(~0u, page, (j & 3) * 8 + ((key / 16) & 7));
                 const bool mine = lane < parts && id >= 0;
                 const uint32_t bytes = __popc(__ballot_sync(~0u, mine)) * (uint32_t)(box * D);
                 const uint32_t bar = at(sm.raw_full[st]);
@@ -454,13 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (mine)
                     ptx::tma_load_4d(ptx::smem_u32(sm.raw[st]) + part * box * D, i < kKeys / kUnit ? &kmap : &vmap, 0,
-                                     ((w.lo + j) * kKeys + key) % P, w.h, id, bar);
+                                     ((w.lo + j) * kKeys + key) & (P - 1), w.h, id, bar);
                 __syncwarp();
             }
         }
         for (int i = max(0, unit - kRaw); i < unit; ++i)
             if (!ptx::mbar_wait(at(sm.raw_full[i % kRaw]), (i / kRaw) & 1, &g_prompt_timeouts)) break;
-    } else if (lane == 0) {
+    } else if (warp == kIssuer && lane == 0) {
         // ------------------------------------------------ MMA issuer.
         const uint32_t qk = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);             // fp16 x fp16 -> fp32, M = 128
         const uint32_t pv = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);    // B along N
