@@ -55,7 +55,7 @@ struct Smem {
     alignas(1024) uint8_t raw[kRaw][kRawBytes];
     float4 exps[kExps][kKeys / 16];              // 2^ke, ve, 2^-ve of each 16 keys
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBuf], k_empty[kBuf], v_full[kBuf], v_empty[kBuf];
-    uint64_t q_full, s_full[2], p_full[2], o_full, e_full[kExps];
+    uint64_t q_full, s_full[2], p_full[2][2], o_full, e_full[kExps];
     uint32_t tmem;
     int poisoned;
 };
@@ -80,6 +80,33 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *r) {
         : "r"(taddr));
 }
 
+// The MMA issuer runs as a whole warp and elects the issuing lane in each instruction:
+// with the control flow uniform, descriptors stay in uniform registers.  Issued from a
+// lane-0 branch instead, each product took 90 cycles to issue and the tensor cores
+// waited.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -98,13 +125,16 @@ __device__ __forceinline__ void fewer_registers() {
 struct Work {
     int b, h, row0, nrows, start, first, len;    // rows row0 .. of nrows; first: position of the first new token
     int lo, n;                                   // first step of 128 keys, and how many
+    int steps;                                   // of all splits together
     int split, unit;
     bool live;
+    // Whether split s of `splits` has any keys.
+    __device__ bool holds(int s, int splits) const { return (int64_t)steps * s / splits < (int64_t)steps * (s + 1) / splits; }
 };
 
 __device__ __forceinline__ Work work_of(const AttentionArgs &p, const PromptGrid &g, int id) {
     Work w{};
-    const int G = p.Hq / p.Hk;
+    const int G = p.G;
     // Ids count down over the row tiles, so that tiles with the most keys start first.
     w.split = id % g.splits;
     w.unit = id / g.splits;
@@ -135,11 +165,12 @@ __device__ __forceinline__ Work work_of(const AttentionArgs &p, const PromptGrid
     const int lo = p.window > 0 ? max(pos_lo - p.window + 1, 0) / kKeys : 0;
     const int n = pos_hi >= 0 ? pos_hi / kKeys + 1 - lo : 0;
     const int a = (int)((int64_t)n * w.split / g.splits), e = (int)((int64_t)n * (w.split + 1) / g.splits);
-    w.lo = lo + a, w.n = e - a;
+    w.lo = lo + a, w.n = e - a, w.steps = n;
     return w;
 }
 
-// Workspace of a (unit, split): 256 x D sums, then 256 (m, l) pairs.
+// Workspace of a (unit, split): D / 4 groups of four sums of each of the 256 rows, then
+// the rows' (m, l) pairs.
 template <int D>
 __device__ __forceinline__ float *part_of(const AttentionArgs &p, const PromptGrid &g, int unit, int split) {
     return p.workspace + g.workspace + ((int64_t)unit * g.splits + split) * (kRows * (D + 2));
@@ -159,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(at(sm.k_full[i]), kConvertWarps), ptx::mbar_init(at(sm.k_empty[i]), 1);
             ptx::mbar_init(at(sm.v_full[i]), kConvertWarps), ptx::mbar_init(at(sm.v_empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(at(sm.s_full[i]), 1), ptx::mbar_init(at(sm.p_full[i]), 4);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(at(sm.s_full[i]), 1), ptx::mbar_init(at(sm.p_full[i][0]), 4), ptx::mbar_init(at(sm.p_full[i][1]), 4);
         for (int i = 0; i < kExps; ++i) ptx::mbar_init(at(sm.e_full[i]), 1);
         ptx::mbar_init(at(sm.q_full), kSoftmaxWarps);
         ptx::mbar_init(at(sm.o_full), 1);
@@ -193,31 +224,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int token = live ? row / G : 0, head = w.h * G + (live ? row - token * G : 0);
         const int pos = live ? w.first + token : -1;
         const int low = p.window > 0 ? pos - p.window : -1;    // keys low < key <= pos are seen
-        float qs;
-        {
-            // The row of q as fp16 times a power of two, into the swizzled operand tile.
-            const uint16_t *q = p.q + (int64_t)(w.start + token) * p.q_token + head * p.q_head;
-            float amax = 0.f;
+        float qs = 0.f;
+        if (w.n > 0) {
+            // The warp's rows of q, one at a time over the lanes, as fp16 times a power of two
+            // per row, into the swizzled operand tile.  A negative scale goes into q: the
+            // maximum is taken before scaling.
+            constexpr int E = D / 32;                                  // values of a lane
+            const int r0 = (warp & 3) * 32, first_row = w.row0 + t * 128 + r0, rows = min(32, w.nrows - first_row);
+            const uint32_t base = ptx::smem_u32(sm.q[t]), sign = p.scale_log2 < 0.f ? 0x80000000u : 0u;
+            const uint32_t half = (uint32_t)(lane * E / 64) * 16384u, chunk = (uint32_t)(lane * E / 8) & 7u, in = (uint32_t)(lane * E * 2) & 15u;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += 16) {
+                uint32_t v[16][E / 2];                                 // all loads of a batch before any is used
 #pragma unroll
-            for (int c = 0; c < D / 4; ++c) {
-                const uint2 v = live ? *reinterpret_cast<const uint2 *>(q + 4 * c) : make_uint2(0u, 0u);
-                const float x[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+                for (int i = 0; i < 16; ++i) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) amax = fabsf(x[k]) < INFINITY ? fmaxf(amax, fabsf(x[k])) : amax;
-            }
-            const int up = query_shift(amax);
-            // A negative scale goes into q: the maximum is taken before scaling.
-            const float f = p.scale_log2 < 0.f ? -exp2_int(up) : exp2_int(up);
-            qs = exp2_int(-up) * fabsf(p.scale_log2);
-            const uint32_t base = ptx::smem_u32(sm.q[t]);
-            const int lr = r & 127;
+                    for (int k = 0; k < E / 2; ++k) v[i][k] = 0u;
+                    if (i0 + i < rows) {
+                        const int tk = (first_row + i0 + i) / G, hq = w.h * G + first_row + i0 + i - tk * G;
+                        const uint16_t *q = p.q + (int64_t)(w.start + tk) * p.q_token + hq * p.q_head + lane * E;
+                        if constexpr (E == 4) {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(q);
+                            v[i][0] = x.x, v[i][1] = x.y;
+                        } else {
+                            v[i][0] = *reinterpret_cast<const uint32_t *>(q);
+                        }
+                    }
+                }
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                const uint2 a = live ? *reinterpret_cast<const uint2 *>(q + 8 * c) : make_uint2(0u, 0u);
-                const uint2 b = live ? *reinterpret_cast<const uint2 *>(q + 8 * c + 4) : make_uint2(0u, 0u);
-                const uint32_t o[4] = {f32x2_to_f16x2(bf16_lo(a.x) * f, bf16_hi(a.x) * f), f32x2_to_f16x2(bf16_lo(a.y) * f, bf16_hi(a.y) * f),
-                                       f32x2_to_f16x2(bf16_lo(b.x) * f, bf16_hi(b.x) * f), f32x2_to_f16x2(bf16_lo(b.y) * f, bf16_hi(b.y) * f)};
-                sts_v4(base + (c >> 3) * 16384 + lr * 128 + (((c & 7) ^ (lr & 7)) << 4), o[0], o[1], o[2], o[3]);
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t top = 0u;                                 // largest finite magnitude, as bf16 bits
+#pragma unroll
+                    for (int k = 0; k < E / 2; ++k) {
+                        const uint32_t a = v[i][k] & 0x7FFFu, b = v[i][k] >> 16 & 0x7FFFu;
+                        top = max(top, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
+                    }
+                    top = __reduce_max_sync(~0u, top);
+                    const int up = query_shift(__uint_as_float(top << 16));
+                    const float f = __uint_as_float(__float_as_uint(exp2_int(up)) | sign);
+                    if (lane == i0 + i) qs = exp2_int(-up) * fabsf(p.scale_log2);
+                    const uint32_t at_q = base + half + (r0 + i0 + i) * 128 + ((chunk ^ (i & 7)) << 4) + in;
+#pragma unroll
+                    for (int k = 0; k < E / 2; ++k) v[i][k] = f32x2_to_f16x2(bf16_lo(v[i][k]) * f, bf16_hi(v[i][k]) * f);
+                    if constexpr (E == 4)
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_q), "r"(v[i][0]), "r"(v[i][1]) : "memory");
+                    else
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at_q), "r"(v[i][0]) : "memory");
+                }
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -243,19 +296,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < kKeys; ++k)
                     if (k > hi || k <= lo) v[k] = -INFINITY;
             }
-            // The row's maximum, by 16 keys (one page at least).  A factor of 0 would make
-            // masked scores NaN.
-            float mx = -INFINITY, f[kKeys / 16];
+            // A factor of 0 would make masked scores NaN.
+            float f[kKeys / 16];
+#pragma unroll
+            for (int g = 0; g < kKeys / 16; ++g) f[g] = fmaxf(qs * ex[g].x, 1.2e-38f);
+            // The row's maximum, by 16 keys (one page at least); m follows it when it has been
+            // outgrown by more than kLag.
+            float mx = -INFINITY;
 #pragma unroll
             for (int g = 0; g < kKeys / 16; ++g) {
                 const float *x = v + g * 16;
-                f[g] = fmaxf(qs * ex[g].x, 1.2e-38f);
                 const float a = max3(max3(x[0], x[1], x[2]), x[3], x[4]), b = max3(max3(x[5], x[6], x[7]), x[8], x[9]);
                 const float c = max3(max3(x[10], x[11], x[12]), x[13], x[14]);
                 mx = fmaxf(mx, fmaf(max3(max3(a, b, c), x[15], x[15]), f[g], ex[g].y));
             }
-            // The maximum in use follows when it lags by more than kLag.
-            const bool move = mx > m + kLag || (m == -INFINITY && mx > m);
+            const bool move = mx > m + kLag;
             if (__any_sync(~0u, move)) {
                 const float a = move ? ex2(m - mx) : 1.f;
                 if (move) m = mx;
@@ -263,17 +318,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j > 0) {
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) {
-                        uint32_t v[16];
-                        ptx::tmem_ld16(oc + c * 16, v);
+                        uint32_t o[16];
+                        ptx::tmem_ld16(oc + c * 16, o);
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * a);
-                        ptx::tmem_st16(oc + c * 16, v);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                        ptx::tmem_st16(oc + c * 16, o);
                     }
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            // Weights, their sum, and fp16 pairs in the place of the scores.
+            // Weights, their sum, and fp16 pairs in the place of the scores; the product may
+            // start on the first 64 keys while the others are weighed.
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t h[16];
@@ -293,11 +349,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l = fmaf(sum.x + sum.y, e.z, l);
                 }
                 ptx::tmem_st16(sc + c * 16, h);
+                if (c & 1) {
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(at(sm.p_full[t][c >> 1]));
+                }
             }
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(at(sm.p_full[t]));
         }
         // ------------------------------------------------ the row's result.
         if (w.n > 0) {
@@ -324,34 +382,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        float *part = grid.splits > 1 ? part_of<D>(p, grid, w.unit, w.split) + r * D : nullptr;
+        // Rows go out by way of shared memory (the q tile's place: its products are done), so
+        // that stores cover whole rows; parts for the join go out value by value, a layout in
+        // which the lanes' rows are neighbours.
+        float4 *part = grid.splits > 1 ? reinterpret_cast<float4 *>(part_of<D>(p, grid, w.unit, w.split)) + r : nullptr;
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        uint16_t *out = p.out + (int64_t)(w.start + token) * p.o_token + head * p.o_head;
+        const int lr = r & 127;
+        const uint32_t stage = ptx::smem_u32(sm.q[t]) + lr * (D * 2);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            uint32_t v[16];
+        for (int c = 0; c < D / 32; ++c) {
+            float v[32];
             if (w.n > 0) {
-                ptx::tmem_ld16(oc + c * 16, v);
+                tmem_ld32(oc + c * 32, v);
                 ptx::tmem_ld_wait();
             } else {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = 0u;
+                for (int k = 0; k < 32; ++k) v[k] = 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (nan[c / 2] >> ((c & 1) * 16 + k) & 1u) v[k] = 0x7FFFFFFFu;
-            if (live) {
-                if (part != nullptr) {
+            for (int k = 0; k < 32; ++k)
+                if (nan[c] >> k & 1u) v[k] = __int_as_float(0x7FFFFFFF);
+            if (part != nullptr) {
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) *reinterpret_cast<uint4 *>(part + c * 16 + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                } else {
-                    uint32_t o[8];
+                for (int k = 0; k < 32; k += 4)
+                    if (live) part[(c * 8 + k / 4) * kRows] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            } else {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        o[k] = f32x2_to_bf16x2(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
-#pragma unroll
-                    for (int k = 0; k < 8; k += 2) *reinterpret_cast<uint2 *>(out + c * 16 + 2 * k) = make_uint2(o[k], o[k + 1]);
-                }
+                for (int k = 0; k < 32; k += 8)
+                    sts_v4(stage + (((c * 4 + k / 8) ^ (lr & 7)) << 4), f32x2_to_bf16x2(v[k] * inv, v[k + 1] * inv),
+                           f32x2_to_bf16x2(v[k + 2] * inv, v[k + 3] * inv), f32x2_to_bf16x2(v[k + 4] * inv, v[k + 5] * inv),
+                           f32x2_to_bf16x2(v[k + 6] * inv, v[k + 7] * inv));
+            }
+        }
+        if (part == nullptr) {
+            __syncwarp();
+            constexpr int E = D / 32;
+            const int r0 = (warp & 3) * 32, first_row = w.row0 + t * 128 + r0, rows = min(32, w.nrows - first_row);
+#pragma unroll 8
+            for (int i = 0; i < rows; ++i) {
+                const int tk = (first_row + i) / G;
+                uint16_t *o = p.out + (int64_t)(w.start + tk) * p.o_token + (w.h * G + first_row + i - tk * G) * p.o_head + lane * E;
+                const uint8_t *from = sm.q[t] + (r0 + i) * (D * 2) + (((lane * E / 8) ^ (i & 7)) << 4) + (lane * E * 2 & 15);
+                if constexpr (E == 4)
+                    *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(from);
+                else
+                    *reinterpret_cast<uint32_t *>(o) = *reinterpret_cast<const uint32_t *>(from);
             }
         }
         if (live) {
@@ -482,39 +557,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = max(0, unit - kRaw); i < unit; ++i)
             if (!ptx::mbar_wait(at(sm.raw_full[i % kRaw]), (i / kRaw) & 1, &g_prompt_timeouts)) break;
-    } else if (warp == kIssuer && lane == 0) {
+    } else if (warp == kIssuer) {
         // ------------------------------------------------ MMA issuer.
         const uint32_t qk = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);             // fp16 x fp16 -> fp32, M = 128
         const uint32_t pv = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);    // B along N
-        bool ok = w.n > 0 && ptx::mbar_wait(at(sm.q_full), 0, &g_prompt_timeouts);
-        auto weighted = [&](int t, int j) {      // O_t += P_t V(j)
-            if (ok) ok = ptx::mbar_wait(at(sm.p_full[t]), j & 1, &g_prompt_timeouts);
-            if (ok) ok = ptx::mbar_wait(at(sm.v_full[j % kBuf]), (j / kBuf) & 1, &g_prompt_timeouts);
-            if (!ok) return;
-            ptx::tc_fence_after();
-            const uint64_t vd = sw128_mn_desc(ptx::smem_u32(sm.v[j % kBuf]), 16384);
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-                ptx::mma_f16_tmem_a(o_col[t], s_col[t] + k * 8, vd + (uint64_t)(k * (2048 >> 4)), pv, j > 0 || k > 0);
+        const uint64_t qd = ptx::sw128_desc(ptx::smem_u32(sm.q)), kd0 = ptx::sw128_desc(ptx::smem_u32(sm.k));
+        const uint64_t vd0 = sw128_mn_desc(ptx::smem_u32(sm.v), 16384);
+        constexpr uint64_t kTileStep = Smem<D>::kTile >> 4;
+        bool ok = w.n > 0;
+        auto wait = [&](const uint64_t &bar, int parity) {
+            if (ok) ok = __all_sync(~0u, ptx::mbar_wait(at(bar), (uint32_t)parity, &g_prompt_timeouts));
         };
+        auto weighted = [&](int t, int j) {      // O_t += P_t V(j)
+            wait(sm.v_full[j % kBuf], (j / kBuf) & 1);
+            const uint64_t vd = vd0 + (uint64_t)(j % kBuf) * kTileStep;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                wait(sm.p_full[t][half], j & 1);
+                if (!ok) return;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int k = half * 4; k < half * 4 + 4; ++k)
+                    mma_ts(o_col[t], s_col[t] + k * 8, vd + (uint64_t)(k * (2048 >> 4)), pv, j > 0 || k > 0);
+            }
+        };
+        wait(sm.q_full, 0);
         for (int j = 0; j < w.n && ok; ++j) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (j > 0) {
                     weighted(t, j - 1);
-                    if (ok && t == 1) ptx::mma_commit(at(sm.v_empty[(j - 1) % kBuf]));
+                    if (ok && t == 1) commit(at(sm.v_empty[(j - 1) % kBuf]));
                 }
-                if (ok) ok = ptx::mbar_wait(at(sm.k_full[j % kBuf]), (j / kBuf) & 1, &g_prompt_timeouts);
+                wait(sm.k_full[j % kBuf], (j / kBuf) & 1);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint64_t qd = ptx::sw128_desc(ptx::smem_u32(sm.q[t])), kd = ptx::sw128_desc(ptx::smem_u32(sm.k[j % kBuf]));
+                const uint64_t kd = kd0 + (uint64_t)(j % kBuf) * kTileStep, qt = qd + (uint64_t)t * kTileStep;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t off = (uint64_t)((k >> 2) * (16384 >> 4) + (k & 3) * 2);
-                    ptx::mma_f16(s_col[t], qd + off, kd + off, qk, k > 0);
+                    mma_ss(s_col[t], qt + off, kd + off, qk, k > 0);
                 }
-                ptx::mma_commit(at(sm.s_full[t]));
-                if (t == 1) ptx::mma_commit(at(sm.k_empty[j % kBuf]));
+                commit(at(sm.s_full[t]));
+                if (t == 1) commit(at(sm.k_empty[j % kBuf]));
             }
         }
         if (ok) {
@@ -522,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             weighted(1, w.n - 1);
         }
         if (w.n > 0) {
-            ptx::mma_commit(at(sm.o_full));
+            commit(at(sm.o_full));
             ptx::mbar_wait(at(sm.o_full), 0, &g_prompt_timeouts);      // nothing in flight when tensor memory is freed
         }
     }
@@ -533,37 +618,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the splits: block (unit, r) takes 8 rows of a unit, a warp each.
+// Joins the splits: block (unit, y) takes 32 rows of a unit, a lane each; warp i takes
+// every eighth group of four values.
 template <int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const AttentionArgs p, const PromptGrid grid) {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const Work w = work_of(p, grid, blockIdx.x * grid.splits);
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (!w.live || w.row0 + r >= w.nrows) return;
-    const int G = p.Hq / p.Hk, token = (w.row0 + r) / G, head = w.h * G + w.row0 + r - token * G;
-    constexpr int kPer = D / 32;
-    float m = -INFINITY, l = 0.f, o[kPer];
+    const int r = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5, row = w.row0 + r;
+    if (!w.live || row >= w.nrows) return;
+    const int i = row / p.G, token = w.start + i, head = w.h * p.G + row - i * p.G;
+    constexpr int kGroups = D / 4 / 8;
+    float m = -INFINITY, l = 0.f;
+    float4 o[kGroups];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+    for (int k = 0; k < kGroups; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = 0; s < grid.splits; ++s) {
-        if (work_of(p, grid, blockIdx.x * grid.splits + s).n == 0) continue;
+        if (!w.holds(s, grid.splits)) continue;                    // no keys: nothing was written
         const float *part = part_of<D>(p, grid, w.unit, s);
         const float2 ml = *reinterpret_cast<const float2 *>(part + kRows * D + 2 * r);
         const float mx = fmaxf(m, ml.x), ref = mx == -INFINITY ? 0.f : mx;
         const float a = ex2(m - ref), b = ex2(ml.x - ref);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = o[i] * a + part[r * D + lane * kPer + i] * b;
+        for (int k = 0; k < kGroups; ++k) {
+            const float4 v = reinterpret_cast<const float4 *>(part)[(warp + 8 * k) * kRows + r];
+            o[k].x = o[k].x * a + v.x * b, o[k].y = o[k].y * a + v.y * b;
+            o[k].z = o[k].z * a + v.z * b, o[k].w = o[k].w * a + v.w * b;
+        }
         l = l * a + ml.y * b;
         m = mx;
     }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    uint16_t *out = p.out + (int64_t)(w.start + token) * p.o_token + head * p.o_head + lane * kPer;
+    uint16_t *out = p.out + token * p.o_token + head * p.o_head;
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2)
-        *reinterpret_cast<uint32_t *>(out + i) = f32x2_to_bf16x2(o[i] * inv, o[i + 1] * inv);
-    if (lane == 0 && p.lse != nullptr)
-        p.lse[(w.start + token) * p.lse_token + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+    for (int k = 0; k < kGroups; ++k)
+        *reinterpret_cast<uint2 *>(out + (warp + 8 * k) * 4) =
+            make_uint2(f32x2_to_bf16x2(o[k].x * inv, o[k].y * inv), f32x2_to_bf16x2(o[k].z * inv, o[k].w * inv));
+    if (warp == 0 && p.lse != nullptr) p.lse[token * p.lse_token + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
 }
 
 template <int D>
@@ -581,7 +672,7 @@ cudaError_t launch(const AttentionArgs &p, const PromptGrid &g, cudaStream_t str
     const unsigned units = (unsigned)(g.tiles * p.Hk);
     e = launch_pdl(prompt_kernel<D>, dim3(units * (unsigned)g.splits), dim3(kThreads), smem, stream, kmap, vmap, p, g);
     if (e != cudaSuccess || g.splits == 1) return e;
-    return launch_pdl(prompt_join_kernel<D>, dim3(units, kRows / 8), dim3(256), 0, stream, p, g);
+    return launch_pdl(prompt_join_kernel<D>, dim3(units, kRows / 32), dim3(256), 0, stream, p, g);
 }
 
 }  // namespace
