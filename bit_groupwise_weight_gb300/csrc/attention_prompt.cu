@@ -13,13 +13,15 @@
 // When there are fewer CTAs than SMs the keys are split between several, and a
 // second launch joins their parts.  Tiles with the most keys start first.
 //
-// Tensor memory (512 columns): S of both tiles (128 fp32 columns each; the fp16
-// weights P take the place of the S they come from), O of both tiles.
+// Tensor memory (512 columns): S of both tiles (128 fp32 columns each, as two halves of
+// 64 keys; the fp16 weights P take the place of the half they come from), O of both.
+// The halves are two buffers: while one is weighed, the other's products run, so that
+// four chains (two tiles, two halves) keep the tensor cores fed.
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (one thread a row, which holds the
 // row's 128 scores in registers: 184 a thread, taken from the other warps), 8-11 turn
-// e4m3 codes into fp16 operand tiles (once per 256 rows), 12 TMA producer, 13 MMA issuer.
-// Order of the issuer, which keeps a tile's S free while its P is read:
-//     PV0(j-1) QK0(j) PV1(j-1) QK1(j) ...
+// e4m3 codes into fp16 operand tiles (once per 256 rows), 12 TMA producer, 13 and 14 MMA
+// issuers, one for each tile, so that neither waits for the other's weights.  Order of an
+// issuer, half-step by half-step: PV(h) QK(h + 2), products of one issuer running in order.
 // Bound: the tensor cores, 4 D flops per row and key; at 128 x 128 x 128 a product
 // takes 512 cycles, and 256 rows x 128 keys 2048; their exponentials 32768 / 16-32
 // per cycle and SM.
@@ -33,13 +35,14 @@ namespace {
 using namespace attn;
 
 constexpr int kKeys = 128;                       // keys of a step
+constexpr int kHalf = 64;                        // keys of a half-step
 constexpr int kRows = 256;                       // rows of a CTA
 constexpr int kUnit = 64;                        // keys of a raw TMA unit
 constexpr int kRaw = 4;                          // raw units in flight
 constexpr int kBuf = 2;                          // fp16 K and V tiles
 constexpr int kExps = 8;                         // steps whose page exponents are kept
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
-constexpr int kProducer = 12, kIssuer = 13;
+constexpr int kProducer = 12, kIssuer = 13;      // and 14
 constexpr int kThreads = 16 * 32;              // whole warpgroups, for the register split
 constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kOtherRegs = 64;   // 2 x 184 + 80 + 64 = 4 x 128
 constexpr float kLag = 8.f;
@@ -54,8 +57,8 @@ struct Smem {
     alignas(1024) uint8_t v[kBuf][kTile];
     alignas(1024) uint8_t raw[kRaw][kRawBytes];
     float4 exps[kExps][kKeys / 16];              // 2^ke, ve, 2^-ve of each 16 keys
-    uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBuf], k_empty[kBuf], v_full[kBuf], v_empty[kBuf];
-    uint64_t q_full, s_full[2], p_full[2][2], o_full, e_full[kExps];
+    uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBuf], v_full[kBuf], kv_empty[kBuf];
+    uint64_t q_full, s_full[2][2], p_full[2][2], o_full, e_full[kExps];
     uint32_t tmem;
     int poisoned;
 };
@@ -182,18 +185,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const PromptGrid grid) {
     extern __shared__ uint8_t raw_smem[];
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw_smem + ((1024 - (ptx::smem_u32(raw_smem) & 1023)) & 1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;      // the warp number, uniform
     auto at = [](const uint64_t &bar) { return ptx::smem_u32(&bar); };
     if (tid == 0) {
         for (int i = 0; i < kRaw; ++i) ptx::mbar_init(at(sm.raw_full[i]), 1), ptx::mbar_init(at(sm.raw_empty[i]), kConvertWarps);
         for (int i = 0; i < kBuf; ++i) {
-            ptx::mbar_init(at(sm.k_full[i]), kConvertWarps), ptx::mbar_init(at(sm.k_empty[i]), 1);
-            ptx::mbar_init(at(sm.v_full[i]), kConvertWarps), ptx::mbar_init(at(sm.v_empty[i]), 1);
+            ptx::mbar_init(at(sm.k_full[i]), kConvertWarps), ptx::mbar_init(at(sm.v_full[i]), kConvertWarps);
+            ptx::mbar_init(at(sm.kv_empty[i]), 2);
         }
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(at(sm.s_full[i]), 1), ptx::mbar_init(at(sm.p_full[i][0]), 4), ptx::mbar_init(at(sm.p_full[i][1]), 4);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(at(sm.s_full[i][0]), 1), ptx::mbar_init(at(sm.s_full[i][1]), 1);
+            ptx::mbar_init(at(sm.p_full[i][0]), 4), ptx::mbar_init(at(sm.p_full[i][1]), 4);
+        }
         for (int i = 0; i < kExps; ++i) ptx::mbar_init(at(sm.e_full[i]), 1);
         ptx::mbar_init(at(sm.q_full), kSoftmaxWarps);
-        ptx::mbar_init(at(sm.o_full), 1);
+        ptx::mbar_init(at(sm.o_full), 2);
         sm.poisoned = 0;
         ptx::fence_mbar_init();
     }
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 256 + D};
     // Steps in which some row of the CTA does not see some key.
     const int pos_lo = w.first + w.row0 / G, pos_hi = w.first + (min(w.row0 + kRows, w.nrows) - 1) / G;
-    auto partial = [&](int key0) { return key0 + kKeys - 1 > pos_lo || (p.window > 0 && key0 <= pos_hi - p.window); };
+    auto partial = [&](int key0, int keys = kKeys) { return key0 + keys - 1 > pos_lo || (p.window > 0 && key0 <= pos_hi - p.window); };
 
     if (warp < kSoftmaxWarps) {
         // ------------------------------------------------ softmax: a thread owns a row.
@@ -230,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // per row, into the swizzled operand tile.  A negative scale goes into q: the
             // maximum is taken before scaling.
             constexpr int E = D / 32;                                  // values of a lane
-            const int r0 = (warp & 3) * 32, first_row = w.row0 + t * 128 + r0, rows = min(32, w.nrows - first_row);
+            const int r0 = (warp & 3) * 32, rows = min(32, w.nrows - (w.row0 + t * 128 + r0));
+            const int64_t mine = (int64_t)(w.start + token) * p.q_token + head * p.q_head;     // this lane's row
             const uint32_t base = ptx::smem_u32(sm.q[t]), sign = p.scale_log2 < 0.f ? 0x80000000u : 0u;
             const uint32_t half = (uint32_t)(lane * E / 64) * 16384u, chunk = (uint32_t)(lane * E / 8) & 7u, in = (uint32_t)(lane * E * 2) & 15u;
 #pragma unroll 1
@@ -240,9 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 16; ++i) {
 #pragma unroll
                     for (int k = 0; k < E / 2; ++k) v[i][k] = 0u;
+                    const int64_t from = __shfl_sync(~0u, mine, i0 + i);
                     if (i0 + i < rows) {
-                        const int tk = (first_row + i0 + i) / G, hq = w.h * G + first_row + i0 + i - tk * G;
-                        const uint16_t *q = p.q + (int64_t)(w.start + tk) * p.q_token + hq * p.q_head + lane * E;
+                        const uint16_t *q = p.q + from + lane * E;
                         if constexpr (E == 4) {
                             const uint2 x = *reinterpret_cast<const uint2 *>(q);
                             v[i][0] = x.x, v[i][1] = x.y;
@@ -279,32 +286,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         float m = -INFINITY, l = 0.f;
         const uint32_t sc = s_col[t] + quarter, oc = o_col[t] + quarter;
-        for (int j = 0; j < w.n; ++j) {
-            const int key0 = (w.lo + j) * kKeys;
-            const bool mask = partial(key0);
-            if (ok) ok = ptx::mbar_wait(at(sm.e_full[j % kExps]), (j / kExps) & 1, &g_prompt_timeouts);
-            if (ok) ok = ptx::mbar_wait(at(sm.s_full[t]), j & 1, &g_prompt_timeouts);
+        for (int hs = 0; hs < 2 * w.n; ++hs) {                          // half-steps of 64 keys
+            const int j = hs >> 1, h = hs & 1, key0 = (w.lo + j) * kKeys + h * kHalf;
+            if (h == 0 && ok) ok = ptx::mbar_wait(at(sm.e_full[j % kExps]), (j / kExps) & 1, &g_prompt_timeouts);
+            if (ok) ok = ptx::mbar_wait(at(sm.s_full[t][h]), j & 1, &g_prompt_timeouts);
             ptx::tc_fence_after();
-            const float4 *ex = sm.exps[j % kExps];
-            float v[kKeys];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, v + c * 32);
+            const float4 *ex = sm.exps[j % kExps] + h * (kHalf / 16);
+            float v[kHalf];
+            tmem_ld32(sc + h * kHalf, v);
+            tmem_ld32(sc + h * kHalf + 32, v + 32);
             ptx::tmem_ld_wait();
-            if (mask) {
-                const int hi = pos - key0, lo = low - key0;            // of the step's keys, those in (lo, hi] are seen
+            if (partial(key0, kHalf)) {
+                const int hi = pos - key0, lo = low - key0;            // of the keys, those in (lo, hi] are seen
 #pragma unroll
-                for (int k = 0; k < kKeys; ++k)
+                for (int k = 0; k < kHalf; ++k)
                     if (k > hi || k <= lo) v[k] = -INFINITY;
             }
             // A factor of 0 would make masked scores NaN.
-            float f[kKeys / 16];
+            float f[kHalf / 16];
 #pragma unroll
-            for (int g = 0; g < kKeys / 16; ++g) f[g] = fmaxf(qs * ex[g].x, 1.2e-38f);
+            for (int g = 0; g < kHalf / 16; ++g) f[g] = fmaxf(qs * ex[g].x, 1.2e-38f);
             // The row's maximum, by 16 keys (one page at least); m follows it when it has been
             // outgrown by more than kLag.
             float mx = -INFINITY;
 #pragma unroll
-            for (int g = 0; g < kKeys / 16; ++g) {
+            for (int g = 0; g < kHalf / 16; ++g) {
                 const float *x = v + g * 16;
                 const float a = max3(max3(x[0], x[1], x[2]), x[3], x[4]), b = max3(max3(x[5], x[6], x[7]), x[8], x[9]);
                 const float c = max3(max3(x[10], x[11], x[12]), x[13], x[14]);
@@ -315,7 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float a = move ? ex2(m - mx) : 1.f;
                 if (move) m = mx;
                 l *= a;
-                if (j > 0) {
+                if (hs > 0) {
+                    // The last half-step's product has to be done: its issuer's next signal says so.
+                    if (ok) ok = ptx::mbar_wait(at(sm.s_full[t][h ^ 1]), ((hs + 1) >> 1) & 1, &g_prompt_timeouts);
+                    ptx::tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) {
                         uint32_t o[16];
@@ -328,11 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            // Weights, their sum, and fp16 pairs in the place of the scores; the product may
-            // start on the first 64 keys while the others are weighed.
+            // Weights, their sum, and fp16 pairs in the place of the scores.
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t h[16];
+            for (int c = 0; c < 2; ++c) {
+                uint32_t hp[16];
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const float4 e = ex[2 * c + g];
@@ -344,18 +352,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::ffma2(x, x, ff, d);
                         x.x = ex2(x.x), x.y = ex2(x.y);
                         sum = ptx::fadd2(sum, x);
-                        h[g * 8 + k / 2] = f32x2_to_f16x2(x.x, x.y);
+                        hp[g * 8 + k / 2] = f32x2_to_f16x2(x.x, x.y);
                     }
                     l = fmaf(sum.x + sum.y, e.z, l);
                 }
-                ptx::tmem_st16(sc + c * 16, h);
-                if (c & 1) {
-                    ptx::tmem_st_wait();
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(at(sm.p_full[t][c >> 1]));
-                }
+                ptx::tmem_st16(sc + h * kHalf + c * 16, hp);
             }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(at(sm.p_full[t][h]));
         }
         // ------------------------------------------------ the row's result.
         if (w.n > 0) {
@@ -417,11 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part == nullptr) {
             __syncwarp();
             constexpr int E = D / 32;
-            const int r0 = (warp & 3) * 32, first_row = w.row0 + t * 128 + r0, rows = min(32, w.nrows - first_row);
+            const int r0 = (warp & 3) * 32, rows = min(32, w.nrows - (w.row0 + t * 128 + r0));
+            const int64_t mine = (int64_t)(w.start + token) * p.o_token + head * p.o_head;     // this lane's row
 #pragma unroll 8
-            for (int i = 0; i < rows; ++i) {
-                const int tk = (first_row + i) / G;
-                uint16_t *o = p.out + (int64_t)(w.start + tk) * p.o_token + (w.h * G + first_row + i - tk * G) * p.o_head + lane * E;
+            for (int i = 0; i < 32; ++i) {
+                uint16_t *o = p.out + __shfl_sync(~0u, mine, i) + lane * E;
+                if (i >= rows) continue;
                 const uint8_t *from = sm.q[t] + (r0 + i) * (D * 2) + (((lane * E / 8) ^ (i & 7)) << 4) + (lane * E * 2 & 15);
                 if constexpr (E == 4)
                     *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(from);
@@ -454,9 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool mask = partial(key0);
 #pragma unroll 1
             for (int which = 0; which < 2; ++which) {
-                uint64_t &full = which ? sm.v_full[buf] : sm.k_full[buf], &empty = which ? sm.v_empty[buf] : sm.k_empty[buf];
+                uint64_t &full = which ? sm.v_full[buf] : sm.k_full[buf];
                 const uint32_t dst = ptx::smem_u32(which ? sm.v[buf] : sm.k[buf]);
-                if (ok && j >= kBuf) ok = ptx::mbar_wait(at(empty), (j / kBuf - 1) & 1, &g_prompt_timeouts);
+                // Release e frees K(e) and V(e - 1): K(j) waits for e = j - 2, V(j) for e = j - 1.
+                const int freed = j - kBuf + which;
+                if (ok && freed >= which) ok = ptx::mbar_wait(at(sm.kv_empty[freed % kBuf]), (freed / kBuf) & 1, &g_prompt_timeouts);
 #pragma unroll 1
                 for (int u = 0; u < kKeys / kUnit; ++u, ++unit) {
                     const int st = unit % kRaw;
@@ -557,56 +566,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = max(0, unit - kRaw); i < unit; ++i)
             if (!ptx::mbar_wait(at(sm.raw_full[i % kRaw]), (i / kRaw) & 1, &g_prompt_timeouts)) break;
-    } else if (warp == kIssuer) {
-        // ------------------------------------------------ MMA issuer.
-        const uint32_t qk = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);             // fp16 x fp16 -> fp32, M = 128
+    } else if (warp == kIssuer || warp == kIssuer + 1) {
+        // ------------------------------------------------ MMA issuers.
+        const int t = warp - kIssuer;
+        const uint32_t qk = (1u << 4) | ((uint32_t)(kHalf >> 3) << 17) | (8u << 24);             // fp16 x fp16 -> fp32, M = 128
         const uint32_t pv = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);    // B along N
-        const uint64_t qd = ptx::sw128_desc(ptx::smem_u32(sm.q)), kd0 = ptx::sw128_desc(ptx::smem_u32(sm.k));
-        const uint64_t vd0 = sw128_mn_desc(ptx::smem_u32(sm.v), 16384);
         constexpr uint64_t kTileStep = Smem<D>::kTile >> 4;
+        const uint64_t qd = ptx::sw128_desc(ptx::smem_u32(sm.q)) + (uint64_t)t * kTileStep;
+        const uint64_t kd0 = ptx::sw128_desc(ptx::smem_u32(sm.k)), vd0 = sw128_mn_desc(ptx::smem_u32(sm.v), 16384);
+        const uint32_t sd = tmem + t * 128, od = tmem + 256 + t * D;
         bool ok = w.n > 0;
         auto wait = [&](const uint64_t &bar, int parity) {
-            if (ok) ok = __all_sync(~0u, ptx::mbar_wait(at(bar), (uint32_t)parity, &g_prompt_timeouts));
+            if (ok) ok = ptx::mbar_wait(at(bar), (uint32_t)parity, &g_prompt_timeouts);
         };
-        auto weighted = [&](int t, int j) {      // O_t += P_t V(j)
-            wait(sm.v_full[j % kBuf], (j / kBuf) & 1);
-            const uint64_t vd = vd0 + (uint64_t)(j % kBuf) * kTileStep;
+        auto scores = [&](int j, int h) {        // S_t half h = q_t K(j)^T
+            const uint64_t kd = kd0 + (uint64_t)(j % kBuf) * kTileStep + (uint64_t)h * (kHalf * 128 >> 4);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                wait(sm.p_full[t][half], j & 1);
-                if (!ok) return;
-                ptx::tc_fence_after();
-#pragma unroll
-                for (int k = half * 4; k < half * 4 + 4; ++k)
-                    mma_ts(o_col[t], s_col[t] + k * 8, vd + (uint64_t)(k * (2048 >> 4)), pv, j > 0 || k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+                const uint64_t off = (uint64_t)((k >> 2) * (16384 >> 4) + (k & 3) * 2);
+                mma_ss(sd + h * kHalf, qd + off, kd + off, qk, k > 0);
             }
         };
         wait(sm.q_full, 0);
-        for (int j = 0; j < w.n && ok; ++j) {
+        wait(sm.k_full[0], 0);
+        if (__all_sync(~0u, ok)) {
+            ptx::tc_fence_after();
+            scores(0, 0);
+            commit(at(sm.s_full[t][0]));
+            scores(0, 1);
+            commit(at(sm.s_full[t][1]));
+            commit(at(sm.kv_empty[0]));
+        }
+        for (int j = 0; j < w.n; ++j) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (j > 0) {
-                    weighted(t, j - 1);
-                    if (ok && t == 1) commit(at(sm.v_empty[(j - 1) % kBuf]));
-                }
-                wait(sm.k_full[j % kBuf], (j / kBuf) & 1);
-                if (!ok) break;
+            for (int h = 0; h < 2; ++h) {
+                if (h == 0) wait(sm.v_full[j % kBuf], (j / kBuf) & 1);
+                wait(sm.p_full[t][h], j & 1);
+                if (!__all_sync(~0u, ok)) break; // a wait that gave up: nothing more is issued
                 ptx::tc_fence_after();
-                const uint64_t kd = kd0 + (uint64_t)(j % kBuf) * kTileStep, qt = qd + (uint64_t)t * kTileStep;
+                const uint64_t vd = vd0 + (uint64_t)(j % kBuf) * kTileStep + (uint64_t)h * (kHalf * 128 >> 4);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t off = (uint64_t)((k >> 2) * (16384 >> 4) + (k & 3) * 2);
-                    mma_ss(s_col[t], qt + off, kd + off, qk, k > 0);
+                for (int k = 0; k < kHalf / 16; ++k)                    // O_t += P_t V(j), half h
+                    mma_ts(od, sd + h * kHalf + k * 8, vd + (uint64_t)(k * (2048 >> 4)), pv, j > 0 || h > 0 || k > 0);
+                if (j + 1 < w.n) {
+                    if (h == 0) {
+                        wait(sm.k_full[(j + 1) % kBuf], ((j + 1) / kBuf) & 1);
+                        if (!__all_sync(~0u, ok)) break;
+                        ptx::tc_fence_after();
+                    }
+                    scores(j + 1, h);
                 }
-                commit(at(sm.s_full[t]));
-                if (t == 1) commit(at(sm.k_empty[j % kBuf]));
+                // Also after the last products, for who waits for them to move O.
+                commit(at(sm.s_full[t][h]));
+                // Frees K(j + 1) and V(j).
+                if (h == 1) commit(at(sm.kv_empty[(j + 1) % kBuf]));
             }
         }
-        if (ok) {
-            weighted(0, w.n - 1);
-            weighted(1, w.n - 1);
-        }
         if (w.n > 0) {
+            __syncwarp();
             commit(at(sm.o_full));
             ptx::mbar_wait(at(sm.o_full), 0, &g_prompt_timeouts);      // nothing in flight when tensor memory is freed
         }
