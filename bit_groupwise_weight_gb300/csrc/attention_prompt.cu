@@ -405,9 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = 0.f;
             }
+            if (nan[c] != 0u) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                if (nan[c] >> k & 1u) v[k] = __int_as_float(0x7FFFFFFF);
+                for (int k = 0; k < 32; ++k)
+                    if (nan[c] >> k & 1u) v[k] = __int_as_float(0x7FFFFFFF);
+            }
             if (part != nullptr) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)

@@ -183,7 +183,8 @@ struct AppendArgs {
     int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
     int64_t page_stride, head_stride, table_stride;
     float factor;
-    int T, B, max_q, Hq, Hk, D, P, pages, width, R, units;
+    int T, B, max_q, Hq, Hk, D, P, pages, width, R;
+    int G, n, pshift, units, table_tokens;                              // set by launch_kv_append
     bool interleaved, qvec, kvec, vvec, ovec;
 };
 cudaError_t launch_kv_append(const AppendArgs &args, cudaStream_t stream);
