@@ -324,7 +324,8 @@ lowbit_status lowbit_attention(const lowbit_attention_args *a, const lowbit_cach
 }
 
 lowbit_status lowbit_sample(const lowbit_sample_args *a, lowbit_stream_t stream) {
-    if (a == nullptr || a->rows < 0 || a->rows > kMaxDim / 8 || a->vocab <= 0) return LOWBIT_EINVAL;
+    if (a == nullptr || a->rows < 0 || a->rows > kMaxDim / 8 || a->vocab <= 0 || a->vocab > (1 << 19))
+        return LOWBIT_EINVAL;
     if (a->dtype != LOWBIT_DTYPE_F32 && a->dtype != LOWBIT_DTYPE_BF16 && a->dtype != LOWBIT_DTYPE_F16)
         return LOWBIT_EINVAL;
     if (a->rows == 0) return LOWBIT_OK;

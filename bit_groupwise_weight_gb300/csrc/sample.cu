@@ -12,19 +12,28 @@
 //     top-p   of those, the ones before which less than ceil(p Z) has been summed,
 //             Z their total.
 // The token is the first index whose running total (index order, kept tokens)
-// passes floor(u Z'), Z' the kept total.  T <= 0: the first largest logit.
+// passes floor(u Z'), Z' the kept total.  T <= 0: the first largest logit.  Tokens
+// with W_i = 0 (s < -21.5) can never be drawn and count for nothing.
 //
-// The prefix is found without sorting.  Level 1 counts tokens (and sums W) in
-// 2048 bins of s; the bin in which the k-th token or the p-th mass falls is then
-// split by the bits of x, over the range that it really holds, until one value
-// is left: the threshold.  Equal logits are taken in index order up to a quota.
-// Tokens with W_i = 0 (s < -21.5) can never be drawn and are left out, which
-// bounds the bins.
+// Most tokens cannot be among the kept, and a bound on x that says so costs little:
+//     top-k   a value that at least k threads' largest logits reach (bisected with
+//             the CTA's counting barrier),
+//     top-p   tokens under (1 - p) Z / V together hold less than (1 - p) Z; the mass of
+//             those above, in 256 bins of s, says in which bin p Z is reached.
+// The tokens above the bound (usually some hundreds) go to one CTA, which sorts them
+// and does the rest by itself.  When they are more than its list holds, that of top-p
+// takes the tokens of the last bin only and finds the threshold among them (the last
+// kept logit, and how many equal ones are kept, in index order); the draw then runs
+// over all tokens above it.  Where even that does not fit (flat logits, very large k)
+// the threshold is found by counting: bins of s, then ranges of the bits of x, until
+// one value is left.
 //
-// Work split: a cluster of up to 8 CTAs takes a row, each keeps its part of the
-// logits in shared memory (read from HBM once), and counts are exchanged through
-// distributed shared memory.  Bound: the chain of cluster-wide steps for few
-// rows, HBM and the shared-memory atomics for many.
+// Work split: a cluster of up to 8 CTAs takes a row and holds it in registers (each
+// logit is read from memory once); what CTAs need of each other goes through
+// distributed shared memory.  Bound: the chain of cluster-wide steps (three for top-k,
+// five to seven for top-p) for few rows, the exponentials of all tokens for many.
+#include <algorithm>
+
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -33,9 +42,12 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048;                        // of the counting path
+constexpr int kCoarse = 256;                       // of the top-p bound
+constexpr int kList = 2048;                        // tokens that one CTA sorts
 constexpr int kMaxCluster = 8;
-constexpr int kHeld = 32768;                       // logits a CTA keeps; more are read again
+constexpr int kHeld = 8;                           // 16-byte vectors that a thread holds
+constexpr int kMaxVecs = 40;                       // that it may have (the others are read again)
 constexpr float kUnit = 1073741824.0f;             // 2^30
 constexpr float kSpan = 21.6f;                     // rint(2^30 e^-s) is 0 beyond
 typedef unsigned long long u64;
@@ -50,52 +62,110 @@ __device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
     return v;
 }
-
-// A logit as fp32; NaN counts as -infinity, -0 as 0.
-__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : x + 0.0f; }
-
-__device__ __forceinline__ float load_logit(const void *row, int dtype, int64_t i) {
-    if (dtype == LOWBIT_DTYPE_F32) return clean(static_cast<const float *>(row)[i]);
-    const uint16_t h = static_cast<const uint16_t *>(row)[i];
-    return clean(dtype == LOWBIT_DTYPE_BF16 ? __uint_as_float((uint32_t)h << 16) : half_bits_to_float(h));
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-// Order-preserving map of floats to unsigned integers.
+// Order-preserving map of floats to unsigned integers (-0 like 0), and back.
 __device__ __forceinline__ uint32_t ordered(float x) {
-    const uint32_t u = __float_as_uint(x);
+    const uint32_t u = __float_as_uint(x + 0.0f);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
 struct Shared {
-    float x[kHeld];
-    uint32_t count[kBins], lo[kBins], hi[kBins];   // W = lo + 2^16 hi, summed apart in 32 bits
+    union {
+        struct {                                   // the list, and the bins of the top-p bound
+            u64 list[kList];
+            uint32_t coarse_lo[kCoarse], coarse_hi[kCoarse];
+        };
+        struct {                                   // the counting path: W = lo + 2^16 hi, summed apart in 32 bits
+            uint32_t count[kBins], lo[kBins], hi[kBins];
+        };
+    };
+    u64 above[kMaxVecs * kWarps];                  // mass above the cut of each run of a warp's vectors, in index order
+    uint32_t equal[kMaxVecs * kWarps];             // tokens equal to it
     u64 pub[2][3];                                 // what this CTA tells the others, in two buffers
     u64 peer[kMaxCluster][3];                      // what each CTA told
     u64 red[kWarps][2];
-    u64 found[3];
+    u64 found[4];
     uint32_t kmin, kmax;
 };
 
-// A row's part in this CTA.
-struct Part {
-    const void *logits;
-    int dtype, n;                                  // its tokens
-    int64_t first;                                 // index of the first
-    float m, inv_t, min_p;
+// A row's part in this CTA: vectors (16 bytes) first, first + kThreads, ... of the row's
+// aligned memory; `lead` values of the first vector are before the row.
+template <int DTYPE>
+struct Row {
+    static constexpr int kVec = DTYPE == LOWBIT_DTYPE_F32 ? 4 : 8;
+    const uint4 *base;
+    int lead, V, first, end, nvec;                 // vectors [first, end) are this CTA's, nvec of a thread at most
+    bool infinite;                                 // the maximum is +infinity: those count as 0, the others as -infinity
+    uint4 held[kHeld];
+
+    __device__ __forceinline__ static float get(const uint4 &w, int v) {
+        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (DTYPE == LOWBIT_DTYPE_F32) return __uint_as_float(a[v]);
+        const uint16_t h = (uint16_t)(a[v >> 1] >> (v & 1 ? 16 : 0));
+        if constexpr (DTYPE == LOWBIT_DTYPE_BF16) return __uint_as_float((uint32_t)h << 16);
+        return half_bits_to_float(h);
+    }
+    __device__ __forceinline__ int vec_of(int it) const { return first + it * kThreads + (int)threadIdx.x; }
+    __device__ __forceinline__ int index_of(int it, int v) const { return vec_of(it) * kVec + v - lead; }
+    // Vector `it` of this thread; what is not of the row is -infinity.
+    __device__ __forceinline__ uint4 load(int it) const {
+        constexpr uint32_t kNone = DTYPE == LOWBIT_DTYPE_F32 ? 0xFF800000u : DTYPE == LOWBIT_DTYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+        uint32_t a[4] = {kNone, kNone, kNone, kNone};
+        const int vec = vec_of(it);
+        if (vec < end) {
+            const uint4 w = __ldg(base + vec);
+            a[0] = w.x, a[1] = w.y, a[2] = w.z, a[3] = w.w;
+            const int i0 = vec * kVec - lead;
+            if (i0 < 0 || i0 + kVec > V || infinite) {
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) {
+                    const bool in = i0 + v >= 0 && i0 + v < V;
+                    bool none = !in, zero = false;
+                    if (infinite) zero = in && get(w, v) == INFINITY, none = !zero;
+                    if constexpr (DTYPE == LOWBIT_DTYPE_F32) {
+                        if (none || zero) a[v] = none ? kNone : 0u;
+                    } else {
+                        const uint32_t m = v & 1 ? 0xFFFF0000u : 0xFFFFu;
+                        if (none || zero) a[v >> 1] = (a[v >> 1] & ~m) | ((none ? kNone : 0u) & m);
+                    }
+                }
+            }
+        }
+        return make_uint4(a[0], a[1], a[2], a[3]);
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(const F &f) const {          // f(x, it, v)
+#pragma unroll
+        for (int it = 0; it < kHeld; ++it)
+            if (it < nvec)
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) f(get(held[it], v), it, v);
+        for (int it = kHeld; it < nvec; ++it) {
+            const uint4 w = load(it);
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) f(get(w, v), it, v);
+        }
+    }
+};
+
+// A row's settings, and its cluster.
+struct Draw {
+    float m, inv_t, T, min_p;
     int rank, ranks, round;                        // in the cluster; exchanges so far
 };
 
-struct Token { float s; uint32_t W; bool in; };
+struct Token { float s, w; uint32_t W; bool in; };
 
-__device__ __forceinline__ float value(const Shared &sm, const Part &r, int i) {
-    return i < kHeld ? sm.x[i] : load_logit(r.logits, r.dtype, r.first + i);
-}
-__device__ __forceinline__ Token weigh(const Part &r, float x) {
+__device__ __forceinline__ Token weigh(const Draw &r, float x) {
     Token t;
-    t.s = x == r.m ? 0.f : __fmul_rn(__fsub_rn(x, r.m), r.inv_t);
-    const float w = expf(t.s);
-    t.W = __float2uint_rn(__fmul_rn(w, kUnit));
-    t.in = t.W > 0u && !(w < r.min_p);
+    t.s = __fmul_rn(__fsub_rn(x, r.m), r.inv_t);
+    t.w = expf(t.s);
+    t.W = __float2uint_rn(__fmul_rn(t.w, kUnit));  // NaN gives 0
+    t.in = t.W > 0u && t.w >= r.min_p;
     return t;
 }
 __device__ __forceinline__ int bin_of(float s) { return min((int)(-s * (kBins / kSpan)), kBins - 1); }
@@ -103,16 +173,25 @@ __device__ __forceinline__ int bin_of(float s) { return min((int)(-s * (kBins / 
 // Cluster-wide exchange: sm.peer[rank] holds every CTA's words (given by its thread
 // 0), for all threads.  A CTA overwrites a buffer only after the next exchange's
 // barrier, which every reader of it has passed.
-__device__ __forceinline__ void exchange(Shared &sm, Part &r, u64 a, u64 b = 0, u64 c = 0) {
+__device__ __forceinline__ void exchange(Shared &sm, Draw &r, u64 a, u64 b = 0, u64 c = 0) {
     u64 *pub = sm.pub[r.round & 1];
-    if (threadIdx.x == 0) pub[0] = a, pub[1] = b, pub[2] = c;
-    ptx::cluster_sync();
-    if ((int)threadIdx.x < 3 * r.ranks) {
-        const uint32_t rank = threadIdx.x / 3, w = threadIdx.x % 3;
-        sm.peer[rank][w] = ld_cluster_u64(ptx::mapa_shared(ptx::smem_u32(pub + w), rank));
+    if (r.ranks == 1) {
+        __syncthreads();
+        if (threadIdx.x == 0) sm.peer[0][0] = a, sm.peer[0][1] = b, sm.peer[0][2] = c;
+    } else {
+        if (threadIdx.x == 0) pub[0] = a, pub[1] = b, pub[2] = c;
+        ptx::cluster_sync();
+        if ((int)threadIdx.x < 3 * r.ranks) {
+            const uint32_t rank = threadIdx.x / 3, w = threadIdx.x % 3;
+            sm.peer[rank][w] = ld_cluster_u64(ptx::mapa_shared(ptx::smem_u32(pub + w), rank));
+        }
     }
     __syncthreads();
     ++r.round;
+}
+__device__ __forceinline__ void cluster_barrier(const Draw &r) {
+    if (r.ranks == 1) __syncthreads();
+    else ptx::cluster_sync();
 }
 
 // Exclusive prefix of (a, b) over the CTA's threads in order; the totals in ta, tb.
@@ -128,19 +207,63 @@ __device__ __forceinline__ void block_scan(Shared &sm, u64 &a, u64 &b, u64 &ta, 
     if (lane == 31) sm.red[warp][0] = ia, sm.red[warp][1] = ib;
     __syncthreads();
     a = ia - a, b = ib - b, ta = tb = 0;
+#pragma unroll
     for (int i = 0; i < kWarps; ++i) {
         if (i < warp) a += sm.red[i][0], b += sm.red[i][1];
         ta += sm.red[i][0], tb += sm.red[i][1];
     }
 }
 
+// floor(u * total), below total.
+__device__ __forceinline__ u64 target_of(float u, u64 total) {
+    const u64 t = u > 0.f ? (u64)floor((double)u * (double)total) : 0ull;
+    return t < total ? t : total - 1;
+}
+
+// The mass that a prefix has to reach for top-p: ceil(p total), at least 1.
+__device__ __forceinline__ u64 limit_of(float top_p, u64 total) {
+    const double want = ceil((double)top_p * (double)total);
+    return want > 1.0 ? (u64)want : 1ull;
+}
+
+// Sorts the first n entries of the list (n a power of two), rising.  Steps over fewer
+// than 32 entries stay in registers.
+__device__ __forceinline__ void sort_list(Shared &sm, int n) {
+    const int tid = threadIdx.x;
+    for (int k = 2; k <= n; k <<= 1) {
+        for (int j = k >> 1; j >= 32; j >>= 1) {
+            for (int p = tid; p < n / 2; p += kThreads) {
+                const int i = ((p & ~(j - 1)) << 1) | (p & (j - 1)), o = i | j;
+                const u64 a = sm.list[i], b = sm.list[o];
+                if ((a > b) == ((i & k) == 0)) sm.list[i] = b, sm.list[o] = a;
+            }
+            __syncthreads();
+        }
+        for (int i0 = 0; i0 < n; i0 += kThreads) {
+            const int i = i0 + tid;
+            if ((i & ~31) < n) {                   // whole warps
+                u64 v = i < n ? sm.list[i] : ~0ull;
+                const bool up = (i & k) == 0;
+                for (int j = min(k >> 1, 16); j > 0; j >>= 1) {
+                    const u64 o = __shfl_xor_sync(~0u, v, j);
+                    v = ((i & j) == 0) == up ? (v < o ? v : o) : (v > o ? v : o);
+                }
+                if (i < n) sm.list[i] = v;
+            }
+        }
+        __syncthreads();
+    }
+}
+__device__ __forceinline__ int power_of_two(int n) { return n <= 2 ? 2 : 1 << (32 - __clz(n - 1)); }
+
 // The kept prefix: tokens whose key is above `key`, and of those equal to it the
 // first `quota` in index order (W each).
 struct Cut { uint32_t key, W; u64 quota; };
 
-// Narrows the prefix to the tokens before which less than `target` tokens (by_mass:
-// units of W) come; the present prefix reaches the target.
-__device__ void narrow(Shared &sm, Part &r, bool by_mass, u64 target, Cut &cut) {
+// The counting path.  Narrows the prefix to the tokens before which less than `target`
+// tokens (by_mass: units of W) come; the present prefix reaches the target.
+template <int DTYPE>
+__device__ __noinline__ void narrow(Shared &sm, const Row<DTYPE> &row, Draw &r, bool by_mass, u64 target, Cut &cut) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int slice = kBins / r.ranks, per = max(slice / kThreads, 1);    // bins of a CTA, of a thread
     u64 n_above = 0, m_above = 0;                  // tokens and mass above the range under search
@@ -148,20 +271,21 @@ __device__ void narrow(Shared &sm, Part &r, bool by_mass, u64 target, Cut &cut) 
     int bin = 0, shift = 0;
     for (int level = 0;; ++level) {
         // Of the tokens above the present cut's key, those in the range.
-        auto inside = [&](uint32_t k, const Token &t) {
-            if (!t.in || k <= cut.key) return false;
-            return level == 0 || (level == 1 ? bin_of(t.s) == bin : (k >= klo && k <= khi));
+        auto inside = [&](uint32_t k, float x, Token &t) {
+            if (k <= cut.key || (level > 1 && (k < klo || k > khi))) return false;
+            t = weigh(r, x);
+            return t.in && (level != 1 || bin_of(t.s) == bin);
         };
         if (level > 0) {
             // The keys that the range really holds; one: that is the threshold.
             if (tid == 0) sm.kmin = ~0u, sm.kmax = 0u;
             __syncthreads();
             uint32_t lo = ~0u, hi = 0u;
-            for (int i = tid; i < r.n; i += kThreads) {
-                const float x = value(sm, r, i);
+            row.each([&](float x, int, int) {
                 const uint32_t k = ordered(x);
-                if (inside(k, weigh(r, x))) lo = min(lo, k), hi = max(hi, k);
-            }
+                Token t;
+                if (inside(k, x, t)) lo = min(lo, k), hi = max(hi, k);
+            });
             lo = __reduce_min_sync(~0u, lo);
             hi = __reduce_max_sync(~0u, hi);
             if (lane == 0) atomicMin(&sm.kmin, lo), atomicMax(&sm.kmax, hi);
@@ -175,17 +299,16 @@ __device__ void narrow(Shared &sm, Part &r, bool by_mass, u64 target, Cut &cut) 
         }
         for (int i = tid; i < kBins; i += kThreads) sm.count[i] = sm.lo[i] = sm.hi[i] = 0u;
         __syncthreads();
-        for (int i = tid; i < r.n; i += kThreads) {
-            const float x = value(sm, r, i);
+        row.each([&](float x, int, int) {
             const uint32_t k = ordered(x);
-            const Token t = weigh(r, x);
-            if (!inside(k, t)) continue;
+            Token t;
+            if (!inside(k, x, t)) return;
             const int at = level == 0 ? bin_of(t.s) : (int)((khi - k) >> shift);
             atomicAdd(&sm.count[at], 1u);
             atomicAdd(&sm.lo[at], t.W & 0xFFFFu);
             atomicAdd(&sm.hi[at], t.W >> 16);
-        }
-        ptx::cluster_sync();
+        });
+        cluster_barrier(r);
         // This CTA's slice of the bins, summed over the cluster.
         u64 cn[kBins / kThreads], cm[kBins / kThreads], en = 0, em = 0, tn, tm;
 #pragma unroll
@@ -241,176 +364,491 @@ __device__ void narrow(Shared &sm, Part &r, bool by_mass, u64 target, Cut &cut) 
     }
     // klo == khi: every token of the range has this key.
     cut.key = khi;
-    cut.W = weigh(r, __uint_as_float(khi & 0x80000000u ? khi ^ 0x80000000u : ~khi)).W;
+    cut.W = weigh(r, unordered(khi)).W;
     cut.quota = by_mass ? (target - m_above + cut.W - 1) / cut.W : target - n_above;
 }
 
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs p) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    Shared &sm = *reinterpret_cast<Shared *>(raw);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    ptx::pdl_launch_dependents();
-    ptx::pdl_wait();
-
-    Part r;
-    uint32_t ranks;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
-    r.ranks = (int)ranks, r.rank = (int)ptx::cluster_ctarank(), r.round = 0;
-    const int b = (int)(blockIdx.x / ranks);
-    const int part = (p.V + r.ranks - 1) / r.ranks;
-    r.first = (int64_t)r.rank * part;
-    r.n = (int)max((int64_t)0, min((int64_t)part, p.V - r.first));
-    r.dtype = p.dtype;
-    r.logits = static_cast<const uint8_t *>(p.logits) + b * p.row_stride * (p.dtype == LOWBIT_DTYPE_F32 ? 4 : 2);
-    const float T = p.temperature != nullptr ? p.temperature[b] : p.temperature_all;
-    const float top_p = p.top_p != nullptr ? p.top_p[b] : p.top_p_all;
-    const float min_p = p.min_p != nullptr ? p.min_p[b] : p.min_p_all;
-    const int top_k = p.top_k != nullptr ? p.top_k[b] : p.top_k_all;
-
-    // The row's part into shared memory; its largest logit, lowest index first.
-    u64 best = 0;
-    for (int i = tid; i < r.n; i += kThreads) {
-        const float x = load_logit(r.logits, r.dtype, r.first + i);
-        if (i < kHeld) sm.x[i] = x;
-        const u64 v = (u64)ordered(x) << 32 | (uint32_t)~(uint32_t)(r.first + i);
-        best = v > best ? v : best;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const u64 v = __shfl_xor_sync(~0u, best, o);
-        best = v > best ? v : best;
-    }
-    if (lane == 0) sm.red[warp][0] = best;
-    __syncthreads();
-    for (int i = 0; i < kWarps; ++i) best = sm.red[i][0] > best ? sm.red[i][0] : best;
-    exchange(sm, r, best);
-    for (int i = 0; i < r.ranks; ++i) best = sm.peer[i][0] > best ? sm.peer[i][0] : best;
-    const uint32_t top = (uint32_t)(best >> 32);
-    r.m = __uint_as_float(top & 0x80000000u ? top ^ 0x80000000u : ~top);
-    const bool empty = r.m == -INFINITY;           // nothing can be drawn
-    if (empty || !(T > 0.f)) {
-        if (r.rank == 0 && tid == 0) {
-            p.token[b] = empty ? -1 : (int64_t)(uint32_t)~(uint32_t)best;
-            if (p.logprob != nullptr) p.logprob[b] = empty ? -INFINITY : 0.f;
-        }
-        ptx::cluster_sync();                       // others may still read this CTA's words
-        return;
-    }
-    r.inv_t = __fdiv_rn(1.f, T);
-    r.min_p = fminf(min_p, 1.f);                   // the largest logit is always kept
-
-    // Tokens within min-p that can be drawn at all, and their mass.
-    Cut cut{0u, 1u, 0};
-    u64 n = 0, mass = 0, tn, tm;
-    for (int i = tid; i < r.n; i += kThreads) {
-        const Token t = weigh(r, value(sm, r, i));
-        if (t.in) ++n, mass += t.W;
-    }
-    block_scan(sm, n, mass, tn, tm);
-    exchange(sm, r, tn, tm);
-    n = mass = 0;
-    for (int i = 0; i < r.ranks; ++i) n += sm.peer[i][0], mass += sm.peer[i][1];
-
-    const int seg = (r.n + 32 * kWarps - 1) / (32 * kWarps) * 32;        // a warp's tokens, in index order
-    const int s0 = min(warp * seg, r.n), s1 = min(s0 + seg, r.n);
-    // Mass above the cut and tokens equal to it: this thread's CTA, warp by warp, in sm.red.
-    auto tally = [&] {
-        u64 above = 0, equal = 0;
-        for (int i = s0 + lane; i < s1; i += 32) {
-            const float x = value(sm, r, i);
-            const uint32_t k = ordered(x);
-            if (k < cut.key) continue;
+// Mass above the cut and tokens equal to it, for each run of a warp's vectors (in index
+// order: vector number, then warp) in sm.above and sm.equal, and of every CTA in sm.peer.
+template <int DTYPE>
+__device__ __forceinline__ void tally(Shared &sm, const Row<DTYPE> &row, Draw &r, const Cut &cut) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 above = 0, all_above = 0;
+    uint32_t equal = 0, all_equal = 0;
+    row.each([&](float x, int it, int v) {
+        const uint32_t k = ordered(x);
+        if (k >= cut.key) {
             const Token t = weigh(r, x);
             if (t.in) {
                 if (k > cut.key) above += t.W;
                 else ++equal;
             }
         }
+        if (v == Row<DTYPE>::kVec - 1) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            above += __shfl_xor_sync(~0u, above, o);
-            equal += __shfl_xor_sync(~0u, equal, o);
+            for (int o = 16; o > 0; o >>= 1) above += __shfl_xor_sync(~0u, above, o);
+            equal = __reduce_add_sync(~0u, equal);
+            if (lane == 0) sm.above[it * kWarps + warp] = above, sm.equal[it * kWarps + warp] = equal;
+            all_above += above, all_equal += equal;
+            above = 0, equal = 0;
         }
-        __syncthreads();
-        if (lane == 0) sm.red[warp][0] = above, sm.red[warp][1] = equal;
-        __syncthreads();
-        above = equal = 0;
-        for (int i = 0; i < kWarps; ++i) above += sm.red[i][0], equal += sm.red[i][1];
-        exchange(sm, r, above, equal);
-    };
-    if (top_k > 0 && (u64)top_k < n) {
-        narrow(sm, r, false, (u64)top_k, cut);
-        tally();
-        mass = cut.quota * cut.W;
-        for (int i = 0; i < r.ranks; ++i) mass += sm.peer[i][0];
-    }
-    if (top_p < 1.f) {
-        const double want = ceil((double)top_p * (double)mass);
-        narrow(sm, r, true, want > 1.0 ? (u64)want : 1ull, cut);
-    }
-    tally();
+    });
+    u64 a = lane == 0 ? all_above : 0, b = lane == 0 ? all_equal : 0, ta, tb;
+    block_scan(sm, a, b, ta, tb);
+    exchange(sm, r, ta, tb);
+}
 
-    // The draw: CTA, warp and token in which the target falls.
-    u64 total = 0, start = 0, equal = 0, mine = 0;                       // start, equal: before this CTA
-    for (int i = 0, eq = 0; i < r.ranks; ++i) {
-        const u64 e = sm.peer[i][1], left = cut.quota > (u64)eq ? cut.quota - eq : 0;
-        const u64 kept = sm.peer[i][0] + (e < left ? e : left) * cut.W;
-        if (i == r.rank) start = total, equal = eq, mine = kept;
-        total += kept;
-        eq += (int)e;
+// The draw from all of the row's tokens above the cut, after tally.
+template <int DTYPE>
+__device__ __forceinline__ void draw_all(Shared &sm, const Row<DTYPE> &row, const Draw &r, const Cut &cut, const SampleArgs &p, int b) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto kept = [&](u64 above, u64 equal, u64 before) {       // of a run with `before` equal tokens before it
+        const u64 left = cut.quota > before ? cut.quota - before : 0;
+        return above + (equal < left ? equal : left) * cut.W;
+    };
+    u64 total = 0, start = 0, mine = 0, eq = 0, eq0 = 0;      // start, eq0: before this CTA
+    for (int i = 0; i < r.ranks; ++i) {
+        const u64 k = kept(sm.peer[i][0], sm.peer[i][1], eq);
+        if (i == r.rank) start = total, eq0 = eq, mine = k;
+        total += k;
+        eq += sm.peer[i][1];
     }
-    const float u = p.u[b];
-    u64 target = u > 0.f ? (u64)floor((double)u * (double)total) : 0ull;
-    target = target < total ? target : total - 1;
-    if (target >= start && target < start + mine) {
-        for (int i = 0; i < kWarps; ++i) {
-            const u64 e = sm.red[i][1], left = cut.quota > equal ? cut.quota - equal : 0;
-            const u64 kept = sm.red[i][0] + (e < left ? e : left) * cut.W;
-            if (target < start + kept) {
-                if (i == warp) {
-                    for (int base = s0; base < s1; base += 32) {
-                        const int at = base + lane;
-                        const float x = at < s1 ? value(sm, r, at) : -INFINITY;
-                        const uint32_t k = ordered(x);
-                        const Token t = weigh(r, x);
-                        const bool tie = t.in && k == cut.key;
-                        const unsigned ties = __ballot_sync(~0u, tie);
-                        const bool kept_tie = tie && equal + __popc(ties & ((1u << lane) - 1u)) < cut.quota;
-                        u64 inc = (t.in && k > cut.key) || kept_tie ? t.W : 0;
+    const u64 target = target_of(p.u[b], total);
+    if (target < start || target >= start + mine) return;     // the same for the whole CTA
+    // The run in which it falls: two runs a thread at most.
+    const int runs = row.nvec * kWarps, per = (runs + kThreads - 1) / kThreads;
+    u64 e = 0, k = 0, te, tk, zero = 0, tz;
+    for (int q = 0; q < per; ++q)
+        if (tid * per + q < runs) e += sm.equal[tid * per + q];
+    block_scan(sm, e, zero, te, tz);
+    e += eq0;
+    u64 run = e;
+    for (int q = 0; q < per; ++q)
+        if (tid * per + q < runs) {
+            k += kept(sm.above[tid * per + q], sm.equal[tid * per + q], run);
+            run += sm.equal[tid * per + q];
+        }
+    u64 z2 = 0;
+    block_scan(sm, k, z2, tk, tz);
+    k += start;
+    for (int q = 0; q < per; ++q)
+        if (tid * per + q < runs) {
+            const int at = tid * per + q;
+            const u64 add = kept(sm.above[at], sm.equal[at], e);
+            if (target >= k && target < k + add) sm.found[0] = (u64)at, sm.found[1] = k, sm.found[2] = e;
+            k += add;
+            e += sm.equal[at];
+        }
+    __syncthreads();
+    const int at = (int)sm.found[0];
+    if (at % kWarps != warp) return;
+    // The lane, then the token.
+    const uint4 w = row.load(at / kWarps);
+    u64 above = 0;
+    uint32_t equal = 0;
 #pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const u64 v = __shfl_up_sync(~0u, inc, o);
-                            if (lane >= o) inc += v;
-                        }
-                        const unsigned past = __ballot_sync(~0u, start + inc > target);
-                        if (past) {
-                            if (lane == __ffs(past) - 1) {
-                                p.token[b] = r.first + at;
-                                if (p.logprob != nullptr)
-                                    p.logprob[b] = t.s - logf((float)total * (1.f / kUnit));
-                            }
-                            break;
-                        }
-                        start += __shfl_sync(~0u, inc, 31);
-                        equal += __popc(ties);
+    for (int v = 0; v < Row<DTYPE>::kVec; ++v) {
+        const float x = Row<DTYPE>::get(w, v);
+        const uint32_t key = ordered(x);
+        const Token t = weigh(r, x);
+        if (t.in && key > cut.key) above += t.W;
+        if (t.in && key == cut.key) ++equal;
+    }
+    u64 ie = equal;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 v = __shfl_up_sync(~0u, ie, o);
+        if (lane >= o) ie += v;
+    }
+    u64 seen = sm.found[2] + ie - equal, ik = kept(above, equal, seen);
+    const u64 own = ik;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 v = __shfl_up_sync(~0u, ik, o);
+        if (lane >= o) ik += v;
+    }
+    u64 sum = sm.found[1] + ik - own;
+    if (target < sum || target >= sum + own) return;
+#pragma unroll
+    for (int v = 0; v < Row<DTYPE>::kVec; ++v) {
+        const float x = Row<DTYPE>::get(w, v);
+        const uint32_t key = ordered(x);
+        const Token t = weigh(r, x);
+        const bool tie = t.in && key == cut.key;
+        const u64 add = (t.in && key > cut.key) || (tie && seen < cut.quota) ? t.W : 0;
+        seen += tie;
+        if (target >= sum && target < sum + add) {
+            p.token[b] = row.index_of(at / kWarps, v);
+            if (p.logprob != nullptr) p.logprob[b] = t.s - logf((float)total * (1.f / kUnit));
+        }
+        sum += add;
+    }
+}
+
+// The cut of the list's n tokens, before which `before` units of mass come: the last kept
+// key and how many of it are kept (this CTA's alone).
+__device__ __forceinline__ Cut cut_listed(Shared &sm, const Draw &r, int n, u64 before, u64 limit) {
+    constexpr int kPer = kList / kThreads;
+    const int tid = threadIdx.x, size = power_of_two(n);
+    for (int i = n + tid; i < size; i += kThreads) sm.list[i] = ~0ull;
+    if (tid == 0) sm.found[0] = 0;
+    __syncthreads();
+    sort_list(sm, size);
+    u64 W[kPer], sum = 0, z = 0, ts, tz;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const int i = tid * kPer + q;
+        W[q] = i < n ? weigh(r, unordered(~(uint32_t)(sm.list[i] >> 32))).W : 0;
+        sum += W[q];
+    }
+    block_scan(sm, sum, z, ts, tz);
+    sum += before;
+    u64 kept = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        kept += tid * kPer + q < n && sum < limit;
+        sum += W[q];
+    }
+    z = 0;
+    block_scan(sm, kept, z, ts, tz);               // ts: kept in all
+    const uint32_t key = ~(uint32_t)(sm.list[ts - 1] >> 32);
+    u64 same = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const int i = tid * kPer + q;
+        same += i < (int)ts && ~(uint32_t)(sm.list[i] >> 32) == key;
+    }
+    z = 0;
+    u64 quota;
+    block_scan(sm, same, z, quota, tz);
+    return Cut{key, weigh(r, unordered(key)).W, quota};
+}
+
+// The rest of the work on the list of n tokens (this CTA's alone): order, top-k, top-p,
+// draw.  total: mass of all tokens within min-p (0: that of the first top_k of the list).
+template <int DTYPE>
+__device__ __forceinline__ void draw_listed(Shared &sm, const Row<DTYPE> &row, const Draw &r, int n, int top_k, float top_p, u64 total,
+                                            const SampleArgs &p, int b) {
+    constexpr int kPer = kList / kThreads;
+    const int tid = threadIdx.x;
+    int size = power_of_two(n);
+    for (int i = n + tid; i < size; i += kThreads) sm.list[i] = ~0ull;
+    __syncthreads();
+    sort_list(sm, size);                           // ~key, index: x falling, index rising
+    // Weights in that order, kPer neighbours a thread.
+    u64 W[kPer], idx[kPer], sum = 0, z = 0, all, tz;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const int i = tid * kPer + q;
+        W[q] = idx[q] = 0;
+        if (i < n) {
+            const Token t = weigh(r, unordered(~(uint32_t)(sm.list[i] >> 32)));
+            if (t.in && (top_k <= 0 || i < top_k)) W[q] = t.W;
+            idx[q] = sm.list[i] & 0xFFFFFFFFull;
+        }
+        sum += W[q];
+    }
+    block_scan(sm, sum, z, all, tz);
+    if (total == 0) total = all;
+    const u64 limit = top_p < 1.f ? limit_of(top_p, total) : ~0ull;
+    u64 kept = 0, count = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const u64 w = W[q];
+        if (sum >= limit) W[q] = 0;
+        sum += w;
+        kept += W[q];
+        count += W[q] != 0;
+    }
+    // The kept in index order.
+    u64 before = kept, place = count, mass, left;
+    block_scan(sm, before, place, mass, left);
+    size = power_of_two((int)left);
+    for (int i = (int)left + tid; i < size; i += kThreads) sm.list[i] = ~0ull;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+        if (W[q] != 0) sm.list[place++] = idx[q] << 32 | W[q];
+    __syncthreads();
+    sort_list(sm, size);
+    u64 own = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const int i = tid * kPer + q;
+        W[q] = i < (int)left ? sm.list[i] & 0xFFFFFFFFull : 0;
+        own += W[q];
+    }
+    u64 zero = 0;
+    block_scan(sm, own, zero, all, tz);
+    const u64 target = target_of(p.u[b], mass);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        if (target >= own && target < own + W[q]) {
+            const int i = (int)(sm.list[tid * kPer + q] >> 32);
+            p.token[b] = i;
+            if (p.logprob != nullptr) {
+                const int at = i + row.lead;
+                float value = r.m;
+                if (!row.infinite) {
+                    const uint4 w = __ldg(row.base + at / Row<DTYPE>::kVec);
+#pragma unroll
+                    for (int v = 0; v < Row<DTYPE>::kVec; ++v)
+                        if (v == at % Row<DTYPE>::kVec) value = Row<DTYPE>::get(w, v);
+                }
+                p.logprob[b] = weigh(r, value).s - logf((float)mass * (1.f / kUnit));
+            }
+        }
+        own += W[q];
+    }
+}
+
+template <int DTYPE>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p) {
+    constexpr int kVec = Row<DTYPE>::kVec;
+    extern __shared__ __align__(16) uint8_t raw[];
+    Shared &sm = *reinterpret_cast<Shared *>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+
+    Draw r;
+    uint32_t ranks;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
+    r.ranks = (int)ranks, r.rank = (int)ptx::cluster_ctarank(), r.round = 0;
+    const int b = (int)(blockIdx.x / ranks);
+    Row<DTYPE> row;
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p.logits) + (int64_t)b * p.row_stride * (DTYPE == LOWBIT_DTYPE_F32 ? 4 : 2);
+        row.base = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
+        row.lead = (int)(at & 15) / (16 / kVec);
+        row.V = p.V;
+        row.infinite = false;
+        const int all = (row.lead + p.V + kVec - 1) / kVec, part = (all + r.ranks - 1) / r.ranks;
+        row.first = r.rank * part;
+        row.end = min(row.first + part, all);
+        row.nvec = (part + kThreads - 1) / kThreads;
+    }
+#pragma unroll
+    for (int it = 0; it < kHeld; ++it)
+        if (it < row.nvec) row.held[it] = row.load(it);
+    r.T = p.temperature != nullptr ? p.temperature[b] : p.temperature_all;
+    const float top_p = p.top_p != nullptr ? p.top_p[b] : p.top_p_all;
+    const float min_p = p.min_p != nullptr ? p.min_p[b] : p.min_p_all;
+    const int top_k = p.top_k != nullptr ? p.top_k[b] : p.top_k_all;
+    const bool greedy = !(r.T > 0.f);
+
+    // The largest logit of the thread, the CTA and the row.
+    float own = -INFINITY;                         // fmaxf leaves NaN out
+    row.each([&](float x, int, int) { own = fmaxf(own, x); });
+    {
+        const uint32_t k = __reduce_max_sync(~0u, ordered(own));
+        if (lane == 0) sm.red[warp][0] = k;
+    }
+    __syncthreads();
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) top = max(top, (uint32_t)sm.red[i][0]);
+    // A value that at least ceil(k / ranks) threads' logits reach, in every CTA: the k
+    // first tokens are not below the least of these.
+    const bool by_k = !greedy && top_k > 0 && top_k <= kThreads / 2 * r.ranks && top_k <= kList / 2;
+    uint32_t reach = 0;
+    if (by_k) {
+        const int need = (top_k + r.ranks - 1) / r.ranks;
+        float hi = unordered(top), lo = hi - 22.f * r.T;
+        if (lo > -INFINITY && __syncthreads_count(own >= lo) >= need) {
+            for (int i = 0; i < 12; ++i) {
+                const float mid = 0.5f * (lo + hi);
+                if (__syncthreads_count(own >= mid) >= need) lo = mid;
+                else hi = mid;
+            }
+            reach = ordered(lo);
+        }
+    }
+    exchange(sm, r, top, reach);
+    reach = ~0u;
+    for (int i = 0; i < r.ranks; ++i) top = max(top, (uint32_t)sm.peer[i][0]), reach = min(reach, (uint32_t)sm.peer[i][1]);
+    r.m = unordered(top);
+    if (r.m == -INFINITY) {                        // nothing can be drawn
+        if (r.rank == 0 && tid == 0) {
+            p.token[b] = -1;
+            if (p.logprob != nullptr) p.logprob[b] = -INFINITY;
+        }
+        cluster_barrier(r);                        // others may still read this CTA's words
+        return;
+    }
+    if (greedy) {
+        int first = INT32_MAX;
+        row.each([&](float x, int it, int v) {
+            if (x == r.m) first = min(first, row.index_of(it, v));
+        });
+        first = __reduce_min_sync(~0u, first);
+        __syncthreads();
+        if (lane == 0) sm.red[warp][0] = (u64)first;
+        __syncthreads();
+        for (int i = 0; i < kWarps; ++i) first = min(first, (int)sm.red[i][0]);
+        exchange(sm, r, (u64)first);
+        for (int i = 0; i < r.ranks; ++i) first = min(first, (int)sm.peer[i][0]);
+        if (r.rank == 0 && tid == 0) {
+            p.token[b] = first;
+            if (p.logprob != nullptr) p.logprob[b] = 0.f;
+        }
+        cluster_barrier(r);
+        return;
+    }
+    if (r.m == INFINITY) {
+        row.infinite = true;
+        r.m = 0.f;
+#pragma unroll
+        for (int it = 0; it < kHeld; ++it)
+            if (it < row.nvec) row.held[it] = row.load(it);
+    }
+    r.inv_t = fminf(__fdiv_rn(1.f, r.T), 3.402823466e38f);
+    r.min_p = fminf(min_p, 1.f);                   // the largest logit is always kept
+
+    u64 total = 0, tokens = 0;                     // mass and number of the tokens within min-p
+    const bool by_p = top_p < 1.f, counted = !by_k && (by_p || top_k > 0);
+    if (counted) {
+        u64 mass = 0;
+        uint32_t n = 0;
+        row.each([&](float x, int, int) {
+            const Token t = weigh(r, x);
+            if (t.in) mass += t.W, ++n;
+        });
+        u64 nn = n, tm, tn;
+        block_scan(sm, mass, nn, tm, tn);
+        exchange(sm, r, tm, tn);
+        for (int i = 0; i < r.ranks; ++i) total += sm.peer[i][0], tokens += sm.peer[i][1];
+    }
+    const bool cut_k = top_k > 0 && (by_k || (u64)top_k < tokens);
+    Cut cut{0u, 1u, 0};
+    if (cut_k || by_p) {
+        // No token below `bound` is kept (margins for rounding only make it lower).
+        float bound = r.m - 21.7f * r.T - fabsf(r.m) * 1e-6f, per = 0.f;
+        int last = -1;                             // top-p: the bin of s in which the limit is reached
+        u64 limit = 0, before = 0;                 // and the mass before it
+        const bool listing = by_k || !cut_k;
+        if (by_k) {
+            if (!row.infinite) bound = fmaxf(bound, unordered(reach));
+        } else if (listing) {
+            const float least = (1.f - top_p) * (float)total / (float)p.V * (1.f / kUnit);
+            const float floor_s = fmaxf(least > 0.f ? logf(least) - 1e-3f : -kSpan, -kSpan);
+            per = kCoarse / -floor_s;
+            for (int i = tid; i < kCoarse; i += kThreads) sm.coarse_lo[i] = sm.coarse_hi[i] = 0u;
+            __syncthreads();
+            const float above = r.m + (floor_s - 1e-3f) * r.T - fabsf(r.m) * 1e-6f;
+            row.each([&](float x, int, int) {
+                if (x >= above) {
+                    const Token t = weigh(r, x);
+                    if (t.in) {
+                        const int bin = min((int)(-t.s * per), kCoarse - 1);
+                        atomicAdd(&sm.coarse_lo[bin], t.W & 0xFFFFu);
+                        atomicAdd(&sm.coarse_hi[bin], t.W >> 16);
                     }
                 }
-                break;
-            }
-            start += kept;
-            equal += e;
+            });
+            cluster_barrier(r);
+            u64 mass = 0, z = 0, tm, tz;
+            if (tid < kCoarse)
+                for (int i = 0; i < r.ranks; ++i)
+                    mass += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_lo[tid]), i)) +
+                            ((u64)ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_hi[tid]), i)) << 16);
+            u64 sum = mass;
+            if (tid == 0) sm.found[0] = kCoarse, sm.found[1] = 0;
+            block_scan(sm, sum, z, tm, tz);
+            limit = limit_of(top_p, total);
+            if (tid < kCoarse && sum < limit && sum + mass >= limit) sm.found[0] = (u64)tid, sm.found[1] = sum;
+            __syncthreads();
+            last = (int)sm.found[0], before = sm.found[1];
+            bound = fmaxf(bound, r.m - ((float)(last + 1) / per + 1e-3f) * r.T - fabsf(r.m) * 1e-6f);
         }
+        auto of_bin = [&](float x) {
+            if (x < bound) return false;
+            const Token t = weigh(r, x);
+            return t.in && min((int)(-t.s * per), kCoarse - 1) == last;
+        };
+        if (listing) {
+            // How many tokens there are from the bound on, and in the last bin alone.
+            u64 mine = 0, in_bin = 0, of_cta, of_bins;
+            row.each([&](float x, int, int) {
+                mine += x >= bound;
+                if (last >= 0) in_bin += of_bin(x);
+            });
+            const u64 own_n = mine, own_bin = in_bin;
+            block_scan(sm, mine, in_bin, of_cta, of_bins);
+            exchange(sm, r, of_cta, of_bins);
+            u64 n = 0, n_bin = 0;
+            for (int i = 0; i < r.ranks; ++i) {
+                if (i == r.rank) mine += n, in_bin += n_bin;
+                n += sm.peer[i][0], n_bin += sm.peer[i][1];
+            }
+            const bool whole = n <= (u64)kList, bin_only = !whole && n_bin > 0 && n_bin <= (u64)kList;
+            if (whole || bin_only) {
+                // They go to the first CTA's list, each CTA and thread at its place.
+                uint32_t at = ptx::mapa_shared(ptx::smem_u32(sm.list), 0u) + (uint32_t)(whole ? mine : in_bin) * 8u;
+                if ((whole ? own_n : own_bin) > 0)
+                    row.each([&](float x, int it, int v) {
+                        if (whole ? x >= bound : of_bin(x)) {
+                            st_cluster_u64(at, (u64)(uint32_t)~ordered(x) << 32 | (uint32_t)row.index_of(it, v));
+                            at += 8;
+                        }
+                    });
+                cluster_barrier(r);
+            }
+            if (whole) {
+                if (r.rank == 0) draw_listed(sm, row, r, (int)n, cut_k ? top_k : 0, top_p, counted ? total : 0, p, b);
+                return;                            // nobody reads another's shared memory any more
+            }
+            if (bin_only) {
+                if (r.rank == 0) cut = cut_listed(sm, r, (int)n_bin, before, limit);
+                exchange(sm, r, cut.key, cut.quota, cut.W);
+                cut = Cut{(uint32_t)sm.peer[0][0], (uint32_t)sm.peer[0][2], sm.peer[0][1]};
+                __syncthreads();
+                tally(sm, row, r, cut);
+                draw_all(sm, row, r, cut, p, b);
+                cluster_barrier(r);
+                return;
+            }
+        }
+        // The counting path.
+        if (!counted) {
+            u64 mass = 0;
+            uint32_t n = 0;
+            row.each([&](float x, int, int) {
+                const Token t = weigh(r, x);
+                if (t.in) mass += t.W, ++n;
+            });
+            u64 nn = n, tm, tn;
+            block_scan(sm, mass, nn, tm, tn);
+            exchange(sm, r, tm, tn);
+            total = tokens = 0;
+            for (int i = 0; i < r.ranks; ++i) total += sm.peer[i][0], tokens += sm.peer[i][1];
+        }
+        if (top_k > 0 && (u64)top_k < tokens) {
+            narrow(sm, row, r, false, (u64)top_k, cut);
+            tally(sm, row, r, cut);
+            total = cut.quota * cut.W;
+            for (int i = 0; i < r.ranks; ++i) total += sm.peer[i][0];
+        }
+        if (by_p) narrow(sm, row, r, true, limit_of(top_p, total), cut);
     }
-    ptx::cluster_sync();
+    tally(sm, row, r, cut);
+    draw_all(sm, row, r, cut, p, b);
+    cluster_barrier(r);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &args, cudaStream_t stream) {
+    // CTAs of a row: as many as hold it in registers, and more while there are SMs for them.
+    const int64_t bytes = (int64_t)args.V * (args.dtype == LOWBIT_DTYPE_F32 ? 4 : 2);
     int ranks = 1;
-    while (ranks < kMaxCluster && (args.V > ranks * 4096) && (args.V > ranks * kHeld || args.B * ranks * 2 <= 152)) ranks *= 2;
+    while (ranks < kMaxCluster && (bytes > (int64_t)ranks * kThreads * kHeld * 16 ||
+                                   (bytes > ranks * 8192 && (int64_t)args.B * ranks < 152)))
+        ranks *= 2;
+    const auto kernel = args.dtype == LOWBIT_DTYPE_F32    ? sample_kernel<LOWBIT_DTYPE_F32>
+                        : args.dtype == LOWBIT_DTYPE_BF16 ? sample_kernel<LOWBIT_DTYPE_BF16>
+                                                          : sample_kernel<LOWBIT_DTYPE_F16>;
     const int smem = (int)sizeof(Shared);
-    const cudaError_t e = raise_smem_limit((const void *)sample_kernel, current_device(), smem);
+    const cudaError_t e = raise_smem_limit((const void *)kernel, current_device(), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ranks * (unsigned)args.B);
@@ -426,7 +864,7 @@ cudaError_t launch_sample(const SampleArgs &args, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_kernel, args);
+    return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
 }  // namespace lowbit

@@ -337,7 +337,7 @@ LOWBIT_API size_t lowbit_attention_workspace(int32_t heads, const lowbit_cache *
  *   temperature, top_p, min_p [rows] fp32 and top_k [rows] int32, device; each may be
  *            NULL: the scalar of the same name holds for every row then.
  *   token    [rows] int64; logprob [rows] fp32 or NULL.
- *   rows >= 0, 1 <= vocab < 2^31.  rows == 0 is a valid empty call.
+ *   rows >= 0, 1 <= vocab <= 2^19.  rows == 0 is a valid empty call.
  * Errors: as for lowbit_kv_append. */
 typedef struct {
     const void *logits;

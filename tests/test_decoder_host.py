@@ -101,7 +101,7 @@ def test_attentions_that_are_refused(lib, args):
 @pytest.mark.parametrize("args", [
     dict(logits=None), dict(u=None), dict(token=None), dict(logits=0x50001), dict(dtype=0, logits=0x50002), dict(u=0x60002),
     dict(token=0x70004), dict(logprob=0x70002), dict(temperature=0x70002), dict(top_p=1), dict(min_p=2), dict(top_k=3),
-    dict(rows=-1), dict(vocab=0), dict(vocab=-5), dict(dtype=3), dict(dtype=-1)])
+    dict(rows=-1), dict(vocab=0), dict(vocab=-5), dict(vocab=(1 << 19) + 1), dict(dtype=3), dict(dtype=-1)])
 def test_samples_that_are_refused(lib, args):
     assert call(lib, "sample", args) == EINVAL
 
