@@ -28,9 +28,11 @@
 // the threshold is found by counting: bins of s, then ranges of the bits of x, until
 // one value is left.
 //
-// Work split: a cluster of up to 8 CTAs takes a row and holds it in registers (each
-// logit is read from memory once); what CTAs need of each other goes through
-// distributed shared memory.  Bound: the chain of cluster-wide steps (three for top-k,
+// Work split: a cluster of up to 8 CTAs takes a row and holds it in shared memory (each
+// logit is read from memory once, and each thread reads back its own vectors; held in
+// registers, every pass had to be unrolled over them, and the code no longer fit the
+// instruction cache); what CTAs need of each other goes through distributed shared
+// memory.  Bound: the chain of cluster-wide steps (three for top-k,
 // five to seven for top-p) for few rows, the exponentials of all tokens for many.
 #include <algorithm>
 
@@ -73,7 +75,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-struct Shared {
+struct alignas(16) Shared {
     union {
         struct {                                   // the list, and the bins of the top-p bound
             u64 list[kList];
@@ -100,7 +102,7 @@ struct Row {
     const uint4 *base;
     int lead, V, first, end, nvec;                 // vectors [first, end) are this CTA's, nvec of a thread at most
     bool infinite;                                 // the maximum is +infinity: those count as 0, the others as -infinity
-    uint4 held[kHeld];
+    uint4 *held;                                   // this thread's vectors, kThreads apart (shared memory)
 
     __device__ __forceinline__ static float get(const uint4 &w, int v) {
         const uint32_t a[4] = {w.x, w.y, w.z, w.w};
@@ -137,15 +139,16 @@ struct Row {
         }
         return make_uint4(a[0], a[1], a[2], a[3]);
     }
+    // Fills `held`.
+    __device__ __forceinline__ void hold() {
+#pragma unroll 4
+        for (int it = 0; it < min(nvec, kHeld); ++it) held[it * kThreads] = load(it);
+    }
     template <typename F>
     __device__ __forceinline__ void each(const F &f) const {          // f(x, it, v)
-#pragma unroll
-        for (int it = 0; it < kHeld; ++it)
-            if (it < nvec)
-#pragma unroll
-                for (int v = 0; v < kVec; ++v) f(get(held[it], v), it, v);
-        for (int it = kHeld; it < nvec; ++it) {
-            const uint4 w = load(it);
+#pragma unroll 1
+        for (int it = 0; it < nvec; ++it) {
+            const uint4 w = it < kHeld ? held[it * kThreads] : load(it);
 #pragma unroll
             for (int v = 0; v < kVec; ++v) f(get(w, v), it, v);
         }
@@ -627,9 +630,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         row.end = min(row.first + part, all);
         row.nvec = (part + kThreads - 1) / kThreads;
     }
-#pragma unroll
-    for (int it = 0; it < kHeld; ++it)
-        if (it < row.nvec) row.held[it] = row.load(it);
+    row.held = reinterpret_cast<uint4 *>(raw + sizeof(Shared)) + tid;
+    row.hold();
     r.T = p.temperature != nullptr ? p.temperature[b] : p.temperature_all;
     const float top_p = p.top_p != nullptr ? p.top_p[b] : p.top_p_all;
     const float min_p = p.min_p != nullptr ? p.min_p[b] : p.min_p_all;
@@ -697,9 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     if (r.m == INFINITY) {
         row.infinite = true;
         r.m = 0.f;
-#pragma unroll
-        for (int it = 0; it < kHeld; ++it)
-            if (it < row.nvec) row.held[it] = row.load(it);
+        row.hold();
     }
     r.inv_t = fminf(__fdiv_rn(1.f, r.T), 3.402823466e38f);
     r.min_p = fminf(min_p, 1.f);                   // the largest logit is always kept
@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &args, cudaStream_t stream) {
-    // CTAs of a row: as many as hold it in registers, and more while there are SMs for them.
+    // CTAs of a row: as many as hold it, and more while there are SMs for them.
     const int64_t bytes = (int64_t)args.V * (args.dtype == LOWBIT_DTYPE_F32 ? 4 : 2);
     int ranks = 1;
     while (ranks < kMaxCluster && (bytes > (int64_t)ranks * kThreads * kHeld * 16 ||
@@ -847,7 +847,8 @@ cudaError_t launch_sample(const SampleArgs &args, cudaStream_t stream) {
     const auto kernel = args.dtype == LOWBIT_DTYPE_F32    ? sample_kernel<LOWBIT_DTYPE_F32>
                         : args.dtype == LOWBIT_DTYPE_BF16 ? sample_kernel<LOWBIT_DTYPE_BF16>
                                                           : sample_kernel<LOWBIT_DTYPE_F16>;
-    const int smem = (int)sizeof(Shared);
+    const int64_t vecs = (bytes / 16 + 2 + ranks - 1) / ranks, held = std::min<int64_t>((vecs + kThreads - 1) / kThreads, kHeld);
+    const int smem = (int)(sizeof(Shared) + held * kThreads * 16);
     const cudaError_t e = raise_smem_limit((const void *)kernel, current_device(), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
