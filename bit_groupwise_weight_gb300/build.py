@@ -1,4 +1,6 @@
-"""Build liblowbit.so in-tree with nvcc for sm_103a (GB300).
+"""Build liblowbit.so in-tree with nvcc for sm_103a (GB300), and beside it the
+extension module _lowbit_torch.so (csrc/binding.cpp: the hot path of the decoder
+operators' Python binding, against the installed PyTorch's headers).
 
 Each .cu under csrc/ compiles to an object in parallel; the objects link into
 one shared library with the CUDA runtime linked statically, so the library
@@ -9,6 +11,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -18,6 +21,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = BUILD / "liblowbit.so"
+BINDING = BUILD / "_lowbit_torch.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++20", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -36,14 +40,38 @@ def sources() -> list[Path]:
 
 
 def _deps() -> list[Path]:
-    return sources() + sorted(CSRC.glob("*.cuh")) + sorted(INCLUDE.glob("*.h")) + [Path(__file__)]
+    return (sources() + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.cpp")) + sorted(INCLUDE.glob("*.h"))
+            + [Path(__file__)])
 
 
 def up_to_date() -> bool:
-    if not LIB.exists():
+    if not LIB.exists() or not BINDING.exists():
         return False
-    t = LIB.stat().st_mtime
+    t = min(LIB.stat().st_mtime, BINDING.stat().st_mtime)
     return all(p.stat().st_mtime <= t for p in _deps())
+
+
+def build_binding(verbose: bool = False) -> None:
+    """The extension module: host code only, linked to PyTorch and not to liblowbit."""
+    import torch
+    root = Path(torch.__file__).resolve().parent
+    cuda = Path(nvcc()).resolve().parent.parent
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("a C++ compiler is needed to build _lowbit_torch")
+    tmp = BINDING.with_suffix(f".{os.getpid()}.tmp")
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in (INCLUDE, root / "include", root / "include/torch/csrc/api/include",
+                                sysconfig.get_paths()["include"], cuda / "include")),
+           str(CSRC / "binding.cpp"), "-o", str(tmp), f"-L{root / 'lib'}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", f"-Wl,-rpath,{root / 'lib'}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the C++ compiler failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ...] = ()) -> Path:
@@ -64,8 +92,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ..
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(compile_one, sources()))
+        binding.result()
     tmp = LIB.with_suffix(f".{os.getpid()}.tmp")
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", *map(str, objs), "-o", str(tmp)]
     r = subprocess.run(cmd, capture_output=True, text=True)

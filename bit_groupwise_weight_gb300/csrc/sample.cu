@@ -49,7 +49,10 @@ constexpr int kCoarse = 256;                       // of the top-p bound
 constexpr int kList = 2048;                        // tokens that one CTA sorts
 constexpr int kMaxCluster = 8;
 constexpr int kHeld = 8;                           // 16-byte vectors that a thread holds
-constexpr int kMaxVecs = 40;                       // that it may have (the others are read again)
+constexpr int kMaxVecs = 64;                       // that it may have (the others are read again)
+constexpr int kMaxTokens = 131071;                 // of a CTA: sums of 15-bit parts of W stay inside 32 bits
+constexpr int kShort = 256;                        // a list that is ordered by counting
+constexpr int kWanted = 152;                       // CTAs of a launch, where rows can be split
 constexpr float kUnit = 1073741824.0f;             // 2^30
 constexpr float kSpan = 21.6f;                     // rint(2^30 e^-s) is 0 beyond
 typedef unsigned long long u64;
@@ -81,7 +84,7 @@ struct alignas(16) Shared {
             u64 list[kList];
             uint32_t coarse_lo[kCoarse], coarse_hi[kCoarse];
         };
-        struct {                                   // the counting path: W = lo + 2^16 hi, summed apart in 32 bits
+        struct {                                   // the counting path: W = lo + 2^15 hi, summed apart in 32 bits
             uint32_t count[kBins], lo[kBins], hi[kBins];
         };
     };
@@ -308,8 +311,8 @@ __device__ __noinline__ void narrow(Shared &sm, const Row<DTYPE> &row, Draw &r, 
             if (!inside(k, x, t)) return;
             const int at = level == 0 ? bin_of(t.s) : (int)((khi - k) >> shift);
             atomicAdd(&sm.count[at], 1u);
-            atomicAdd(&sm.lo[at], t.W & 0xFFFFu);
-            atomicAdd(&sm.hi[at], t.W >> 16);
+            atomicAdd(&sm.lo[at], t.W & 0x7FFFu);
+            atomicAdd(&sm.hi[at], t.W >> 15);
         });
         cluster_barrier(r);
         // This CTA's slice of the bins, summed over the cluster.
@@ -322,7 +325,7 @@ __device__ __noinline__ void narrow(Shared &sm, const Row<DTYPE> &row, Draw &r, 
                 for (int i = 0; i < r.ranks; ++i) {
                     cn[q] += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.count[at]), i));
                     cm[q] += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.lo[at]), i)) +
-                             ((u64)ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.hi[at]), i)) << 16);
+                             ((u64)ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.hi[at]), i)) << 15);
                 }
             }
             en += cn[q], em += cm[q];
@@ -527,6 +530,74 @@ __device__ __forceinline__ Cut cut_listed(Shared &sm, const Draw &r, int n, u64 
     return Cut{key, weigh(r, unordered(key)).W, quota};
 }
 
+// Writes the drawn token.
+template <int DTYPE>
+__device__ __forceinline__ void write_token(const Row<DTYPE> &row, const Draw &r, int i, u64 mass, const SampleArgs &p, int b) {
+    p.token[b] = i;
+    if (p.logprob == nullptr) return;
+    float x = r.m;
+    if (!row.infinite) {
+        const int at = i + row.lead;
+        const uint4 w = __ldg(row.base + at / Row<DTYPE>::kVec);
+#pragma unroll
+        for (int v = 0; v < Row<DTYPE>::kVec; ++v)
+            if (v == at % Row<DTYPE>::kVec) x = Row<DTYPE>::get(w, v);
+    }
+    p.logprob[b] = weigh(r, x).s - logf((float)mass * (1.f / kUnit));
+}
+
+// The rest of the work on a short list, a token a thread: places and the mass before each
+// by comparing with all others.
+template <int DTYPE>
+__device__ __forceinline__ void draw_short(Shared &sm, const Row<DTYPE> &row, const Draw &r, int n, int top_k, float top_p, u64 total,
+                                           const SampleArgs &p, int b) {
+    const int tid = threadIdx.x;
+    u64 *weight = sm.list + kShort;                // W beside the entries
+    const u64 me = tid < n ? sm.list[tid] : ~0ull;
+    const Token t = weigh(r, unordered(~(uint32_t)(me >> 32)));
+    const uint32_t W = tid < n && t.in ? t.W : 0u;
+    if (tid < kShort) weight[tid] = W;
+    __syncthreads();
+    if (tid >= ((n + 31) & ~31)) return;           // whole warps
+    int place = 0;
+    u64 before = 0, all = 0;
+    for (int j = 0; j < n; ++j) {
+        const bool earlier = sm.list[j] < me;
+        place += earlier;
+        if (earlier) before += weight[j];
+    }
+    // Of the first top_k (all): the mass.
+    if (total == 0) {
+        // Places are a permutation: the mass before place top_k is the largest of before + W there.
+        u64 upto = tid < n && (top_k <= 0 || place < top_k) ? before + W : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const u64 v = __shfl_xor_sync(~0u, upto, o);
+            upto = v > upto ? v : upto;
+        }
+        if ((tid & 31) == 0) sm.red[tid >> 5][0] = upto;
+        ptx::named_sync(1, (uint32_t)((n + 31) & ~31));
+        for (int i = 0; i < (n + 31) / 32; ++i) all = sm.red[i][0] > all ? sm.red[i][0] : all;
+    } else {
+        all = total;
+    }
+    const u64 limit = top_p < 1.f ? limit_of(top_p, all) : ~0ull;
+    const bool kept = W != 0 && (top_k <= 0 || place < top_k) && before < limit;
+    ptx::named_sync(1, (uint32_t)((n + 31) & ~31));
+    if (tid < kShort) weight[tid] = kept ? W : 0;
+    ptx::named_sync(1, (uint32_t)((n + 31) & ~31));
+    // The running total in index order, and the whole.
+    const uint32_t index = (uint32_t)me;
+    u64 ahead = 0, mass = 0;
+    for (int j = 0; j < n; ++j) {
+        const u64 w = weight[j];
+        mass += w;
+        if ((uint32_t)sm.list[j] < index) ahead += w;
+    }
+    const u64 target = target_of(p.u[b], mass);
+    if (kept && target >= ahead && target < ahead + W) write_token(row, r, (int)index, mass, p, b);
+}
+
 // The rest of the work on the list of n tokens (this CTA's alone): order, top-k, top-p,
 // draw.  total: mass of all tokens within min-p (0: that of the first top_k of the list).
 template <int DTYPE>
@@ -585,21 +656,8 @@ __device__ __forceinline__ void draw_listed(Shared &sm, const Row<DTYPE> &row, c
     const u64 target = target_of(p.u[b], mass);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-        if (target >= own && target < own + W[q]) {
-            const int i = (int)(sm.list[tid * kPer + q] >> 32);
-            p.token[b] = i;
-            if (p.logprob != nullptr) {
-                const int at = i + row.lead;
-                float value = r.m;
-                if (!row.infinite) {
-                    const uint4 w = __ldg(row.base + at / Row<DTYPE>::kVec);
-#pragma unroll
-                    for (int v = 0; v < Row<DTYPE>::kVec; ++v)
-                        if (v == at % Row<DTYPE>::kVec) value = Row<DTYPE>::get(w, v);
-                }
-                p.logprob[b] = weigh(r, value).s - logf((float)mass * (1.f / kUnit));
-            }
-        }
+        if (target >= own && target < own + W[q])
+            write_token(row, r, (int)(sm.list[tid * kPer + q] >> 32), mass, p, b);
         own += W[q];
     }
 }
@@ -651,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     for (int i = 0; i < kWarps; ++i) top = max(top, (uint32_t)sm.red[i][0]);
     // A value that at least ceil(k / ranks) threads' logits reach, in every CTA: the k
     // first tokens are not below the least of these.
-    const bool by_k = !greedy && top_k > 0 && top_k <= kThreads / 2 * r.ranks && top_k <= kList / 2;
+    const bool by_k = !greedy && top_k > 0 && top_k <= (kThreads - kThreads / 8) * r.ranks && top_k <= kList / 2;
     uint32_t reach = 0;
     if (by_k) {
         const int need = (top_k + r.ranks - 1) / r.ranks;
@@ -740,8 +798,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
                     const Token t = weigh(r, x);
                     if (t.in) {
                         const int bin = min((int)(-t.s * per), kCoarse - 1);
-                        atomicAdd(&sm.coarse_lo[bin], t.W & 0xFFFFu);
-                        atomicAdd(&sm.coarse_hi[bin], t.W >> 16);
+                        atomicAdd(&sm.coarse_lo[bin], t.W & 0x7FFFu);
+                        atomicAdd(&sm.coarse_hi[bin], t.W >> 15);
                     }
                 }
             });
@@ -750,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             if (tid < kCoarse)
                 for (int i = 0; i < r.ranks; ++i)
                     mass += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_lo[tid]), i)) +
-                            ((u64)ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_hi[tid]), i)) << 16);
+                            ((u64)ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_hi[tid]), i)) << 15);
             u64 sum = mass;
             if (tid == 0) sm.found[0] = kCoarse, sm.found[1] = 0;
             block_scan(sm, sum, z, tm, tz);
@@ -794,7 +852,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
                 cluster_barrier(r);
             }
             if (whole) {
-                if (r.rank == 0) draw_listed(sm, row, r, (int)n, cut_k ? top_k : 0, top_p, counted ? total : 0, p, b);
+                if (r.rank != 0) return;
+                if (n <= (u64)kShort) draw_short(sm, row, r, (int)n, cut_k ? top_k : 0, top_p, counted ? total : 0, p, b);
+                else draw_listed(sm, row, r, (int)n, cut_k ? top_k : 0, top_p, counted ? total : 0, p, b);
                 return;                            // nobody reads another's shared memory any more
             }
             if (bin_only) {
@@ -838,11 +898,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &args, cudaStream_t stream) {
-    // CTAs of a row: as many as hold it, and more while there are SMs for them.
+    // CTAs of a row: more while there are SMs for them, and as many as its vectors need.
     const int64_t bytes = (int64_t)args.V * (args.dtype == LOWBIT_DTYPE_F32 ? 4 : 2);
     int ranks = 1;
-    while (ranks < kMaxCluster && (bytes > (int64_t)ranks * kThreads * kHeld * 16 ||
-                                   (bytes > ranks * 8192 && (int64_t)args.B * ranks < 152)))
+    while (ranks < kMaxCluster && (bytes + 32 > (int64_t)ranks * kThreads * kMaxVecs * 16 || args.V > ranks * kMaxTokens - 16 ||
+                                   (bytes > ranks * 8192 && (int64_t)args.B * ranks < kWanted)))
         ranks *= 2;
     const auto kernel = args.dtype == LOWBIT_DTYPE_F32    ? sample_kernel<LOWBIT_DTYPE_F32>
                         : args.dtype == LOWBIT_DTYPE_BF16 ? sample_kernel<LOWBIT_DTYPE_BF16>

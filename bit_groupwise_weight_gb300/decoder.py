@@ -15,15 +15,37 @@ where each sequence's begin (None: the same number of tokens each).
 """
 from __future__ import annotations
 
+import ctypes
+import importlib.util
 import math
 import struct
 
 import torch
 
 from . import _abi
+from . import build as _build
 
-# The C ABI's descriptors, packed (a ctypes.Structure takes several times as long to fill,
-# and a decode step's kernels run for less time than the host needs to describe them).
+_hot = None
+
+
+def _load():
+    """The extension module that makes the accepted calls (csrc/binding.cpp)."""
+    global _hot
+    if _hot is None:
+        lib = _abi.abi()
+        if not _build.BINDING.exists():
+            raise ImportError(f"_lowbit_torch is not built ({_build.BINDING} missing); run bit_groupwise_weight_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_lowbit_torch", str(_build.BINDING))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.lowbit_kv_append, lib.lowbit_attention, lib.lowbit_attention_workspace, lib.lowbit_sample)))
+        _hot = module
+    return _hot
+
+
+# What follows describes a call in Python: how one that the extension did not accept is
+# explained.  The C ABI's descriptors, packed:
 _CACHE = struct.Struct("@PPPPqqiiii").pack          # lowbit_cache
 _SEQUENCES = struct.Struct("@PPPqiiii").pack        # lowbit_sequences
 _KV_APPEND = struct.Struct("@PPPPqqqqqqqqPfiii").pack
@@ -174,6 +196,10 @@ def kv_append(q, k, v, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q=No
     rotated part.  ``max_q``: the largest number of new tokens of a sequence (with cu_q;
     None: no bound known).
     """
+    done = (_hot or _load()).kv_append(q, k, v, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q, max_q, turns, interleaved,
+                                       factor, out)
+    if done is not None:
+        return done if done.__class__ is not int else _abi._check(done, "lowbit_kv_append")
     dev = _first(q, "q", 3)
     T, heads, dim = q.shape
     q_at, qt, qh = _rows(q, "q", dev, T, heads, dim)
@@ -204,6 +230,10 @@ def attention(q, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q=None, ma
     ``lse``: fp32 [tokens, heads], receives the scores' log-sum-exp.  ``workspace``: a uint8
     tensor of ``attention_workspace`` bytes to use again from call to call on one stream.
     """
+    done = (_hot or _load()).attention(q, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q, max_q, scale, window, out, lse,
+                                       workspace)
+    if done is not None:
+        return done if done.__class__ is not int else _abi._check(done, "lowbit_attention")
     dev = _first(q, "q", 3)
     T, heads, dim = q.shape
     q_at, qt, qh = _rows(q, "q", dev, T, heads, dim)
@@ -248,6 +278,9 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, 
     the fewest that hold top_p of the mass.  ``logprob``: fp32 [rows], receives the token's
     log-probability among the kept.
     """
+    done = (_hot or _load()).sample(logits, u, temperature, top_k, top_p, min_p, out, logprob)
+    if done is not None:
+        return done if done.__class__ is not int else _abi._check(done, "lowbit_sample")
     if not isinstance(logits, torch.Tensor) or logits.dtype not in _abi._W_DTYPES:
         raise ValueError("logits must be a float32, bfloat16 or float16 CUDA tensor")
     dev = _first(logits, "logits", 2)
