@@ -28,8 +28,15 @@
 // the new tokens times the heads of the group; its keys come in tiles of 64.  All
 // items' tiles form one list, each item's preceded by kItemCost units that stand for
 // its other cost, and the list is cut into equal ranges, one per CTA: sequences of any
-// lengths fill the machine evenly.  An item that a cut divides leaves its parts'
-// (m, l, O) in the workspace, and a second launch joins them.
+// lengths fill the machine evenly.  The CTAs of an item that cuts divide leave their
+// parts' (m, l, O) in the workspace; the last of them, when its own range is done, waits
+// for the others (which came before it in the grid, and leave their parts before they
+// wait for any) and joins the parts.  A part's flag holds a
+// number of the call's own, so that the workspace may come with any content, and is
+// cleared by who reads it, so that a captured call may run again.  Items in many parts
+// (few items, long ones) are joined by a second launch instead, many CTAs to an item: the
+// 57 parts of each of 8 heads over 131001 keys cost 6 us more in one CTA, while for fewer
+// parts the second launch costs more (3 us, most of it on the host).
 //
 // A CTA: one producer warp (TMA: K and V tile of 64 keys per stage, 128- or 64-byte
 // swizzle; pages smaller than a tile take one copy each) and four consumer warps of
@@ -39,6 +46,8 @@
 // heads wastes nothing.
 // Bound: HBM, 2 D bytes per key and kv head.
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 
 #include "attention.cuh"
 
@@ -47,11 +56,12 @@ namespace {
 
 using namespace attn;
 
+typedef unsigned long long u64;
 constexpr int kTile = 64;                        // keys of a stage
 constexpr int kWarps = 4;                        // consumer warps, 16 keys each
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kItemCost = 6;                     // what an item costs beside its tiles, in tiles
-constexpr int kMinChunk = 7;                     // of a CTA's range
+constexpr int kMinChunk = 6;                     // of a CTA's range
 constexpr int kCtas = kSms * 3;                  // at most
 constexpr float kLag = 8.f;
 
@@ -170,17 +180,27 @@ struct Smem {
     alignas(8) uint64_t full[kStages<D, ROWS>], empty[kStages<D, ROWS>];
 };
 
-// What the join needs to know of an item that cuts divide: written by the CTA that
-// begins it.  parts == 0: nothing.
-struct Cut { int parts, start, nrows, row0, h, pad[3]; };
+// What the second launch needs to know of an item: written by the CTA that ends it, from
+// CTA `begun` on (below 0: none).
+struct Join { int begun, start, nrows, row0, h, pad; };
+constexpr int kManyParts = 12;
 
-// Workspace: a Cut per CTA, then partial results: slot 2c is the item that CTA c
-// continues, slot 2c + 1 the one that it leaves unfinished.  A slot: ROWS x D sums,
-// then ROWS (m, l) pairs.
-__device__ __forceinline__ Cut *cut_of(const AttentionArgs &p, int cta) { return reinterpret_cast<Cut *>(p.workspace) + cta; }
+// Workspace: a flag and a Join per CTA, then two slots per CTA: for the part of an item that it leaves
+// to a later CTA (it leaves one at most), and for the part of the item that it joins
+// itself.  A slot: ROWS x D sums, then ROWS (m, l) pairs.
+__device__ __forceinline__ u64 *flag_of(const AttentionArgs &p, int cta) { return reinterpret_cast<u64 *>(p.workspace) + cta; }
+__device__ __forceinline__ Join *join_of(const AttentionArgs &p, int cta) { return reinterpret_cast<Join *>(p.workspace + kCtas * 2) + cta; }
 template <int D, int ROWS>
 __device__ __forceinline__ float *slot_of(const AttentionArgs &p, int slot) {
-    return p.workspace + kCtas * (sizeof(Cut) / 4) + (int64_t)slot * (ROWS * (D + 2));
+    return p.workspace + kCtas * (2 + (int)sizeof(Join) / 4) + (int64_t)slot * (ROWS * (D + 2));
+}
+__device__ __forceinline__ u64 load_acquire(const u64 *at) {
+    u64 v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_release(u64 *at, u64 v) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(at), "l"(v) : "memory");
 }
 
 // Four values of a row's result.
@@ -357,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
     ptx::pdl_wait();
     const Plan plan = make_plan<ROWS>(p, blockIdx.x, gridDim.x);
     if (plan.begin >= plan.end) {
-        if (tid == 0) cut_of(p, blockIdx.x)->parts = 0;
+        if (p.defer && tid == 0) join_of(p, blockIdx.x)->begun = -1;
         return;
     }
     __syncthreads();
@@ -450,15 +470,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
     // of the chunk number, so chunk c is at (address ^ c << 4).
     const int mkey = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
     const uint32_t moff = mkey * D + (((lane >> 4) ^ (D == 128 ? mkey & 7 : (mkey >> 1) & 3)) << 4);
-    bool ok = true, cut = false;
+    bool ok = true;
     int st = 0;
     uint32_t round = 0;
+    Join join{-1, 0, 0, 0, 0, 0};                                        // the item that this CTA ends and others began
     State<D, ROWS> a;
     for (long long idx = plan.begin; idx < plan.end;) {
         const Seq s = locate<ROWS>(p, idx, pl);
         const int units = (int)min((long long)(s.nt - pl.t), plan.end - idx);
         const int t0 = max(pl.t, 0), cnt = pl.t + units - t0;            // this CTA's tiles of the item
-        const long long item_end = idx + (s.nt - pl.t);
+        const long long first_tile = idx - pl.t;                         // place of the item's first tile
         idx += units;
         if (cnt <= 0) continue;
         const int nrows = s.n * p.G, row0 = pl.rt * ROWS, first = s.len - s.n;
@@ -517,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
 
         // The warps' parts of the item are joined in shared memory, 8 rows at a time.
         const bool continued = t0 > 0, unfinished = t0 + cnt < s.nt;
-        float *slot = slot_of<D, ROWS>(p, 2 * (int)blockIdx.x + (continued ? 0 : 1));
+        float *slot = slot_of<D, ROWS>(p, 2 * (int)blockIdx.x + (unfinished ? 0 : 1));
+        if (continued && !unfinished) join = Join{(int)(first_tile / plan.chunk), s.start, nrows, row0, pl.h, 0};
 #pragma unroll
         for (int n = 0; n < N; ++n) {
 #pragma unroll
@@ -556,18 +578,58 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
             }
             ptx::named_sync(1, kWarps * 32);
         }
-        if (unfinished && !continued) {
-            // The CTA that begins a divided item describes it to the join.
-            cut = true;
-            if (tid == 0)
-                *cut_of(p, blockIdx.x) = Cut{(int)((item_end - 1) / plan.chunk) - (int)blockIdx.x + 1, s.start, nrows, row0, pl.h, {}};
+        if (unfinished && !p.defer) {                                    // nothing follows in this CTA's range
+            __threadfence();
+            ptx::named_sync(1, kWarps * 32);
+            if (tid == 0) store_release(flag_of(p, blockIdx.x), p.call);
         }
     }
-    if (!cut && tid == 0) cut_of(p, blockIdx.x)->parts = 0;
+    if (p.defer && tid == 0) *join_of(p, blockIdx.x) = join;
+    if (p.defer || join.begun < 0) return;
+
+    // The parts of the CTAs before this one have to be there.
+    for (int c = join.begun + tid; c < (int)blockIdx.x; c += kWarps * 32) {
+        const u64 t0 = ptx::globaltimer_ns();
+        while (load_acquire(flag_of(p, c)) != p.call)
+            if (ptx::globaltimer_ns() - t0 > ptx::kWaitLimitNs) {
+                atomicAdd(&g_attn_timeouts, 1u);
+                break;
+            }
+        *flag_of(p, c) = 0;
+    }
+    ptx::named_sync(1, kWarps * 32);
+    // A thread joins kPer groups of four values; their loads of several parts go out together.
+    constexpr int kPer = ROWS * (D / 4) / (kWarps * 32);
+    float m[kPer], l[kPer];
+    float4 o[kPer];
+    int r[kPer];
+    const int d = tid % (D / 4) * 4;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        r[q] = (tid + q * kWarps * 32) / (D / 4);
+        m[q] = -INFINITY, l[q] = 0.f, o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll(8 / kPer)
+    for (int c = join.begun; c <= (int)blockIdx.x; ++c) {
+        const float *part = slot_of<D, ROWS>(p, 2 * c + (c == (int)blockIdx.x));
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + ROWS * D + 2 * r[q]));
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + r[q] * D + d));
+            const float mx = fmaxf(m[q], ml.x), base = mx == -INFINITY ? 0.f : mx;
+            const float e = ex2(m[q] - base), f = ex2(ml.x - base);
+            o[q].x = o[q].x * e + v.x * f, o[q].y = o[q].y * e + v.y * f;
+            o[q].z = o[q].z * e + v.z * f, o[q].w = o[q].w * e + v.w * f;
+            l[q] = l[q] * e + ml.y * f;
+            m[q] = mx;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+        if (join.row0 + r[q] < join.nrows) write_row(p, join.start, join.h, join.row0 + r[q], d, o[q], m[q], l[q]);
 }
 
-// Joins the parts of the items that cuts divide: block (c, r) takes row r of the item
-// that CTA c began and did not finish.
+// The second launch: block (c, r) takes row r of the item that CTA c ends.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs p) {
     constexpr int kGroups = 128 / (D / 4);                       // parts read at a time
@@ -576,8 +638,8 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const int c = blockIdx.x, r = blockIdx.y;
-    const Cut cut = *cut_of(p, c);
-    if (cut.parts == 0 || cut.row0 + r >= cut.nrows) return;
+    const Join join = *join_of(p, c);
+    if (join.begun < 0 || join.row0 + r >= join.nrows) return;
     const int grp = threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -589,8 +651,8 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
         m = mx;
     };
 #pragma unroll 4
-    for (int i = grp; i < cut.parts; i += kGroups) {
-        const float *slot = slot_of<D, ROWS>(p, i == 0 ? 2 * c + 1 : 2 * (c + i));
+    for (int i = join.begun + grp; i <= c; i += kGroups) {
+        const float *slot = slot_of<D, ROWS>(p, 2 * i + (i == c));
         const float2 ml = *reinterpret_cast<const float2 *>(slot + ROWS * D + 2 * r);
         add(ml.x, ml.y, *reinterpret_cast<const float4 *>(slot + r * D + d));
     }
@@ -600,12 +662,13 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
     if (grp == 0) {
 #pragma unroll
         for (int k = 1; k < kGroups; ++k) add(sml[k].x, sml[k].y, so[k][d / 4]);
-        write_row(p, cut.start, cut.h, cut.row0 + r, d, o, m, l);
+        write_row(p, join.start, join.h, join.row0 + r, d, o, m, l);
     }
 }
 
 template <int D, int ROWS>
-cudaError_t launch(const AttentionArgs &p, cudaStream_t stream) {
+cudaError_t launch(const AttentionArgs &args, cudaStream_t stream) {
+    AttentionArgs p = args;
     const uint32_t box_rows = (uint32_t)std::min(p.P, kTile);
     const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.P, (uint64_t)p.Hk, (uint64_t)p.pages};
     const uint64_t strides[3] = {(uint64_t)D, (uint64_t)p.head_stride, (uint64_t)p.page_stride};
@@ -623,10 +686,10 @@ cudaError_t launch(const AttentionArgs &p, cudaStream_t stream) {
     const int64_t items = (int64_t)p.B * p.Hk * ((rows_max + ROWS - 1) / ROWS);
     const int64_t tiles = ((int64_t)p.width * p.P + kTile - 1) / kTile;
     const int ctas = (int)std::min<int64_t>(kSms * kPerSm<D, ROWS>, std::max<int64_t>(1, (items * (kItemCost + tiles) + kMinChunk - 1) / kMinChunk));
-    e = launch_pdl(attention_kernel<D, ROWS>, dim3(ctas), dim3(kThreads), smem, stream, kmap, vmap, p);
-    // A tile list of one range each needs no join.
-    if (e != cudaSuccess || ctas == 1) return e;
-    return launch_pdl(attention_join_kernel<D, ROWS>, dim3(ctas - 1, ROWS), dim3(128), 0, stream, p);
+    p.defer = ctas > kManyParts * items;
+    e = launch_pdl(attention_kernel<D, ROWS>, dim3(ctas), dim3(kThreads), smem, stream, kmap, vmap, (const AttentionArgs)p);
+    if (e != cudaSuccess || !p.defer) return e;
+    return launch_pdl(attention_join_kernel<D, ROWS>, dim3(ctas, ROWS), dim3(128), 0, stream, (const AttentionArgs)p);
 }
 
 // Which kernels a call needs: sequences are sorted by their number of query rows (new
@@ -640,7 +703,7 @@ Kernels kernels_for(int max_q, bool uniform, int G) {
 
 size_t few_workspace_bytes(int max_q, int G, int D) {
     const int rows = (int64_t)max_q * G <= 8 ? 8 : 16;
-    return (size_t)kCtas * (sizeof(Cut) + 2 * rows * (D + 2) * sizeof(float));
+    return (size_t)kCtas * (sizeof(u64) + sizeof(Join) + 2 * rows * (D + 2) * sizeof(float));
 }
 
 }  // namespace
@@ -673,6 +736,9 @@ cudaError_t launch_attention(const AttentionArgs &args, cudaStream_t stream) {
     while ((1 << p.pshift) < p.P) ++p.pshift;
     const Kernels k = kernels_for(p.max_q, uniform, p.G);
     p.few_rows = k.few_rows;
+    // A number that no other call's flags hold, and no other content of the workspace is likely to.
+    static std::atomic<u64> calls{(u64)std::chrono::steady_clock::now().time_since_epoch().count() * 0x9E3779B97F4A7C15ull};
+    p.call = calls.fetch_add(1, std::memory_order_relaxed) | 1ull << 63;
     if (k.many) {
         PromptGrid g = prompt_grid(p.T, p.B, p.max_q, uniform, p.Hq, p.Hk, (int64_t)p.width * p.P);
         g.workspace = k.few ? (int64_t)(few_workspace_bytes(p.max_q, p.G, p.D) / sizeof(float)) : 0;

@@ -202,6 +202,8 @@ struct AttentionArgs {
     float scale_log2;                    // softmax scale * log2(e)
     int T, B, max_q, Hq, Hk, D, P, pages, width, window;
     int G, n, pshift;                    // Hq / Hk; tokens a sequence without cu_q; log2 P (set by launch_attention)
+    unsigned long long call;             // a number of this call
+    bool defer;                          // parts are joined by a second launch
     int few_rows;                        // more query rows than this: a sequence for the prompt kernel
 };
 size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D, int64_t max_len);
