@@ -52,7 +52,9 @@ constexpr int kHeld = 8;                           // 16-byte vectors that a thr
 constexpr int kMaxVecs = 64;                       // that it may have (the others are read again)
 constexpr int kMaxTokens = 131071;                 // of a CTA: sums of 15-bit parts of W stay inside 32 bits
 constexpr int kShort = 256;                        // a list that is ordered by counting
-constexpr int kWanted = 152;                       // CTAs of a launch, where rows can be split
+constexpr int kWanted = 152;                       // CTAs of a launch, where small batches are split
+constexpr int64_t kShare = 128 * 1024;             // bytes of a row that one CTA is left with (see launch_sample)
+constexpr int64_t kSmallShare = 8 * 1024;
 constexpr float kUnit = 1073741824.0f;             // 2^30
 constexpr float kSpan = 21.6f;                     // rint(2^30 e^-s) is 0 beyond
 typedef unsigned long long u64;
@@ -90,8 +92,8 @@ struct alignas(16) Shared {
     };
     u64 above[kMaxVecs * kWarps];                  // mass above the cut of each run of a warp's vectors, in index order
     uint32_t equal[kMaxVecs * kWarps];             // tokens equal to it
-    u64 pub[2][3];                                 // what this CTA tells the others, in two buffers
-    u64 peer[kMaxCluster][3];                      // what each CTA told
+    u64 pub[2][4];                                 // what this CTA tells the others, in two buffers
+    u64 peer[kMaxCluster][4];                      // what each CTA told
     u64 red[kWarps][2];
     u64 found[4];
     uint32_t kmin, kmax;
@@ -179,16 +181,16 @@ __device__ __forceinline__ int bin_of(float s) { return min((int)(-s * (kBins / 
 // Cluster-wide exchange: sm.peer[rank] holds every CTA's words (given by its thread
 // 0), for all threads.  A CTA overwrites a buffer only after the next exchange's
 // barrier, which every reader of it has passed.
-__device__ __forceinline__ void exchange(Shared &sm, Draw &r, u64 a, u64 b = 0, u64 c = 0) {
+__device__ __forceinline__ void exchange(Shared &sm, Draw &r, u64 a, u64 b = 0, u64 c = 0, u64 d = 0) {
     u64 *pub = sm.pub[r.round & 1];
     if (r.ranks == 1) {
         __syncthreads();
-        if (threadIdx.x == 0) sm.peer[0][0] = a, sm.peer[0][1] = b, sm.peer[0][2] = c;
+        if (threadIdx.x == 0) sm.peer[0][0] = a, sm.peer[0][1] = b, sm.peer[0][2] = c, sm.peer[0][3] = d;
     } else {
-        if (threadIdx.x == 0) pub[0] = a, pub[1] = b, pub[2] = c;
+        if (threadIdx.x == 0) pub[0] = a, pub[1] = b, pub[2] = c, pub[3] = d;
         ptx::cluster_sync();
-        if ((int)threadIdx.x < 3 * r.ranks) {
-            const uint32_t rank = threadIdx.x / 3, w = threadIdx.x % 3;
+        if ((int)threadIdx.x < 4 * r.ranks) {
+            const uint32_t rank = threadIdx.x >> 2, w = threadIdx.x & 3;
             sm.peer[rank][w] = ld_cluster_u64(ptx::mapa_shared(ptx::smem_u32(pub + w), rank));
         }
     }
@@ -218,6 +220,14 @@ __device__ __forceinline__ void block_scan(Shared &sm, u64 &a, u64 &b, u64 &ta, 
         if (i < warp) a += sm.red[i][0], b += sm.red[i][1];
         ta += sm.red[i][0], tb += sm.red[i][1];
     }
+}
+
+// a + W in one instruction.
+__device__ __forceinline__ void accumulate(u64 &a, uint32_t W) { asm("mad.wide.u32 %0, %1, 1, %0;" : "+l"(a) : "r"(W)); }
+// Sum over the warp of values below 2^57.
+__device__ __forceinline__ u64 warp_sum(u64 a) {
+    return __reduce_add_sync(~0u, (uint32_t)a & 0x3FFFFFFu) + ((u64)__reduce_add_sync(~0u, (uint32_t)(a >> 26) & 0x3FFFFFFu) << 26) +
+           ((u64)__reduce_add_sync(~0u, (uint32_t)(a >> 52)) << 52);
 }
 
 // floor(u * total), below total.
@@ -376,26 +386,29 @@ __device__ __noinline__ void narrow(Shared &sm, const Row<DTYPE> &row, Draw &r, 
 
 // Mass above the cut and tokens equal to it, for each run of a warp's vectors (in index
 // order: vector number, then warp) in sm.above and sm.equal, and of every CTA in sm.peer.
+// upto: tokens above it are in sm.above already (a key; ~0: none are).
 template <int DTYPE>
-__device__ __forceinline__ void tally(Shared &sm, const Row<DTYPE> &row, Draw &r, const Cut &cut) {
+__device__ __forceinline__ void tally(Shared &sm, const Row<DTYPE> &row, Draw &r, const Cut &cut, uint32_t upto) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float from = cut.key == 0 ? -INFINITY : unordered(cut.key), to = upto == ~0u ? INFINITY : unordered(upto);
     u64 above = 0, all_above = 0;
     uint32_t equal = 0, all_equal = 0;
     row.each([&](float x, int it, int v) {
-        const uint32_t k = ordered(x);
-        if (k >= cut.key) {
+        if (x >= from && x <= to) {
             const Token t = weigh(r, x);
             if (t.in) {
-                if (k > cut.key) above += t.W;
+                if (x > from) accumulate(above, t.W);
                 else ++equal;
             }
         }
         if (v == Row<DTYPE>::kVec - 1) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) above += __shfl_xor_sync(~0u, above, o);
+            above = warp_sum(above);
             equal = __reduce_add_sync(~0u, equal);
-            if (lane == 0) sm.above[it * kWarps + warp] = above, sm.equal[it * kWarps + warp] = equal;
-            all_above += above, all_equal += equal;
+            if (lane == 0) {
+                if (upto != ~0u) above += sm.above[it * kWarps + warp];
+                sm.above[it * kWarps + warp] = above, sm.equal[it * kWarps + warp] = equal;
+                all_above += above, all_equal += equal;
+            }
             above = 0, equal = 0;
         }
     });
@@ -764,12 +777,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
 
     u64 total = 0, tokens = 0;                     // mass and number of the tokens within min-p
     const bool by_p = top_p < 1.f, counted = !by_k && (by_p || top_k > 0);
+    float per = 0.f;                               // top-p: bins of a unit of s
     if (counted) {
+        float floor_s = 0.f, above = INFINITY;     // tokens below are not binned
+        if (by_p) {
+            // The threads' largest tokens give a lower bound of Z.
+            const Token t = weigh(r, row.infinite ? (own == INFINITY ? 0.f : -INFINITY) : own);
+            u64 least = t.in ? t.W : 0, z = 0, tl, tz;
+            block_scan(sm, least, z, tl, tz);
+            for (int i = tid; i < kCoarse; i += kThreads) sm.coarse_lo[i] = sm.coarse_hi[i] = 0u;
+            exchange(sm, r, tl);
+            tl = 0;
+            for (int i = 0; i < r.ranks; ++i) tl += sm.peer[i][0];
+            const float share = (1.f - top_p) * (float)tl / (float)p.V * (1.f / kUnit);
+            floor_s = fmaxf(share > 0.f ? logf(share) - 1e-3f : -kSpan, -kSpan);
+            per = kCoarse / -floor_s;
+            above = r.m + (floor_s - 1e-3f) * r.T - fabsf(r.m) * 1e-6f;
+        }
         u64 mass = 0;
         uint32_t n = 0;
         row.each([&](float x, int, int) {
             const Token t = weigh(r, x);
-            if (t.in) mass += t.W, ++n;
+            if (t.in) {
+                accumulate(mass, t.W), ++n;
+                if (x >= above) {
+                    // In parts of 15 bits, large weights to the nearest 2^15: one addition mostly.
+                    const int at = min((int)(-t.s * per), kCoarse - 1);
+                    const uint32_t hi = t.W < 1u << 22 ? t.W >> 15 : (t.W + (1u << 14)) >> 15;
+                    if (t.W < 1u << 22) atomicAdd(&sm.coarse_lo[at], t.W & 0x7FFFu);
+                    if (hi != 0u) atomicAdd(&sm.coarse_hi[at], hi);
+                }
+            }
         });
         u64 nn = n, tm, tn;
         block_scan(sm, mass, nn, tm, tn);
@@ -780,71 +818,69 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     Cut cut{0u, 1u, 0};
     if (cut_k || by_p) {
         // No token below `bound` is kept (margins for rounding only make it lower).
-        float bound = r.m - 21.7f * r.T - fabsf(r.m) * 1e-6f, per = 0.f;
+        float bound = r.m - 21.7f * r.T - fabsf(r.m) * 1e-6f, over = INFINITY;
         int last = -1;                             // top-p: the bin of s in which the limit is reached
-        u64 limit = 0, before = 0;                 // and the mass before it
+        const u64 limit = by_p && counted ? limit_of(top_p, total) : 0;
         const bool listing = by_k || !cut_k;
         if (by_k) {
             if (!row.infinite) bound = fmaxf(bound, unordered(reach));
         } else if (listing) {
-            const float least = (1.f - top_p) * (float)total / (float)p.V * (1.f / kUnit);
-            const float floor_s = fmaxf(least > 0.f ? logf(least) - 1e-3f : -kSpan, -kSpan);
-            per = kCoarse / -floor_s;
-            for (int i = tid; i < kCoarse; i += kThreads) sm.coarse_lo[i] = sm.coarse_hi[i] = 0u;
-            __syncthreads();
-            const float above = r.m + (floor_s - 1e-3f) * r.T - fabsf(r.m) * 1e-6f;
-            row.each([&](float x, int, int) {
-                if (x >= above) {
-                    const Token t = weigh(r, x);
-                    if (t.in) {
-                        const int bin = min((int)(-t.s * per), kCoarse - 1);
-                        atomicAdd(&sm.coarse_lo[bin], t.W & 0x7FFFu);
-                        atomicAdd(&sm.coarse_hi[bin], t.W >> 15);
-                    }
-                }
-            });
-            cluster_barrier(r);
-            u64 mass = 0, z = 0, tm, tz;
+            // By the bins' rounded sums: what is found from them is checked exactly below.
+            u64 sum = 0, z = 0, tm, tz;
             if (tid < kCoarse)
                 for (int i = 0; i < r.ranks; ++i)
-                    mass += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_lo[tid]), i)) +
-                            ((u64)ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_hi[tid]), i)) << 15);
-            u64 sum = mass;
-            if (tid == 0) sm.found[0] = kCoarse, sm.found[1] = 0;
+                    sum += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_lo[tid]), i)) +
+                           ((u64)ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_hi[tid]), i)) << 15);
+            const u64 of_bin = sum;
+            if (tid == 0) sm.found[0] = kCoarse;
             block_scan(sm, sum, z, tm, tz);
-            limit = limit_of(top_p, total);
-            if (tid < kCoarse && sum < limit && sum + mass >= limit) sm.found[0] = (u64)tid, sm.found[1] = sum;
+            if (tid < kCoarse && sum < limit && sum + of_bin >= limit) sm.found[0] = (u64)tid;
             __syncthreads();
-            last = (int)sm.found[0], before = sm.found[1];
+            last = (int)sm.found[0];
             bound = fmaxf(bound, r.m - ((float)(last + 1) / per + 1e-3f) * r.T - fabsf(r.m) * 1e-6f);
+            over = r.m - ((float)last / per - 1e-3f) * r.T + fabsf(r.m) * 1e-6f;      // above: an earlier bin
         }
-        auto of_bin = [&](float x) {
-            if (x < bound) return false;
-            const Token t = weigh(r, x);
-            return t.in && min((int)(-t.s * per), kCoarse - 1) == last;
-        };
         if (listing) {
-            // How many tokens there are from the bound on, and in the last bin alone.
-            u64 mine = 0, in_bin = 0, of_cta, of_bins;
-            row.each([&](float x, int, int) {
-                mine += x >= bound;
-                if (last >= 0) in_bin += of_bin(x);
+            // How many tokens there are from the bound on, and between it and `over`; the mass
+            // above `over` of each run, of the CTA, and that between.
+            uint32_t n_mine = 0, n_between = 0;
+            u64 run = 0, above = 0, between = 0;
+            row.each([&](float x, int it, int v) {
+                if (x >= bound) {
+                    ++n_mine;
+                    if (last >= 0) {
+                        const Token t = weigh(r, x);
+                        if (t.in) {
+                            if (x > over) accumulate(run, t.W);
+                            else accumulate(between, t.W), ++n_between;
+                        }
+                    }
+                }
+                if (v == kVec - 1 && last >= 0) {
+                    run = warp_sum(run);
+                    if (lane == 0) sm.above[it * kWarps + warp] = run, above += run;
+                    run = 0;
+                }
             });
-            const u64 own_n = mine, own_bin = in_bin;
-            block_scan(sm, mine, in_bin, of_cta, of_bins);
-            exchange(sm, r, of_cta, of_bins);
-            u64 n = 0, n_bin = 0;
+            u64 mine = n_mine, mine_between = n_between, of_cta, of_between, cta_above = 0, cta_between = 0;
+            block_scan(sm, mine, mine_between, of_cta, of_between);
+            if (last >= 0) block_scan(sm, above, between, cta_above, cta_between);
+            exchange(sm, r, of_cta, of_between, cta_above, cta_between);
+            u64 n = 0, n_bin = 0, before = 0, of_bin = 0;
             for (int i = 0; i < r.ranks; ++i) {
-                if (i == r.rank) mine += n, in_bin += n_bin;
-                n += sm.peer[i][0], n_bin += sm.peer[i][1];
+                if (i == r.rank) mine += n, mine_between += n_bin;
+                n += sm.peer[i][0], n_bin += sm.peer[i][1], before += sm.peer[i][2], of_bin += sm.peer[i][3];
             }
-            const bool whole = n <= (u64)kList, bin_only = !whole && n_bin > 0 && n_bin <= (u64)kList;
+            // The list may hold all of them, or those of the last bin if the limit is indeed there.
+            const bool whole = n <= (u64)kList && (last < 0 || before + of_bin >= limit);
+            const bool bin_only = !whole && last >= 0 && n_bin > 0 && n_bin <= (u64)kList && before < limit && before + of_bin >= limit;
             if (whole || bin_only) {
                 // They go to the first CTA's list, each CTA and thread at its place.
-                uint32_t at = ptx::mapa_shared(ptx::smem_u32(sm.list), 0u) + (uint32_t)(whole ? mine : in_bin) * 8u;
-                if ((whole ? own_n : own_bin) > 0)
+                uint32_t at = ptx::mapa_shared(ptx::smem_u32(sm.list), 0u) + (uint32_t)(whole ? mine : mine_between) * 8u;
+                const float to = whole ? INFINITY : over;
+                if ((whole ? n_mine : n_between) > 0)
                     row.each([&](float x, int it, int v) {
-                        if (whole ? x >= bound : of_bin(x)) {
+                        if (x >= bound && x <= to && (whole || weigh(r, x).in)) {
                             st_cluster_u64(at, (u64)(uint32_t)~ordered(x) << 32 | (uint32_t)row.index_of(it, v));
                             at += 8;
                         }
@@ -862,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
                 exchange(sm, r, cut.key, cut.quota, cut.W);
                 cut = Cut{(uint32_t)sm.peer[0][0], (uint32_t)sm.peer[0][2], sm.peer[0][1]};
                 __syncthreads();
-                tally(sm, row, r, cut);
+                tally(sm, row, r, cut, ordered(over));
                 draw_all(sm, row, r, cut, p, b);
                 cluster_barrier(r);
                 return;
@@ -884,13 +920,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         }
         if (top_k > 0 && (u64)top_k < tokens) {
             narrow(sm, row, r, false, (u64)top_k, cut);
-            tally(sm, row, r, cut);
+            tally(sm, row, r, cut, ~0u);
             total = cut.quota * cut.W;
             for (int i = 0; i < r.ranks; ++i) total += sm.peer[i][0];
         }
         if (by_p) narrow(sm, row, r, true, limit_of(top_p, total), cut);
     }
-    tally(sm, row, r, cut);
+    tally(sm, row, r, cut, ~0u);
     draw_all(sm, row, r, cut, p, b);
     cluster_barrier(r);
 }
@@ -898,18 +934,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &args, cudaStream_t stream) {
-    // CTAs of a row: more while there are SMs for them, and as many as its vectors need.
+    // CTAs of a row: as many as its tokens need, then more while each has over kShare bytes,
+    // and for small batches while there are SMs for them and over kSmallShare bytes each.
+    // (A step over the cluster costs the same for any share, and rows differ in their work,
+    // so that more and smaller CTAs even out: 256 rows of 128256 floats take 244 us with one
+    // CTA each, 180 with two, 169 with four and 193 with eight; 192 rows of 19439 floats 18.8
+    // us with one and 24.8 with two.)
     const int64_t bytes = (int64_t)args.V * (args.dtype == LOWBIT_DTYPE_F32 ? 4 : 2);
     int ranks = 1;
     while (ranks < kMaxCluster && (bytes + 32 > (int64_t)ranks * kThreads * kMaxVecs * 16 || args.V > ranks * kMaxTokens - 16 ||
-                                   (bytes > ranks * 8192 && (int64_t)args.B * ranks < kWanted)))
+                                   bytes > ranks * kShare ||
+                                   (bytes > ranks * kSmallShare && (int64_t)args.B * ranks < kWanted)))
         ranks *= 2;
     const auto kernel = args.dtype == LOWBIT_DTYPE_F32    ? sample_kernel<LOWBIT_DTYPE_F32>
                         : args.dtype == LOWBIT_DTYPE_BF16 ? sample_kernel<LOWBIT_DTYPE_BF16>
                                                           : sample_kernel<LOWBIT_DTYPE_F16>;
     const int64_t vecs = (bytes / 16 + 2 + ranks - 1) / ranks, held = std::min<int64_t>((vecs + kThreads - 1) / kThreads, kHeld);
     const int smem = (int)(sizeof(Shared) + held * kThreads * 16);
-    const cudaError_t e = raise_smem_limit((const void *)kernel, current_device(), smem);
+    const cudaError_t e = raise_smem_limit((const void *)kernel, current_device(), (int)sizeof(Shared) + kHeld * kThreads * 16);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ranks * (unsigned)args.B);

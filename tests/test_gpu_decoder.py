@@ -555,5 +555,11 @@ def test_sample_draws_follow_the_distribution():
     assert np.all(np.abs(np.bincount(token, minlength=V) - n * p / p.sum()) <= 1.01)
 
 
+def test_sample_row_sizes_in_turn():
+    """Large rows, small ones, large ones again: each launch has the shared memory it needs."""
+    for V in (90_000, 100, 90_000, 3000, 300_000, 40_000):
+        check_rows(make_logits(73, 3, V, torch.float32), np.array([0.2, 0.6, 0.95]), 1.0, [0, 50, 0], [0.9, 1.0, 1.0], 0.0)
+
+
 def test_sample_large_vocabulary_beyond_what_is_held():
     check_rows(make_logits(70, 2, 400_003, torch.float32), np.array([0.2, 0.95]), 1.0, [0, 1000], [0.95, 1.0], 0.0)
