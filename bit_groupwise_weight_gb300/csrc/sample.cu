@@ -19,21 +19,25 @@
 //     top-k   a value that at least k threads' largest logits reach (bisected with
 //             the CTA's counting barrier),
 //     top-p   tokens under (1 - p) Z / V together hold less than (1 - p) Z; the mass of
-//             those above, in 256 bins of s, says in which bin p Z is reached.
-// The tokens above the bound (usually some hundreds) go to one CTA, which sorts them
-// and does the rest by itself.  When they are more than its list holds, that of top-p
-// takes the tokens of the last bin only and finds the threshold among them (the last
-// kept logit, and how many equal ones are kept, in index order); the draw then runs
-// over all tokens above it.  Where even that does not fit (flat logits, very large k)
-// the threshold is found by counting: bins of s, then ranges of the bits of x, until
-// one value is left.
+//             those above, in 1024 bins of s, says in which bin p Z is reached.
+// The tokens above the bound (usually some hundreds) go to one CTA, which does the rest by
+// itself: each of top-k, top-p and the draw looks for one token of its list, by 512 bins
+// of the range that may hold it (two or three passes over the list; ordering the list
+// took twice as long).  When they are more than the list holds, that of top-p takes the
+// tokens of the last bin only and finds the last kept one among them; the draw then runs
+// over all tokens, by the sums of runs of them.  Where even that does not fit (flat
+// logits, very large k) the threshold is found by counting: bins of s, then ranges of the
+// bits of x, until one value is left.
 //
 // Work split: a cluster of up to 8 CTAs takes a row and holds it in shared memory (each
 // logit is read from memory once, and each thread reads back its own vectors; held in
 // registers, every pass had to be unrolled over them, and the code no longer fit the
 // instruction cache); what CTAs need of each other goes through distributed shared
-// memory.  Bound: the chain of cluster-wide steps (three for top-k,
-// five to seven for top-p) for few rows, the exponentials of all tokens for many.
+// memory.  Bound: for few rows the chain of some twenty barriers of the CTA and three
+// (top-k) to six (top-p) of the cluster, for many the instructions of the pass that
+// weighs all tokens (some 35 a token, of which two at a quarter of the rate or less).
+// One row of 128256 in bfloat16 takes 16 us, 64 rows of them with top-p 53 us (0.3 TB/s),
+// 256 rows in float32 of mixed settings 137 us (1.0 TB/s).
 #include <algorithm>
 
 #include "common.cuh"
@@ -45,13 +49,13 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;                        // of the counting path
-constexpr int kCoarse = 256;                       // of the top-p bound
-constexpr int kList = 2048;                        // tokens that one CTA sorts
+constexpr int kCoarse = 1024;                      // of the top-p bound
+constexpr int kList = 2048;                        // tokens of the list, less one
 constexpr int kMaxCluster = 8;
 constexpr int kHeld = 8;                           // 16-byte vectors that a thread holds
 constexpr int kMaxVecs = 64;                       // that it may have (the others are read again)
+constexpr int kFew = 32;                           // of its tokens that are compared all with all
 constexpr int kMaxTokens = 131071;                 // of a CTA: sums of 15-bit parts of W stay inside 32 bits
-constexpr int kShort = 256;                        // a list that is ordered by counting
 constexpr int kWanted = 152;                       // CTAs of a launch, where small batches are split
 constexpr int64_t kShare = 128 * 1024;             // bytes of a row that one CTA is left with (see launch_sample)
 constexpr int64_t kSmallShare = 8 * 1024;
@@ -73,6 +77,10 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
+__device__ __forceinline__ void add_cluster_u64(uint32_t addr, u64 v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
 // Order-preserving map of floats to unsigned integers (-0 like 0), and back.
 __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t u = __float_as_uint(x + 0.0f);
@@ -80,22 +88,32 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
+// A token's place among the others as one number: larger logits, then lower indexes,
+// are larger.
+constexpr int kIndexBits = 20;
+constexpr u64 kIndexMask = (1u << kIndexBits) - 1;
+__device__ __forceinline__ u64 place_of(float x, int index) { return (u64)ordered(x) << kIndexBits | (kIndexMask - (uint32_t)index); }
+__device__ __forceinline__ int index_at(u64 place) { return (int)(kIndexMask - (place & kIndexMask)); }
+
 struct alignas(16) Shared {
     union {
-        struct {                                   // the list, and the bins of the top-p bound
+        struct {                                   // the list with its weights, and the bins of the top-p bound
             u64 list[kList];
-            uint32_t coarse_lo[kCoarse], coarse_hi[kCoarse];
+            uint32_t weight[kList];
+            uint32_t coarse[kCoarse];              // each at a scale of its own (scale_bits)
         };
         struct {                                   // the counting path: W = lo + 2^15 hi, summed apart in 32 bits
             uint32_t count[kBins], lo[kBins], hi[kBins];
         };
     };
-    u64 above[kMaxVecs * kWarps];                  // mass above the cut of each run of a warp's vectors, in index order
-    uint32_t equal[kMaxVecs * kWarps];             // tokens equal to it
+    u64 runs[kMaxVecs * kWarps];                   // mass (or tokens) of each run of a warp's vectors, in index order
     u64 pub[2][4];                                 // what this CTA tells the others, in two buffers
     u64 peer[kMaxCluster][4];                      // what each CTA told
     u64 red[kWarps][2];
     u64 found[4];
+    u64 few[kFew];                                 // of a search
+    uint32_t few_weight[kFew];
+    int fews;
     uint32_t kmin, kmax;
 };
 
@@ -105,7 +123,7 @@ template <int DTYPE>
 struct Row {
     static constexpr int kVec = DTYPE == LOWBIT_DTYPE_F32 ? 4 : 8;
     const uint4 *base;
-    int lead, V, first, end, nvec;                 // vectors [first, end) are this CTA's, nvec of a thread at most
+    int lead, V, all, part, first, end, nvec;      // vectors [first, end) of `all` are this CTA's (part), nvec of a thread at most
     bool infinite;                                 // the maximum is +infinity: those count as 0, the others as -infinity
     uint4 *held;                                   // this thread's vectors, kThreads apart (shared memory)
 
@@ -149,14 +167,20 @@ struct Row {
 #pragma unroll 4
         for (int it = 0; it < min(nvec, kHeld); ++it) held[it * kThreads] = load(it);
     }
-    template <typename F>
-    __device__ __forceinline__ void each(const F &f) const {          // f(x, it, v)
+    // f(x, it, v) for each token; after a vector the whole warp comes to done(it).
+    template <typename F, typename G>
+    __device__ __forceinline__ void each(const F &f, const G &done) const {
 #pragma unroll 1
         for (int it = 0; it < nvec; ++it) {
             const uint4 w = it < kHeld ? held[it * kThreads] : load(it);
 #pragma unroll
             for (int v = 0; v < kVec; ++v) f(get(w, v), it, v);
+            done(it);
         }
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(const F &f) const {
+        each(f, [](int) {});
     }
 };
 
@@ -230,56 +254,104 @@ __device__ __forceinline__ u64 warp_sum(u64 a) {
            ((u64)__reduce_add_sync(~0u, (uint32_t)(a >> 52)) << 52);
 }
 
+// The whole part of f * total for 0 <= f < 1, and whether there is a rest: in whole numbers
+// (double precision is slow on this device).
+struct Product { u64 whole; bool rest; };
+__device__ __forceinline__ Product times(float f, u64 total) {
+    const uint32_t bits = __float_as_uint(f), e = max(bits >> 23, 1u);
+    const u64 m = (bits & 0x7FFFFFu) | (bits >> 23 != 0 ? 0x800000u : 0u), lo = m * total, hi = __umul64hi(m, total);
+    const uint32_t shift = 150u - e;               // f = m / 2^shift, shift >= 24
+    if (shift >= 128) return {0ull, (lo | hi) != 0};
+    if (shift >= 64) return {hi >> (shift - 64), (lo | (hi & ((1ull << (shift - 64)) - 1))) != 0};
+    return {hi << (64 - shift) | lo >> shift, (lo & ((1ull << shift) - 1)) != 0};
+}
 // floor(u * total), below total.
 __device__ __forceinline__ u64 target_of(float u, u64 total) {
-    const u64 t = u > 0.f ? (u64)floor((double)u * (double)total) : 0ull;
-    return t < total ? t : total - 1;
+    return !(u > 0.f) ? 0ull : u >= 1.f ? total - 1 : times(u, total).whole;
 }
-
-// The mass that a prefix has to reach for top-p: ceil(p total), at least 1.
+// The mass that a prefix has to reach for top-p (below 1): ceil(p total), at least 1.
 __device__ __forceinline__ u64 limit_of(float top_p, u64 total) {
-    const double want = ceil((double)top_p * (double)total);
-    return want > 1.0 ? (u64)want : 1ull;
+    const Product p = times(top_p, total);
+    return max(p.whole + p.rest, 1ull);
 }
 
-// Sorts the first n entries of the list (n a power of two), rising.  Steps over fewer
-// than 32 entries stay in registers.
-__device__ __forceinline__ void sort_list(Shared &sm, int n) {
-    const int tid = threadIdx.x;
-    for (int k = 2; k <= n; k <<= 1) {
-        for (int j = k >> 1; j >= 32; j >>= 1) {
-            for (int p = tid; p < n / 2; p += kThreads) {
-                const int i = ((p & ~(j - 1)) << 1) | (p & (j - 1)), o = i | j;
-                const u64 a = sm.list[i], b = sm.list[o];
-                if ((a > b) == ((i & k) == 0)) sm.list[i] = b, sm.list[o] = a;
-            }
-            __syncthreads();
-        }
-        for (int i0 = 0; i0 < n; i0 += kThreads) {
-            const int i = i0 + tid;
-            if ((i & ~31) < n) {                   // whole warps
-                u64 v = i < n ? sm.list[i] : ~0ull;
-                const bool up = (i & k) == 0;
-                for (int j = min(k >> 1, 16); j > 0; j >>= 1) {
-                    const u64 o = __shfl_xor_sync(~0u, v, j);
-                    v = ((i & j) == 0) == up ? (v < o ? v : o) : (v > o ? v : o);
-                }
-                if (i < n) sm.list[i] = v;
-            }
+// The least v in (lo, hi] for which the entries of the list with (entry & mask) > v hold
+// less than `need`, in mass or in number: hi is one, lo is not, and v is an entry (they
+// differ).  512 bins of the range, one of which is the next range, until few are left.
+__device__ __noinline__ u64 search(Shared &sm, int n, u64 mask, bool by_mass, u64 need, u64 lo, u64 hi) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    uint32_t *const number = sm.coarse, *const high = sm.coarse + kThreads;      // number << 21 | low 10 bits of W; the others
+    u64 above = 0;                                 // of the entries over hi
+    int left = n;
+    __syncthreads();
+    while (left > kFew) {
+        const int shift = max(55 - __clzll((long long)(hi - lo - 1)), 0);
+        number[tid] = high[tid] = 0u;
+        if (tid == 0) sm.found[3] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const u64 v = sm.list[i] & mask;
+            if (v <= lo || v > hi) continue;
+            const uint32_t W = by_mass ? sm.weight[i] : 1u, at = kThreads - 1 - (uint32_t)((v - lo - 1) >> shift);
+            atomicAdd(number + at, 1u << 21 | (W & 0x3FFu));
+            if (W >> 10 != 0) atomicAdd(high + at, W >> 10);
         }
         __syncthreads();
+        const uint32_t word = number[tid];
+        const u64 mine = (word & 0x1FFFFFu) + ((u64)high[tid] << 10);
+        u64 before = mine, z = 0, t, tz;
+        block_scan(sm, before, z, t, tz);
+        before += above;
+        if (before < need && before + mine >= need) sm.found[3] = (u64)(word >> 21) << 32 | (uint32_t)(tid + 1), sm.found[2] = before;
+        __syncthreads();
+        if (sm.found[3] == 0) return hi;
+        left = (int)(sm.found[3] >> 32), above = sm.found[2];
+        const u64 at = (u64)(kThreads - (int)(uint32_t)sm.found[3]);
+        hi = min(lo + ((at + 1) << shift), hi), lo += at << shift;
+        __syncthreads();
     }
+    if (tid == 0) sm.fews = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+        const u64 v = sm.list[i] & mask;
+        if (v <= lo || v > hi) continue;
+        const int at = atomicAdd(&sm.fews, 1) & (kFew - 1);
+        sm.few[at] = v, sm.few_weight[at] = by_mass ? sm.weight[i] : 1u;
+    }
+    __syncthreads();
+    // Every warp compares all of them with all.
+    const int few = min(sm.fews, kFew);
+    const u64 v = lane < few ? sm.few[lane] : 0ull;
+    u64 before = above;
+    for (int j = 0; j < few; ++j) accumulate(before, sm.few[j] > v ? sm.few_weight[j] : 0u);
+    const uint32_t is = __ballot_sync(~0u, lane < few && before < need && before + sm.few_weight[lane] >= need);
+    return is != 0 ? __shfl_sync(~0u, v, __ffs(is) - 1) : hi;
 }
-__device__ __forceinline__ int power_of_two(int n) { return n <= 2 ? 2 : 1 << (32 - __clz(n - 1)); }
+// Weights of the list's entries, of those at `cut` and above; their sum.
+__device__ __noinline__ u64 weigh_list(Shared &sm, const Draw r, int n, u64 cut) {
+    const int tid = threadIdx.x;
+    u64 sum = 0, z = 0, all, tz;
+    for (int i = tid; i < n; i += kThreads) {
+        const u64 place = sm.list[i];
+        const Token t = weigh(r, unordered((uint32_t)(place >> kIndexBits)));
+        const uint32_t W = t.in && place >= cut ? t.W : 0u;
+        sm.weight[i] = W;
+        sum += W;
+    }
+    block_scan(sm, sum, z, all, tz);
+    return all;
+}
 
-// The kept prefix: tokens whose key is above `key`, and of those equal to it the
-// first `quota` in index order (W each).
-struct Cut { uint32_t key, W; u64 quota; };
+// The kept prefix: tokens whose key is above `key`, and of those equal to it (W each) the
+// first `quota` in index order, which are those up to index `last`.
+struct Cut { uint32_t key, W; u64 quota; int last; };
 
 // The counting path.  Narrows the prefix to the tokens before which less than `target`
-// tokens (by_mass: units of W) come; the present prefix reaches the target.
+// tokens (by_mass: units of W) come; the present prefix reaches the target.  `mass` is that
+// of the prefix (by number only), `round` the exchanges so far.
+struct Narrowed { Cut cut; u64 mass; int round; };
 template <int DTYPE>
-__device__ __noinline__ void narrow(Shared &sm, const Row<DTYPE> &row, Draw &r, bool by_mass, u64 target, Cut &cut) {
+__device__ __noinline__ Narrowed narrow(Shared &sm, const Row<DTYPE> row, Draw r, bool by_mass, u64 target, Cut cut) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int slice = kBins / r.ranks, per = max(slice / kThreads, 1);    // bins of a CTA, of a thread
     u64 n_above = 0, m_above = 0;                  // tokens and mass above the range under search
@@ -366,7 +438,7 @@ __device__ __noinline__ void narrow(Shared &sm, const Row<DTYPE> &row, Draw &r, 
         if (hit < 0) {
             const u64 need = by_mass ? (target - all_m + cut.W - 1) / cut.W : target - all_n;
             cut.quota = need < cut.quota ? need : cut.quota;
-            return;
+            return Narrowed{cut, 0, r.round};
         }
         const int at = (int)sm.peer[hit][0] - 1;
         n_above = sm.peer[hit][1], m_above = sm.peer[hit][2];
@@ -382,165 +454,92 @@ __device__ __noinline__ void narrow(Shared &sm, const Row<DTYPE> &row, Draw &r, 
     cut.key = khi;
     cut.W = weigh(r, unordered(khi)).W;
     cut.quota = by_mass ? (target - m_above + cut.W - 1) / cut.W : target - n_above;
+    return Narrowed{cut, m_above + cut.quota * cut.W, r.round};
 }
 
-// Mass above the cut and tokens equal to it, for each run of a warp's vectors (in index
-// order: vector number, then warp) in sm.above and sm.equal, and of every CTA in sm.peer.
-// upto: tokens above it are in sm.above already (a key; ~0: none are).
+// What counts of a token: its weight if it is kept, or (equals) one if its key is the cut's.
+struct Count {
+    float from;
+    int last;
+    bool equals;
+    __device__ __forceinline__ Count(const Cut &cut, bool equals)
+        : from(cut.key == 0 ? -INFINITY : unordered(cut.key)), last(cut.last), equals(equals) {}
+    __device__ __forceinline__ uint32_t of(const Draw &r, float x, int index) const {
+        if (!(x >= from) || (x == from ? !equals && index > last : equals)) return 0u;
+        const Token t = weigh(r, x);
+        return !t.in ? 0u : equals ? 1u : t.W;
+    }
+};
+
+// The sum of each run of a warp's vectors (in index order: vector number, then warp).
 template <int DTYPE>
-__device__ __forceinline__ void tally(Shared &sm, const Row<DTYPE> &row, Draw &r, const Cut &cut, uint32_t upto) {
+__device__ __noinline__ void tally(Shared &sm, const Row<DTYPE> row, const Draw r, const Count count) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float from = cut.key == 0 ? -INFINITY : unordered(cut.key), to = upto == ~0u ? INFINITY : unordered(upto);
-    u64 above = 0, all_above = 0;
-    uint32_t equal = 0, all_equal = 0;
-    row.each([&](float x, int it, int v) {
-        if (x >= from && x <= to) {
-            const Token t = weigh(r, x);
-            if (t.in) {
-                if (x > from) accumulate(above, t.W);
-                else ++equal;
-            }
-        }
-        if (v == Row<DTYPE>::kVec - 1) {
-            above = warp_sum(above);
-            equal = __reduce_add_sync(~0u, equal);
-            if (lane == 0) {
-                if (upto != ~0u) above += sm.above[it * kWarps + warp];
-                sm.above[it * kWarps + warp] = above, sm.equal[it * kWarps + warp] = equal;
-                all_above += above, all_equal += equal;
-            }
-            above = 0, equal = 0;
-        }
-    });
-    u64 a = lane == 0 ? all_above : 0, b = lane == 0 ? all_equal : 0, ta, tb;
-    block_scan(sm, a, b, ta, tb);
-    exchange(sm, r, ta, tb);
+    u64 sum = 0;
+    row.each([&](float x, int it, int v) { accumulate(sum, count.of(r, x, row.index_of(it, v))); },
+             [&](int it) {
+                 __syncwarp();
+                 sum = warp_sum(sum);
+                 if (lane == 0) sm.runs[it * kWarps + warp] = sum;
+                 sum = 0;
+             });
 }
 
-// The draw from all of the row's tokens above the cut, after tally.
+// The token in which the running total in index order passes a target: that of the given
+// uniform number, or (count.equals) of the cut's quota.  One thread of the cluster gets
+// its index, the others -1; `total` is the sum.  Begins with a barrier of the CTA; counts as
+// one exchange.
+struct Found { int index; u64 total; };
 template <int DTYPE>
-__device__ __forceinline__ void draw_all(Shared &sm, const Row<DTYPE> &row, const Draw &r, const Cut &cut, const SampleArgs &p, int b) {
+__device__ __noinline__ Found locate(Shared &sm, const Row<DTYPE> row, Draw r, const Count count, u64 quota, float u) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto kept = [&](u64 above, u64 equal, u64 before) {       // of a run with `before` equal tokens before it
-        const u64 left = cut.quota > before ? cut.quota - before : 0;
-        return above + (equal < left ? equal : left) * cut.W;
-    };
-    u64 total = 0, start = 0, mine = 0, eq = 0, eq0 = 0;      // start, eq0: before this CTA
-    for (int i = 0; i < r.ranks; ++i) {
-        const u64 k = kept(sm.peer[i][0], sm.peer[i][1], eq);
-        if (i == r.rank) start = total, eq0 = eq, mine = k;
-        total += k;
-        eq += sm.peer[i][1];
-    }
-    const u64 target = target_of(p.u[b], total);
-    if (target < start || target >= start + mine) return;     // the same for the whole CTA
-    // The run in which it falls: two runs a thread at most.
+    // Two runs a thread at most.
     const int runs = row.nvec * kWarps, per = (runs + kThreads - 1) / kThreads;
-    u64 e = 0, k = 0, te, tk, zero = 0, tz;
-    for (int q = 0; q < per; ++q)
-        if (tid * per + q < runs) e += sm.equal[tid * per + q];
-    block_scan(sm, e, zero, te, tz);
-    e += eq0;
-    u64 run = e;
-    for (int q = 0; q < per; ++q)
-        if (tid * per + q < runs) {
-            k += kept(sm.above[tid * per + q], sm.equal[tid * per + q], run);
-            run += sm.equal[tid * per + q];
-        }
-    u64 z2 = 0;
-    block_scan(sm, k, z2, tk, tz);
-    k += start;
-    for (int q = 0; q < per; ++q)
-        if (tid * per + q < runs) {
-            const int at = tid * per + q;
-            const u64 add = kept(sm.above[at], sm.equal[at], e);
-            if (target >= k && target < k + add) sm.found[0] = (u64)at, sm.found[1] = k, sm.found[2] = e;
-            k += add;
-            e += sm.equal[at];
-        }
     __syncthreads();
-    const int at = (int)sm.found[0];
-    if (at % kWarps != warp) return;
-    // The lane, then the token.
-    const uint4 w = row.load(at / kWarps);
-    u64 above = 0;
-    uint32_t equal = 0;
-#pragma unroll
-    for (int v = 0; v < Row<DTYPE>::kVec; ++v) {
-        const float x = Row<DTYPE>::get(w, v);
-        const uint32_t key = ordered(x);
-        const Token t = weigh(r, x);
-        if (t.in && key > cut.key) above += t.W;
-        if (t.in && key == cut.key) ++equal;
+    u64 mine = 0, z = 0, of_cta, tz;
+    for (int q = 0; q < per; ++q)
+        if (tid * per + q < runs) mine += sm.runs[tid * per + q];
+    block_scan(sm, mine, z, of_cta, tz);
+    exchange(sm, r, of_cta);
+    u64 total = 0;
+    for (int i = 0; i < r.ranks; ++i) {
+        if (i == r.rank) mine += total;
+        total += sm.peer[i][0];
     }
-    u64 ie = equal;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 v = __shfl_up_sync(~0u, ie, o);
-        if (lane >= o) ie += v;
-    }
-    u64 seen = sm.found[2] + ie - equal, ik = kept(above, equal, seen);
-    const u64 own = ik;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 v = __shfl_up_sync(~0u, ik, o);
-        if (lane >= o) ik += v;
-    }
-    u64 sum = sm.found[1] + ik - own;
-    if (target < sum || target >= sum + own) return;
-#pragma unroll
-    for (int v = 0; v < Row<DTYPE>::kVec; ++v) {
-        const float x = Row<DTYPE>::get(w, v);
-        const uint32_t key = ordered(x);
-        const Token t = weigh(r, x);
-        const bool tie = t.in && key == cut.key;
-        const u64 add = (t.in && key > cut.key) || (tie && seen < cut.quota) ? t.W : 0;
-        seen += tie;
-        if (target >= sum && target < sum + add) {
-            p.token[b] = row.index_of(at / kWarps, v);
-            if (p.logprob != nullptr) p.logprob[b] = t.s - logf((float)total * (1.f / kUnit));
-        }
-        sum += add;
-    }
-}
-
-// The cut of the list's n tokens, before which `before` units of mass come: the last kept
-// key and how many of it are kept (this CTA's alone).
-__device__ __forceinline__ Cut cut_listed(Shared &sm, const Draw &r, int n, u64 before, u64 limit) {
-    constexpr int kPer = kList / kThreads;
-    const int tid = threadIdx.x, size = power_of_two(n);
-    for (int i = n + tid; i < size; i += kThreads) sm.list[i] = ~0ull;
+    const u64 target = count.equals ? quota - 1 : target_of(u, total);
     if (tid == 0) sm.found[0] = 0;
     __syncthreads();
-    sort_list(sm, size);
-    u64 W[kPer], sum = 0, z = 0, ts, tz;
+    for (int q = 0; q < per; ++q)
+        if (tid * per + q < runs) {
+            const u64 add = sm.runs[tid * per + q];
+            if (target >= mine && target < mine + add) sm.found[0] = (u64)(tid * per + q + 1), sm.found[1] = mine;
+            mine += add;
+        }
+    __syncthreads();
+    const int at = (int)sm.found[0] - 1;
+    if (at < 0 || at % kWarps != warp) return Found{-1, total};
+    // The lane, then the token.
+    const uint4 w = row.load(at / kWarps);
+    u64 own = 0;
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        const int i = tid * kPer + q;
-        W[q] = i < n ? weigh(r, unordered(~(uint32_t)(sm.list[i] >> 32))).W : 0;
-        sum += W[q];
-    }
-    block_scan(sm, sum, z, ts, tz);
-    sum += before;
-    u64 kept = 0;
+    for (int v = 0; v < Row<DTYPE>::kVec; ++v) own += count.of(r, Row<DTYPE>::get(w, v), row.index_of(at / kWarps, v));
+    u64 sum = own;
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        kept += tid * kPer + q < n && sum < limit;
-        sum += W[q];
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 v = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += v;
     }
-    z = 0;
-    block_scan(sm, kept, z, ts, tz);               // ts: kept in all
-    const uint32_t key = ~(uint32_t)(sm.list[ts - 1] >> 32);
-    u64 same = 0;
+    sum += sm.found[1] - own;
+    if (target < sum || target >= sum + own) return Found{-1, total};
+    int index = -1;
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        const int i = tid * kPer + q;
-        same += i < (int)ts && ~(uint32_t)(sm.list[i] >> 32) == key;
+    for (int v = 0; v < Row<DTYPE>::kVec; ++v) {
+        const int i = row.index_of(at / kWarps, v);
+        const u64 add = count.of(r, Row<DTYPE>::get(w, v), i);
+        if (target >= sum && target < sum + add) index = i;
+        sum += add;
     }
-    z = 0;
-    u64 quota;
-    block_scan(sm, same, z, quota, tz);
-    return Cut{key, weigh(r, unordered(key)).W, quota};
+    return Found{index, total};
 }
 
 // Writes the drawn token.
@@ -556,124 +555,65 @@ __device__ __forceinline__ void write_token(const Row<DTYPE> &row, const Draw &r
         for (int v = 0; v < Row<DTYPE>::kVec; ++v)
             if (v == at % Row<DTYPE>::kVec) x = Row<DTYPE>::get(w, v);
     }
-    p.logprob[b] = weigh(r, x).s - logf((float)mass * (1.f / kUnit));
+    p.logprob[b] = __fmul_rn(__fsub_rn(x, r.m), r.inv_t) - logf((float)mass * (1.f / kUnit));
 }
 
-// The rest of the work on a short list, a token a thread: places and the mass before each
-// by comparing with all others.
+// What a token of a warp has before it: how many of the others' places & mask are larger,
+// and their mass.
+struct Before { int number; u64 mass; };
+__device__ __forceinline__ Before before_of(int n, u64 place, uint32_t W, u64 mask) {
+    Before b{0, 0ull};
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+        const bool is = (__shfl_sync(~0u, place, j) & mask) > (place & mask);
+        const uint32_t w = __shfl_sync(~0u, W, j);
+        b.number += is;
+        accumulate(b.mass, is ? w : 0u);
+    }
+    return b;
+}
+// draw_listed (below) for up to 32 tokens, a token a lane.
 template <int DTYPE>
-__device__ __forceinline__ void draw_short(Shared &sm, const Row<DTYPE> &row, const Draw &r, int n, int top_k, float top_p, u64 total,
-                                           const SampleArgs &p, int b) {
-    const int tid = threadIdx.x;
-    u64 *weight = sm.list + kShort;                // W beside the entries
-    const u64 me = tid < n ? sm.list[tid] : ~0ull;
-    const Token t = weigh(r, unordered(~(uint32_t)(me >> 32)));
-    const uint32_t W = tid < n && t.in ? t.W : 0u;
-    if (tid < kShort) weight[tid] = W;
-    __syncthreads();
-    if (tid >= ((n + 31) & ~31)) return;           // whole warps
-    int place = 0;
-    u64 before = 0, all = 0;
-    for (int j = 0; j < n; ++j) {
-        const bool earlier = sm.list[j] < me;
-        place += earlier;
-        if (earlier) before += weight[j];
-    }
-    // Of the first top_k (all): the mass.
-    if (total == 0) {
-        // Places are a permutation: the mass before place top_k is the largest of before + W there.
-        u64 upto = tid < n && (top_k <= 0 || place < top_k) ? before + W : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const u64 v = __shfl_xor_sync(~0u, upto, o);
-            upto = v > upto ? v : upto;
-        }
-        if ((tid & 31) == 0) sm.red[tid >> 5][0] = upto;
-        ptx::named_sync(1, (uint32_t)((n + 31) & ~31));
-        for (int i = 0; i < (n + 31) / 32; ++i) all = sm.red[i][0] > all ? sm.red[i][0] : all;
-    } else {
-        all = total;
-    }
-    const u64 limit = top_p < 1.f ? limit_of(top_p, all) : ~0ull;
-    const bool kept = W != 0 && (top_k <= 0 || place < top_k) && before < limit;
-    ptx::named_sync(1, (uint32_t)((n + 31) & ~31));
-    if (tid < kShort) weight[tid] = kept ? W : 0;
-    ptx::named_sync(1, (uint32_t)((n + 31) & ~31));
-    // The running total in index order, and the whole.
-    const uint32_t index = (uint32_t)me;
-    u64 ahead = 0, mass = 0;
-    for (int j = 0; j < n; ++j) {
-        const u64 w = weight[j];
-        mass += w;
-        if ((uint32_t)sm.list[j] < index) ahead += w;
-    }
-    const u64 target = target_of(p.u[b], mass);
-    if (kept && target >= ahead && target < ahead + W) write_token(row, r, (int)index, mass, p, b);
+__device__ __noinline__ void draw_few(Shared &sm, const Row<DTYPE> row, const Draw r, int n, int top_k, float top_p, u64 total,
+                                      const SampleArgs &p, int b) {
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x >= 32) return;
+    const u64 place = lane < n ? sm.list[lane] : 0ull;
+    const Token t = weigh(r, unordered((uint32_t)(place >> kIndexBits)));
+    const uint32_t W = lane < n && t.in ? t.W : 0u;
+    const float u = p.u[b];
+    const Before of = before_of(n, place, W, ~0ull);
+    bool kept = W != 0 && (top_k <= 0 || of.number < top_k);
+    const u64 all = warp_sum(kept ? W : 0u);
+    if (top_p < 1.f) kept = kept && of.mass < limit_of(top_p, total != 0 ? total : all);
+    const u64 mass = warp_sum(kept ? W : 0u), target = target_of(u, mass);
+    const Before ahead = before_of(n, place, kept ? W : 0u, kIndexMask);
+    if (kept && target >= ahead.mass && target < ahead.mass + W) write_token(row, r, index_at(place), mass, p, b);
 }
 
-// The rest of the work on the list of n tokens (this CTA's alone): order, top-k, top-p,
-// draw.  total: mass of all tokens within min-p (0: that of the first top_k of the list).
+// The rest of the work on the list of n tokens (this CTA's alone; places in (lo, hi]):
+// top-k, top-p, draw.  total: mass of all tokens within min-p (0: that of the first top_k
+// of the list).
 template <int DTYPE>
-__device__ __forceinline__ void draw_listed(Shared &sm, const Row<DTYPE> &row, const Draw &r, int n, int top_k, float top_p, u64 total,
-                                            const SampleArgs &p, int b) {
-    constexpr int kPer = kList / kThreads;
-    const int tid = threadIdx.x;
-    int size = power_of_two(n);
-    for (int i = n + tid; i < size; i += kThreads) sm.list[i] = ~0ull;
-    __syncthreads();
-    sort_list(sm, size);                           // ~key, index: x falling, index rising
-    // Weights in that order, kPer neighbours a thread.
-    u64 W[kPer], idx[kPer], sum = 0, z = 0, all, tz;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        const int i = tid * kPer + q;
-        W[q] = idx[q] = 0;
-        if (i < n) {
-            const Token t = weigh(r, unordered(~(uint32_t)(sm.list[i] >> 32)));
-            if (t.in && (top_k <= 0 || i < top_k)) W[q] = t.W;
-            idx[q] = sm.list[i] & 0xFFFFFFFFull;
+__device__ __noinline__ void draw_listed(Shared &sm, const Row<DTYPE> row, const Draw r, int n, u64 lo, u64 hi, int top_k, float top_p,
+                                         u64 total, const SampleArgs &p, int b) {
+    u64 cut = 0;
+    if (top_k > 0 && top_k < n) cut = search(sm, n, ~0ull, false, (u64)top_k, lo, hi);
+    u64 mass = weigh_list(sm, r, n, cut);
+    if (top_p < 1.f) {
+        const u64 limit = limit_of(top_p, total == 0 ? mass : total);
+        if (mass >= limit) {
+            cut = search(sm, n, ~0ull, true, limit, cut == 0 ? lo : cut - 1, hi);
+            mass = weigh_list(sm, r, n, cut);
         }
-        sum += W[q];
     }
-    block_scan(sm, sum, z, all, tz);
-    if (total == 0) total = all;
-    const u64 limit = top_p < 1.f ? limit_of(top_p, total) : ~0ull;
-    u64 kept = 0, count = 0;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        const u64 w = W[q];
-        if (sum >= limit) W[q] = 0;
-        sum += w;
-        kept += W[q];
-        count += W[q] != 0;
-    }
-    // The kept in index order.
-    u64 before = kept, place = count, mass, left;
-    block_scan(sm, before, place, mass, left);
-    size = power_of_two((int)left);
-    for (int i = (int)left + tid; i < size; i += kThreads) sm.list[i] = ~0ull;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q)
-        if (W[q] != 0) sm.list[place++] = idx[q] << 32 | W[q];
-    __syncthreads();
-    sort_list(sm, size);
-    u64 own = 0;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        const int i = tid * kPer + q;
-        W[q] = i < (int)left ? sm.list[i] & 0xFFFFFFFFull : 0;
-        own += W[q];
-    }
-    u64 zero = 0;
-    block_scan(sm, own, zero, all, tz);
-    const u64 target = target_of(p.u[b], mass);
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        if (target >= own && target < own + W[q])
-            write_token(row, r, (int)(sm.list[tid * kPer + q] >> 32), mass, p, b);
-        own += W[q];
-    }
+    const u64 at = search(sm, n, kIndexMask, true, target_of(p.u[b], mass) + 1, 0ull, kIndexMask);
+    if (threadIdx.x == 0) write_token(row, r, index_at(at), mass, p, b);
 }
+
+// 2^15 to 2^46, a power of two by which the weights of bin `at` of the top-p bound are
+// multiplied: at most 2^15 of them.  drop: 2^23 / (bins of a halving).
+__device__ __forceinline__ uint32_t scale_bits(int at, int drop) { return (uint32_t)(at * drop + (142 << 23)) & 0x7F800000u; }
 
 template <int DTYPE>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p) {
@@ -696,15 +636,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         row.lead = (int)(at & 15) / (16 / kVec);
         row.V = p.V;
         row.infinite = false;
-        const int all = (row.lead + p.V + kVec - 1) / kVec, part = (all + r.ranks - 1) / r.ranks;
-        row.first = r.rank * part;
-        row.end = min(row.first + part, all);
-        row.nvec = (part + kThreads - 1) / kThreads;
+        row.all = (row.lead + p.V + kVec - 1) / kVec;
+        row.part = (row.all + r.ranks - 1) / r.ranks;
+        row.first = r.rank * row.part;
+        row.end = min(row.first + row.part, row.all);
+        row.nvec = (row.part + kThreads - 1) / kThreads;
     }
     row.held = reinterpret_cast<uint4 *>(raw + sizeof(Shared)) + tid;
     row.hold();
     r.T = p.temperature != nullptr ? p.temperature[b] : p.temperature_all;
-    const float top_p = p.top_p != nullptr ? p.top_p[b] : p.top_p_all;
+    const float top_p = fmaxf(p.top_p != nullptr ? p.top_p[b] : p.top_p_all, 0.f);
     const float min_p = p.min_p != nullptr ? p.min_p[b] : p.min_p_all;
     const int top_k = p.top_k != nullptr ? p.top_k[b] : p.top_k_all;
     const bool greedy = !(r.T > 0.f);
@@ -778,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     u64 total = 0, tokens = 0;                     // mass and number of the tokens within min-p
     const bool by_p = top_p < 1.f, counted = !by_k && (by_p || top_k > 0);
     float per = 0.f;                               // top-p: bins of a unit of s
+    int drop = 0;
     if (counted) {
         float floor_s = 0.f, above = INFINITY;     // tokens below are not binned
         if (by_p) {
@@ -785,13 +727,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             const Token t = weigh(r, row.infinite ? (own == INFINITY ? 0.f : -INFINITY) : own);
             u64 least = t.in ? t.W : 0, z = 0, tl, tz;
             block_scan(sm, least, z, tl, tz);
-            for (int i = tid; i < kCoarse; i += kThreads) sm.coarse_lo[i] = sm.coarse_hi[i] = 0u;
+            for (int i = tid; i < kCoarse; i += kThreads) sm.coarse[i] = 0u;
             exchange(sm, r, tl);
             tl = 0;
             for (int i = 0; i < r.ranks; ++i) tl += sm.peer[i][0];
             const float share = (1.f - top_p) * (float)tl / (float)p.V * (1.f / kUnit);
             floor_s = fmaxf(share > 0.f ? logf(share) - 1e-3f : -kSpan, -kSpan);
             per = kCoarse / -floor_s;
+            drop = (int)(8388608.f * 1.442695f / per);
             above = r.m + (floor_s - 1e-3f) * r.T - fabsf(r.m) * 1e-6f;
         }
         u64 mass = 0;
@@ -801,11 +744,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             if (t.in) {
                 accumulate(mass, t.W), ++n;
                 if (x >= above) {
-                    // In parts of 15 bits, large weights to the nearest 2^15: one addition mostly.
-                    const int at = min((int)(-t.s * per), kCoarse - 1);
-                    const uint32_t hi = t.W < 1u << 22 ? t.W >> 15 : (t.W + (1u << 14)) >> 15;
-                    if (t.W < 1u << 22) atomicAdd(&sm.coarse_lo[at], t.W & 0x7FFFu);
-                    if (hi != 0u) atomicAdd(&sm.coarse_hi[at], hi);
+                    // floor(-s per) by adding 1.5 2^23 (a conversion would take eight times as long).
+                    const int at = (int)min(__float_as_uint(__fadd_rn(fmaf(-t.s, per, -0.5f), 12582912.f)) - 0x4B400000u,
+                                            (uint32_t)kCoarse - 1u);
+                    // The product's integer, by adding 2^23.
+                    atomicAdd(&sm.coarse[at], __float_as_uint(fmaf(t.w, __uint_as_float(scale_bits(at, drop)), 8388608.f)) - 0x4B000000u);
                 }
             }
         });
@@ -815,7 +758,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         for (int i = 0; i < r.ranks; ++i) total += sm.peer[i][0], tokens += sm.peer[i][1];
     }
     const bool cut_k = top_k > 0 && (by_k || (u64)top_k < tokens);
-    Cut cut{0u, 1u, 0};
+    Cut cut{0u, 1u, 0, INT32_MAX};
+    bool tallied = false;                          // the runs' sums are there
     if (cut_k || by_p) {
         // No token below `bound` is kept (margins for rounding only make it lower).
         float bound = r.m - 21.7f * r.T - fabsf(r.m) * 1e-6f, over = INFINITY;
@@ -826,15 +770,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             if (!row.infinite) bound = fmaxf(bound, unordered(reach));
         } else if (listing) {
             // By the bins' rounded sums: what is found from them is checked exactly below.
-            u64 sum = 0, z = 0, tm, tz;
-            if (tid < kCoarse)
+            u64 of_bin[kCoarse / kThreads], sum = 0, z = 0, tm, tz;
+#pragma unroll
+            for (int q = 0; q < kCoarse / kThreads; ++q) {
+                const int at = tid * (kCoarse / kThreads) + q;
+                of_bin[q] = 0;
                 for (int i = 0; i < r.ranks; ++i)
-                    sum += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_lo[tid]), i)) +
-                           ((u64)ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse_hi[tid]), i)) << 15);
-            const u64 of_bin = sum;
+                    of_bin[q] += ld_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.coarse[at]), i));
+                of_bin[q] = of_bin[q] << 30 >> ((scale_bits(at, drop) >> 23) - 127);
+                sum += of_bin[q];
+            }
             if (tid == 0) sm.found[0] = kCoarse;
             block_scan(sm, sum, z, tm, tz);
-            if (tid < kCoarse && sum < limit && sum + of_bin >= limit) sm.found[0] = (u64)tid;
+#pragma unroll
+            for (int q = 0; q < kCoarse / kThreads; ++q) {
+                if (sum < limit && sum + of_bin[q] >= limit) sm.found[0] = (u64)(tid * (kCoarse / kThreads) + q);
+                sum += of_bin[q];
+            }
             __syncthreads();
             last = (int)sm.found[0];
             bound = fmaxf(bound, r.m - ((float)(last + 1) / per + 1e-3f) * r.T - fabsf(r.m) * 1e-6f);
@@ -845,23 +797,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             // above `over` of each run, of the CTA, and that between.
             uint32_t n_mine = 0, n_between = 0;
             u64 run = 0, above = 0, between = 0;
-            row.each([&](float x, int it, int v) {
-                if (x >= bound) {
-                    ++n_mine;
-                    if (last >= 0) {
-                        const Token t = weigh(r, x);
-                        if (t.in) {
-                            if (x > over) accumulate(run, t.W);
-                            else accumulate(between, t.W), ++n_between;
+            if (last < 0) {
+                row.each([&](float x, int, int) { n_mine += x >= bound; });
+            } else {
+                row.each(
+                    [&](float x, int, int) {
+                        if (x >= bound) {
+                            ++n_mine;
+                            const Token t = weigh(r, x);
+                            const uint32_t W = t.in ? t.W : 0u;
+                            accumulate(run, x > over ? W : 0u);
+                            accumulate(between, x > over ? 0u : W);
+                            n_between += t.in && !(x > over);
                         }
-                    }
-                }
-                if (v == kVec - 1 && last >= 0) {
-                    run = warp_sum(run);
-                    if (lane == 0) sm.above[it * kWarps + warp] = run, above += run;
-                    run = 0;
-                }
-            });
+                    },
+                    [&](int it) {
+                        __syncwarp();
+                        if (__any_sync(~0u, run != 0)) run = warp_sum(run);
+                        if (lane == 0) sm.runs[it * kWarps + warp] = run, above += run;
+                        run = 0;
+                    });
+            }
             u64 mine = n_mine, mine_between = n_between, of_cta, of_between, cta_above = 0, cta_between = 0;
             block_scan(sm, mine, mine_between, of_cta, of_between);
             if (last >= 0) block_scan(sm, above, between, cta_above, cta_between);
@@ -872,62 +828,88 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
                 n += sm.peer[i][0], n_bin += sm.peer[i][1], before += sm.peer[i][2], of_bin += sm.peer[i][3];
             }
             // The list may hold all of them, or those of the last bin if the limit is indeed there.
-            const bool whole = n <= (u64)kList && (last < 0 || before + of_bin >= limit);
-            const bool bin_only = !whole && last >= 0 && n_bin > 0 && n_bin <= (u64)kList && before < limit && before + of_bin >= limit;
+            const bool there = last >= 0 && before < limit && before + of_bin >= limit;
+            const bool whole = n < (u64)kList && (last < 0 || there);
+            const bool bin_only = !whole && there && n_bin < (u64)kList;
             if (whole || bin_only) {
                 // They go to the first CTA's list, each CTA and thread at its place.
                 uint32_t at = ptx::mapa_shared(ptx::smem_u32(sm.list), 0u) + (uint32_t)(whole ? mine : mine_between) * 8u;
-                const float to = whole ? INFINITY : over;
                 if ((whole ? n_mine : n_between) > 0)
                     row.each([&](float x, int it, int v) {
-                        if (x >= bound && x <= to && (whole || weigh(r, x).in)) {
-                            st_cluster_u64(at, (u64)(uint32_t)~ordered(x) << 32 | (uint32_t)row.index_of(it, v));
+                        if (x >= bound && (whole || (!(x > over) && weigh(r, x).in))) {
+                            st_cluster_u64(at, place_of(x, row.index_of(it, v)));
                             at += 8;
                         }
                     });
                 cluster_barrier(r);
             }
+            const u64 lo = place_of(bound, 0) - kIndexMask - 1, hi = place_of(whole ? r.m : fminf(over, r.m), 0);
             if (whole) {
                 if (r.rank != 0) return;
-                if (n <= (u64)kShort) draw_short(sm, row, r, (int)n, cut_k ? top_k : 0, top_p, counted ? total : 0, p, b);
-                else draw_listed(sm, row, r, (int)n, cut_k ? top_k : 0, top_p, counted ? total : 0, p, b);
+                if (n <= 32) draw_few(sm, row, r, (int)n, cut_k ? top_k : 0, top_p, counted ? total : 0, p, b);
+                else draw_listed(sm, row, r, (int)n, lo, hi, cut_k ? top_k : 0, top_p, counted ? total : 0, p, b);
                 return;                            // nobody reads another's shared memory any more
             }
             if (bin_only) {
-                if (r.rank == 0) cut = cut_listed(sm, r, (int)n_bin, before, limit);
-                exchange(sm, r, cut.key, cut.quota, cut.W);
-                cut = Cut{(uint32_t)sm.peer[0][0], (uint32_t)sm.peer[0][2], sm.peer[0][1]};
-                __syncthreads();
-                tally(sm, row, r, cut, ordered(over));
-                draw_all(sm, row, r, cut, p, b);
-                cluster_barrier(r);
-                return;
+                u64 place = 0;
+                if (r.rank == 0) {
+                    weigh_list(sm, r, (int)n_bin, 0ull);
+                    place = search(sm, (int)n_bin, ~0ull, true, limit - before, lo, hi);
+                    // The kept ones join the runs that they are of.
+                    for (int i = tid; i < (int)n_bin; i += kThreads) {
+                        if (sm.list[i] < place) continue;
+                        const int vec = (index_at(sm.list[i]) + row.lead) / kVec, of = vec / row.part;
+                        add_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sm.runs[(vec - of * row.part) / 32]), (uint32_t)of), sm.weight[i]);
+                    }
+                }
+                exchange(sm, r, place);
+                place = sm.peer[0][0];
+                cut.key = (uint32_t)(place >> kIndexBits), cut.last = index_at(place);
+                tallied = true;
             }
         }
-        // The counting path.
-        if (!counted) {
-            u64 mass = 0;
-            uint32_t n = 0;
-            row.each([&](float x, int, int) {
-                const Token t = weigh(r, x);
-                if (t.in) mass += t.W, ++n;
-            });
-            u64 nn = n, tm, tn;
-            block_scan(sm, mass, nn, tm, tn);
-            exchange(sm, r, tm, tn);
-            total = tokens = 0;
-            for (int i = 0; i < r.ranks; ++i) total += sm.peer[i][0], tokens += sm.peer[i][1];
+        if (!tallied) {
+            // The counting path.
+            if (!counted) {
+                u64 mass = 0;
+                uint32_t n = 0;
+                row.each([&](float x, int, int) {
+                    const Token t = weigh(r, x);
+                    if (t.in) accumulate(mass, t.W), ++n;
+                });
+                u64 nn = n, tm, tn;
+                block_scan(sm, mass, nn, tm, tn);
+                exchange(sm, r, tm, tn);
+                total = tokens = 0;
+                for (int i = 0; i < r.ranks; ++i) total += sm.peer[i][0], tokens += sm.peer[i][1];
+            }
+            if (top_k > 0 && (u64)top_k < tokens) {
+                const Narrowed to = narrow(sm, row, r, false, (u64)top_k, cut);
+                cut = to.cut, total = to.mass, r.round = to.round;
+            }
+            if (by_p) {
+                const Narrowed to = narrow(sm, row, r, true, limit_of(top_p, total), cut);
+                cut = to.cut, r.round = to.round;
+            }
         }
-        if (top_k > 0 && (u64)top_k < tokens) {
-            narrow(sm, row, r, false, (u64)top_k, cut);
-            tally(sm, row, r, cut, ~0u);
-            total = cut.quota * cut.W;
-            for (int i = 0; i < r.ranks; ++i) total += sm.peer[i][0];
-        }
-        if (by_p) narrow(sm, row, r, true, limit_of(top_p, total), cut);
     }
-    tally(sm, row, r, cut, ~0u);
-    draw_all(sm, row, r, cut, p, b);
+    if (!tallied) {
+        if (cut.key != 0) {                        // the last kept token of the cut's key
+            const Count equals(cut, true);
+            if (tid == 0) sm.found[2] = 0;
+            tally(sm, row, r, equals);
+            const Found last = locate(sm, row, r, equals, cut.quota, 0.f);
+            ++r.round;
+            if (last.index >= 0) sm.found[2] = (u64)last.index + 1;
+            __syncthreads();
+            exchange(sm, r, sm.found[2]);
+            for (int i = 0; i < r.ranks; ++i)
+                if (sm.peer[i][0] != 0) cut.last = (int)sm.peer[i][0] - 1;
+        }
+        tally(sm, row, r, Count(cut, false));
+    }
+    const Found drawn = locate(sm, row, r, Count(cut, false), 0, p.u[b]);
+    if (drawn.index >= 0) write_token(row, r, drawn.index, drawn.total, p, b);
     cluster_barrier(r);
 }
 
@@ -937,9 +919,10 @@ cudaError_t launch_sample(const SampleArgs &args, cudaStream_t stream) {
     // CTAs of a row: as many as its tokens need, then more while each has over kShare bytes,
     // and for small batches while there are SMs for them and over kSmallShare bytes each.
     // (A step over the cluster costs the same for any share, and rows differ in their work,
-    // so that more and smaller CTAs even out: 256 rows of 128256 floats take 244 us with one
-    // CTA each, 180 with two, 169 with four and 193 with eight; 192 rows of 19439 floats 18.8
-    // us with one and 24.8 with two.)
+    // so that some more CTAs than there is room for even out: 256 rows of 128256 floats take
+    // 178 us with one CTA each, 137 with two, 136 with four and 164 with eight; 192 rows of
+    // 19439 floats 18.3 us with one and 23.4 with two; 64 rows of 128256 bfloat16 53 us with
+    // four and 77 with eight.)
     const int64_t bytes = (int64_t)args.V * (args.dtype == LOWBIT_DTYPE_F32 ? 4 : 2);
     int ranks = 1;
     while (ranks < kMaxCluster && (bytes + 32 > (int64_t)ranks * kThreads * kMaxVecs * 16 || args.V > ranks * kMaxTokens - 16 ||

@@ -555,6 +555,26 @@ def test_sample_draws_follow_the_distribution():
     assert np.all(np.abs(np.bincount(token, minlength=V) - n * p / p.sum()) <= 1.01)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [900, 3000, 50_000])
+def test_sample_many_kept_tokens(V, dtype):
+    """Flat rows: lists of all lengths up to the longest and beyond, with many equal logits."""
+    u = np.random.default_rng([74, V]).random(10)
+    x = make_logits(75, 10, V, dtype, 0.3)
+    check_rows(x, u, 1.0, [33, 100, 400, 880, 0, 0, 500, 0, 0, 31], [1.0, 0.9, 0.5, 0.99, 0.02, 0.3, 1.0, 0.9, 0.999, 0.5],
+               [0.0] * 9 + [0.9])
+
+
+def test_sample_top_p_at_its_ends():
+    """Zero, and what is below it: the first token.  One, and what is above it: all."""
+    x = make_logits(76, 6, 5000, torch.float32)
+    first = [int(i) for i in x.argmax(1)]
+    token, logprob = run_sample(x, [0.99] * 6, 1.0, 0, [0.0, -0.5, -1e30, 1e-38, 1.0, 2.0], 0.0)
+    assert token[:4].tolist() == first[:4] and (logprob[:4] == 0).all()
+    for b in (4, 5):
+        ref.check_sample(ref.f64(x)[b], float(np.float32(0.99)), 1.0, 0, 1.0, 0.0, int(token[b]), float(logprob[b]))
+
+
 def test_sample_row_sizes_in_turn():
     """Large rows, small ones, large ones again: each launch has the shared memory it needs."""
     for V in (90_000, 100, 90_000, 3000, 300_000, 40_000):
