@@ -58,7 +58,7 @@ struct Smem {
     alignas(1024) uint8_t raw[kRaw][kRawBytes];
     float4 exps[kExps][kKeys / 16];              // 2^ke, ve, 2^-ve of each 16 keys
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBuf], v_full[kBuf], kv_empty[kBuf];
-    uint64_t q_full, s_full[2][2], p_full[2][2], o_full, e_full[kExps];
+    uint64_t s_full[2][2], p_full[2][2], o_full, e_full[kExps];
     uint32_t tmem;
     int poisoned;
 };
@@ -110,6 +110,15 @@ __device__ __forceinline__ void commit(uint32_t bar) {
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
         ::"r"(bar) : "memory");
 }
+// 8 bytes from global to shared memory, zeros beyond `bytes`.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -132,7 +141,9 @@ struct Work {
     int split, unit;
     bool live;
     // Whether split s of `splits` has any keys.
-    __device__ bool holds(int s, int splits) const { return (int64_t)steps * s / splits < (int64_t)steps * (s + 1) / splits; }
+    __device__ bool holds(int s, int splits) const { return first_of(s, splits) < first_of(s + 1, splits); }
+    // The first step of split s: at most 2^24 steps, and no more splits than SMs.
+    __device__ int first_of(int s, int splits) const { return splits == 1 ? s * steps : (int)((uint32_t)steps * (uint32_t)s / (uint32_t)splits); }
 };
 
 __device__ __forceinline__ Work work_of(const AttentionArgs &p, const PromptGrid &g, int id) {
@@ -167,8 +178,9 @@ __device__ __forceinline__ Work work_of(const AttentionArgs &p, const PromptGrid
     const int pos_lo = w.first + w.row0 / G, pos_hi = w.first + (min(w.row0 + kRows, w.nrows) - 1) / G;
     const int lo = p.window > 0 ? max(pos_lo - p.window + 1, 0) / kKeys : 0;
     const int n = pos_hi >= 0 ? pos_hi / kKeys + 1 - lo : 0;
-    const int a = (int)((int64_t)n * w.split / g.splits), e = (int)((int64_t)n * (w.split + 1) / g.splits);
-    w.lo = lo + a, w.n = e - a, w.steps = n;
+    w.steps = n;
+    const int a = w.first_of(w.split, g.splits), e = w.first_of(w.split + 1, g.splits);
+    w.lo = lo + a, w.n = e - a;
     return w;
 }
 
@@ -198,11 +210,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(at(sm.p_full[i][0]), 4), ptx::mbar_init(at(sm.p_full[i][1]), 4);
         }
         for (int i = 0; i < kExps; ++i) ptx::mbar_init(at(sm.e_full[i]), 1);
-        ptx::mbar_init(at(sm.q_full), kSoftmaxWarps);
         ptx::mbar_init(at(sm.o_full), 2);
         sm.poisoned = 0;
         ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&kmap);
+        ptx::prefetch_tensormap(&vmap);
     }
+    __syncthreads();
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const Work w = work_of(p, grid, blockIdx.x);
@@ -212,11 +226,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(ptx::smem_u32(&sm.tmem), 512);
         ptx::tmem_relinquish();
     }
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    const uint32_t tmem = sm.tmem;
-    const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 256 + D};
+    // The softmax warps and the issuers meet here when the q tile is there; the first keys are
+    // fetched and turned meanwhile.
+    auto meet = [&] {
+        ptx::tc_fence_before();
+        ptx::named_sync(1, 32 * (kSoftmaxWarps + 2));
+        ptx::tc_fence_after();
+        return sm.tmem;
+    };
     // Steps in which some row of the CTA does not see some key.
     const int pos_lo = w.first + w.row0 / G, pos_hi = w.first + (min(w.row0 + kRows, w.nrows) - 1) / G;
     auto partial = [&](int key0, int keys = kKeys) { return key0 + keys - 1 > pos_lo || (p.window > 0 && key0 <= pos_hi - p.window); };
@@ -232,60 +249,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int low = p.window > 0 ? pos - p.window : -1;    // keys low < key <= pos are seen
         float qs = 0.f;
         if (w.n > 0) {
-            // The warp's rows of q, one at a time over the lanes, as fp16 times a power of two
-            // per row, into the swizzled operand tile.  A negative scale goes into q: the
-            // maximum is taken before scaling.
-            constexpr int E = D / 32;                                  // values of a lane
-            const int r0 = (warp & 3) * 32, rows = min(32, w.nrows - (w.row0 + t * 128 + r0));
-            const int64_t mine = (int64_t)(w.start + token) * p.q_token + head * p.q_head;     // this lane's row
-            const uint32_t base = ptx::smem_u32(sm.q[t]), sign = p.scale_log2 < 0.f ? 0x80000000u : 0u;
-            const uint32_t half = (uint32_t)(lane * E / 64) * 16384u, chunk = (uint32_t)(lane * E / 8) & 7u, in = (uint32_t)(lane * E * 2) & 15u;
-#pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += 16) {
-                uint32_t v[16][E / 2];                                 // all loads of a batch before any is used
+            // The warp's rows of q are copied to their places in the swizzled operand tile, whole
+            // rows at a time, and turned there by a thread each into fp16 times a power of two. A
+            // negative scale goes into q: the maximum is taken before scaling.  (Turned on the way,
+            // a row over the lanes, with a reduction each, they took three times as long.)
+            constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;       // lanes of a row (8 bytes each), rows of a copy
+            const int r0 = (warp & 3) * 32, rows = min(32, w.nrows - (w.row0 + t * 128 + r0)), in = lane % kLanes;
+            const uint16_t *mine = p.q + (int64_t)(w.start + token) * p.q_token + head * p.q_head;     // this lane's row
+            const uint32_t base = ptx::smem_u32(sm.q[t]), to = base + (uint32_t)(in / 16) * 16384u + (in & 1) * 8;
+#pragma unroll 8
+            for (int i = lane / kLanes; i < 32; i += kAtOnce) {
+                const uint16_t *from = reinterpret_cast<const uint16_t *>(__shfl_sync(~0u, reinterpret_cast<uint64_t>(mine), i)) + in * 4;
+                cp_async8(to + (r0 + i) * 128 + (((in >> 1 & 7) ^ (i & 7)) << 4), from, i < rows ? 8 : 0);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            const uint32_t own = base + (r0 + lane) * 128;
+            uint4 x[D / 8];
+            uint32_t top = 0u;                                         // largest finite magnitude, as bf16 bits
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+            for (int c = 0; c < D / 8; ++c) {
+                x[c] = lds_v4(own + (c >> 3) * 16384u + (((c & 7) ^ (lane & 7)) << 4));
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[c].x & 0x7FFF7FFFu, x[c].y & 0x7FFF7FFFu),
+                                             __vmaxu2(x[c].z & 0x7FFF7FFFu, x[c].w & 0x7FFF7FFFu)));
+            }
+            top = max(top & 0xFFFFu, top >> 16);
+            if (top >= 0x7F80u) {
+                top = 0u;
 #pragma unroll
-                    for (int k = 0; k < E / 2; ++k) v[i][k] = 0u;
-                    const int64_t from = __shfl_sync(~0u, mine, i0 + i);
-                    if (i0 + i < rows) {
-                        const uint16_t *q = p.q + from + lane * E;
-                        if constexpr (E == 4) {
-                            const uint2 x = *reinterpret_cast<const uint2 *>(q);
-                            v[i][0] = x.x, v[i][1] = x.y;
-                        } else {
-                            v[i][0] = *reinterpret_cast<const uint32_t *>(q);
-                        }
-                    }
-                }
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint32_t words[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    uint32_t top = 0u;                                 // largest finite magnitude, as bf16 bits
-#pragma unroll
-                    for (int k = 0; k < E / 2; ++k) {
-                        const uint32_t a = v[i][k] & 0x7FFFu, b = v[i][k] >> 16 & 0x7FFFu;
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t a = words[k] & 0x7FFFu, b = words[k] >> 16 & 0x7FFFu;
                         top = max(top, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
                     }
-                    top = __reduce_max_sync(~0u, top);
-                    const int up = query_shift(__uint_as_float(top << 16));
-                    const float f = __uint_as_float(__float_as_uint(exp2_int(up)) | sign);
-                    if (lane == i0 + i) qs = exp2_int(-up) * fabsf(p.scale_log2);
-                    const uint32_t at_q = base + half + (r0 + i0 + i) * 128 + ((chunk ^ (i & 7)) << 4) + in;
-#pragma unroll
-                    for (int k = 0; k < E / 2; ++k) v[i][k] = f32x2_to_f16x2(bf16_lo(v[i][k]) * f, bf16_hi(v[i][k]) * f);
-                    if constexpr (E == 4)
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_q), "r"(v[i][0]), "r"(v[i][1]) : "memory");
-                    else
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at_q), "r"(v[i][0]) : "memory");
                 }
             }
+            const int up = query_shift(__uint_as_float(top << 16));
+            const float f = __uint_as_float(__float_as_uint(exp2_int(up)) | (p.scale_log2 < 0.f ? 0x80000000u : 0u));
+            qs = exp2_int(-up) * fabsf(p.scale_log2);
+            auto turn = [&](uint32_t v) {
+                const float2 y = ptx::fmul2(make_float2(bf16_lo(v), bf16_hi(v)), make_float2(f, f));
+                return f32x2_to_f16x2(y.x, y.y);
+            };
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                sts_v4(own + (c >> 3) * 16384u + (((c & 7) ^ (lane & 7)) << 4), turn(x[c].x), turn(x[c].y), turn(x[c].z), turn(x[c].w));
             ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(at(sm.q_full));
         }
         bool ok = true;
         float m = -INFINITY, l = 0.f;
-        const uint32_t sc = s_col[t] + quarter, oc = o_col[t] + quarter;
+        const uint32_t tmem = meet(), sc = tmem + t * 128 + quarter, oc = tmem + 256 + t * D + quarter;
         for (int hs = 0; hs < 2 * w.n; ++hs) {                          // half-steps of 64 keys
             const int j = hs >> 1, h = hs & 1, key0 = (w.lo + j) * kKeys + h * kHalf;
             if (h == 0 && ok) ok = ptx::mbar_wait(at(sm.e_full[j % kExps]), (j / kExps) & 1, &g_prompt_timeouts);
@@ -536,18 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         look(0);
-        look_exps();
         for (int j = 0; j < w.n && ok; ++j) {
-            if ((j & 3) == 0) {
-                page = next, ke = min(max(nke, kExpMin), kExpMax), ve = min(max(nve, kExpMin), kExpMax);
-                look(j + 4);
-            } else if ((j & 3) == 2) {
-                look_exps();
-            }
-            // Steps back to j - kExps have long been weighed: K of step j - 2 is released after them.
-            if ((lane >> 3) == (j & 3)) sm.exps[j % kExps][lane & 7] = make_float4(exp2_int(ke), (float)ve, exp2_int(-ve), 0.f);
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(at(sm.e_full[j % kExps]));
+            if ((j & 3) == 0) page = next;
             for (int i = 0; i < 2 * (kKeys / kUnit) && ok; ++i, ++unit) {
                 const int u = i % (kKeys / kUnit), st = unit % kRaw;
                 if (unit >= kRaw)
@@ -565,6 +570,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      ((w.lo + j) * kKeys + key) & (P - 1), w.h, id, bar);
                 __syncwarp();
             }
+            if (j == 0 || (j & 3) == 2) look_exps();
+            if ((j & 3) == 0) {
+                ke = min(max(nke, kExpMin), kExpMax), ve = min(max(nve, kExpMin), kExpMax);
+                look(j + 4);
+            }
+            // Steps back to j - kExps have long been weighed: K of step j - 2 is released after them.
+            if ((lane >> 3) == (j & 3)) sm.exps[j % kExps][lane & 7] = make_float4(exp2_int(ke), (float)ve, exp2_int(-ve), 0.f);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(at(sm.e_full[j % kExps]));
         }
         for (int i = max(0, unit - kRaw); i < unit; ++i)
             if (!ptx::mbar_wait(at(sm.raw_full[i % kRaw]), (i / kRaw) & 1, &g_prompt_timeouts)) break;
@@ -576,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint64_t kTileStep = Smem<D>::kTile >> 4;
         const uint64_t qd = ptx::sw128_desc(ptx::smem_u32(sm.q)) + (uint64_t)t * kTileStep;
         const uint64_t kd0 = ptx::sw128_desc(ptx::smem_u32(sm.k)), vd0 = sw128_mn_desc(ptx::smem_u32(sm.v), 16384);
-        const uint32_t sd = tmem + t * 128, od = tmem + 256 + t * D;
+        const uint32_t tmem = meet(), sd = tmem + t * 128, od = tmem + 256 + t * D;
         bool ok = w.n > 0;
         auto wait = [&](const uint64_t &bar, int parity) {
             if (ok) ok = ptx::mbar_wait(at(bar), (uint32_t)parity, &g_prompt_timeouts);
@@ -589,7 +603,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_ss(sd + h * kHalf, qd + off, kd + off, qk, k > 0);
             }
         };
-        wait(sm.q_full, 0);
         wait(sm.k_full[0], 0);
         if (__all_sync(~0u, ok)) {
             ptx::tc_fence_after();
@@ -633,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == kIssuer) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc(sm.tmem, 512);
     }
 }
 
