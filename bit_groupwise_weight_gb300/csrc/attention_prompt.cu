@@ -10,8 +10,9 @@
 // Work split.  A CTA takes 256 rows (new tokens x heads of a group) of one sequence
 // and kv head, as two 128-row tiles whose softmax and products alternate: while one
 // tile's weights are computed, the other's products run.  Keys come 128 at a time.
-// When there are fewer CTAs than SMs the keys are split between several, and a
-// second launch joins their parts.  Tiles with the most keys start first.
+// Where CTAs are few or some sequences far longer than others, the keys of the tiles are
+// split between several, and a second launch joins their parts (find_listed, prompt_grid).
+// Tiles with the most keys start first.
 //
 // Tensor memory (512 columns): S of both tiles (128 fp32 columns each, as two halves of
 // 64 keys; the fp16 weights P take the place of the half they come from), O of both.
@@ -22,9 +23,13 @@
 // e4m3 codes into fp16 operand tiles (once per 256 rows), 12 TMA producer, 13 and 14 MMA
 // issuers, one for each tile, so that neither waits for the other's weights.  Order of an
 // issuer, half-step by half-step: PV(h) QK(h + 2), products of one issuer running in order.
-// Bound: the tensor cores, 4 D flops per row and key; at 128 x 128 x 128 a product
-// takes 512 cycles, and 256 rows x 128 keys 2048; their exponentials 32768 / 16-32
-// per cycle and SM.
+// Bound: shared memory, nearly.  256 rows x 128 keys at D = 128 take the tensor cores 2048
+// cycles, the exponentials as many, and shared memory about 3070: 1536 for the operands of
+// QK (q is read again for every half; both halves in one product read it once, 2560 in all,
+// but leave the weights waiting: 152 us against 132), 512 for V, 1024 to bring in, turn and
+// store the codes.  A step takes 3100; a CTA beside its steps about 15000 (its queries and
+// first keys 8000, its last product and result 6000).  4096 tokens, 32 heads of 128 over 8:
+// 124 us, 1.1 PFLOP/s (0.58 of the rate of a library product).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -45,6 +50,12 @@ constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kProducer = 12, kIssuer = 13;      // and 14
 constexpr int kThreads = 16 * 32;              // whole warpgroups, for the register split
 constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kOtherRegs = 64;   // 2 x 184 + 80 + 64 = 4 x 128
+constexpr int kMinSteps = 2;                     // of a part
+constexpr int kShortSteps = 8;                   // of sequences whose tiles are never split
+constexpr float kCtaCost = 5.f;                   // what a CTA costs beside its steps, in steps
+constexpr float kJoinCost = 0.03f;               // what a part costs when it is joined
+constexpr int kMostCtas = 5 * kSms;              // where keys may be split
+constexpr int kLongSteps = 32;                   // of sequences whose tiles are split although they fill the SMs
 constexpr float kLag = 8.f;
 
 __device__ unsigned int g_prompt_timeouts;
@@ -137,58 +148,142 @@ __device__ __forceinline__ void fewer_registers() {
 struct Work {
     int b, h, row0, nrows, start, first, len;    // rows row0 .. of nrows; first: position of the first new token
     int lo, n;                                   // first step of 128 keys, and how many
-    int steps;                                   // of all splits together
-    int split, unit;
+    int part, parts, slot;                       // this part of how many of the row tile's keys; the first one's place
+    int steps;                                   // of all parts together
     bool live;
-    // Whether split s of `splits` has any keys.
-    __device__ bool holds(int s, int splits) const { return first_of(s, splits) < first_of(s + 1, splits); }
-    // The first step of split s: at most 2^24 steps, and no more splits than SMs.
-    __device__ int first_of(int s, int splits) const { return splits == 1 ? s * steps : (int)((uint32_t)steps * (uint32_t)s / (uint32_t)splits); }
+    // The first step of a part: at most 2^24 steps, and no more parts than SMs.
+    __device__ int first_of(int i) const { return (int)((uint32_t)steps * (uint32_t)i / (uint32_t)parts); }
 };
 
-__device__ __forceinline__ Work work_of(const AttentionArgs &p, const PromptGrid &g, int id) {
+// The steps of row tile t of a sequence: how many, and the first.
+__device__ __forceinline__ int steps_of(const AttentionArgs &p, const Span &s, int t, int &lo) {
+    const int first = s.len - s.n, pos_lo = first + t * kRows / p.G, pos_hi = first + (min((t + 1) * kRows, s.n * p.G) - 1) / p.G;
+    lo = p.window > 0 ? max(pos_lo - p.window + 1, 0) / kKeys : 0;
+    return pos_hi >= 0 ? pos_hi / kKeys + 1 - lo : 0;
+}
+
+// Where the keys may be split, the parts of all sequences' tiles form one list.  With
+// `all` the steps of all tiles and `most` those of the longest, there are u = all / most
+// tiles' worth of work; cut into q parts each, it goes through the SMs in ceil(u q / SMs)
+// rounds of most / q steps and what a CTA costs beside them.  The best of 1 and the q
+// that fill one to four rounds gives the length of a part; sequences with fewer keys have fewer.
+// Finds the index'th part (or tile, if not by_part) of the list.  (Rounded operations
+// throughout: the join has to come to the same parts.)
+struct Listed { int b, tiles, parts, rest, before; };       // rest: index in the sequence; before: parts of earlier ones
+__device__ __forceinline__ Listed find_listed(const AttentionArgs &p, const PromptGrid &g, int index, bool by_part) {
+    const int lane = threadIdx.x & 31;
+    auto tiles_of = [&](const Span &s) { return s.n * p.G > p.few_rows ? (s.n * p.G + kRows - 1) / kRows : 0; };
+    float all = 0.f;
+    int most = 1, tiles = 0, steps = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const Span s = span(p, b);
+        int lo;
+        tiles = tiles_of(s), steps = tiles > 0 ? steps_of(p, s, tiles - 1, lo) : 0;
+        if (tiles > 0) all = __fadd_rn(all, __fmul_rn((float)tiles * 0.5f, (float)(steps_of(p, s, 0, lo) + steps)));
+        most = max(most, steps);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all = __fadd_rn(all, __shfl_xor_sync(~0u, all, o));
+    most = __reduce_max_sync(~0u, most);
+    const float u = fmaxf(__fdiv_rn(__fmul_rn(all, (float)p.Hk), (float)most), 1e-3f);
+    float least = INFINITY;
+    int length = most;
+#pragma unroll
+    for (int r = 0; r <= 4; ++r) {                                    // 0: whole tiles
+        const float q = floorf(fminf(fmaxf(__fdiv_rn((float)(kSms * r), u), 1.f), (float)g.splits));
+        const float rounds = fmaxf(ceilf(__fadd_rn(__fmul_rn(__fmul_rn(u, q), 1.f / kSms), -0.01f)), 1.f);
+        const float each = ceilf(__fdiv_rn((float)most, q));
+        float cost = __fmul_rn(rounds, __fadd_rn(each, kCtaCost));
+        if (q > 1.f) cost = __fadd_rn(cost, __fmul_rn(__fmul_rn(u, q), kJoinCost));
+        if (cost < least) least = cost, length = (int)each;
+    }
+    length = max(length, kMinSteps);
+    Listed at{0, 0, 1, -1, 0};
+    for (int b0 = 0; b0 < p.B && at.rest < 0; b0 += 32) {
+        if (p.B > 32) {
+            tiles = steps = 0;
+            if (b0 + lane < p.B) {
+                const Span s = span(p, b0 + lane);
+                int lo;
+                tiles = tiles_of(s), steps = tiles > 0 ? steps_of(p, s, tiles - 1, lo) : 0;
+            }
+        }
+        const int parts = max(min((steps + length - 1) / length, g.splits), 1), count = tiles * p.Hk;
+        int listed = count * parts, found = by_part ? listed : count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int l = __shfl_up_sync(~0u, listed, o), f = __shfl_up_sync(~0u, found, o);
+            if (lane >= o) listed += l, found += f;
+        }
+        const uint32_t hit = __ballot_sync(~0u, index < found);
+        if (hit != 0) {
+            const int l = __ffs(hit) - 1;
+            at.b = b0 + l;
+            at.tiles = __shfl_sync(~0u, tiles, l), at.parts = __shfl_sync(~0u, parts, l);
+            at.rest = index - __shfl_sync(~0u, found - (by_part ? count * parts : count), l);
+            at.before += __shfl_sync(~0u, listed - count * parts, l);
+        } else {
+            index -= __shfl_sync(~0u, found, 31);
+            at.before += __shfl_sync(~0u, listed, 31);
+        }
+    }
+    // From lane 0, so that the work is uniform for the compiler too.
+    at.b = __shfl_sync(~0u, at.b, 0), at.tiles = __shfl_sync(~0u, at.tiles, 0), at.parts = __shfl_sync(~0u, at.parts, 0);
+    at.rest = __shfl_sync(~0u, at.rest, 0), at.before = __shfl_sync(~0u, at.before, 0);
+    return at;
+}
+
+// The work of a CTA, or (not by_part) of the tile-th tile for the join.
+__device__ __forceinline__ Work work_of(const AttentionArgs &p, const PromptGrid &g, int id, bool by_part) {
     Work w{};
     const int G = p.G;
-    // Ids count down over the row tiles, so that tiles with the most keys start first.
-    w.split = id % g.splits;
-    w.unit = id / g.splits;
-    w.h = w.unit % p.Hk;
-    const int tile = g.tiles - 1 - w.unit / p.Hk;
     int b, t;
-    if (p.cu_q == nullptr) {
-        const int per = g.tiles / p.B;
-        b = tile % p.B, t = tile / p.B;
-        if (t >= per) return w;
+    w.parts = 1;
+    if (g.splits > 1) {
+        const Listed at = find_listed(p, g, id, by_part);
+        if (at.rest < 0) return w;
+        const int tile = by_part ? at.rest / at.parts : at.rest;
+        w.part = by_part ? at.rest - tile * at.parts : 0;
+        w.parts = at.parts, w.slot = at.before + tile * at.parts;
+        b = at.b, t = at.tiles - 1 - tile / p.Hk, w.h = tile % p.Hk;
     } else {
-        // Sequence b owns the tiles from cu_q[b] G / 256 + b on: enough for its rows.
-        auto base = [&](int i) { return (int)((int64_t)min(max(p.cu_q[i], 0), p.T) * G / kRows) + i; };
-        int lo = 0, hi = p.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (base(mid) <= tile) lo = mid;
-            else hi = mid - 1;
+        // Ids count down over the row tiles, so that tiles with the most keys start first.
+        w.h = id % p.Hk;
+        const int tile = g.tiles - 1 - id / p.Hk;
+        if (p.cu_q == nullptr) {
+            const int per = g.tiles / p.B;
+            b = tile % p.B, t = tile / p.B;
+            if (t >= per) return w;
+        } else {
+            // Sequence b owns the tiles from cu_q[b] G / 256 + b on: enough for its rows.
+            auto base = [&](int i) { return (int)((int64_t)min(max(p.cu_q[i], 0), p.T) * G / kRows) + i; };
+            int lo = 0, hi = p.B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (base(mid) <= tile) lo = mid;
+                else hi = mid - 1;
+            }
+            b = lo, t = tile - base(lo);
         }
-        b = lo, t = tile - base(lo);
     }
     const Span s = span(p, b);
     w.b = b, w.start = s.start, w.len = s.len, w.first = s.len - s.n;
     w.nrows = s.n * G, w.row0 = t * kRows;
     w.live = t >= 0 && w.row0 < w.nrows && w.nrows > p.few_rows;
     if (!w.live) return w;
-    const int pos_lo = w.first + w.row0 / G, pos_hi = w.first + (min(w.row0 + kRows, w.nrows) - 1) / G;
-    const int lo = p.window > 0 ? max(pos_lo - p.window + 1, 0) / kKeys : 0;
-    const int n = pos_hi >= 0 ? pos_hi / kKeys + 1 - lo : 0;
-    w.steps = n;
-    const int a = w.first_of(w.split, g.splits), e = w.first_of(w.split + 1, g.splits);
-    w.lo = lo + a, w.n = e - a;
+    int lo;
+    const uint32_t n = (uint32_t)steps_of(p, s, t, lo);
+    w.steps = (int)n;
+    w.lo = lo, w.n = (int)n;
+    if (w.parts > 1) w.lo += w.first_of(w.part), w.n = w.first_of(w.part + 1) - w.first_of(w.part);
     return w;
 }
 
-// Workspace of a (unit, split): D / 4 groups of four sums of each of the 256 rows, then
+// Workspace of a part: D / 4 groups of four sums of each of the 256 rows, then
 // the rows' (m, l) pairs.
 template <int D>
-__device__ __forceinline__ float *part_of(const AttentionArgs &p, const PromptGrid &g, int unit, int split) {
-    return p.workspace + g.workspace + ((int64_t)unit * g.splits + split) * (kRows * (D + 2));
+__device__ __forceinline__ float *part_of(const AttentionArgs &p, const PromptGrid &g, int slot) {
+    return p.workspace + g.workspace + (int64_t)slot * (kRows * (D + 2));
 }
 
 template <int D>
@@ -219,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const Work w = work_of(p, grid, blockIdx.x);
-    if (!w.live || (w.n == 0 && grid.splits > 1)) return;      // the join leaves empty parts out too
+    const Work w = work_of(p, grid, blockIdx.x, true);
+    if (!w.live || (w.n == 0 && w.parts > 1)) return;          // the join leaves empty parts out too
     const int G = p.Hq / p.Hk, P = p.P;
     if (warp == kIssuer) {
         ptx::tmem_alloc(ptx::smem_u32(&sm.tmem), 512);
@@ -406,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Rows go out by way of shared memory (the q tile's place: its products are done), so
         // that stores cover whole rows; parts for the join go out value by value, a layout in
         // which the lanes' rows are neighbours.
-        float4 *part = grid.splits > 1 ? reinterpret_cast<float4 *>(part_of<D>(p, grid, w.unit, w.split)) + r : nullptr;
+        float4 *part = w.parts > 1 ? reinterpret_cast<float4 *>(part_of<D>(p, grid, w.slot + w.part)) + r : nullptr;
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         const int lr = r & 127;
         const uint32_t stage = ptx::smem_u32(sm.q[t]) + lr * (D * 2);
@@ -455,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (live) {
             if (part != nullptr)
-                *reinterpret_cast<float2 *>(part_of<D>(p, grid, w.unit, w.split) + kRows * D + 2 * r) = make_float2(m, l);
+                *reinterpret_cast<float2 *>(part_of<D>(p, grid, w.slot + w.part) + kRows * D + 2 * r) = make_float2(m, l);
             else if (p.lse != nullptr)
                 p.lse[(w.start + token) * p.lse_token + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
         }
@@ -656,18 +751,19 @@ template <int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const AttentionArgs p, const PromptGrid grid) {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const Work w = work_of(p, grid, blockIdx.x * grid.splits);
+    const Work w = work_of(p, grid, blockIdx.x, false);
     const int r = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5, row = w.row0 + r;
-    if (!w.live || row >= w.nrows) return;
+    if (!w.live || w.parts == 1 || row >= w.nrows) return;
+    if (w.slot + w.parts > (int)gridDim.x * grid.splits) return;     // cu_q that does not rise
     const int i = row / p.G, token = w.start + i, head = w.h * p.G + row - i * p.G;
     constexpr int kGroups = D / 4 / 8;
     float m = -INFINITY, l = 0.f;
     float4 o[kGroups];
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < grid.splits; ++s) {
-        if (!w.holds(s, grid.splits)) continue;                    // no keys: nothing was written
-        const float *part = part_of<D>(p, grid, w.unit, s);
+    for (int s = 0; s < w.parts; ++s) {
+        if (w.first_of(s) == w.first_of(s + 1)) continue;          // no keys: nothing was written
+        const float *part = part_of<D>(p, grid, w.slot + s);
         const float2 ml = *reinterpret_cast<const float2 *>(part + kRows * D + 2 * r);
         const float mx = fmaxf(m, ml.x), ref = mx == -INFINITY ? 0.f : mx;
         const float a = ex2(m - ref), b = ex2(ml.x - ref);
@@ -713,9 +809,15 @@ PromptGrid prompt_grid(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk
     const int G = Hq / Hk;
     PromptGrid g{};
     g.tiles = uniform ? B * (int)(((int64_t)max_q * G + kRows - 1) / kRows) : (int)(T * G / kRows) + B;
-    // Keys are split only while CTAs are fewer than SMs, into no less than two steps each.
-    const int64_t steps = std::max<int64_t>(1, max_len / (2 * kKeys));
-    g.splits = (int)std::min<int64_t>(steps, std::max(1, kSms / std::max(1, g.tiles * Hk)));
+    // The most parts that find_listed may choose.  Where splitting is in question, the list
+    // and the join's launch cost 5-7 us (two prompts of 256 tokens: 18.9 us without, 25.3
+    // with), and CTAs without a part 1.5 us each on their SM (4096 tokens, 512 tiles: 124 us
+    // against 150 with as many such); what it gains: 701 tokens behind 8300 beside three short
+    // prompts 127 -> 117 us, two of 512 behind 15500 (one shorter) 217 -> 135, eight of 100
+    // behind up to 5900 100 -> 65.
+    const int64_t units = std::max<int64_t>(1, (int64_t)g.tiles * Hk), steps = (max_len + kKeys - 1) / kKeys;
+    g.splits = steps < kShortSteps || (units >= kSms * 3 / 4 && steps < kLongSteps) ? 1
+               : (int)std::max<int64_t>(1, std::min(std::min<int64_t>(steps / kMinSteps, kSms), kMostCtas / units));
     return g;
 }
 

@@ -83,6 +83,23 @@ def test_ragged_prompts_and_single_tokens_together(heads, kv_heads, dim):
     check_attention(b, queries(6, sum(news), heads, dim))
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 128), (16, 2, 64)])
+@pytest.mark.parametrize("window", [0, 700])
+def test_prompts_behind_lengths_far_apart(heads, kv_heads, dim, window):
+    """Some tiles' keys are split between CTAs, others' are not, some sequences have none."""
+    lens, news = [5000, 90, 0, 2100, 1300, 300], [100, 90, 0, 70, 1, 300]
+    b = ref.make_batch(80, lens, news, kv_heads, dim, 64)
+    check_attention(b, queries(81, sum(news), heads, dim), window=window)
+
+
+def test_prompts_of_many_sequences():
+    """More sequences than lanes, a few of them long."""
+    lens = [20 + 3 * i for i in range(40)] + [3000, 0, 1500]
+    news = [20] * 40 + [33, 0, 21]
+    b = ref.make_batch(82, lens, news, 1, 64, 32)
+    check_attention(b, queries(83, sum(news), 4, 64))
+
+
 @pytest.mark.parametrize("window", [1, 2, 17, 64, 100, 1000])
 @pytest.mark.parametrize("n", [1, 7, 150])
 @pytest.mark.parametrize("dim", [64, 128])
