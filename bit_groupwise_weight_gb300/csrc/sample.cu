@@ -134,6 +134,21 @@ struct Row {
         if constexpr (DTYPE == LOWBIT_DTYPE_BF16) return __uint_as_float((uint32_t)h << 16);
         return half_bits_to_float(h);
     }
+    // The largest of a vector's values; NaN are left out.
+    __device__ __forceinline__ static float largest(const uint4 &w) {
+        if constexpr (DTYPE == LOWBIT_DTYPE_F32) {
+            return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+        } else {
+            const uint32_t a = larger2(larger2(w.x, w.y), larger2(w.z, w.w));
+            return fmaxf(get(make_uint4(a, 0u, 0u, 0u), 0), get(make_uint4(a, 0u, 0u, 0u), 1));
+        }
+    }
+    __device__ __forceinline__ static uint32_t larger2(uint32_t a, uint32_t b) {
+        uint32_t d;
+        if constexpr (DTYPE == LOWBIT_DTYPE_BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        else asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
     __device__ __forceinline__ int vec_of(int it) const { return first + it * kThreads + (int)threadIdx.x; }
     __device__ __forceinline__ int index_of(int it, int v) const { return vec_of(it) * kVec + v - lead; }
     // Vector `it` of this thread; what is not of the row is -infinity.
@@ -162,10 +177,16 @@ struct Row {
         }
         return make_uint4(a[0], a[1], a[2], a[3]);
     }
-    // Fills `held`.
-    __device__ __forceinline__ void hold() {
+    // Fills `held`; the thread's largest value.
+    __device__ __forceinline__ float hold() {
+        float top = -INFINITY;
 #pragma unroll 4
-        for (int it = 0; it < min(nvec, kHeld); ++it) held[it * kThreads] = load(it);
+        for (int it = 0; it < nvec; ++it) {
+            const uint4 w = load(it);
+            if (it < kHeld) held[it * kThreads] = w;
+            top = fmaxf(top, largest(w));
+        }
+        return top;
     }
     // f(x, it, v) for each token; after a vector the whole warp comes to done(it).
     template <typename F, typename G>
@@ -643,16 +664,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         row.nvec = (row.part + kThreads - 1) / kThreads;
     }
     row.held = reinterpret_cast<uint4 *>(raw + sizeof(Shared)) + tid;
-    row.hold();
+    const float own = row.hold();                  // NaN left out
     r.T = p.temperature != nullptr ? p.temperature[b] : p.temperature_all;
     const float top_p = fmaxf(p.top_p != nullptr ? p.top_p[b] : p.top_p_all, 0.f);
     const float min_p = p.min_p != nullptr ? p.min_p[b] : p.min_p_all;
     const int top_k = p.top_k != nullptr ? p.top_k[b] : p.top_k_all;
     const bool greedy = !(r.T > 0.f);
 
-    // The largest logit of the thread, the CTA and the row.
-    float own = -INFINITY;                         // fmaxf leaves NaN out
-    row.each([&](float x, int, int) { own = fmaxf(own, x); });
+    // The largest logit of the CTA and the row.
     {
         const uint32_t k = __reduce_max_sync(~0u, ordered(own));
         if (lane == 0) sm.red[warp][0] = k;
@@ -741,16 +760,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         uint32_t n = 0;
         row.each([&](float x, int, int) {
             const Token t = weigh(r, x);
-            if (t.in) {
-                accumulate(mass, t.W), ++n;
-                if (x >= above) {
-                    // floor(-s per) by adding 1.5 2^23 (a conversion would take eight times as long).
-                    const int at = (int)min(__float_as_uint(__fadd_rn(fmaf(-t.s, per, -0.5f), 12582912.f)) - 0x4B400000u,
-                                            (uint32_t)kCoarse - 1u);
-                    // The product's integer, by adding 2^23.
-                    atomicAdd(&sm.coarse[at], __float_as_uint(fmaf(t.w, __uint_as_float(scale_bits(at, drop)), 8388608.f)) - 0x4B000000u);
-                }
-            }
+            accumulate(mass, t.in ? t.W : 0u);
+            n += t.in;
+            // The bin, floor(-s per), by adding 1.5 2^23 (a conversion would take eight times as
+            // long); the weight at the bin's scale, by adding 2^23.
+            const int at = (int)min(__float_as_uint(__fadd_rn(fmaf(-t.s, per, -0.5f), 12582912.f)) - 0x4B400000u, (uint32_t)kCoarse - 1u);
+            const uint32_t add = __float_as_uint(fmaf(t.w, __uint_as_float(scale_bits(at, drop)), 8388608.f)) - 0x4B000000u;
+            if (t.in && x >= above) atomicAdd(&sm.coarse[at], add);
         });
         u64 nn = n, tm, tn;
         block_scan(sm, mass, nn, tm, tn);
