@@ -761,15 +761,16 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const AttentionArgs p,
     float4 o[kGroups];
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int s = 0; s < w.parts; ++s) {
-        if (w.first_of(s) == w.first_of(s + 1)) continue;          // no keys: nothing was written
+        const bool any = w.first_of(s) != w.first_of(s + 1);       // without keys nothing was written
         const float *part = part_of<D>(p, grid, w.slot + s);
-        const float2 ml = *reinterpret_cast<const float2 *>(part + kRows * D + 2 * r);
+        const float2 ml = any ? __ldcs(reinterpret_cast<const float2 *>(part + kRows * D + 2 * r)) : make_float2(-INFINITY, 0.f);
         const float mx = fmaxf(m, ml.x), ref = mx == -INFINITY ? 0.f : mx;
         const float a = ex2(m - ref), b = ex2(ml.x - ref);
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
-            const float4 v = reinterpret_cast<const float4 *>(part)[(warp + 8 * k) * kRows + r];
+            const float4 v = any ? __ldcs(reinterpret_cast<const float4 *>(part) + (warp + 8 * k) * kRows + r) : make_float4(0.f, 0.f, 0.f, 0.f);
             o[k].x = o[k].x * a + v.x * b, o[k].y = o[k].y * a + v.y * b;
             o[k].z = o[k].z * a + v.z * b, o[k].w = o[k].w * a + v.w * b;
         }
