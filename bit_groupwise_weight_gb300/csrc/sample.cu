@@ -796,17 +796,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
                 of_bin[q] = of_bin[q] << 30 >> ((scale_bits(at, drop) >> 23) - 127);
                 sum += of_bin[q];
             }
-            if (tid == 0) sm.found[0] = kCoarse;
+            if (tid == 0) sm.found[0] = sm.found[1] = kCoarse;
             block_scan(sm, sum, z, tm, tz);
+            // The bins in which the limit may lie for what rounding may have moved it: one and the
+            // same for all but one row in some hundreds, which took the counting path otherwise.
+            const u64 from = limit - (limit >> 15), to = max(min(limit + (limit >> 15), tm), limit);
 #pragma unroll
             for (int q = 0; q < kCoarse / kThreads; ++q) {
-                if (sum < limit && sum + of_bin[q] >= limit) sm.found[0] = (u64)(tid * (kCoarse / kThreads) + q);
-                sum += of_bin[q];
+                const u64 upto = sum + of_bin[q];
+                if (sum < from && upto >= from) sm.found[0] = (u64)(tid * (kCoarse / kThreads) + q);
+                if (sum < to && upto >= to) sm.found[1] = (u64)(tid * (kCoarse / kThreads) + q);
+                sum = upto;
             }
             __syncthreads();
-            last = (int)sm.found[0];
+            last = (int)sm.found[1];
             bound = fmaxf(bound, r.m - ((float)(last + 1) / per + 1e-3f) * r.T - fabsf(r.m) * 1e-6f);
-            over = r.m - ((float)last / per - 1e-3f) * r.T + fabsf(r.m) * 1e-6f;      // above: an earlier bin
+            over = r.m - ((float)(int)sm.found[0] / per - 1e-3f) * r.T + fabsf(r.m) * 1e-6f;      // above: an earlier bin
         }
         if (listing) {
             // How many tokens there are from the bound on, and between it and `over`; the mass
