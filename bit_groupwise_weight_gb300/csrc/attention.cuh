@@ -34,19 +34,23 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Where a sequence's new tokens lie, and its length with them.
+// Where a sequence's new tokens lie, and its length with them.  Of tokens past max_q, which are
+// left out, neither n nor len counts any: the first one stands at len - n either way.
 struct Span { int start, n, len; };
 
 __device__ __forceinline__ Span span(const AttentionArgs &p, int b) {
     Span s;
+    int over = 0;
     if (p.cu_q == nullptr) {
         s.n = p.n;
         s.start = b * s.n;
     } else {
         s.start = min(max(p.cu_q[b], 0), p.T);
-        s.n = min(max(min(p.cu_q[b + 1], p.T) - s.start, 0), p.max_q);
+        const int all = max(min(p.cu_q[b + 1], p.T) - s.start, 0);
+        s.n = min(all, p.max_q);
+        over = all - s.n;
     }
-    s.len = min(max(p.lens[b], 0), p.width * p.P);
+    s.len = min(max(p.lens[b], 0), p.width * p.P) - over;     // below 0: all before position 0
     return s;
 }
 

@@ -49,17 +49,21 @@ enum Kind { kKey, kValue, kQuery };
 
 struct Seq { int start, n, len; };
 
-// Where a sequence's new tokens lie in q, k and v, and its length with them.
+// Where a sequence's new tokens lie in q, k and v, and its length with them.  Of tokens past
+// max_q, which are left out, neither n nor len counts any: the first one stands at len - n.
 __device__ __forceinline__ Seq sequence(const AppendArgs &p, int b) {
     Seq s;
+    int over = 0;
     if (p.cu_q == nullptr) {
         s.n = p.n;
         s.start = b * s.n;
     } else {
         s.start = min(max(p.cu_q[b], 0), p.T);
-        s.n = min(max(min(p.cu_q[b + 1], p.T) - s.start, 0), p.max_q);
+        const int all = max(min(p.cu_q[b + 1], p.T) - s.start, 0);
+        s.n = min(all, p.max_q);
+        over = all - s.n;
     }
-    s.len = max(p.lens[b], 0);
+    s.len = max(p.lens[b], 0) - over;
     return s;
 }
 

@@ -250,7 +250,8 @@ typedef struct {
     int32_t width;              /* columns of page_table: lengths are at most width * page  */
     int32_t batch, tokens;
     int32_t max_q;              /* bound of a sequence's new tokens (cu_q given); tokens past
-                                   it are left out                                         */
+                                   it are left out: no output of theirs is written, and the
+                                   tokens before them keep their positions                 */
 } lowbit_sequences;
 
 /* Rotary positions on q and k, and k and v into the cache, in one launch.
