@@ -319,7 +319,10 @@ lowbit_status lowbit_attention(const lowbit_attention_args *a, const lowbit_cach
     p.page_stride = c->page_stride, p.head_stride = c->head_stride, p.table_stride = s->table_stride;
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.T = s->tokens, p.B = s->batch, p.max_q = s->max_q, p.Hq = a->heads, p.Hk = c->kv_heads;
-    p.D = c->head_dim, p.P = c->page, p.pages = c->pages, p.width = s->width, p.window = a->window;
+    p.D = c->head_dim, p.P = c->page, p.pages = c->pages, p.width = s->width;
+    // A window of all positions hides nothing, and smaller ones keep positions less windows inside int32,
+    // also those of rows before position 0.
+    p.window = (int64_t)a->window >= (int64_t)s->width * c->page ? 0 : a->window;
     return from_cuda(lowbit::launch_attention(p, (cudaStream_t)stream));
 }
 

@@ -35,7 +35,8 @@ def attend(b, q, scale=None, window=0, max_q=None):
 
 
 def close(got, want, bound):
-    bad = ~(np.abs(got - want) <= bound)
+    with np.errstate(invalid="ignore"):
+        bad = ~(np.abs(got - want) <= bound)
     bad &= ~((got == want) | (np.isnan(got) & np.isnan(want)))
     assert not bad.any(), f"{bad.sum()} of {bad.size}, first {np.argwhere(bad)[0].tolist()}: {got[bad][0]} for {want[bad][0]}"
 
@@ -82,3 +83,19 @@ def test_append_leaves_tokens_past_max_q_out(page, news, lens, max_q):
                               [m - n + f for m, n, f in zip(lens, news, fewer)], max_q)
     assert torch.equal(out[kept], want) and (out[~kept] == 7).all()
     assert all(torch.equal(c, w) for c, w in zip(cache, want_cache))
+
+
+# ---------------------------------------------------------------------------
+# Windows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens,news", [([5, 40, 0], [10, 10, 10]), ([60, 300, 3], [200, 200, 200]), ([40, 2000], [400, 333])])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 7, 1 << 30])
+def test_largest_windows_hide_nothing(lens, news, window):
+    """As no window, also for rows before position 0."""
+    b = ref.make_batch(104, lens, news, 2, 64, 32)
+    q = queries(105, sum(news), 4, 64)
+    want, want_lse, bound, lse_bound = ref.attention(ref.f64(q), b, 0.125, 0)
+    out, lse = attend(b, q, window=window)
+    close(out, want, bound)
+    close(lse, want_lse, lse_bound)
