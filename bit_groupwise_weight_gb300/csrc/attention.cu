@@ -13,10 +13,9 @@
 // exponent, so that one weight serves the product:
 //     w_t = 2^(s_t + ve(t) - m),  O += fp16(w_t) Vc_t,  l += w_t 2^-ve(t),
 //     out = O / l,  lse = ln2 (m + log2 l),
-// m following the maximum of s_t + ve(t) when that has grown past m + kLag: w stays
-// below 2^kLag, where fp16 holds it to 2^-11 of itself (2^-25 absolute below 2^-14),
-// and most steps need neither a reduction over the warp nor a rescaling.  m, l, O
-// are fp32.  q is multiplied by a power of two per row that puts its largest value
+// m following the maximum of s_t + ve(t) when that has outgrown it (attention.cuh): fp16
+// holds w to 2^-11 of itself, or to 2^-32 of the row's largest where that is more, and
+// most steps need neither a reduction over the warp nor a rescaling.  m, l, O are fp32.  q is multiplied by a power of two per row that puts its largest value
 // into [2^10, 2^11): its 8 significant bits fit fp16's 11.
 //
 // A row that sees nothing has l = 0: out = 0, lse = -inf.  Masked scores are
@@ -69,7 +68,6 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kItemCost = 6;                     // what an item costs beside its tiles, in tiles
 constexpr int kMinChunk = 6;                     // of a CTA's range
 constexpr int kCtas = kSms * 3;                  // at most
-constexpr float kLag = 8.f;
 
 __device__ unsigned int g_attn_timeouts;
 
@@ -271,7 +269,7 @@ __device__ __forceinline__ void slice(const AttentionArgs &p, State<D, ROWS> &st
                 if (!see) x[n][i] = -INFINITY, seen[n] &= ~(1u << i);
             }
         }
-        grown |= fmaxf(x[n][0], x[n][2]) > st.m[n][0] + kLag || fmaxf(x[n][1], x[n][3]) > st.m[n][1] + kLag;
+        grown |= fmaxf(x[n][0], x[n][2]) > st.m[n][0] + kPeak || fmaxf(x[n][1], x[n][3]) > st.m[n][1] + kPeak;
     }
     if (__any_sync(~0u, grown)) {                // rows whose maximum has outgrown m (the first keys seen: from -inf)
 #pragma unroll
@@ -282,15 +280,26 @@ __device__ __forceinline__ void slice(const AttentionArgs &p, State<D, ROWS> &st
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-                const float to = mx > st.m[n][c] ? mx : st.m[n][c];
-                const float a = to == st.m[n][c] ? 1.f : ex2(st.m[n][c] - to);
+                const float to = fmaxf(mx - kStart, st.m[n][c]);
+                const Rescale by(to == st.m[n][c] ? 0.f : st.m[n][c] - to);
+                const float a = by.of_o();
                 st.m[n][c] = to;
-                st.l[n][c] *= a;
+                st.l[n][c] = by.of_l(st.l[n][c]);
 #pragma unroll
                 for (int k = 0; k < KS; ++k) st.o[k][n][c] *= a, st.o[k][n][c + 2] *= a;
             }
     }
-    const float back = exp2_int(-e.y);
+    const bool deep = ve < kDeep;
+    const float back = deep ? 0.f : exp2_int(-e.y);
+    if (__builtin_expect(deep, 0)) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float ref = ve + (EDGE && st.m[n][c] == -INFINITY ? 0.f : st.m[n][c]);
+                st.l[n][c] += ex2(x[n][c] - ref) + ex2(x[n][c + 2] - ref);
+            }
+    }
     uint32_t pb[N][2];                           // P^T: B fragments
 #pragma unroll
     for (int n = 0; n < N; ++n) {
@@ -569,11 +578,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
                 float ll = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float f = ex2(sm.m[w][r] - ref);
+                    const Rescale by(sm.m[w][r] - ref);
+                    const float f = by.of_o();
                     const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][r][d]);
                     acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
                     acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
-                    ll = fmaf(f, sm.l[w][r], ll);
+                    ll += by.of_l(sm.l[w][r]);
                 }
                 if (continued || unfinished) {
                     *reinterpret_cast<float4 *>(slot + (8 * n + r) * D + d) = acc;
@@ -623,10 +633,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, ROWS>)
             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + ROWS * D + 2 * r[q]));
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + r[q] * D + d));
             const float mx = fmaxf(m[q], ml.x), base = mx == -INFINITY ? 0.f : mx;
-            const float e = ex2(m[q] - base), f = ex2(ml.x - base);
+            const Rescale old(m[q] - base), add(ml.x - base);
+            const float e = old.of_o(), f = add.of_o();
             o[q].x = o[q].x * e + v.x * f, o[q].y = o[q].y * e + v.y * f;
             o[q].z = o[q].z * e + v.z * f, o[q].w = o[q].w * e + v.w * f;
-            l[q] = l[q] * e + ml.y * f;
+            l[q] = old.of_l(l[q]) + add.of_l(ml.y);
             m[q] = mx;
         }
     }
@@ -651,9 +662,10 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float pm, float pl, float4 po) {
         const float mx = fmaxf(m, pm), ref = mx == -INFINITY ? 0.f : mx;
-        const float a = ex2(m - ref), b = ex2(pm - ref);
+        const Rescale old(m - ref), more(pm - ref);
+        const float a = old.of_o(), b = more.of_o();
         o.x = o.x * a + po.x * b, o.y = o.y * a + po.y * b, o.z = o.z * a + po.z * b, o.w = o.w * a + po.w * b;
-        l = l * a + pl * b;
+        l = old.of_l(l) + more.of_l(pl);
         m = mx;
     };
 #pragma unroll 4

@@ -34,6 +34,23 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// A row's weights are 2^(s + ve - m), as fp16 for the product: m is set 2^kStart below the largest
+// s + ve when that has passed m + kPeak, so that they lie below 2^kPeak (fp16 holds less than
+// 2^16), the largest at 2^kStart at least.  fp16 then holds them to 2^-11 of themselves down to
+// 2^-21 of the largest, and to 2^-32 of it below.  (A kStart of 11 or 13 holds 4 or 6 bits more, but
+// m moves more often: a prompt of 4096 tokens 149 or 162 us instead of 126.)
+constexpr float kStart = 7.f, kPeak = 15.f;
+// The weights' sum l does not have ve in it, and what counts in it may count for nothing in the
+// product (a page of zeros).  For ve below kDeep, where the weight may be under fp32's range, it
+// takes 2^(s - m) by itself; and l is rescaled in two halves of the exponent, which may be past -126.
+constexpr float kDeep = -38.f;
+struct Rescale {
+    float half;
+    __device__ __forceinline__ explicit Rescale(float exponent) : half(ex2(0.5f * exponent)) {}
+    __device__ __forceinline__ float of_o() const { return half * half; }
+    __device__ __forceinline__ float of_l(float l) const { return l * half * half; }
+};
+
 // Where a sequence's new tokens lie, and its length with them.  Of tokens past max_q, which are
 // left out, neither n nor len counts any: the first one stands at len - n either way.
 struct Span { int start, n, len; };

@@ -2,10 +2,8 @@
 // (prompts), on the tcgen05 tensor cores with accumulators in tensor memory.
 //
 // Mathematics: as attention.cu (codes multiplied as fp16 numbers, page exponents
-// applied in fp32, V's exponent inside the softmax exponent).  The running maximum
-// may lag: O and l are rescaled only when a row's maximum has grown by more than
-// 2^kLag since it was last taken, so weights reach 2^kLag (fp16 holds 2^15) and the
-// rescaling of O, a round trip through tensor memory, is rare.
+// applied in fp32, V's exponent inside the softmax exponent).  As m may lag behind the
+// maximum (attention.cuh), the rescaling of O, a round trip through tensor memory, is rare.
 //
 // Work split.  A CTA takes 256 rows (new tokens x heads of a group) of one sequence
 // and kv head, as two 128-row tiles whose softmax and products alternate: while one
@@ -56,7 +54,6 @@ constexpr float kCtaCost = 5.f;                   // what a CTA costs beside its
 constexpr float kJoinCost = 0.03f;               // what a part costs when it is joined
 constexpr int kMostCtas = 5 * kSms;              // where keys may be split
 constexpr int kLongSteps = 32;                   // of sequences whose tiles are split although they fill the SMs
-constexpr float kLag = 8.f;
 
 __device__ unsigned int g_prompt_timeouts;
 
@@ -67,7 +64,7 @@ struct Smem {
     alignas(1024) uint8_t k[kBuf][kTile];
     alignas(1024) uint8_t v[kBuf][kTile];
     alignas(1024) uint8_t raw[kRaw][kRawBytes];
-    float4 exps[kExps][kKeys / 16];              // 2^ke, ve, 2^-ve of each 16 keys
+    float4 exps[kExps][kKeys / 16];              // of each 16 keys: 2^ke, ve, 2^-ve (0 below kDeep), whether one of the 64 is below
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBuf], v_full[kBuf], kv_empty[kBuf];
     uint64_t s_full[2][2], p_full[2][2], o_full, e_full[kExps];
     uint32_t tmem;
@@ -406,31 +403,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(sc + h * kHalf, v);
             tmem_ld32(sc + h * kHalf + 32, v + 32);
             ptx::tmem_ld_wait();
-            if (partial(key0, kHalf)) {
+            // A factor of 0 would make masked scores NaN.
+            auto factor = [&](int g) { return fmaxf(qs * ex[g].x, 1.2e-38f); };
+            // The row's maximum, by 16 keys (all of one page).
+            auto largest = [&] {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < kHalf / 16; ++g) {
+                    const float *x = v + g * 16;
+                    const float a = max3(max3(x[0], x[1], x[2]), x[3], x[4]), b = max3(max3(x[5], x[6], x[7]), x[8], x[9]);
+                    const float c = max3(max3(x[10], x[11], x[12]), x[13], x[14]);
+                    mx = fmaxf(mx, fmaf(max3(max3(a, b, c), x[15], x[15]), factor(g), ex[g].y));
+                }
+                return mx;
+            };
+            float deep = 0.f;                                          // of l: the keys with ve below kDeep
+            if (partial(key0, kHalf) || ex[0].w != 0.f) {
                 const int hi = pos - key0, lo = low - key0;            // of the keys, those in (lo, hi] are seen
 #pragma unroll
                 for (int k = 0; k < kHalf; ++k)
                     if (k > hi || k <= lo) v[k] = -INFINITY;
+                if (ex[0].w != 0.f) {
+                    const float mx = largest(), to = mx > m + kPeak ? mx - kStart : m, ref = to == -INFINITY ? 0.f : to;
+#pragma unroll
+                    for (int k = 0; k < kHalf; ++k) deep += ex[k / 16].y < kDeep ? ex2(fmaf(v[k], factor(k / 16), -ref)) : 0.f;
+                }
             }
-            // A factor of 0 would make masked scores NaN.
             float f[kHalf / 16];
 #pragma unroll
-            for (int g = 0; g < kHalf / 16; ++g) f[g] = fmaxf(qs * ex[g].x, 1.2e-38f);
-            // The row's maximum, by 16 keys (one page at least); m follows it when it has been
-            // outgrown by more than kLag.
-            float mx = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < kHalf / 16; ++g) {
-                const float *x = v + g * 16;
-                const float a = max3(max3(x[0], x[1], x[2]), x[3], x[4]), b = max3(max3(x[5], x[6], x[7]), x[8], x[9]);
-                const float c = max3(max3(x[10], x[11], x[12]), x[13], x[14]);
-                mx = fmaxf(mx, fmaf(max3(max3(a, b, c), x[15], x[15]), f[g], ex[g].y));
-            }
-            const bool move = mx > m + kLag;
+            for (int g = 0; g < kHalf / 16; ++g) f[g] = factor(g);
+            // m follows the maximum when it has been outgrown.
+            const float mx = largest();
+            const bool move = mx > m + kPeak;
             if (__any_sync(~0u, move)) {
-                const float a = move ? ex2(m - mx) : 1.f;
-                if (move) m = mx;
-                l *= a;
+                const Rescale by(move ? m - (mx - kStart) : 0.f);
+                const float a = by.of_o();
+                if (move) m = mx - kStart;
+                l = by.of_l(l);
                 if (hs > 0) {
                     // The last half-step's product has to be done: its issuer's next signal says so.
                     if (ok) ok = ptx::mbar_wait(at(sm.s_full[t][h ^ 1]), ((hs + 1) >> 1) & 1, &g_prompt_timeouts);
@@ -446,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            l += deep;
             const float ref = m == -INFINITY ? 0.f : m;
             // Weights, their sum, and fp16 pairs in the place of the scores.
 #pragma unroll
@@ -671,7 +681,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 look(j + 4);
             }
             // Steps back to j - kExps have long been weighed: K of step j - 2 is released after them.
-            if ((lane >> 3) == (j & 3)) sm.exps[j % kExps][lane & 7] = make_float4(exp2_int(ke), (float)ve, exp2_int(-ve), 0.f);
+            const uint32_t deep = __ballot_sync(~0u, (float)ve < kDeep);
+            if ((lane >> 3) == (j & 3))
+                sm.exps[j % kExps][lane & 7] = make_float4(exp2_int(ke), (float)ve, (float)ve < kDeep ? 0.f : exp2_int(-ve),
+                                                           deep >> (lane & ~3) & 0xFu ? 1.f : 0.f);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(at(sm.e_full[j % kExps]));
         }
@@ -767,14 +780,15 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const AttentionArgs p,
         const float *part = part_of<D>(p, grid, w.slot + s);
         const float2 ml = any ? __ldcs(reinterpret_cast<const float2 *>(part + kRows * D + 2 * r)) : make_float2(-INFINITY, 0.f);
         const float mx = fmaxf(m, ml.x), ref = mx == -INFINITY ? 0.f : mx;
-        const float a = ex2(m - ref), b = ex2(ml.x - ref);
+        const Rescale old(m - ref), more(ml.x - ref);
+        const float a = old.of_o(), b = more.of_o();
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
             const float4 v = any ? __ldcs(reinterpret_cast<const float4 *>(part) + (warp + 8 * k) * kRows + r) : make_float4(0.f, 0.f, 0.f, 0.f);
             o[k].x = o[k].x * a + v.x * b, o[k].y = o[k].y * a + v.y * b;
             o[k].z = o[k].z * a + v.z * b, o[k].w = o[k].w * a + v.w * b;
         }
-        l = l * a + ml.y * b;
+        l = old.of_l(l) + more.of_l(ml.y);
         m = mx;
     }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);

@@ -291,8 +291,10 @@ LOWBIT_API lowbit_status lowbit_kv_append(const lowbit_kv_append_args *args, con
  * at position pos, over the keys t <= pos (and t > pos - window when window > 0)
  *     out = sum_t softmax_t(scale q.k_t) v_t,   lse = ln sum_t e^(scale q.k_t),
  * with k and v the cached values (code * 2^exp), head h reading key-value head
- * h / (heads / kv_heads).  Scores, softmax and sums in fp32; out rounded once to
- * bf16.  A row that sees no key gives out 0 and lse -infinity.  What the cache holds
+ * h / (heads / kv_heads).  Scores, softmax and sums in fp32; for the product with
+ * the codes of v the weights are rounded to fp16, to 2^-11 of themselves, or to 2^-32
+ * of the row's largest e^(..) 2^exp (weight times page scale of v) where that is more;
+ * out rounded once to bf16.  A row that sees no key gives out 0 and lse -infinity.  What the cache holds
  * at keys that a row does not see (NaN codes among it) does not reach that row.
  *   q, out   [tokens, heads, head_dim] bf16, strides in elements (multiples of 4),
  *            head_dim contiguous, 8-byte aligned.

@@ -99,3 +99,78 @@ def test_largest_windows_hide_nothing(lens, news, window):
     out, lse = attend(b, q, window=window)
     close(out, want, bound)
     close(lse, want_lse, lse_bound)
+
+
+# ---------------------------------------------------------------------------
+# Page exponents of V
+# ---------------------------------------------------------------------------
+
+def definition(b, q, scale):
+    """(out, its bound, lse).
+
+    Weights are held to 2^-11 of themselves, or to 2^-32 of the row's largest product of weight
+    and page scale of V where that is more; scores and 2^x are off by 2^-16 here (sizes below 30),
+    l by 2^-18.  So |error| <= 2^-8 |out| (bf16) + 2^-10 sum p |v| + 2^-32 max(p 2^e) sum |codes|."""
+    T, heads, dim = q.shape
+    group = heads // b.k.shape[1]
+    out, bound, lse = np.zeros_like(q), np.zeros_like(q), np.zeros((T, heads))
+    for s, n in enumerate(b.news):
+        rows = slice(b.starts[s], b.starts[s] + n)
+        seen = np.arange(b.lens[s])[None] <= b.lens[s] - n + np.arange(n)[:, None]
+        for h in range(heads):
+            k, v = ref.cached(b, s, h // group, "k"), ref.cached(b, s, h // group, "v")
+            x = np.where(seen, q[rows, h] @ k.T * scale, -np.inf)
+            m = x.max(1, keepdims=True)
+            w = np.exp(x - m)
+            z = w.sum(1, keepdims=True)
+            p = w / z
+            e = 2.0 ** np.repeat(b.v_exp[b.table[s], h // group].astype(float), b.page)[:b.lens[s]]
+            floor = np.max(p * e, 1, keepdims=True) * (seen @ np.abs(v / e[:, None])) * 2.0 ** -32
+            out[rows, h] = p @ v
+            bound[rows, h] = 2.0 ** -8 * np.abs(p @ v) + 2.0 ** -10 * (p @ np.abs(v)) + floor
+            lse[rows, h] = (np.log(z) + m)[:, 0]
+    return out, bound, lse
+
+
+@pytest.mark.parametrize("n", [1, 5, 80])
+@pytest.mark.parametrize("order", ["high first", "low first", "in turn"])
+@pytest.mark.parametrize("scores", ["equal", "random"])
+def test_v_exponents_at_both_limits(n, order, scores):
+    """Half of the weight lies on pages whose scale is 2^-64, the other half on pages of 2^64."""
+    b = ref.make_batch(106, [256, 192], [n, n], 2, 64, 32, garbage=False)
+    b.k_exp[:] = -9
+    for s in range(2):
+        pages = -(-b.lens[s] // 32)
+        at = np.arange(pages)
+        high = {"high first": at < pages // 2, "low first": at >= pages // 2, "in turn": at % 2 == 0}[order]
+        b.v_exp[b.table[s, :pages]] = np.where(high, 64, -64)[:, None]
+    q = queries(107, 2 * n, 4, 64)
+    if scores == "equal":
+        q = torch.zeros_like(q)
+    want, bound, want_lse = definition(b, ref.f64(q), 1.0)
+    out, lse = attend(b, q, scale=1.0)
+    close(lse, want_lse, 2.0 ** -15)
+    close(out, want, bound)
+
+
+@pytest.mark.parametrize("n", [1, 5, 80])
+@pytest.mark.parametrize("at", [3, 5000, 16200])
+@pytest.mark.parametrize("apart", [0, 7, 12])
+def test_v_exponent_of_one_page_above_the_others(n, at, apart):
+    """One key with half of the weight on a page of a large scale and small codes, among 16000
+    alike with the other half, which may not be lost."""
+    length, page, dim = 16384, 64, 64
+    b = ref.make_batch(108, [length], [n], 1, dim, page, garbage=False)
+    b.k[:] = 0
+    b.k_exp[:], b.v_exp[:] = 0, -6
+    b.k[b.table[0, at // page], 0, at % page, 0] = 0x38                      # 1.0
+    b.v[:] &= 0x7F                                                           # one sign: nothing cancels
+    b.v[b.table[0, at // page]] = 0x01
+    b.v_exp[b.table[0, at // page]] += apart
+    q = torch.zeros(n, 2, dim, dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    scale = float(np.log(length - 1.0))
+    want, bound, want_lse = definition(b, ref.f64(q), scale)
+    out, lse = attend(b, q, scale=scale)
+    close(lse, want_lse, 2.0 ** -15)
+    close(out, want, bound)
