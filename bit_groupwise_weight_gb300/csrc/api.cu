@@ -88,7 +88,10 @@ lowbit_status check_linear_args(const uint16_t *x, const uint8_t *w, const uint1
     return LOWBIT_OK;
 }
 
-lowbit_status check_cache(const lowbit_cache *c, const lowbit_sequences *s, int heads) {
+bool empty(const lowbit_sequences *s) { return s->batch == 0 || s->tokens == 0; }
+
+// The sizes alone: what the workspace's size follows from.
+lowbit_status check_sizes(const lowbit_cache *c, const lowbit_sequences *s, int heads) {
     if (c == nullptr || s == nullptr) return LOWBIT_EINVAL;
     if (s->batch < 0 || s->tokens < 0 || s->batch > kMaxDim || s->tokens > kMaxDim || s->width < 0 || s->width > kMaxDim)
         return LOWBIT_EINVAL;
@@ -100,9 +103,15 @@ lowbit_status check_cache(const lowbit_cache *c, const lowbit_sequences *s, int 
     if ((int64_t)s->tokens * (heads / c->kv_heads) > kMaxDim || (int64_t)s->width * c->page > kMaxDim ||
         (int64_t)s->width * c->page * c->kv_heads > (int64_t)1 << 34)
         return LOWBIT_EINVAL;
-    if (s->batch == 0 || s->tokens == 0) return LOWBIT_OK;
+    if (empty(s)) return LOWBIT_OK;
     if (s->cu_q == nullptr ? s->tokens % s->batch != 0 : s->max_q <= 0) return LOWBIT_EINVAL;
-    if (c->pages == 0 || s->width == 0 || s->table_stride < s->width) return LOWBIT_EINVAL;
+    return c->pages == 0 || s->width == 0 ? LOWBIT_EINVAL : LOWBIT_OK;
+}
+
+lowbit_status check_cache(const lowbit_cache *c, const lowbit_sequences *s, int heads) {
+    const lowbit_status st = check_sizes(c, s, heads);
+    if (st != LOWBIT_OK || empty(s)) return st;
+    if (s->table_stride < s->width) return LOWBIT_EINVAL;
     if (!c->k || !c->v || !c->k_exp || !c->v_exp || !s->page_table || !s->lens) return LOWBIT_EINVAL;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(s->page_table, 4) || !aligned(s->lens, 4) ||
         (s->cu_q != nullptr && !aligned(s->cu_q, 4)))
@@ -287,9 +296,7 @@ lowbit_status lowbit_kv_append(const lowbit_kv_append_args *a, const lowbit_cach
 }
 
 size_t lowbit_attention_workspace(int32_t heads, const lowbit_cache *c, const lowbit_sequences *s) {
-    if (c == nullptr || s == nullptr || s->batch <= 0 || s->tokens <= 0 || c->kv_heads <= 0 || heads <= 0 ||
-        heads % c->kv_heads != 0 || (s->cu_q != nullptr && s->max_q <= 0))
-        return 0;
+    if (check_sizes(c, s, heads) != LOWBIT_OK || empty(s)) return 0;
     const bool uniform = s->cu_q == nullptr;
     return lowbit::attention_workspace_bytes(s->tokens, s->batch, uniform ? s->tokens / s->batch : s->max_q, uniform,
                                              heads, c->kv_heads, c->head_dim, (int64_t)s->width * c->page);
