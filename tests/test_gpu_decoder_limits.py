@@ -38,6 +38,7 @@ def close(got, want, bound):
     with np.errstate(invalid="ignore"):
         bad = ~(np.abs(got - want) <= bound)
     bad &= ~((got == want) | (np.isnan(got) & np.isnan(want)))
+    want = np.broadcast_to(want, got.shape)
     assert not bad.any(), f"{bad.sum()} of {bad.size}, first {np.argwhere(bad)[0].tolist()}: {got[bad][0]} for {want[bad][0]}"
 
 
@@ -153,24 +154,26 @@ def test_v_exponents_at_both_limits(n, order, scores):
     close(out, want, bound)
 
 
-@pytest.mark.parametrize("n", [1, 5, 80])
-@pytest.mark.parametrize("at", [3, 5000, 16200])
-@pytest.mark.parametrize("apart", [0, 7, 12])
-def test_v_exponent_of_one_page_above_the_others(n, at, apart):
-    """One key with half of the weight on a page of a large scale and small codes, among 16000
-    alike with the other half, which may not be lost."""
-    length, page, dim = 16384, 64, 64
-    b = ref.make_batch(108, [length], [n], 1, dim, page, garbage=False)
+@pytest.mark.parametrize("n,copies", [(1, 64), (5, 64), (80, 8)])
+@pytest.mark.parametrize("at", [3, 2000])
+@pytest.mark.parametrize("apart", [0, 7, 14])
+def test_v_exponent_of_one_page_above_the_others(n, copies, at, apart):
+    """One key with half of the weight on a page of a large scale and small codes, among 4000
+    alike with the other half, which may not be lost.  As many sequences over the same pages as
+    leave no one's keys split between CTAs: one running maximum serves them all."""
+    length, page, dim, heads = 4000, 64, 64, 16
+    b = ref.make_batch(108, [length], [n], heads, dim, page, garbage=False)
     b.k[:] = 0
     b.k_exp[:], b.v_exp[:] = 0, -6
-    b.k[b.table[0, at // page], 0, at % page, 0] = 0x38                      # 1.0
+    b.k[b.table[0, at // page], :, at % page, 0] = 0x38                      # 1.0
     b.v[:] &= 0x7F                                                           # one sign: nothing cancels
     b.v[b.table[0, at // page]] = 0x01
     b.v_exp[b.table[0, at // page]] += apart
-    q = torch.zeros(n, 2, dim, dtype=torch.bfloat16)
+    q = torch.zeros(n, heads, dim, dtype=torch.bfloat16)
     q[:, :, 0] = 1.0
     scale = float(np.log(length - 1.0))
     want, bound, want_lse = definition(b, ref.f64(q), scale)
-    out, lse = attend(b, q, scale=scale)
-    close(lse, want_lse, 2.0 ** -15)
-    close(out, want, bound)
+    many = ref.Batch([length] * copies, [n] * copies, np.repeat(b.table, copies, 0), b.k, b.v, b.k_exp, b.v_exp)
+    out, lse = attend(many, q.repeat(copies, 1, 1), scale=scale)
+    close(lse.reshape(copies, n, heads), want_lse, 2.0 ** -15)
+    close(out.reshape(copies, n, heads, dim), want, bound)
