@@ -1,5 +1,5 @@
 """Build liblowbit.so in-tree with nvcc for sm_103a (GB300), and beside it the
-extension module _lowbit_torch.so (csrc/binding.cpp: the hot path of the decoder
+extension module _lowbit_torch (csrc/binding.cpp: the hot path of the decoder
 operators' Python binding, against the installed PyTorch's headers).
 
 Each .cu under csrc/ compiles to an object in parallel; the objects link into
@@ -21,7 +21,6 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = BUILD / "liblowbit.so"
-BINDING = BUILD / "_lowbit_torch.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++20", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -44,10 +43,19 @@ def _deps() -> list[Path]:
             + [Path(__file__)])
 
 
+def binding() -> Path:
+    """The extension module's file, named after the PyTorch and the Python that it is compiled
+    against, so that another one's is neither loaded nor taken for up to date."""
+    import torch
+    commit = (torch.version.git_version or "")[:8]
+    return BUILD / f"_lowbit_torch-{torch.__version__}-{commit}{sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
 def up_to_date() -> bool:
-    if not LIB.exists() or not BINDING.exists():
+    module = binding()
+    if not LIB.exists() or not module.exists():
         return False
-    t = min(LIB.stat().st_mtime, BINDING.stat().st_mtime)
+    t = min(LIB.stat().st_mtime, module.stat().st_mtime)
     return all(p.stat().st_mtime <= t for p in _deps())
 
 
@@ -59,7 +67,8 @@ def build_binding(verbose: bool = False) -> None:
     cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         raise RuntimeError("a C++ compiler is needed to build _lowbit_torch")
-    tmp = BINDING.with_suffix(f".{os.getpid()}.tmp")
+    module = binding()
+    tmp = module.with_suffix(f".{os.getpid()}.tmp")
     cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{p}" for p in (INCLUDE, root / "include", root / "include/torch/csrc/api/include",
@@ -71,7 +80,7 @@ def build_binding(verbose: bool = False) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"the C++ compiler failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, module)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ...] = ()) -> Path:
@@ -93,9 +102,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ..
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 4))) as ex:
-        binding = ex.submit(build_binding, verbose)
+        module = ex.submit(build_binding, verbose)
         objs = list(ex.map(compile_one, sources()))
-        binding.result()
+        module.result()
     tmp = LIB.with_suffix(f".{os.getpid()}.tmp")
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", *map(str, objs), "-o", str(tmp)]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -33,9 +33,10 @@ def _load():
     global _hot
     if _hot is None:
         lib = _abi.abi()
-        if not _build.BINDING.exists():
-            raise ImportError(f"_lowbit_torch is not built ({_build.BINDING} missing); run bit_groupwise_weight_gb300.build.build()")
-        spec = importlib.util.spec_from_file_location("_lowbit_torch", str(_build.BINDING))
+        path = _build.binding()
+        if not path.exists():
+            raise ImportError(f"_lowbit_torch is not built ({path} missing); run bit_groupwise_weight_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_lowbit_torch", str(path))
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (

@@ -3,9 +3,11 @@ needed)."""
 from __future__ import annotations
 
 import pytest
+import torch
 
 import bit_groupwise_weight_gb300 as lb
 from bit_groupwise_weight_gb300 import build as lbuild
+from bit_groupwise_weight_gb300 import decoder
 from test_decoder_host import ATTN, CACHE, EINVAL, SEQS, call, descriptor
 
 
@@ -38,3 +40,13 @@ def test_workspace_follows_from_the_sizes_alone(lib):
     """It can be asked for before there is a cache or a table."""
     nothing = dict(k=None, v=None, k_exp=None, v_exp=None, page_stride=0, head_stride=0)
     assert workspace(lib, cache=nothing, seqs=dict(page_table=None, lens=None, table_stride=0)) == workspace(lib) > 0
+
+
+def test_extension_module_of_another_pytorch_is_not_used(lib, monkeypatch):
+    """It is compiled against PyTorch's C++ headers: after an upgrade it has to be built again."""
+    assert lbuild.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.0.0+other")
+    assert not lbuild.up_to_date()
+    monkeypatch.setattr(decoder, "_hot", None)
+    with pytest.raises(ImportError, match="not built"):
+        decoder._load()
