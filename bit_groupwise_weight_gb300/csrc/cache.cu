@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
     if (s.n == 0) return;
     const int P = 1 << p.pshift, first = s.len - s.n;     // position of the first new token
     const int slot = (first >> p.pshift) + j;             // page of the sequence (rounded down)
-    const int lo = max(slot * P, first), hi = min(slot * P + P, s.len);
+    if (slot > (s.len - 1) >> p.pshift) return;           // past the last token: slot * P may not be an int
+    const int lo = max(slot * P, first), hi = slot * P + min(P, s.len - slot * P);
     if (lo >= hi) return;                                 // also what negative j gives: nothing
     const bool stored = slot >= 0 && slot < p.width;
     const int page = stored ? p.page_table[(int64_t)b * p.table_stride + slot] : -1;

@@ -177,3 +177,26 @@ def test_v_exponent_of_one_page_above_the_others(n, copies, at, apart):
     out, lse = attend(many, q.repeat(copies, 1, 1), scale=scale)
     close(lse.reshape(copies, n, heads), want_lse, 2.0 ** -15)
     close(out.reshape(copies, n, heads, dim), want, bound)
+
+
+# ---------------------------------------------------------------------------
+# Lengths at the end of 32 bits
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("page", [16, 256])
+def test_append_rotates_at_the_last_positions(n, page):
+    """Past the page table: rotated, not stored."""
+    heads, kv_heads, dim = 4, 2, 64
+    last = 2 ** 31 - 1
+    b = ref.make_batch(111, [20], [n], kv_heads, dim, page)
+    cache, table, _, _ = b.device()
+    before = [c.view(torch.uint8).clone() for c in cache]
+    x = queries(112, n, heads + 2 * kv_heads, dim)
+    q, k, v = x.cuda().split([heads, kv_heads, kv_heads], 1)
+    turns = lb.rotary_turns(dim)
+    out = torch.full((n, heads, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    lb.kv_append(q, k, v, *cache, table, torch.tensor([last], dtype=torch.int32, device="cuda"), turns=turns.cuda(), out=out)
+    want, mag = ref.rotate(ref.f64(x)[:, :heads], [last - n + i for i in range(n)], turns.tolist(), False, 1.0)
+    close(ref.f64(out), want, 2.0 ** (np.frexp(want)[1] - 9.0) + mag * 2.0 ** -20)
+    assert all(torch.equal(c.view(torch.uint8), o) for c, o in zip(cache, before))
