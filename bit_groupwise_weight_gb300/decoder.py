@@ -47,11 +47,22 @@ def _load():
 
 # What follows describes a call in Python: how one that the extension did not accept is
 # explained.  The C ABI's descriptors, packed:
-_CACHE = struct.Struct("@PPPPqqiiii").pack          # lowbit_cache
-_SEQUENCES = struct.Struct("@PPPqiiii").pack        # lowbit_sequences
-_KV_APPEND = struct.Struct("@PPPPqqqqqqqqPfiii").pack
-_ATTENTION = struct.Struct("@PPPqqqqqPNfii4x").pack
-_SAMPLE = struct.Struct("@PPPPPPPPqfffiiii4x").pack
+def _packer(layout: str, of: str):
+    pack = struct.Struct(layout).pack
+
+    def packed(*values):
+        try:
+            return pack(*values)
+        except (struct.error, OverflowError) as e:      # not a number, or past 32 bits
+            raise ValueError(f"a number among {of} is not one or does not fit: {e}") from None
+    return packed
+
+
+_CACHE = _packer("@PPPPqqiiii", "the cache's sizes")                       # lowbit_cache
+_SEQUENCES = _packer("@PPPqiiii", "the sequences' sizes and max_q")        # lowbit_sequences
+_KV_APPEND = _packer("@PPPPqqqqqqqqPfiii", "the sizes and factor")
+_ATTENTION = _packer("@PPPqqqqqPNfii4x", "the sizes, scale and window")
+_SAMPLE = _packer("@PPPPPPPPqfffiiii4x", "the sizes, temperature, top_p, min_p and top_k")
 
 _BF16, _F32, _I32, _I8, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.int64, torch.uint8
 _CODES = (torch.float8_e4m3fn, _U8)
