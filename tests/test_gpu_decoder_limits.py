@@ -200,3 +200,21 @@ def test_append_rotates_at_the_last_positions(n, page):
     want, mag = ref.rotate(ref.f64(x)[:, :heads], [last - n + i for i in range(n)], turns.tolist(), False, 1.0)
     close(ref.f64(out), want, 2.0 ** (np.frexp(want)[1] - 9.0) + mag * 2.0 ** -20)
     assert all(torch.equal(c.view(torch.uint8), o) for c, o in zip(cache, before))
+
+
+# ---------------------------------------------------------------------------
+# Signs of the scale
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [1, 5, 80])
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("scale", [-0.125, 0.0, -0.0])
+def test_negative_and_zero_scales(n, window, scale):
+    """As -q with a positive scale; zero: the mean of what a row sees."""
+    b = ref.make_batch(109, [200, 129], [n, n], 2, 64, 32)
+    q = queries(110, 2 * n, 8, 64)
+    out, lse = attend(b, q, scale=scale, window=window)
+    x = ref.f64(q) * (np.sign(scale) if scale else 0.0)
+    want, want_lse, bound, lse_bound = ref.attention(x, b, 0.125, window)
+    close(out, want, bound)
+    close(lse, want_lse, lse_bound)
