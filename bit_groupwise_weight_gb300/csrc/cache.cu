@@ -378,11 +378,8 @@ cudaError_t launch(AppendArgs &p, int n, int64_t gx, cudaStream_t stream) {
                         : vec && !p.interleaved && p.R % 16 == 0 ? kv_append_kernel<THREADS, D, kHalves>
                                                                  : kv_append_kernel<THREADS, D, kAny>;
     p.table_tokens = std::min(std::min(n, p.P), kChunk);
+    static_assert(kChunk * D * sizeof(float) <= 48 * 1024, "the table fits what a kernel may use without asking");
     const size_t smem = (size_t)p.table_tokens * (size_t)p.R * sizeof(float);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = raise_smem_limit((const void *)kernel, current_device(), 64 * 1024);
-        if (e != cudaSuccess) return e;
-    }
     return launch_pdl(kernel, dim3((unsigned)gx, (unsigned)p.Hk), dim3(THREADS), smem, stream, (const AppendArgs)p);
 }
 
