@@ -72,7 +72,8 @@ __device__ __forceinline__ Span span(const AttentionArgs &p, int b) {
 }
 
 // Power of two that brings a row of q whose largest finite magnitude is amax into
-// [2^10, 2^11): bf16's 8 bits are then exact in fp16 down to 2^-35 of it.
+// [2^10, 2^11): bf16's 8 bits are then exact in fp16 down to 2^-28 of it (2^-17, fp16's last
+// bit being 2^-24), and what is smaller is off by 2^-35 of it at most.
 __device__ __forceinline__ int query_shift(float amax) { return min(10 + 127 - (int)(__float_as_uint(amax) >> 23), 100); }
 
 }  // namespace attn
