@@ -336,6 +336,8 @@ LOWBIT_API size_t lowbit_attention_workspace(int32_t heads, const lowbit_cache *
  * NaN logits count as -infinity; a row without any logit above that gives token -1
  * and logprob -infinity.  Tokens under 2^-31 of the likeliest are never drawn.
  *   logits   [rows, vocab] of `dtype`, rows row_stride elements apart, naturally aligned.
+ *            Read in aligned vectors of 16 bytes: up to 15 bytes before and after a row are
+ *            read with it, and not used.
  *   u        [rows] fp32 in [0, 1).
  *   temperature, top_p, min_p [rows] fp32 and top_k [rows] int32, device; each may be
  *            NULL: the scalar of the same name holds for every row then.
