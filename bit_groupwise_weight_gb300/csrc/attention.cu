@@ -44,12 +44,12 @@
 // operand are keys (values), its 8 columns query rows, so that a group of up to 8
 // heads wastes nothing.
 // Bound: HBM, 2 D bytes per key and kv head, for long sequences (one of 131001 keys, 8 kv
-// heads of 128: 49 us, 5.4 TB/s, 0.80 of a copy's rate); for many and short ones what an item
+// heads of 128: 49.7 us, 5.4 TB/s, 0.80 of a copy's rate); for many and short ones what an item
 // costs beside its tiles (queries, first tiles' latency, the join of the warps: some 6 tiles'
-// time): 48 sequences of up to 8192 keys 25 us, 3.8 TB/s; 96 windows of 1000 keys of 64 values
-// in pages of 16 17 us, 1.5 TB/s; one sequence of some hundred keys 7 us, of which 5 are one
+// time): 48 sequences of up to 8192 keys 25.5 us, 3.8 TB/s; 96 windows of 1000 keys of 64 values
+// in pages of 16 17.5 us, 1.5 TB/s; one sequence of 257 keys 7.4 us, of which 5 are one
 // launch's shortest.  (More CTAs of an SM for 64 values, four for three: 16.8 for 17.4 us, and
-// 10.5 for 9.3 with few sequences; other item costs and ranges lose more than they gain.)
+// 10.5 for 9.3 with few sequences.)
 #include <algorithm>
 #include <atomic>
 #include <chrono>
@@ -65,8 +65,15 @@ typedef unsigned long long u64;
 constexpr int kTile = 64;                        // keys of a stage
 constexpr int kWarps = 4;                        // consumer warps, 16 keys each
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kItemCost = 6;                     // what an item costs beside its tiles, in tiles
-constexpr int kMinChunk = 6;                     // of a CTA's range
+// What an item costs beside its tiles, in tiles: with 3 and 9 instead of 6, 48 sequences of up to
+// 8192 keys take 26.8 and 25.9 us instead of 25.5, 96 windows of 1000 keys 16.9 and 18.4 instead of
+// 17.3, one sequence of 257 keys 9.2 and 7.6 instead of 7.5, 7 sequences of 10 tokens 12.6 and 8.7
+// instead of 8.6.
+constexpr int kItemCost = 6;
+// The least range of a CTA: 3 and 12 instead of 6 give 7.1 and 10.1 us for 257 keys, 18.6 and 19.7
+// for 8 sequences of 5 tokens (18.7), 9.6 and 12.5 for a window of 3778 keys in one sequence (11.3);
+// a step of it is a CTA more to wait for.
+constexpr int kMinChunk = 6;
 constexpr int kCtas = kSms * 3;                  // at most
 
 __device__ unsigned int g_attn_timeouts;
@@ -187,6 +194,10 @@ struct Smem {
 // What the second launch needs to know of an item: written by the CTA that ends it, from
 // CTA `begun` on (below 0: none).
 struct Join { int begun, start, nrows, row0, h, pad; };
+// More CTAs than this for each item that the page table allows: a second launch joins the parts.
+// (By the last CTA always, 131001 keys take 55.6 us instead of 49.6; with 4 or 48 instead of 12 no
+// measured case changes by more than 1.2 us.  The lengths may be far below the table's width, and
+// the second launch is then for little: 66 keys take 5.6 us with a table of 2 pages, 9.6 with 2048.)
 constexpr int kManyParts = 12;
 
 // Workspace: a flag and a Join per CTA, then two slots per CTA: for the part of an item that it leaves
@@ -711,7 +722,15 @@ cudaError_t launch(const AttentionArgs &args, cudaStream_t stream) {
 }
 
 // Which kernels a call needs: sequences are sorted by their number of query rows (new
-// tokens times heads of a group), on the device when the host does not know it.
+// tokens times heads of a group), on the device when the host does not know it.  Where the two
+// cross depends on how much else there is: for 16, 32, 48, 64, 96 and 128 rows a sequence this kernel
+// and the prompt kernel (from 32 on) take, in us,
+//   8 x 6000 keys of 128 values: 29, 45, 61, 75, 106, 136 and 56, 57, 57, 58, 59;
+//   8 x 6000 keys of 64:         18, 25, 34, 43, 59, 75 and 53, 53, 53, 54, 55;
+//   1 x 8000 keys of 128:        14, 17, 20, 22, 26, 31 and 32, 33, 33, 35, 35;
+//   1 x 300 keys of 128:         10, 11, 11, 11, 12, 12 and 13, 13, 13, 13, 13.
+// 64 lies between: full batches of 128 values would cross at 45, of 64 values at 90, single
+// sequences at 150.
 constexpr int kFewRows = 64;
 struct Kernels { bool few, many; int few_rows; };
 Kernels kernels_for(int max_q, bool uniform, int G) {

@@ -27,7 +27,7 @@
 // but leave the weights waiting: 152 us against 132), 512 for V, 1024 to bring in, turn and
 // store the codes.  A step takes 3100; a CTA beside its steps about 15000 (its queries and
 // first keys 8000, its last product and result 6000).  4096 tokens, 32 heads of 128 over 8:
-// 124 us, 1.1 PFLOP/s (0.58 of the rate of a library product).
+// 125 us, 1.1 PFLOP/s (0.58 of the rate of a library product).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -50,8 +50,8 @@ constexpr int kThreads = 16 * 32;              // whole warpgroups, for the regi
 constexpr int kSoftmaxRegs = 184, kConvertRegs = 80, kOtherRegs = 64;   // 2 x 184 + 80 + 64 = 4 x 128
 constexpr int kMinSteps = 2;                     // of a part
 constexpr int kShortSteps = 8;                   // of sequences whose tiles are never split
-constexpr float kCtaCost = 5.f;                   // what a CTA costs beside its steps, in steps
-constexpr float kJoinCost = 0.03f;               // what a part costs when it is joined
+constexpr float kCtaCost = 5.f;                  // what a CTA costs beside its steps, in steps (2, 10: nothing changes)
+constexpr float kJoinCost = 0.03f;               // what a part costs when it is joined (0.01: the same; 0.1: chunks 117 -> 140 us)
 constexpr int kMostCtas = 5 * kSms;              // where keys may be split
 constexpr int kLongSteps = 32;                   // of sequences whose tiles are split although they fill the SMs
 
@@ -827,9 +827,11 @@ PromptGrid prompt_grid(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk
     // The most parts that find_listed may choose.  Where splitting is in question, the list
     // and the join's launch cost 5-7 us (two prompts of 256 tokens: 18.9 us without, 25.3
     // with), and CTAs without a part 1.5 us each on their SM (4096 tokens, 512 tiles: 124 us
-    // against 150 with as many such); what it gains: 701 tokens behind 8300 beside three short
+    // against 150 with as many such then); what it gains: 701 tokens behind 8300 beside three short
     // prompts 127 -> 117 us, two of 512 behind 15500 (one shorter) 217 -> 135, eight of 100
-    // behind up to 5900 100 -> 65.
+    // behind up to 5900 100 -> 65.  The lengths are not known here, and the page table's width
+    // stands for them: with a table of 2048 pages of 64 a prompt of 66 tokens behind nothing takes
+    // 17.2 us and 100 MB of workspace, with one of 2 pages 10.2 us and none.
     const int64_t units = std::max<int64_t>(1, (int64_t)g.tiles * Hk), steps = (max_len + kKeys - 1) / kKeys;
     g.splits = steps < kShortSteps || (units >= kSms * 3 / 4 && steps < kLongSteps) ? 1
                : (int)std::max<int64_t>(1, std::min(std::min<int64_t>(steps / kMinSteps, kSms), kMostCtas / units));

@@ -22,8 +22,8 @@
 // 88 us for 16002 tokens).  Rows are loaded one set ahead of the one in work.
 //
 // Bound: HBM (T D (4 Hq + 6 Hk) bytes) for prompts, launch latency for decode.  16002 tokens
-// of 32 + 8 heads of 128 take 84 us, 4.2 TB/s (0.61 of a copy's rate; the CTAs of an SM hold
-// too few loads in flight for more); one token 4.0 us.
+// of 32 + 8 heads of 128 take 84.5 us, 4.1 TB/s (0.61 of a copy's rate: the CTAs of an SM hold
+// too few loads in flight this way); one token 3.9 us.
 #include <algorithm>
 #include <type_traits>
 

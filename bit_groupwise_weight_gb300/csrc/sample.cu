@@ -36,7 +36,7 @@
 // memory.  Bound: for few rows the chain of some twenty barriers of the CTA and three
 // (top-k) to six (top-p) of the cluster, for many the instructions of the pass that
 // weighs all tokens (some 35 a token, of which two at a quarter of the rate or less).
-// One row of 128256 in bfloat16 takes 16 us, 64 rows of them with top-p 53 us (0.3 TB/s),
+// One row of 128256 in bfloat16 takes 16 us, 64 rows of them with top-p 54 us (0.3 TB/s),
 // 256 rows in float32 of mixed settings 137 us (1.0 TB/s).
 #include <algorithm>
 
