@@ -42,6 +42,7 @@ from ._abi import (  # noqa: F401
 from .decoder import (  # noqa: F401
     attention,
     attention_workspace,
+    cache_values,
     empty_cache,
     kv_append,
     rotary_turns,
@@ -51,7 +52,7 @@ from .module import LowbitGateUp, LowbitLinear, quantize_  # noqa: F401
 
 __all__ = [
     "LowbitError", "LowbitGateUp", "LowbitLinear", "PATH_AUTO", "PATH_QMM", "PATH_QMV", "abi", "attention",
-    "attention_workspace", "empty_cache", "kv_append", "linear", "linear_ptr", "rotary_turns", "sample",
+    "attention_workspace", "cache_values", "empty_cache", "kv_append", "linear", "linear_ptr", "rotary_turns", "sample",
     "linear_swiglu", "linear_swiglu_ptr",
     "pack_weights", "packed_bytes", "quantize_weights", "select_path", "selftest_wait_timeout", "status_string", "unpack_weights",
     "quantize_", "wait_timeouts",

@@ -53,6 +53,14 @@ def _bind(lib):
     lib.lowbit_attention.restype = ci
     lib.lowbit_attention_workspace.argtypes = [ctypes.c_int32, vp, vp]
     lib.lowbit_attention_workspace.restype = ctypes.c_size_t
+    lib.lowbit_kv_append_ex.argtypes = lib.lowbit_kv_append4.argtypes = [vp, vp, vp, vp, vp]
+    lib.lowbit_kv_append_ex.restype = lib.lowbit_kv_append4.restype = ci
+    lib.lowbit_attention4.argtypes = [vp, vp, vp, vp]
+    lib.lowbit_attention4.restype = ci
+    lib.lowbit_attention4_workspace.argtypes = [ctypes.c_int32, vp, vp]
+    lib.lowbit_attention4_workspace.restype = ctypes.c_size_t
+    lib.lowbit_cache_values.argtypes = lib.lowbit_cache4_values.argtypes = [vp, vp, vp, vp]
+    lib.lowbit_cache_values.restype = lib.lowbit_cache4_values.restype = ci
     lib.lowbit_sample.argtypes = [vp, vp]
     lib.lowbit_sample.restype = ci
     lib.lowbit_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint32), ci]

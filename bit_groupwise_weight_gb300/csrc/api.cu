@@ -91,14 +91,17 @@ lowbit_status check_linear_args(const uint16_t *x, const uint8_t *w, const uint1
 bool empty(const lowbit_sequences *s) { return s->batch == 0 || s->tokens == 0; }
 
 // The sizes alone: what the workspace's size follows from.
-lowbit_status check_sizes(const lowbit_cache *c, const lowbit_sequences *s, int heads) {
+template <typename Cache>
+lowbit_status check_heads(const Cache *c) {
+    if (c->kv_heads <= 0 || c->kv_heads > 65535 || c->pages < 0 || (c->head_dim != 64 && c->head_dim != 128)) return LOWBIT_EINVAL;
+    return c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) != 0 ? LOWBIT_EINVAL : LOWBIT_OK;
+}
+template <typename Cache>
+lowbit_status check_sizes(const Cache *c, const lowbit_sequences *s, int heads) {
     if (c == nullptr || s == nullptr) return LOWBIT_EINVAL;
     if (s->batch < 0 || s->tokens < 0 || s->batch > kMaxDim || s->tokens > kMaxDim || s->width < 0 || s->width > kMaxDim)
         return LOWBIT_EINVAL;
-    if (c->kv_heads <= 0 || c->kv_heads > 65535 || heads <= 0 || heads % c->kv_heads != 0 || c->pages < 0 ||
-        (c->head_dim != 64 && c->head_dim != 128))
-        return LOWBIT_EINVAL;
-    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) != 0) return LOWBIT_EINVAL;
+    if (check_heads(c) != LOWBIT_OK || heads <= 0 || heads % c->kv_heads != 0) return LOWBIT_EINVAL;
     // Rows (tokens times heads of a group), lengths and a sequence's tiles stay inside int32.
     if ((int64_t)s->tokens * (heads / c->kv_heads) > kMaxDim || (int64_t)s->width * c->page > kMaxDim ||
         (int64_t)s->width * c->page * c->kv_heads > (int64_t)1 << 34)
@@ -108,23 +111,141 @@ lowbit_status check_sizes(const lowbit_cache *c, const lowbit_sequences *s, int 
     return c->pages == 0 || s->width == 0 ? LOWBIT_EINVAL : LOWBIT_OK;
 }
 
-lowbit_status check_cache(const lowbit_cache *c, const lowbit_sequences *s, int heads) {
+bool stride_ok(int64_t stride, int64_t least) { return stride >= least && stride % 16 == 0 && stride < (int64_t)1 << 40; }
+
+// A cache's pointers and strides.
+lowbit_status check_layout(const lowbit_cache *c) {
+    if (!c->k || !c->v || !c->k_exp || !c->v_exp || !aligned(c->k, 16) || !aligned(c->v, 16)) return LOWBIT_EINVAL;
+    const int64_t tile = (int64_t)c->page * c->head_dim;
+    return stride_ok(c->head_stride, tile) && stride_ok(c->page_stride, tile) ? LOWBIT_OK : LOWBIT_EINVAL;
+}
+lowbit_status check_layout(const lowbit_cache4 *c) {
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale || !aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) ||
+        !aligned(c->v_scale, 16))
+        return LOWBIT_EINVAL;
+    const int64_t tile = (int64_t)c->page * c->head_dim / 2, scales = (int64_t)c->page * c->head_dim / 32;
+    return stride_ok(c->head_stride, tile) && stride_ok(c->page_stride, tile) && stride_ok(c->scale_head_stride, scales) &&
+                   stride_ok(c->scale_page_stride, scales)
+               ? LOWBIT_OK : LOWBIT_EINVAL;
+}
+
+template <typename Cache>
+lowbit_status check_cache(const Cache *c, const lowbit_sequences *s, int heads) {
     const lowbit_status st = check_sizes(c, s, heads);
     if (st != LOWBIT_OK || empty(s)) return st;
     if (s->table_stride < s->width) return LOWBIT_EINVAL;
-    if (!c->k || !c->v || !c->k_exp || !c->v_exp || !s->page_table || !s->lens) return LOWBIT_EINVAL;
-    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(s->page_table, 4) || !aligned(s->lens, 4) ||
-        (s->cu_q != nullptr && !aligned(s->cu_q, 4)))
+    if (!s->page_table || !s->lens || !aligned(s->page_table, 4) || !aligned(s->lens, 4) || (s->cu_q != nullptr && !aligned(s->cu_q, 4)))
         return LOWBIT_EINVAL;
-    const int64_t tile = (int64_t)c->page * c->head_dim;
-    if (c->head_stride < tile || c->page_stride < tile || c->head_stride % 16 != 0 || c->page_stride % 16 != 0 ||
-        c->head_stride >= ((int64_t)1 << 40) || c->page_stride >= ((int64_t)1 << 40))
-        return LOWBIT_EINVAL;
-    return LOWBIT_OK;
+    return check_layout(c);
 }
 
 // Rows of head_dim 16-bit values that can be moved in 16-byte vectors.
 bool vector_rows(const void *p, int64_t token, int64_t head) { return aligned(p, 16) && token % 8 == 0 && head % 8 == 0; }
+
+// What a write into a cache of either kind is launched with, checked; *launch: whether there is anything to do.
+template <typename Cache>
+lowbit_status append_args(const lowbit_kv_append_args *a, const lowbit_kv_prologue *before, const Cache *c,
+                          const lowbit_sequences *s, lowbit::AppendArgs *out, bool *launch) {
+    if (a == nullptr) return LOWBIT_EINVAL;
+    lowbit_status st = check_cache(c, s, a->heads);
+    if (st != LOWBIT_OK) return st;
+    if (a->rotary_dim < 0 || a->rotary_dim > c->head_dim || a->rotary_dim % 2 != 0) return LOWBIT_EINVAL;
+    lowbit::AppendArgs &p = *out;
+    if (before != nullptr) {
+        if (before->q_norm != nullptr || before->k_norm != nullptr) {
+            const uintptr_t size = before->norm_dtype == LOWBIT_DTYPE_F32 ? 4 : 2;
+            if (before->norm_dtype != LOWBIT_DTYPE_F32 && before->norm_dtype != LOWBIT_DTYPE_BF16 && before->norm_dtype != LOWBIT_DTYPE_F16)
+                return LOWBIT_EINVAL;
+            if (!aligned(before->q_norm, size) || !aligned(before->k_norm, size) || !(before->eps >= 0.f && before->eps < 1e30f))
+                return LOWBIT_EINVAL;
+            p.q_norm = before->q_norm, p.k_norm = before->k_norm, p.norm_dtype = (int)before->norm_dtype, p.eps = before->eps;
+        }
+        if (before->positions != nullptr) {
+            if (!aligned(before->positions, 4) || before->axes < 1 || before->axes > 255) return LOWBIT_EINVAL;
+            p.positions = before->positions, p.axis = before->axis, p.axes = before->axes;
+            p.positions_token = before->positions_token;
+        }
+    }
+    if (empty(s)) return LOWBIT_OK;
+    if (!a->q || !a->k || !a->v || !a->q_out || !aligned(a->q, 2) || !aligned(a->k, 2) || !aligned(a->v, 2) ||
+        !aligned(a->q_out, 2))
+        return LOWBIT_EINVAL;
+    if (a->rotary_dim > 0 && (a->turns == nullptr || !aligned(a->turns, 8))) return LOWBIT_EINVAL;
+    if ((st = check_device()) != LOWBIT_OK) return st;
+    p.q = a->q, p.k = a->k, p.v = a->v, p.q_out = a->q_out;
+    p.k_cache = c->k, p.v_cache = c->v;
+    p.page_table = s->page_table, p.lens = s->lens, p.cu_q = s->cu_q, p.turns = a->turns;
+    p.q_token = a->q_token, p.q_head = a->q_head, p.k_token = a->k_token, p.k_head = a->k_head;
+    p.v_token = a->v_token, p.v_head = a->v_head, p.o_token = a->o_token, p.o_head = a->o_head;
+    p.page_stride = c->page_stride, p.head_stride = c->head_stride, p.table_stride = s->table_stride;
+    p.factor = a->factor;
+    p.T = s->tokens, p.B = s->batch, p.max_q = s->max_q, p.Hq = a->heads, p.Hk = c->kv_heads;
+    p.D = c->head_dim, p.P = c->page, p.pages = c->pages, p.width = s->width, p.R = a->rotary_dim;
+    p.interleaved = a->interleaved != 0;
+    p.qvec = vector_rows(a->q, a->q_token, a->q_head);
+    p.kvec = vector_rows(a->k, a->k_token, a->k_head);
+    p.vvec = vector_rows(a->v, a->v_token, a->v_head);
+    p.ovec = vector_rows(a->q_out, a->o_token, a->o_head);
+    *launch = true;
+    return LOWBIT_OK;
+}
+
+// The same of a cache's values.
+template <typename Cache>
+lowbit_status values_args(const Cache *c, uint16_t *k_out, uint16_t *v_out, lowbit::ValuesArgs *out, bool *launch) {
+    if (c == nullptr) return LOWBIT_EINVAL;
+    lowbit_status st = check_heads(c);
+    if (st != LOWBIT_OK || c->pages == 0) return st;
+    if ((st = check_layout(c)) != LOWBIT_OK) return st;
+    if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return LOWBIT_EINVAL;
+    if ((st = check_device()) != LOWBIT_OK) return st;
+    out->k = c->k, out->v = c->v, out->k_out = k_out, out->v_out = v_out;
+    out->page_stride = c->page_stride, out->head_stride = c->head_stride;
+    out->pages = c->pages, out->Hk = c->kv_heads, out->P = c->page, out->D = c->head_dim;
+    *launch = true;
+    return LOWBIT_OK;
+}
+
+template <typename Cache>
+size_t attention_workspace(int32_t heads, const Cache *c, const lowbit_sequences *s) {
+    if (check_sizes(c, s, heads) != LOWBIT_OK || empty(s)) return 0;
+    const bool uniform = s->cu_q == nullptr;
+    return lowbit::attention_workspace_bytes(s->tokens, s->batch, uniform ? s->tokens / s->batch : s->max_q, uniform,
+                                             heads, c->kv_heads, c->head_dim, (int64_t)s->width * c->page);
+}
+
+// What an attention over a cache of either kind is launched with, checked.
+template <typename Cache>
+lowbit_status attention_args(const lowbit_attention_args *a, const Cache *c, const lowbit_sequences *s, lowbit::AttentionArgs *out,
+                             bool *launch) {
+    if (a == nullptr) return LOWBIT_EINVAL;
+    lowbit_status st = check_cache(c, s, a->heads);
+    if (st != LOWBIT_OK) return st;
+    if (a->window < 0 || !(a->scale > -1e30f && a->scale < 1e30f)) return LOWBIT_EINVAL;
+    if (empty(s)) return LOWBIT_OK;
+    if (!a->q || !a->out || !aligned(a->q, 8) || !aligned(a->out, 8) || (a->lse != nullptr && !aligned(a->lse, 4)))
+        return LOWBIT_EINVAL;
+    if (a->q_token % 4 != 0 || a->q_head % 4 != 0 || a->o_token % 4 != 0 || a->o_head % 4 != 0) return LOWBIT_EINVAL;
+    if (a->workspace == nullptr || !aligned(a->workspace, 16) || a->workspace_bytes < attention_workspace(a->heads, c, s))
+        return LOWBIT_EINVAL;
+    if ((st = check_device()) != LOWBIT_OK) return st;
+    lowbit::AttentionArgs &p = *out;
+    p.q = a->q, p.out = a->out, p.lse = a->lse;
+    p.k_cache = c->k, p.v_cache = c->v;
+    p.page_table = s->page_table, p.lens = s->lens, p.cu_q = s->cu_q;
+    p.workspace = static_cast<float *>(a->workspace);
+    p.q_token = a->q_token, p.q_head = a->q_head, p.o_token = a->o_token, p.o_head = a->o_head;
+    p.lse_token = a->lse_token;
+    p.page_stride = c->page_stride, p.head_stride = c->head_stride, p.table_stride = s->table_stride;
+    p.scale_log2 = a->scale * 1.4426950408889634f;
+    p.T = s->tokens, p.B = s->batch, p.max_q = s->max_q, p.Hq = a->heads, p.Hk = c->kv_heads;
+    p.D = c->head_dim, p.P = c->page, p.pages = c->pages, p.width = s->width;
+    // A window of all positions hides nothing, and smaller ones keep positions less windows inside int32,
+    // also those of rows before position 0.
+    p.window = (int64_t)a->window >= (int64_t)s->width * c->page ? 0 : a->window;
+    *launch = true;
+    return LOWBIT_OK;
+}
 
 // Crossover between the decode kernels and the batched tensor-core kernel
 // (qmm), measured on GB300 in-stream at b = 4 for the Llama-3.1-8B shapes and
@@ -267,70 +388,76 @@ lowbit_status lowbit_linear_swiglu(const uint16_t *x, const uint8_t *packed_w, c
 
 lowbit_status lowbit_kv_append(const lowbit_kv_append_args *a, const lowbit_cache *c, const lowbit_sequences *s,
                                lowbit_stream_t stream) {
-    if (a == nullptr) return LOWBIT_EINVAL;
-    lowbit_status st = check_cache(c, s, a->heads);
-    if (st != LOWBIT_OK) return st;
-    if (a->rotary_dim < 0 || a->rotary_dim > c->head_dim || a->rotary_dim % 2 != 0) return LOWBIT_EINVAL;
-    if (s->batch == 0 || s->tokens == 0) return LOWBIT_OK;
-    if (!a->q || !a->k || !a->v || !a->q_out || !aligned(a->q, 2) || !aligned(a->k, 2) || !aligned(a->v, 2) ||
-        !aligned(a->q_out, 2))
-        return LOWBIT_EINVAL;
-    if (a->rotary_dim > 0 && (a->turns == nullptr || !aligned(a->turns, 8))) return LOWBIT_EINVAL;
-    if ((st = check_device()) != LOWBIT_OK) return st;
+    return lowbit_kv_append_ex(a, nullptr, c, s, stream);
+}
+
+lowbit_status lowbit_kv_append_ex(const lowbit_kv_append_args *a, const lowbit_kv_prologue *before, const lowbit_cache *c,
+                                  const lowbit_sequences *s, lowbit_stream_t stream) {
     lowbit::AppendArgs p{};
-    p.q = a->q, p.k = a->k, p.v = a->v, p.q_out = a->q_out;
-    p.k_cache = c->k, p.v_cache = c->v, p.k_exp = c->k_exp, p.v_exp = c->v_exp;
-    p.page_table = s->page_table, p.lens = s->lens, p.cu_q = s->cu_q, p.turns = a->turns;
-    p.q_token = a->q_token, p.q_head = a->q_head, p.k_token = a->k_token, p.k_head = a->k_head;
-    p.v_token = a->v_token, p.v_head = a->v_head, p.o_token = a->o_token, p.o_head = a->o_head;
-    p.page_stride = c->page_stride, p.head_stride = c->head_stride, p.table_stride = s->table_stride;
-    p.factor = a->factor;
-    p.T = s->tokens, p.B = s->batch, p.max_q = s->max_q, p.Hq = a->heads, p.Hk = c->kv_heads;
-    p.D = c->head_dim, p.P = c->page, p.pages = c->pages, p.width = s->width, p.R = a->rotary_dim;
-    p.interleaved = a->interleaved != 0;
-    p.qvec = vector_rows(a->q, a->q_token, a->q_head);
-    p.kvec = vector_rows(a->k, a->k_token, a->k_head);
-    p.vvec = vector_rows(a->v, a->v_token, a->v_head);
-    p.ovec = vector_rows(a->q_out, a->o_token, a->o_head);
+    bool launch = false;
+    const lowbit_status st = append_args(a, before, c, s, &p, &launch);
+    if (st != LOWBIT_OK || !launch) return st;
+    p.k_exp = c->k_exp, p.v_exp = c->v_exp;
     return from_cuda(lowbit::launch_kv_append(p, (cudaStream_t)stream));
 }
 
+lowbit_status lowbit_kv_append4(const lowbit_kv_append_args *a, const lowbit_kv_prologue *before, const lowbit_cache4 *c,
+                                const lowbit_sequences *s, lowbit_stream_t stream) {
+    lowbit::AppendArgs p{};
+    bool launch = false;
+    const lowbit_status st = append_args(a, before, c, s, &p, &launch);
+    if (st != LOWBIT_OK || !launch) return st;
+    p.k_scale = c->k_scale, p.v_scale = c->v_scale;
+    p.scale_page_stride = c->scale_page_stride, p.scale_head_stride = c->scale_head_stride;
+    return from_cuda(lowbit::launch_kv_append4(p, (cudaStream_t)stream));
+}
+
+lowbit_status lowbit_cache_values(const lowbit_cache *c, uint16_t *k_out, uint16_t *v_out, lowbit_stream_t stream) {
+    lowbit::ValuesArgs p{};
+    bool launch = false;
+    const lowbit_status st = values_args(c, k_out, v_out, &p, &launch);
+    if (st != LOWBIT_OK || !launch) return st;
+    p.k_exp = c->k_exp, p.v_exp = c->v_exp;
+    return from_cuda(lowbit::launch_cache_values(p, (cudaStream_t)stream));
+}
+
+lowbit_status lowbit_cache4_values(const lowbit_cache4 *c, uint16_t *k_out, uint16_t *v_out, lowbit_stream_t stream) {
+    lowbit::ValuesArgs p{};
+    bool launch = false;
+    const lowbit_status st = values_args(c, k_out, v_out, &p, &launch);
+    if (st != LOWBIT_OK || !launch) return st;
+    p.k_scale = c->k_scale, p.v_scale = c->v_scale;
+    p.scale_page_stride = c->scale_page_stride, p.scale_head_stride = c->scale_head_stride;
+    return from_cuda(lowbit::launch_cache_values(p, (cudaStream_t)stream));
+}
+
 size_t lowbit_attention_workspace(int32_t heads, const lowbit_cache *c, const lowbit_sequences *s) {
-    if (check_sizes(c, s, heads) != LOWBIT_OK || empty(s)) return 0;
-    const bool uniform = s->cu_q == nullptr;
-    return lowbit::attention_workspace_bytes(s->tokens, s->batch, uniform ? s->tokens / s->batch : s->max_q, uniform,
-                                             heads, c->kv_heads, c->head_dim, (int64_t)s->width * c->page);
+    return attention_workspace(heads, c, s);
+}
+
+size_t lowbit_attention4_workspace(int32_t heads, const lowbit_cache4 *c, const lowbit_sequences *s) {
+    return attention_workspace(heads, c, s);
 }
 
 lowbit_status lowbit_attention(const lowbit_attention_args *a, const lowbit_cache *c, const lowbit_sequences *s,
                                lowbit_stream_t stream) {
-    if (a == nullptr) return LOWBIT_EINVAL;
-    lowbit_status st = check_cache(c, s, a->heads);
-    if (st != LOWBIT_OK) return st;
-    if (a->window < 0 || !(a->scale > -1e30f && a->scale < 1e30f)) return LOWBIT_EINVAL;
-    if (s->batch == 0 || s->tokens == 0) return LOWBIT_OK;
-    if (!a->q || !a->out || !aligned(a->q, 8) || !aligned(a->out, 8) || (a->lse != nullptr && !aligned(a->lse, 4)))
-        return LOWBIT_EINVAL;
-    if (a->q_token % 4 != 0 || a->q_head % 4 != 0 || a->o_token % 4 != 0 || a->o_head % 4 != 0) return LOWBIT_EINVAL;
-    if (a->workspace == nullptr || !aligned(a->workspace, 16) ||
-        a->workspace_bytes < lowbit_attention_workspace(a->heads, c, s))
-        return LOWBIT_EINVAL;
-    if ((st = check_device()) != LOWBIT_OK) return st;
     lowbit::AttentionArgs p{};
-    p.q = a->q, p.out = a->out, p.lse = a->lse;
-    p.k_cache = c->k, p.v_cache = c->v, p.k_exp = c->k_exp, p.v_exp = c->v_exp;
-    p.page_table = s->page_table, p.lens = s->lens, p.cu_q = s->cu_q;
-    p.workspace = static_cast<float *>(a->workspace);
-    p.q_token = a->q_token, p.q_head = a->q_head, p.o_token = a->o_token, p.o_head = a->o_head;
-    p.lse_token = a->lse_token;
-    p.page_stride = c->page_stride, p.head_stride = c->head_stride, p.table_stride = s->table_stride;
-    p.scale_log2 = a->scale * 1.4426950408889634f;
-    p.T = s->tokens, p.B = s->batch, p.max_q = s->max_q, p.Hq = a->heads, p.Hk = c->kv_heads;
-    p.D = c->head_dim, p.P = c->page, p.pages = c->pages, p.width = s->width;
-    // A window of all positions hides nothing, and smaller ones keep positions less windows inside int32,
-    // also those of rows before position 0.
-    p.window = (int64_t)a->window >= (int64_t)s->width * c->page ? 0 : a->window;
+    bool launch = false;
+    const lowbit_status st = attention_args(a, c, s, &p, &launch);
+    if (st != LOWBIT_OK || !launch) return st;
+    p.k_exp = c->k_exp, p.v_exp = c->v_exp;
     return from_cuda(lowbit::launch_attention(p, (cudaStream_t)stream));
+}
+
+lowbit_status lowbit_attention4(const lowbit_attention_args *a, const lowbit_cache4 *c, const lowbit_sequences *s,
+                                lowbit_stream_t stream) {
+    lowbit::AttentionArgs p{};
+    bool launch = false;
+    const lowbit_status st = attention_args(a, c, s, &p, &launch);
+    if (st != LOWBIT_OK || !launch) return st;
+    p.k_scale = c->k_scale, p.v_scale = c->v_scale;
+    p.scale_page_stride = c->scale_page_stride, p.scale_head_stride = c->scale_head_stride;
+    return LOWBIT_EUNSUPPORTED;
 }
 
 lowbit_status lowbit_sample(const lowbit_sample_args *a, lowbit_stream_t stream) {

@@ -28,9 +28,14 @@ using at::ScalarType;
 using at::Tensor;
 
 struct {
-    decltype(&lowbit_kv_append) kv_append;
+    decltype(&lowbit_kv_append_ex) kv_append;
+    decltype(&lowbit_kv_append4) kv_append4;
     decltype(&lowbit_attention) attention;
+    decltype(&lowbit_attention4) attention4;
     decltype(&lowbit_attention_workspace) workspace;
+    decltype(&lowbit_attention4_workspace) workspace4;
+    decltype(&lowbit_cache_values) values;
+    decltype(&lowbit_cache4_values) values4;
     decltype(&lowbit_sample) sample;
 } fn;
 
@@ -60,22 +65,49 @@ bool rows(const Tensor *t, int dev, int64_t T, int64_t H, int64_t D, Rows *r) {
 
 bool small(int64_t n) { return n >= 0 && n <= INT32_MAX; }
 
-bool cache_of(PyObject *const *a, int dev, int64_t dim, lowbit_cache *c) {
-    const Tensor *k = tensor(a[0]), *v = tensor(a[1]), *e[2] = {tensor(a[2]), tensor(a[3])};
+// A cache of either kind.
+struct Cache {
+    bool four;
+    lowbit_cache c8;
+    lowbit_cache4 c4;
+    int32_t kv_heads() const { return four ? c4.kv_heads : c8.kv_heads; }
+};
+
+// Two tensors [pages, heads, page, n] of the same strides, each head's page contiguous.
+bool pages_of(const Tensor *k, const Tensor *v, int dev, ScalarType type, int64_t n) {
     for (const Tensor *t : {k, v})
         if (t == nullptr || !t->is_cuda() || t->get_device() != dev || t->dim() != 4 ||
-            (t->scalar_type() != ScalarType::Float8_e4m3fn && t->scalar_type() != ScalarType::Byte))
+            (t->scalar_type() != type && t->scalar_type() != ScalarType::Byte))
             return false;
-    if (k->sizes() != v->sizes() || k->strides() != v->strides() || k->size(3) != dim) return false;
-    if (k->numel() > 0 && (k->stride(2) != dim || k->stride(3) != 1)) return false;
-    if (!small(k->size(0)) || !small(k->size(1)) || !small(k->size(2))) return false;
+    if (k->sizes() != v->sizes() || k->strides() != v->strides() || k->size(3) != n) return false;
+    if (k->numel() > 0 && (k->stride(2) != n || k->stride(3) != 1)) return false;
+    return small(k->size(0)) && small(k->size(1)) && small(k->size(2));
+}
+
+template <typename T>
+T *at(const Tensor *t) { return static_cast<T *>(t->data_ptr()); }
+
+bool cache_of(PyObject *const *a, int dev, int64_t dim, Cache *c) {
+    const Tensor *k = tensor(a[0]), *v = tensor(a[1]), *e[2] = {tensor(a[2]), tensor(a[3])};
+    *c = {};
+    c->four = e[0] != nullptr && e[0]->dim() == 4;
+    if (c->four) {                               // the 4-bit kind: a scale for each 32 values
+        if (dim % 32 != 0 || !pages_of(k, v, dev, ScalarType::Byte, dim / 2) || !pages_of(e[0], e[1], dev, ScalarType::Float8_e5m2, dim / 32))
+            return false;
+        if (k->size(0) != e[0]->size(0) || k->size(1) != e[0]->size(1) || k->size(2) != e[0]->size(2)) return false;
+        c->c4.k = at<uint8_t>(k), c->c4.v = at<uint8_t>(v), c->c4.k_scale = at<uint8_t>(e[0]), c->c4.v_scale = at<uint8_t>(e[1]);
+        c->c4.page_stride = k->stride(0), c->c4.head_stride = k->stride(1);
+        c->c4.scale_page_stride = e[0]->stride(0), c->c4.scale_head_stride = e[0]->stride(1);
+        c->c4.pages = (int32_t)k->size(0), c->c4.kv_heads = (int32_t)k->size(1), c->c4.page = (int32_t)k->size(2);
+        c->c4.head_dim = (int32_t)dim;
+        return true;
+    }
+    if (!pages_of(k, v, dev, ScalarType::Float8_e4m3fn, dim)) return false;
     for (const Tensor *t : e)
         if (!is(t, ScalarType::Char, dev, 2) || t->size(0) != k->size(0) || t->size(1) != k->size(1) || !t->is_contiguous()) return false;
-    *c = {};
-    c->k = static_cast<uint8_t *>(k->data_ptr()), c->v = static_cast<uint8_t *>(v->data_ptr());
-    c->k_exp = static_cast<int8_t *>(e[0]->data_ptr()), c->v_exp = static_cast<int8_t *>(e[1]->data_ptr());
-    c->page_stride = k->stride(0), c->head_stride = k->stride(1);
-    c->pages = (int32_t)k->size(0), c->kv_heads = (int32_t)k->size(1), c->page = (int32_t)k->size(2), c->head_dim = (int32_t)dim;
+    c->c8.k = at<uint8_t>(k), c->c8.v = at<uint8_t>(v), c->c8.k_exp = at<int8_t>(e[0]), c->c8.v_exp = at<int8_t>(e[1]);
+    c->c8.page_stride = k->stride(0), c->c8.head_stride = k->stride(1);
+    c->c8.pages = (int32_t)k->size(0), c->c8.kv_heads = (int32_t)k->size(1), c->c8.page = (int32_t)k->size(2), c->c8.head_dim = (int32_t)dim;
     return true;
 }
 
@@ -126,25 +158,58 @@ PyObject *refuse() { Py_RETURN_NONE; }
 PyObject *result(lowbit_status st, const Tensor &out) { return st != LOWBIT_OK ? PyLong_FromLong(st) : THPVariable_Wrap(out); }
 lowbit_stream_t stream(int dev) { return reinterpret_cast<lowbit_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream()); }
 
-// q, k, v, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q, max_q, turns, interleaved, factor, out
+// What stands before the write; a: q_norm, k_norm, eps, positions, axes.
+bool prologue_of(PyObject *const *a, int dev, int64_t T, int64_t D, int64_t pairs, lowbit_kv_prologue *b) {
+    *b = {};
+    const Tensor *first = nullptr;
+    const void **norms[2] = {&b->q_norm, &b->k_norm};
+    for (int i = 0; i < 2; ++i) {
+        if (a[i] == Py_None) continue;
+        const Tensor *w = tensor(a[i]);
+        if (w == nullptr || (first != nullptr && w->scalar_type() != first->scalar_type()) || !vector(a[i], w->scalar_type(), dev, D, norms[i]))
+            return false;
+        switch (w->scalar_type()) {
+            case ScalarType::Float: b->norm_dtype = LOWBIT_DTYPE_F32; break;
+            case ScalarType::BFloat16: b->norm_dtype = LOWBIT_DTYPE_BF16; break;
+            case ScalarType::Half: b->norm_dtype = LOWBIT_DTYPE_F16; break;
+            default: return false;
+        }
+        first = w;
+    }
+    if (!number(a[2], &b->eps)) return false;
+    if (a[3] == Py_None) return a[4] == Py_None;
+    const Tensor *p = tensor(a[3]);
+    if (p == nullptr || p->dim() < 1 || !is(p, ScalarType::Int, dev, p->dim() == 1 ? 1 : 2) || p->size(0) != T) return false;
+    const int64_t axes = p->dim() == 1 ? 1 : p->size(1);
+    if (axes < 1 || axes > 255 || (axes > 1 && (p->stride(1) != 1 || a[4] == Py_None))) return false;
+    if (a[4] != Py_None && !vector(a[4], ScalarType::Byte, dev, pairs, &b->axis)) return false;
+    b->positions = at<int32_t>(p), b->positions_token = p->stride(0), b->axes = (int32_t)axes;
+    // An empty tensor has no address: nothing of it is read, but positions they are.
+    return b->positions != nullptr || T == 0;
+}
+
+// q, k, v, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q, max_q, turns, interleaved, factor, out[, q_norm, k_norm,
+// eps, positions, axes]
 PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (n != 15) return refuse();
+    if (n != 15 && n != 20) return refuse();
     const Tensor *q = tensor(a[0]);
     if (q == nullptr || !q->is_cuda() || q->dim() != 3) return refuse();
     const int dev = q->get_device();
     const int64_t T = q->size(0), H = q->size(1), D = q->size(2);
     Rows rq, rk, rv, ro;
-    lowbit_cache c;
+    Cache c;
     lowbit_sequences s;
+    lowbit_kv_prologue before = {};
     lowbit_kv_append_args args = {};
-    if (!small(H) || !small(D) || !rows(q, dev, T, H, D, &rq) || !cache_of(a + 3, dev, D, &c) || !rows(tensor(a[1]), dev, T, c.kv_heads, D, &rk) ||
-        !rows(tensor(a[2]), dev, T, c.kv_heads, D, &rv) || !sequences_of(a + 7, dev, T, &s) || !number(a[13], &args.factor))
+    if (!small(H) || !small(D) || !rows(q, dev, T, H, D, &rq) || !cache_of(a + 3, dev, D, &c) || !rows(tensor(a[1]), dev, T, c.kv_heads(), D, &rk) ||
+        !rows(tensor(a[2]), dev, T, c.kv_heads(), D, &rv) || !sequences_of(a + 7, dev, T, &s) || !number(a[13], &args.factor))
         return refuse();
     if (a[11] != Py_None) {
         const Tensor *t = tensor(a[11]);
         if (t == nullptr || t->dim() != 1 || t->size(0) > 4096 || !vector(a[11], ScalarType::Long, dev, t->size(0), &args.turns)) return refuse();
         args.rotary_dim = 2 * (int32_t)t->size(0);
     }
+    if (n == 20 && !prologue_of(a + 15, dev, T, D, args.rotary_dim / 2, &before)) return refuse();
     const int interleaved = PyObject_IsTrue(a[12]);
     if (interleaved < 0) return PyErr_Clear(), refuse();
     const c10::cuda::OptionalCUDAGuard guard(q->device());
@@ -154,7 +219,7 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     args.q_token = rq.token, args.q_head = rq.head, args.k_token = rk.token, args.k_head = rk.head;
     args.v_token = rv.token, args.v_head = rv.head, args.o_token = ro.token, args.o_head = ro.head;
     args.heads = (int32_t)H, args.interleaved = interleaved;
-    return result(fn.kv_append(&args, &c, &s, stream(dev)), out);
+    return result(c.four ? fn.kv_append4(&args, &before, &c.c4, &s, stream(dev)) : fn.kv_append(&args, &before, &c.c8, &s, stream(dev)), out);
 }
 
 // q, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q, max_q, scale, window, out, lse, workspace
@@ -165,7 +230,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int dev = q->get_device();
     const int64_t T = q->size(0), H = q->size(1), D = q->size(2);
     Rows rq, ro;
-    lowbit_cache c;
+    Cache c;
     lowbit_sequences s;
     lowbit_attention_args args = {};
     if (!small(H) || !small(D) || !rows(q, dev, T, H, D, &rq) || !cache_of(a + 1, dev, D, &c) || !sequences_of(a + 5, dev, T, &s) ||
@@ -183,7 +248,8 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!out.defined() || !rows(&out, dev, T, H, D, &ro)) return refuse();
     Tensor own;
     if (a[13] == Py_None) {
-        own = at::empty({(int64_t)fn.workspace((int32_t)H, &c, &s)}, q->options().dtype(at::kByte));
+        const size_t bytes = c.four ? fn.workspace4((int32_t)H, &c.c4, &s) : fn.workspace((int32_t)H, &c.c8, &s);
+        own = at::empty({(int64_t)bytes}, q->options().dtype(at::kByte));
         args.workspace = own.data_ptr(), args.workspace_bytes = (size_t)own.numel();
     } else {
         const Tensor *w = tensor(a[13]);
@@ -193,7 +259,41 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     args.q = rq.at, args.out = ro.at;
     args.q_token = rq.token, args.q_head = rq.head, args.o_token = ro.token, args.o_head = ro.head;
     args.heads = (int32_t)H;
-    return result(fn.attention(&args, &c, &s, stream(dev)), out);
+    return result(c.four ? fn.attention4(&args, &c.c4, &s, stream(dev)) : fn.attention(&args, &c.c8, &s, stream(dev)), out);
+}
+
+// k_cache, v_cache, k_exp, v_exp, k_out, v_out
+PyObject *cache_values(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 6) return refuse();
+    const Tensor *k = tensor(a[0]), *e = tensor(a[2]);
+    if (k == nullptr || !k->is_cuda() || k->dim() != 4 || e == nullptr || !small(k->size(3))) return refuse();
+    const int dev = k->get_device();
+    const int64_t D = k->size(3) * (e->dim() == 4 ? 2 : 1);
+    Cache c;
+    if (!cache_of(a, dev, D, &c)) return refuse();
+    const c10::cuda::OptionalCUDAGuard guard(k->device());
+    Tensor out[2];
+    for (int i = 0; i < 2; ++i) {
+        if (a[4 + i] == Py_None) {
+            out[i] = at::empty({k->size(0), k->size(1), k->size(2), D}, k->options().dtype(at::kBFloat16));
+            continue;
+        }
+        const Tensor *t = tensor(a[4 + i]);
+        if (!is(t, ScalarType::BFloat16, dev, 4) || t->size(0) != k->size(0) || t->size(1) != k->size(1) || t->size(2) != k->size(2) ||
+            t->size(3) != D || !t->is_contiguous())
+            return refuse();
+        out[i] = *t;
+    }
+    uint16_t *ko = at<uint16_t>(&out[0]), *vo = at<uint16_t>(&out[1]);
+    const lowbit_status st = c.four ? fn.values4(&c.c4, ko, vo, stream(dev)) : fn.values(&c.c8, ko, vo, stream(dev));
+    if (st != LOWBIT_OK) return PyLong_FromLong(st);
+    PyObject *pair = PyTuple_New(2);
+    for (int i = 0; i < 2 && pair != nullptr; ++i) {
+        PyObject *o = THPVariable_Wrap(out[i]);
+        if (o == nullptr) Py_CLEAR(pair);
+        else PyTuple_SET_ITEM(pair, i, o);
+    }
+    return pair;
 }
 
 // logits, u, temperature, top_k, top_p, min_p, out, logprob
@@ -230,14 +330,17 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return result(fn.sample(&args, stream(dev)), out);
 }
 
-// The addresses of lowbit_kv_append, _attention, _attention_workspace and _sample.
+// The addresses of the library's functions, in the order of `fn`.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    void *p[4];
-    if (n != 4) return PyErr_SetString(PyExc_TypeError, "bind takes four addresses"), nullptr;
-    for (int i = 0; i < 4; ++i)
+    constexpr int kFunctions = 9;
+    void *p[kFunctions];
+    if (n != kFunctions) return PyErr_SetString(PyExc_TypeError, "bind takes nine addresses"), nullptr;
+    for (int i = 0; i < kFunctions; ++i)
         if ((p[i] = PyLong_AsVoidPtr(a[i])) == nullptr) return PyErr_Occurred() ? nullptr : (PyErr_SetString(PyExc_ValueError, "null address"), nullptr);
-    fn = {reinterpret_cast<decltype(fn.kv_append)>(p[0]), reinterpret_cast<decltype(fn.attention)>(p[1]),
-          reinterpret_cast<decltype(fn.workspace)>(p[2]), reinterpret_cast<decltype(fn.sample)>(p[3])};
+    int i = 0;
+    auto next = [&](auto &f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(p[i++]); };
+    next(fn.kv_append), next(fn.kv_append4), next(fn.attention), next(fn.attention4), next(fn.workspace), next(fn.workspace4);
+    next(fn.values), next(fn.values4), next(fn.sample);
     Py_RETURN_NONE;
 }
 
@@ -250,7 +353,7 @@ PyObject *guarded(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(guarded<name>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(bind), METHOD(kv_append), METHOD(attention), METHOD(sample), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(bind), METHOD(kv_append), METHOD(attention), METHOD(cache_values), METHOD(sample), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lowbit_torch", "Hot path of the decoder operators' binding.", -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -27,12 +27,14 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.cuh"
+#include "append.cuh"
 #include "fp8.cuh"
 #include "ptx.cuh"
 
 namespace lowbit {
 namespace {
+
+using namespace append;
 
 // The big CTA holds 64 tokens of 128 values (128 of 64) in vectors of 8, the small one
 // 4 (8): fewer registers and instructions for decode (5.4 -> 4.5 us a call).
@@ -42,9 +44,6 @@ constexpr int kVecsOf = THREADS == kBigThreads ? 4 : 1;       // vectors of a th
 template <int THREADS>
 constexpr int kPerSm = 512 / THREADS;                         // CTAs of an SM
 
-// How rows are read and rotated: any layout value by value, or in 16-byte vectors
-// with the pairs' halves, or neighbours, in whole vectors.
-enum Form { kAny, kHalves, kNeighbours };
 enum Kind { kKey, kValue, kQuery };
 
 struct Seq { int start, n, len; };
@@ -67,23 +66,6 @@ __device__ __forceinline__ Seq sequence(const AppendArgs &p, int b) {
     return s;
 }
 
-__device__ __forceinline__ void widen(const uint4 &v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
-
-// Eight consecutive bf16 values, as they are.
-template <Form FORM>
-__device__ __forceinline__ uint4 load8(const uint16_t *p) {
-    if constexpr (FORM != kAny) return *reinterpret_cast<const uint4 *>(p);
-    return make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16, p[4] | (uint32_t)p[5] << 16,
-                      p[6] | (uint32_t)p[7] << 16);
-}
-
 // A thread's vectors of a set of rows: its own values and, for kHalves, their mates.
 template <Form FORM, int kVecs>
 struct Rows {
@@ -93,10 +75,11 @@ struct Rows {
 
 // Values d0 .. d0+7 of a row, rotated.  cs, sn: the token's cosines and sines, one a
 // pair.  Products and sums are rounded one by one (not contracted): the page's
-// exponent then follows from the same fp32 values in any implementation.
-template <Form FORM>
+// exponent then follows from the same fp32 values in any implementation.  With PRE, x comes
+// normed, and its mates are: times `norm`, times their weights `wt`.
+template <Form FORM, bool PRE>
 __device__ __forceinline__ void rotate(const AppendArgs &p, const uint16_t *row, int d0, const uint4 &mate, const float *cs,
-                                       const float *sn, float (&x)[8]) {
+                                       const float *sn, float (&x)[8], float norm, const float *wt) {
     if (d0 >= p.R) return;
     const int half = p.R >> 1;
     if constexpr (FORM == kHalves) {
@@ -105,6 +88,7 @@ __device__ __forceinline__ void rotate(const AppendArgs &p, const uint16_t *row,
         const uint32_t flip = upper ? 0u : 0x80008000u;
         float y[8];
         widen(make_uint4(mate.x ^ flip, mate.y ^ flip, mate.z ^ flip, mate.w ^ flip), y);
+        if constexpr (PRE) weigh(y, norm, wt + (upper ? j0 : d0 + half));
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
             const float4 c = *reinterpret_cast<const float4 *>(cs + j0 + i), s = *reinterpret_cast<const float4 *>(sn + j0 + i);
@@ -141,7 +125,8 @@ __device__ __forceinline__ void rotate(const AppendArgs &p, const uint16_t *row,
             if (d < p.R) {
                 const bool upper = d >= half;
                 const int j = upper ? d - half : d;
-                const float y = __uint_as_float((uint32_t)row[upper ? j : d + half] << 16);
+                float y = __uint_as_float((uint32_t)row[upper ? j : d + half] << 16);
+                if constexpr (PRE) y = __fmul_rn(__fmul_rn(y, norm), wt[upper ? j : d + half]);
                 const float t = __fmul_rn(x[i], cs[j]), u = __fmul_rn(y, sn[j]);
                 x[i] = upper ? __fadd_rn(u, t) : __fsub_rn(t, u);
             }
@@ -149,12 +134,14 @@ __device__ __forceinline__ void rotate(const AppendArgs &p, const uint16_t *row,
     }
 }
 
-template <int THREADS, int D, Form FORM>
+// PRE: with norms of q or k, or positions of the caller's own.
+template <int THREADS, int D, Form FORM, bool PRE>
 __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(const AppendArgs p) {
     constexpr int kVecs = kVecsOf<THREADS>;
     constexpr int kRow = D / 8, kStep = THREADS / kRow, kChunk = kStep * kVecs;      // vectors of a row; tokens apart; of a set
     extern __shared__ __align__(16) float table[];        // [tokens][R / 2] cosines, then sines
     __shared__ float red[2][THREADS / 32];
+    __shared__ __align__(16) float weights[2][PRE ? D : 4];              // of the norms of q and k
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
 
@@ -195,6 +182,13 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
     int8_t *k_exp = p.k_exp + (int64_t)page * p.Hk + head, *v_exp = p.v_exp + (int64_t)page * p.Hk + head;
     const int was[2] = {older ? *k_exp : kExpMin, older ? *v_exp : kExpMin};
     int phase = 0;
+    if constexpr (PRE) {
+        for (int i = tid; i < 2 * D; i += THREADS) {
+            const void *w = i < D ? p.q_norm : p.k_norm;
+            weights[i / D][i % D] = w == nullptr ? 1.f : norm_weight(w, p.norm_dtype, i % D);
+        }
+        __syncthreads();
+    }
 
     // Cosines and sines of tokens t0 .. t0 + nt.
     auto make_table = [&](int t0, int nt) {
@@ -202,12 +196,8 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
         __syncthreads();
         for (int i = tid; i < nt * half; i += THREADS) {
             const int t = i / half, jj = i - t * half;
-            // As a signed fraction of a turn, the nearest way round.
-            const int32_t ph = (int32_t)(((uint64_t)(int64_t)(t0 + t) * (uint64_t)p.turns[jj]) >> 32);
-            float sn, cs;
-            sincosf((float)ph * 1.4629180792671596e-9f, &sn, &cs);        // 2 pi / 2^32
-            table[i] = __fmul_rn(cs, p.factor);
-            table[p.table_tokens * half + i] = __fmul_rn(sn, p.factor);
+            const int pos = PRE ? position_of(p, s.start + (t0 - first) + t, t0 + t, jj) : t0 + t;
+            turn_of(p, pos, jj, table[i], table[p.table_tokens * half + i]);
         }
         __syncthreads();
     };
@@ -221,9 +211,16 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
                 if (rotated && mated && in) r.mate[v] = *reinterpret_cast<const uint4 *>(row + j0);
         }
     };
-    auto turned = [&](const Rows<FORM, kVecs> &r, int v, const uint16_t *row, int t, float (&x)[8]) {
+    auto turned = [&](const Rows<FORM, kVecs> &r, int v, const uint16_t *row, int t, float (&x)[8], int kind) {
         widen(r.own[v], x);
-        rotate<FORM>(p, row, d0, r.mate[FORM == kHalves ? v : 0], table + t * half, table + (p.table_tokens + t) * half, x);
+        const float *wt = weights[kind == kQuery ? 0 : 1];
+        float norm = 1.f;
+        if constexpr (PRE) {
+            if ((kind == kQuery ? p.q_norm : p.k_norm) != nullptr) norm = row_norm<kRow>(x, p.eps);
+            weigh(x, norm, wt + d0);
+        }
+        rotate<FORM, PRE>(p, row, d0, r.mate[FORM == kHalves ? v : 0], table + t * half, table + (p.table_tokens + t) * half, x,
+                          norm, wt);
     };
     // Largest value over the CTA.
     auto reduce = [&](float m) {
@@ -254,7 +251,7 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) {
                 const int t = t_in + v * kStep;
-                if (kind == kKey && t < nt) turned(r, v, row + v * pitch, t, x[v]);
+                if (kind == kKey && t < nt) turned(r, v, row + v * pitch, t, x[v], kKey);
                 else widen(r.own[v], x[v]);
             }
         };
@@ -342,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
             for (int v = 0; v < kVecs; ++v) {
                 const int t = t_in + v * kStep;
                 float y[8];
-                if (t < nt) turned(x, v, q + h * p.q_head + v * kStep * p.q_token, t, y);
+                if (t < nt) turned(x, v, q + h * p.q_head + v * kStep * p.q_token, t, y, kQuery);
                 if (FORM == kAny) __syncwarp();
                 if (t < nt) {
                     uint16_t *to = o + h * p.o_head + v * kStep * p.o_token;
@@ -370,17 +367,24 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
     }
 }
 
-template <int THREADS, int D>
+template <int THREADS, int D, bool PRE>
 cudaError_t launch(AppendArgs &p, int n, int64_t gx, cudaStream_t stream) {
     constexpr int kChunk = THREADS / (D / 8) * kVecsOf<THREADS>;
     const bool vec = p.qvec && p.kvec && p.vvec && p.ovec;
-    const auto kernel = vec && p.interleaved && p.R % 8 == 0 ? kv_append_kernel<THREADS, D, kNeighbours>
-                        : vec && !p.interleaved && p.R % 16 == 0 ? kv_append_kernel<THREADS, D, kHalves>
-                                                                 : kv_append_kernel<THREADS, D, kAny>;
+    const auto kernel = vec && p.interleaved && p.R % 8 == 0 ? kv_append_kernel<THREADS, D, kNeighbours, PRE>
+                        : vec && !p.interleaved && p.R % 16 == 0 ? kv_append_kernel<THREADS, D, kHalves, PRE>
+                                                                 : kv_append_kernel<THREADS, D, kAny, PRE>;
     p.table_tokens = std::min(std::min(n, p.P), kChunk);
     static_assert(kChunk * D * sizeof(float) <= 48 * 1024, "the table fits what a kernel may use without asking");
     const size_t smem = (size_t)p.table_tokens * (size_t)p.R * sizeof(float);
     return launch_pdl(kernel, dim3((unsigned)gx, (unsigned)p.Hk), dim3(THREADS), smem, stream, (const AppendArgs)p);
+}
+
+template <bool PRE>
+cudaError_t launch_sized(AppendArgs &p, int n, int64_t gx, bool small, cudaStream_t stream) {
+    if (p.D == 128)
+        return small ? launch<kSmallThreads, 128, PRE>(p, n, gx, stream) : launch<kBigThreads, 128, PRE>(p, n, gx, stream);
+    return small ? launch<kSmallThreads, 64, PRE>(p, n, gx, stream) : launch<kBigThreads, 64, PRE>(p, n, gx, stream);
 }
 
 }  // namespace
@@ -396,8 +400,8 @@ cudaError_t launch_kv_append(const AppendArgs &args, cudaStream_t stream) {
     p.units = n == 1 ? 1 : (n - 1) / p.P + 2;
     const int64_t gx = p.cu_q == nullptr ? (int64_t)p.B * p.units : (int64_t)p.T / p.P + 2 * (int64_t)p.B;
     const bool small = std::min(n, p.P) * p.D <= kSmallThreads * kVecsOf<kSmallThreads> * 8;
-    if (p.D == 128) return small ? launch<kSmallThreads, 128>(p, n, gx, stream) : launch<kBigThreads, 128>(p, n, gx, stream);
-    return small ? launch<kSmallThreads, 64>(p, n, gx, stream) : launch<kBigThreads, 64>(p, n, gx, stream);
+    const bool pre = p.q_norm != nullptr || p.k_norm != nullptr || p.positions != nullptr;
+    return pre ? launch_sized<true>(p, n, gx, small, stream) : launch_sized<false>(p, n, gx, small, stream);
 }
 
 }  // namespace lowbit

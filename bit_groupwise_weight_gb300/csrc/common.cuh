@@ -186,8 +186,29 @@ struct AppendArgs {
     int T, B, max_q, Hq, Hk, D, P, pages, width, R;
     int G, n, pshift, units, table_tokens;                              // set by launch_kv_append
     bool interleaved, qvec, kvec, vvec, ovec;
+    // Norms of the heads (null: none) and positions of the caller's own (null: places in the sequence).
+    const void *q_norm, *k_norm;
+    const int32_t *positions;
+    const uint8_t *axis;                                                // of a pair; null: the first
+    int64_t positions_token;
+    float eps;
+    int norm_dtype, axes;
+    // The 4-bit cache's scales (cache4.cu).
+    uint8_t *k_scale, *v_scale;
+    int64_t scale_page_stride, scale_head_stride;
 };
 cudaError_t launch_kv_append(const AppendArgs &args, cudaStream_t stream);
+cudaError_t launch_kv_append4(const AppendArgs &args, cudaStream_t stream);   // into the 4-bit cache (cache4.cu)
+// The values that a cache holds, bf16 [pages, Hk, P, D] (cache4.cu); exps of the 8-bit one, or scales of the 4-bit one.
+struct ValuesArgs {
+    const uint8_t *k, *v;
+    const int8_t *k_exp, *v_exp;
+    const uint8_t *k_scale, *v_scale;
+    uint16_t *k_out, *v_out;
+    int64_t page_stride, head_stride, scale_page_stride, scale_head_stride;
+    int pages, Hk, P, D;
+};
+cudaError_t launch_cache_values(const ValuesArgs &args, cudaStream_t stream);
 // Attention over that cache (attention.cu).
 struct AttentionArgs {
     const uint16_t *q;
@@ -195,6 +216,8 @@ struct AttentionArgs {
     float *lse;                          // may be null
     const uint8_t *k_cache, *v_cache;
     const int8_t *k_exp, *v_exp;
+    const uint8_t *k_scale, *v_scale;    // of a 4-bit cache; null: an 8-bit one
+    int64_t scale_page_stride, scale_head_stride;
     const int32_t *page_table, *lens, *cu_q;
     float *workspace;
     int64_t q_token, q_head, o_token, o_head, lse_token;

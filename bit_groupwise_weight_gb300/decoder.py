@@ -1,5 +1,5 @@
-"""What a decode step does between the linear layers: rotary positions and the write
-into an 8-bit key-value cache, attention over that cache, and sampling.
+"""What a decode step does between the linear layers: norms of the heads, rotary positions
+and the write into an 8-bit or 4-bit key-value cache, attention over that cache, and sampling.
 
 Same rules as the linear layer's binding (``_abi``): tensors on the GPU with the
 dtypes include/lowbit.h documents, argument marshalling only, the current CUDA
@@ -8,7 +8,11 @@ stream, and ``LowbitError`` for a non-zero status.
 The cache is four tensors: ``k`` and ``v`` [pages, kv_heads, page, head_dim] in
 ``torch.float8_e4m3fn`` (``uint8`` bit patterns are taken too) and ``k_exp``, ``v_exp``
 [pages, kv_heads] int8: value = code * 2**exp, one exponent for each page of tokens and
-head (``empty_cache`` makes them).  ``page_table`` [batch, width] int32 names each
+head (``empty_cache`` makes them).  In 4 bits (``empty_cache(..., bits=4)``) they are ``k``
+and ``v`` [pages, kv_heads, page, head_dim / 2] uint8, two codes a byte, and a scale for each
+32 values of a token's head, [pages, kv_heads, page, head_dim / 32] ``torch.float8_e5m2``, in
+the place of the exponents: value = (code - 8) * scale.  Every function takes either kind.
+``page_table`` [batch, width] int32 names each
 sequence's pages in order, ``lens`` [batch] int32 its length with its new tokens.
 The new tokens of all sequences stand one after another; ``cu_q`` [batch + 1] int32 says
 where each sequence's begin (None: the same number of tokens each).
@@ -40,7 +44,9 @@ def _load():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.lowbit_kv_append, lib.lowbit_attention, lib.lowbit_attention_workspace, lib.lowbit_sample)))
+            lib.lowbit_kv_append_ex, lib.lowbit_kv_append4, lib.lowbit_attention, lib.lowbit_attention4,
+            lib.lowbit_attention_workspace, lib.lowbit_attention4_workspace, lib.lowbit_cache_values, lib.lowbit_cache4_values,
+            lib.lowbit_sample)))
         _hot = module
     return _hot
 
@@ -59,6 +65,8 @@ def _packer(layout: str, of: str):
 
 
 _CACHE = _packer("@PPPPqqiiii", "the cache's sizes")                       # lowbit_cache
+_CACHE4 = _packer("@PPPPqqqqiiii", "the cache's sizes")                    # lowbit_cache4
+_PROLOGUE = _packer("@PPPPqfii4x", "the axes, the positions' stride and eps")  # lowbit_kv_prologue
 _SEQUENCES = _packer("@PPPqiiii", "the sequences' sizes and max_q")        # lowbit_sequences
 _KV_APPEND = _packer("@PPPPqqqqqqqqPfiii", "the sizes and factor")
 _ATTENTION = _packer("@PPPqqqqqPNfii4x", "the sizes, scale and window")
@@ -66,6 +74,7 @@ _SAMPLE = _packer("@PPPPPPPPqfffiiii4x", "the sizes, temperature, top_p, min_p a
 
 _BF16, _F32, _I32, _I8, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.int64, torch.uint8
 _CODES = (torch.float8_e4m3fn, _U8)
+_SCALES = (torch.float8_e5m2, _U8)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else _abi._stream
 
 
@@ -115,25 +124,84 @@ def _rows(t, name: str, dev: int, T: int, H: int, D: int):
     _refuse(t, name, (_BF16,), dev, (T, H, D))
 
 
-def _cache_of(k, v, k_exp, v_exp, dev: int, dim: int):
-    """(lowbit_cache, kv_heads)."""
-    if not (isinstance(k, torch.Tensor) and k.dtype in _CODES and k.get_device() == dev and k.dim() == 4):
-        _refuse(k, "k_cache", _CODES, dev, (None,) * 4)
-    shape = k.shape
-    if not (isinstance(v, torch.Tensor) and v.dtype in _CODES and v.get_device() == dev and v.shape == shape):
-        _refuse(v, "v_cache", _CODES, dev, tuple(shape))
-    pages, heads, page, d = shape
+class _Cache:
+    """A cache's descriptor, and the library's functions that take it."""
+
+    def __init__(self, packed, kv_heads: int, bits: int):
+        self.packed, self.kv_heads, self.bits = packed, kv_heads, bits
+
+    def fn(self, what: str):
+        names = {"append": ("lowbit_kv_append_ex", "lowbit_kv_append4"), "attention": ("lowbit_attention", "lowbit_attention4"),
+                 "workspace": ("lowbit_attention_workspace", "lowbit_attention4_workspace"),
+                 "values": ("lowbit_cache_values", "lowbit_cache4_values")}
+        return getattr(_abi.abi(), names[what][self.bits == 4])
+
+
+def _pair_of(k, v, names, dtypes, dev: int):
+    """Strides of two tensors [pages, kv_heads, page, n] with the same strides, each head's page contiguous."""
+    if not (isinstance(k, torch.Tensor) and k.dtype in dtypes and k.get_device() == dev and k.dim() == 4):
+        _refuse(k, names[0], dtypes, dev, (None,) * 4)
+    if not (isinstance(v, torch.Tensor) and v.dtype in dtypes and v.get_device() == dev and v.shape == k.shape):
+        _refuse(v, names[1], dtypes, dev, tuple(k.shape))
+    strides = k.stride()
+    if strides != v.stride() or (strides[2] != k.shape[3] or strides[3] != 1) and k.numel():
+        raise ValueError(f"{names[0]} and {names[1]} must have the same strides, each head's page contiguous")
+    return strides
+
+
+def _cache_of(k, v, k_exp, v_exp, dev: int, dim: int) -> _Cache:
+    if isinstance(k_exp, torch.Tensor) and k_exp.dim() == 4:                  # scales: the 4-bit kind
+        strides = _pair_of(k, v, ("k_cache", "v_cache"), (_U8,), dev)
+        pages, heads, page, half = k.shape
+        if 2 * half != dim:
+            raise ValueError(f"q has head_dim {dim}, the cache {2 * half}")
+        apart = _pair_of(k_exp, v_exp, ("k_exp", "v_exp"), _SCALES, dev)
+        if dim % 32 or tuple(k_exp.shape) != (pages, heads, page, dim // 32):
+            _refuse(k_exp, "k_exp", _SCALES, dev, (pages, heads, page, dim // 32))
+        return _Cache(_CACHE4(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), strides[0], strides[1], apart[0],
+                              apart[1], pages, heads, dim, page), heads, 4)
+    strides = _pair_of(k, v, ("k_cache", "v_cache"), _CODES, dev)
+    pages, heads, page, d = k.shape
     if d != dim:
         raise ValueError(f"q has head_dim {dim}, the cache {d}")
-    strides = k.stride()
-    if strides != v.stride() or (strides[2] != d or strides[3] != 1) and k.numel():
-        raise ValueError("k_cache and v_cache must have the same strides, each head's page contiguous")
     for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
         if not (isinstance(t, torch.Tensor) and t.dtype is _I8 and t.get_device() == dev and t.shape == (pages, heads)
                 and t.is_contiguous()):
             _refuse(t, name, (_I8,), dev, (pages, heads))
-    return _CACHE(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), strides[0], strides[1], pages, heads, d,
-                  page), heads
+    return _Cache(_CACHE(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), strides[0], strides[1], pages, heads, d,
+                         page), heads, 8)
+
+
+def _prologue_of(q_norm, k_norm, eps, positions, axes, dev: int, tokens: int, dim: int, pairs: int):
+    """lowbit_kv_prologue."""
+    at, dtype = [0, 0], None
+    for i, (w, name) in enumerate(((q_norm, "q_norm"), (k_norm, "k_norm"))):
+        if w is None:
+            continue
+        if not isinstance(w, torch.Tensor) or w.dtype not in _abi._W_DTYPES:
+            raise ValueError(f"{name} must be a float32, bfloat16 or float16 CUDA tensor")
+        if dtype not in (None, w.dtype):
+            raise ValueError(f"q_norm and k_norm must have one dtype, got {dtype} and {w.dtype}")
+        dtype = w.dtype
+        at[i] = _vector(w, name, dtype, dev, dim)
+    where = token = count = axes_at = 0
+    if positions is None:
+        if axes is not None:
+            raise ValueError("axes say which column of positions each pair turns by: they need positions")
+    else:
+        if not (isinstance(positions, torch.Tensor) and positions.dtype is _I32 and positions.get_device() == dev
+                and positions.dim() in (1, 2) and positions.shape[0] == tokens):
+            _refuse(positions, "positions", (_I32,), dev, (tokens,) + (None,) * (isinstance(positions, torch.Tensor) and positions.dim() > 1))
+        where, token, count = positions.data_ptr(), positions.stride(0), 1 if positions.dim() == 1 else positions.shape[1]
+        if not 1 <= count <= 255:
+            raise ValueError(f"positions must have 1 to 255 axes, got {count}")
+        if count > 1 and positions.stride(1) != 1:
+            _refuse(positions, "positions", (_I32,), dev, (tokens, None))
+        if axes is not None:
+            axes_at = _vector(axes, "axes", _U8, dev, pairs)
+        elif count > 1:
+            raise ValueError("positions of several axes need axes: the one that each pair turns by")
+    return _PROLOGUE(*at, where, axes_at, token, eps, count, 0 if dtype is None else _abi._W_DTYPES[dtype])
 
 
 def _sequences_of(page_table, lens, cu_q, max_q, tokens: int, dev: int):
@@ -154,12 +222,44 @@ def _sequences_of(page_table, lens, cu_q, max_q, tokens: int, dev: int):
     return _SEQUENCES(page_table.data_ptr(), lens_at, cu_at, max(apart, width), width, batch, tokens, max_q)
 
 
-def empty_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda"):
-    """(k, v, k_exp, v_exp) of a cache of ``pages`` pages of ``page`` tokens, zeroed."""
+def empty_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda", bits: int = 8):
+    """(k, v, k_exp, v_exp) of a cache of ``pages`` pages of ``page`` tokens, zeroed; with ``bits=4``
+    (k, v, k_scale, v_scale), half the size: 4.25 bits a value."""
+    if bits not in (4, 8):
+        raise ValueError(f"bits must be 4 or 8, got {bits}")
+    if bits == 4:
+        if head_dim not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+        k, v = (torch.zeros((pages, kv_heads, page, head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2))
+        k_scale, v_scale = (torch.zeros((pages, kv_heads, page, head_dim // 32), dtype=torch.uint8, device=device)
+                            .view(torch.float8_e5m2) for _ in range(2))
+        return k, v, k_scale, v_scale
     k, v = (torch.zeros((pages, kv_heads, page, head_dim), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
             for _ in range(2))
     k_exp, v_exp = (torch.zeros((pages, kv_heads), dtype=torch.int8, device=device) for _ in range(2))
     return k, v, k_exp, v_exp
+
+
+def cache_values(k_cache, v_cache, k_exp, v_exp, out=(None, None)):
+    """(k, v): the values that a cache holds, bf16 [pages, kv_heads, page, head_dim] (or writes the
+    two tensors ``out``).  Exact: a value of either kind of cache is a bf16 number."""
+    k_out, v_out = out
+    done = (_hot or _load()).cache_values(k_cache, v_cache, k_exp, v_exp, k_out, v_out)
+    if done is not None:
+        return done if done.__class__ is not int else _abi._check(done, "lowbit_cache_values")
+    dev = _first(k_cache, "k_cache", 4)
+    pages, heads, page, n = k_cache.shape
+    dim = 2 * n if isinstance(k_exp, torch.Tensor) and k_exp.dim() == 4 else n
+    cache = _cache_of(k_cache, v_cache, k_exp, v_exp, dev, dim)
+    shape, outs = (pages, heads, page, dim), []
+    for t, name in ((k_out, "out[0]"), (v_out, "out[1]")):
+        if t is None:
+            t = torch.empty(shape, dtype=_BF16, device=k_cache.device)
+        elif not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.get_device() == dev and t.shape == shape and t.is_contiguous()):
+            _refuse(t, name, (_BF16,), dev, shape)
+        outs.append(t)
+    _call(cache.fn("values"), "lowbit_cache_values", dev, cache.packed, outs[0].data_ptr(), outs[1].data_ptr())
+    return tuple(outs)
 
 
 def rotary_turns(dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -197,7 +297,8 @@ def rotary_turns(dim: int, base: float = 10000.0, scaling: str | None = None, fa
 
 
 def kv_append(q, k, v, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q=None, max_q: int | None = None, turns=None,
-              interleaved: bool = False, factor: float = 1.0, out=None) -> torch.Tensor:
+              interleaved: bool = False, factor: float = 1.0, out=None, *, q_norm=None, k_norm=None, eps: float = 1e-6,
+              positions=None, axes=None) -> torch.Tensor:
     """Rotate q and k to their positions and write k and v into the cache; returns q
     rotated, bf16 [tokens, heads, head_dim] (or writes ``out``, which may be q).
 
@@ -207,28 +308,40 @@ def kv_append(q, k, v, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q=No
     ``interleaved`` pairs neighbours, otherwise the halves; ``factor`` multiplies the
     rotated part.  ``max_q``: the largest number of new tokens of a sequence (with cu_q;
     None: no bound known).
+
+    Before the rotation, in the same pass: ``q_norm``, ``k_norm`` (bf16, fp16 or fp32 [head_dim],
+    either or both), weights by which each head's q or k is multiplied after division by its root
+    mean square, sqrt(mean(x * x) + ``eps``).  ``positions`` (int32 [tokens]) are what tokens turn
+    by in place of their places in the sequence; with several axes, as time, height and width of
+    an image's patches, [tokens, n], and ``axes`` (uint8 [len(turns)]) is the column that each pair
+    turns by.  Where a token is written follows from lens all the same.
     """
-    done = (_hot or _load()).kv_append(q, k, v, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q, max_q, turns, interleaved,
-                                       factor, out)
+    if q_norm is None and k_norm is None and positions is None and axes is None:
+        done = (_hot or _load()).kv_append(q, k, v, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q, max_q, turns, interleaved,
+                                           factor, out)
+    else:
+        done = (_hot or _load()).kv_append(q, k, v, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q, max_q, turns, interleaved,
+                                           factor, out, q_norm, k_norm, eps, positions, axes)
     if done is not None:
         return done if done.__class__ is not int else _abi._check(done, "lowbit_kv_append")
     dev = _first(q, "q", 3)
     T, heads, dim = q.shape
     q_at, qt, qh = _rows(q, "q", dev, T, heads, dim)
-    cache, kv_heads = _cache_of(k_cache, v_cache, k_exp, v_exp, dev, dim)
-    k_at, kt, kh = _rows(k, "k", dev, T, kv_heads, dim)
-    v_at, vt, vh = _rows(v, "v", dev, T, kv_heads, dim)
+    cache = _cache_of(k_cache, v_cache, k_exp, v_exp, dev, dim)
+    k_at, kt, kh = _rows(k, "k", dev, T, cache.kv_heads, dim)
+    v_at, vt, vh = _rows(v, "v", dev, T, cache.kv_heads, dim)
     turns_at = pairs = 0
     if turns is not None:
         pairs = turns.numel()
         turns_at = _vector(turns, "turns", _I64, dev, pairs)
     seqs = _sequences_of(page_table, lens, cu_q, max_q, T, dev)
+    before = _prologue_of(q_norm, k_norm, eps, positions, axes, dev, T, dim, pairs)
     if out is None:
         out = torch.empty_like(q)
     out_at, ot, oh = _rows(out, "out", dev, T, heads, dim)
     args = _KV_APPEND(q_at, k_at, v_at, out_at, qt, qh, kt, kh, vt, vh, ot, oh, turns_at, factor, heads, 2 * pairs,
                       bool(interleaved))
-    _call(_abi.abi().lowbit_kv_append, "lowbit_kv_append", dev, args, cache, seqs)
+    _call(cache.fn("append"), "lowbit_kv_append", dev, args, before, cache.packed, seqs)
     return out
 
 
@@ -249,7 +362,7 @@ def attention(q, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q=None, ma
     dev = _first(q, "q", 3)
     T, heads, dim = q.shape
     q_at, qt, qh = _rows(q, "q", dev, T, heads, dim)
-    cache, _ = _cache_of(k_cache, v_cache, k_exp, v_exp, dev, dim)
+    cache = _cache_of(k_cache, v_cache, k_exp, v_exp, dev, dim)
     seqs = _sequences_of(page_table, lens, cu_q, max_q, T, dev)
     if out is None:
         out = torch.empty_like(q)
@@ -262,22 +375,21 @@ def attention(q, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q=None, ma
         if one != 1 and heads > 1:
             _refuse(lse, "lse", (_F32,), dev, (T, heads))
         lse_at = lse.data_ptr()
-    lib = _abi.abi()
     if workspace is None:
-        workspace = torch.empty(lib.lowbit_attention_workspace(heads, cache, seqs), dtype=_U8, device=q.device)
+        workspace = torch.empty(cache.fn("workspace")(heads, cache.packed, seqs), dtype=_U8, device=q.device)
     n = workspace.numel()
     args = _ATTENTION(q_at, out_at, lse_at, qt, qh, ot, oh, lse_token, _vector(workspace, "workspace", _U8, dev, n), n,
                       dim ** -0.5 if scale is None else scale, heads, window)
-    _call(lib.lowbit_attention, "lowbit_attention", dev, args, cache, seqs)
+    _call(cache.fn("attention"), "lowbit_attention", dev, args, cache.packed, seqs)
     return out
 
 
 def attention_workspace(q, k_cache, v_cache, k_exp, v_exp, page_table, lens, cu_q=None, max_q: int | None = None) -> int:
     """Bytes of workspace that ``attention`` needs for these tensors."""
     dev = _first(q, "q", 3)
-    cache, _ = _cache_of(k_cache, v_cache, k_exp, v_exp, dev, q.shape[2])
+    cache = _cache_of(k_cache, v_cache, k_exp, v_exp, dev, q.shape[2])
     seqs = _sequences_of(page_table, lens, cu_q, max_q, q.shape[0], dev)
-    return int(_abi.abi().lowbit_attention_workspace(q.shape[1], cache, seqs))
+    return int(cache.fn("workspace")(q.shape[1], cache.packed, seqs))
 
 
 def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, logprob=None) -> torch.Tensor:

@@ -287,6 +287,69 @@ typedef struct {
 LOWBIT_API lowbit_status lowbit_kv_append(const lowbit_kv_append_args *args, const lowbit_cache *cache,
                                           const lowbit_sequences *seqs, lowbit_stream_t stream);
 
+/* What may stand before the rotation and the write, in the same pass:
+ *   norms      each head's q and k over its root mean square, times weights:
+ *              y = (x r) w, r = 1 / sqrt(mean x^2 + eps), in fp32, every operation rounded
+ *              by itself and the squares added in pairs (neighbours, then neighbouring
+ *              sums), so that codes next to a border come out the same in any implementation.
+ *              q_norm, k_norm [head_dim] of norm_dtype, naturally aligned, each may be NULL.
+ *   positions  token t's pairs turn by positions[t * positions_token + axis[j]] instead of
+ *              its place in its sequence (which still says where it is written): several
+ *              axes, as time, height and width of an image's patches.  positions int32,
+ *              [tokens, axes] (negative ones turn the other way); axis uint8
+ *              [rotary_dim / 2], or NULL: axis 0 for all.  An axis past the last counts as the
+ *              last.  axes 1 .. 255.
+ * A NULL descriptor, or one with NULL members: none of them. */
+typedef struct {
+    const void *q_norm, *k_norm;
+    const int32_t *positions;
+    const uint8_t *axis;
+    int64_t positions_token;             /* elements */
+    float eps;                           /* not negative */
+    int32_t axes;
+    lowbit_dtype norm_dtype;
+} lowbit_kv_prologue;
+
+/* lowbit_kv_append with norms, or positions of the caller's own, before the write.
+ * Errors: also LOWBIT_EINVAL for an eps, axes or norm_dtype out of range, and
+ * misaligned pointers. */
+LOWBIT_API lowbit_status lowbit_kv_append_ex(const lowbit_kv_append_args *args, const lowbit_kv_prologue *before,
+                                             const lowbit_cache *cache, const lowbit_sequences *seqs,
+                                             lowbit_stream_t stream);
+
+/* The cache in 4 bits: a token's head in groups of 32 values, each with a scale,
+ *     value = (code - 8) * scale,
+ * scale an e5m2 number (the upper byte of an fp16), code 4 bits, two to a byte (the even
+ * value in the low bits).  Written are codes 1 .. 15 and the smallest scale s >= 2^-14 with
+ * amax <= 7.5 s, amax the largest finite magnitude of the group, code - 8 the nearest
+ * whole number to value / s (ties to even, within -7 .. 7).  Infinities, and values
+ * past 7 * 57344, are stored as 7 s; a group that holds a NaN gets a NaN scale.
+ * Scales are read as they are, and have to be not negative; one that is infinite or no number makes its 32
+ * values NaN. */
+typedef struct {
+    uint8_t *k, *v;              /* [pages, kv_heads, page, head_dim / 2], 16-byte aligned           */
+    uint8_t *k_scale, *v_scale;  /* [pages, kv_heads, page, head_dim / 32] e5m2, 16-byte aligned      */
+    int64_t page_stride, head_stride;              /* bytes, of k and v, as for lowbit_cache          */
+    int64_t scale_page_stride, scale_head_stride;  /* bytes, of k_scale and v_scale, the same rules   */
+    int32_t pages, kv_heads;
+    int32_t head_dim;            /* 64 or 128                                                        */
+    int32_t page;                /* tokens of a page: 16, 32, 64, 128 or 256                         */
+} lowbit_cache4;
+
+/* lowbit_kv_append_ex into a 4-bit cache.  A token's codes depend on no other token. */
+LOWBIT_API lowbit_status lowbit_kv_append4(const lowbit_kv_append_args *args, const lowbit_kv_prologue *before,
+                                           const lowbit_cache4 *cache, const lowbit_sequences *seqs,
+                                           lowbit_stream_t stream);
+
+/* The values that a cache holds, for inspection or another use of them: bf16 (exact)
+ * [pages, kv_heads, page, head_dim], contiguous, 16-byte aligned.  Codes and scales may
+ * be anything.  Errors: LOWBIT_EINVAL for sizes that lowbit_kv_append refuses, null or
+ * misaligned pointers or strides; LOWBIT_EUNSUPPORTED, LOWBIT_ECUDA as elsewhere. */
+LOWBIT_API lowbit_status lowbit_cache_values(const lowbit_cache *cache, uint16_t *k_out, uint16_t *v_out,
+                                             lowbit_stream_t stream);
+LOWBIT_API lowbit_status lowbit_cache4_values(const lowbit_cache4 *cache, uint16_t *k_out, uint16_t *v_out,
+                                              lowbit_stream_t stream);
+
 /* Softmax attention of the new tokens over the cache: for query row (token, head)
  * at position pos, over the keys t <= pos (and t > pos - window when window > 0)
  *     out = sum_t softmax_t(scale q.k_t) v_t,   lse = ln sum_t e^(scale q.k_t),
@@ -320,6 +383,14 @@ LOWBIT_API lowbit_status lowbit_attention(const lowbit_attention_args *args, con
  * head counts and dim; of the sequences, batch, tokens, width, max_q and whether
  * cu_q is NULL).  Host-only.  0 for sizes that lowbit_attention rejects. */
 LOWBIT_API size_t lowbit_attention_workspace(int32_t heads, const lowbit_cache *cache, const lowbit_sequences *seqs);
+
+/* lowbit_attention over a 4-bit cache, with the same arguments, sizes and guarantees.
+ * Scores are taken from the codes and scaled in fp32; the weights are rounded to fp16 for
+ * the product with v, to 2^-11 of themselves, or to 2^-32 of the row's largest where that
+ * is more. */
+LOWBIT_API lowbit_status lowbit_attention4(const lowbit_attention_args *args, const lowbit_cache4 *cache,
+                                           const lowbit_sequences *seqs, lowbit_stream_t stream);
+LOWBIT_API size_t lowbit_attention4_workspace(int32_t heads, const lowbit_cache4 *cache, const lowbit_sequences *seqs);
 
 /* One token for each row of logits, from a given uniform number.  With m the row's
  * largest logit, s_i = (x_i - m) / temperature and W_i = rint(2^30 e^s_i) (weights
