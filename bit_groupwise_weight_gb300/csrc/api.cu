@@ -457,7 +457,7 @@ lowbit_status lowbit_attention4(const lowbit_attention_args *a, const lowbit_cac
     if (st != LOWBIT_OK || !launch) return st;
     p.k_scale = c->k_scale, p.v_scale = c->v_scale;
     p.scale_page_stride = c->scale_page_stride, p.scale_head_stride = c->scale_head_stride;
-    return LOWBIT_EUNSUPPORTED;
+    return from_cuda(lowbit::launch_attention(p, (cudaStream_t)stream));
 }
 
 lowbit_status lowbit_sample(const lowbit_sample_args *a, lowbit_stream_t stream) {

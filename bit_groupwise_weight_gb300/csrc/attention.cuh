@@ -1,5 +1,5 @@
-// attention.cuh -- shared by the attention kernels over the 8-bit paged cache
-// (attention.cu: few query rows a sequence; attention_prompt.cu: many).
+// attention.cuh -- shared by the attention kernels over a paged cache of 8 or 4 bits
+// (attention_few.cuh: few query rows a sequence; attention_prompt.cu: many).
 #pragma once
 
 #include "common.cuh"
@@ -18,6 +18,9 @@ PromptGrid prompt_grid(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk
 size_t prompt_workspace_bytes(const PromptGrid &g, int Hk, int D);
 cudaError_t launch_prompt(const AttentionArgs &p, const PromptGrid &g, cudaStream_t stream);
 uint32_t prompt_timeouts(bool reset);
+// Few query rows a sequence over a 4-bit cache (attention4.cu).
+cudaError_t launch_attention4(const AttentionArgs &p, cudaStream_t stream);
+uint32_t attention4_timeouts(bool reset);
 
 namespace attn {
 

@@ -1,0 +1,386 @@
+// attention4.cu -- attention over the 4-bit paged cache for few query rows a sequence: what
+// attention_few.cuh needs to know of the format (int4.cuh).
+//
+// Mathematics, beside attention.cu's.  A key's value is (c - 8) s, s the scale of its group of 32
+// values, so
+//     q . k = sum over groups of s (q . c - 8 sum q),
+// and the products run on the codes c alone, groups apart: masking two nibbles out of a word of
+// eight leaves a pair of fp16 subnormals c 2^-24 (c 2^-20 for the second nibble of a byte, whose q
+// is held 2^4 smaller instead), exact, one instruction for two codes.  The accumulators start at
+// -8 sum q; scales are applied to the groups' sums in fp32.
+// In the product with V the groups run along the rows of the result and the scales along the sum:
+// there codes become values first.  A nibble in the mantissa of 1.0 is 1 + c / 64, and
+//     (1 + c / 64) s - 1.125 s = (c - 8) s / 64,
+// one fused operation for two codes, exact in fp16 (3 + 3 bits) for every scale.  The result is
+// multiplied by 64 at the end.
+//
+// Operands: the four bytes that a lane gets from ldmatrix are eight codes of one key (K), or, transposed,
+// four codes of two neighbouring keys (V): the order of the values within a group is the codes' own,
+// q is laid out to match, and a lane's four rows of the result are four neighbouring values.
+#include "attention_few.cuh"
+#include "int4.cuh"
+
+namespace lowbit {
+namespace {
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// The values / 64 of nibble I of both halves of w; s, t: the halves' scales, and -1.125 of them.
+template <int I>
+__device__ __forceinline__ uint32_t values4(uint32_t w, uint32_t s, uint32_t t) {
+    const uint32_t in = I == 0 ? w << 4 : w >> (4 * I - 4);
+    return hfma2(ptx::lop3_and_or(in, 0x00F000F0u, 0x3C003C00u), s, t);
+}
+// Bytes that hold an infinite or no number (e5m2), as 0xFF each.
+__device__ __forceinline__ uint32_t bad_scales(uint32_t v) {
+    return ((((v & 0x7C7C7C7Cu) + 0x04040404u) & 0x80808080u) >> 7) * 0xFFu;
+}
+
+// The 4-bit cache.
+struct Four {
+    static constexpr int kTile = 128, kTileBits = 7, kWarpKeys = 32;
+    static constexpr int kItemCost = 4;
+    static constexpr int kMinChunk = 4;
+    static constexpr int per_sm(int D, int ROWS) { return D == 128 && ROWS == 16 ? 2 : 3; }
+    static constexpr int stages(int D, int ROWS) { return D == 64 ? 6 : (ROWS == 16 ? 5 : 3); }
+    static constexpr float kUnit = 64.f;
+    template <int D>
+    static constexpr int kKeyBytes = D + D / 16;                          // codes and scales of K and V
+
+    struct Maps { CUtensorMap k, v, k_scale, v_scale; };
+    template <int D>
+    struct Stage {
+        alignas(1024) uint8_t k[kTile * D / 2];
+        alignas(1024) uint8_t v[kTile * D / 2];
+        alignas(128) uint8_t k_scale[kTile / 16 * 128];                   // up to eight pages' slots
+        alignas(128) uint8_t v_scale[kTile / 16 * 128];
+    };
+    // A copy's place in shared memory is a multiple of 128 bytes: so far apart are the scales of pages in a stage.
+    template <int D>
+    static __device__ __forceinline__ int slot_of_box(int box) { return max(box * (D / kGroup4), 128); }
+
+    struct StageBeside {};
+    struct Beside {};
+
+    static __device__ __forceinline__ void prefetch(const Maps &m) {
+        ptx::prefetch_tensormap(&m.k);
+        ptx::prefetch_tensormap(&m.v);
+        ptx::prefetch_tensormap(&m.k_scale);
+        ptx::prefetch_tensormap(&m.v_scale);
+    }
+    static __device__ __forceinline__ Beside beside(const AttentionArgs &, int, int) { return {}; }
+    template <int D>
+    static __device__ __forceinline__ void copy(const Maps &m, Stage<D> &s, int part, int box, int row, int head, int page,
+                                                uint32_t bar) {
+        constexpr int kCodes = D / 2;
+        const int x = row * (D / kGroup4) / 4, slot = part * slot_of_box<D>(box);
+        ptx::tma_load_4d(ptx::smem_u32(s.k) + part * box * kCodes, &m.k, 0, row, head, page, bar);
+        ptx::tma_load_4d(ptx::smem_u32(s.k_scale) + slot, &m.k_scale, x, head, page, 0, bar);
+        ptx::tma_load_4d(ptx::smem_u32(s.v) + part * box * kCodes, &m.v, 0, row, head, page, bar);
+        ptx::tma_load_4d(ptx::smem_u32(s.v_scale) + slot, &m.v_scale, x, head, page, 0, bar);
+    }
+    static __device__ __forceinline__ void put_beside(StageBeside &, const Beside &, int, int) {}
+
+    // A lane's ldmatrix address in the first 16 keys of its warp's 32, without the chunk of 16 bytes (32
+    // codes, a group): chunk c is at (address ^ c << 4), the second 16 keys 8 D bytes on.
+    template <int D>
+    struct Lane {
+        uint32_t off, scales[2];                     // scales: of the first key of each 16
+        __device__ __forceinline__ Lane(const AttentionArgs &p, int warp) {
+            const int box = min(p.P, kTile), slot = slot_of_box<D>(box);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int first = warp * kWarpKeys + 16 * i;
+                scales[i] = first / box * slot + first % box * (D / kGroup4);
+            }
+            const int lane = threadIdx.x & 31, key = warp * kWarpKeys + ((lane >> 3) & 1) * 8 + (lane & 7);
+            off = key * (D / 2) + (((lane >> 4) ^ (D == 128 ? (key >> 1) & 3 : (key >> 2) & 1)) << 4);
+        }
+    };
+
+    // A consumer warp's state of an item.  Lane (g, t) = (lane / 4, lane % 4); column pair
+    // n: query rows 8n + 2t and 8n + 2t + 1.
+    template <int D, int ROWS>
+    struct State {
+        static constexpr int KS = D / 16, N = ROWS / 8, G = D / kGroup4;
+        uint32_t q[KS][N][2];                        // B fragments of q^T: values 8t + (0, 4), (1, 5); (2, 6), (3, 7) of a group
+        float start[G][N][2];                        // -8 sum q of the group, as the accumulators hold it
+        float qs[N][2];                              // factor of the row's scores
+        int pos[N][2];
+        float o[KS][N][4];                           // O^T
+        float m[N][2], l[N][2];
+    };
+    static __device__ __forceinline__ int value_of(int k, int g) { return 32 * (k >> 1) + 4 * g + 2 * (k & 1); }
+
+    // Query fragments: fp16, each row times a power of two, 2^4 more than for the 8-bit cache where the
+    // codes are 2^-24 of themselves.
+    template <int D, int ROWS>
+    static __device__ __forceinline__ void queries(const AttentionArgs &p, State<D, ROWS> &a, const Seq &s, int h, int row0) {
+        constexpr int KS = D / 16, N = ROWS / 8, G = D / kGroup4;
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, nrows = s.n * p.G, first = s.len - s.n;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int r = row0 + 8 * n + g;
+            const bool live = r < nrows;
+            const int i = live ? r / p.G : 0, hq = h * p.G + (live ? r - i * p.G : 0);
+            const uint16_t *q = p.q + (int64_t)(s.start + i) * p.q_token + hq * p.q_head + 8 * t;
+            uint2 v[G][2];
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) v[j][c] = live ? *reinterpret_cast<const uint2 *>(q + 32 * j + 4 * c) : make_uint2(0u, 0u);
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float x[4] = {bf16_lo(v[j][c].x), bf16_hi(v[j][c].x), bf16_lo(v[j][c].y), bf16_hi(v[j][c].y)};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) amax = fabsf(x[k]) < INFINITY ? fmaxf(amax, fabsf(x[k])) : amax;
+                }
+            amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+            const int up = query_shift(amax);
+            const float odd = exp2_int(up), even = exp2_int(up + 4), scale = exp2_int(-up) * p.scale_log2;
+            float sum[G];
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const uint2 lo = v[j][0], hi = v[j][1];                     // values 0 .. 3 and 4 .. 7 of the lane's eight
+                a.q[2 * j][n][0] = f32x2_to_f16x2(bf16_lo(lo.x) * even, bf16_lo(hi.x) * even);
+                a.q[2 * j][n][1] = f32x2_to_f16x2(bf16_hi(lo.x) * odd, bf16_hi(hi.x) * odd);
+                a.q[2 * j + 1][n][0] = f32x2_to_f16x2(bf16_lo(lo.y) * even, bf16_lo(hi.y) * even);
+                a.q[2 * j + 1][n][1] = f32x2_to_f16x2(bf16_hi(lo.y) * odd, bf16_hi(hi.y) * odd);
+                float half[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a.q[2 * j][n][c]));
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&a.q[2 * j + 1][n][c]));
+                    half[c] = (x.x + x.y) + (y.x + y.y);
+                }
+                sum[j] = fmaf(half[1], 16.f, half[0]) * (-8.f * 0x1p-24f);
+                sum[j] += __shfl_xor_sync(~0u, sum[j], 1);
+                sum[j] += __shfl_xor_sync(~0u, sum[j], 2);
+            }
+            // This lane's columns are rows 2t and 2t + 1.
+            const int position = live ? first + i : -1;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int j = 0; j < G; ++j) a.start[j][n][c] = __shfl_sync(~0u, sum[j], 8 * t + 4 * c);
+                a.qs[n][c] = __shfl_sync(~0u, scale, 8 * t + 4 * c);
+                a.pos[n][c] = __shfl_sync(~0u, position, 8 * t + 4 * c);
+                a.m[n][c] = -INFINITY, a.l[n][c] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < KS; ++c) a.o[c][n][0] = a.o[c][n][1] = a.o[c][n][2] = a.o[c][n][3] = 0.f;
+        }
+    }
+
+    // The scales of a key's groups as fp32.
+    template <int D>
+    static __device__ __forceinline__ void key_scales(uint32_t at, float (&s)[D / kGroup4]) {
+        const uint32_t u = D == 128 ? ptx::lds_u32(at) : (uint32_t)ptx::lds_u16(at);
+#pragma unroll
+        for (int j = 0; j < D / kGroup4; j += 2) {
+            const uint32_t h = ptx::prmt(u, 0u, j == 0 ? 0x1404u : 0x3424u);
+            const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            s[j] = x.x, s[j + 1] = x.y;
+        }
+    }
+
+    // A warp's 32 keys of a stage, in two halves of 16.  EDGE: some row does not see some key of them.
+    template <int D, int ROWS, bool EDGE>
+    static __device__ __forceinline__ void slice(const AttentionArgs &p, State<D, ROWS> &st, const Lane<D> &at, const Stage<D> &stage,
+                                                 const StageBeside &, int key0, int len) {
+        constexpr int N = ROWS / 8, G = D / kGroup4;
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const uint32_t kat = ptx::smem_u32(stage.k) + at.off, vat = ptx::smem_u32(stage.v) + at.off;
+        const uint32_t kst = ptx::smem_u32(stage.k_scale) + g * G, vst = ptx::smem_u32(stage.v_scale) + 2 * t * G;
+        float x[2][N][4];
+        uint32_t seen[2][N];                         // bit i: value i of the pair is seen
+        bool grown = false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float s0[G], s1[G];                      // of keys g and g + 8
+            key_scales<D>(kst + at.scales[half], s0);
+            key_scales<D>(kst + at.scales[half] + 8 * G, s1);
+#pragma unroll
+            for (int c = 0; c < G; c += 2) {
+                uint32_t r[4];
+                ldsm_x4((kat + half * 8 * D) ^ (c << 4), r);     // (keys 0-7, chunk c), (8-15, c), (0-7, c+1), (8-15, c+1)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = c + i;
+                    const uint32_t a = r[2 * i], b = r[2 * i + 1], a8 = a >> 8, b8 = b >> 8;
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        float acc[4] = {st.start[j][n][0], st.start[j][n][1], st.start[j][n][0], st.start[j][n][1]};
+                        ptx::mma_16816_f16(acc, a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u, b & 0x00F000F0u,
+                                           st.q[2 * j][n][0], st.q[2 * j][n][1]);
+                        ptx::mma_16816_f16(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u,
+                                           st.q[2 * j + 1][n][0], st.q[2 * j + 1][n][1]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float s = k < 2 ? s0[j] : s1[j];
+                            x[half][n][k] = j == 0 ? acc[k] * s : fmaf(acc[k], s, x[half][n][k]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                seen[half][n] = 0xFu;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {        // (key g, row 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
+                    x[half][n][i] = x[half][n][i] * 0x1p20f * st.qs[n][i & 1];
+                    if constexpr (EDGE) {
+                        const int key = key0 + half * 16 + g + 8 * (i >> 1), pos = st.pos[n][i & 1];
+                        const bool see = key <= pos && (p.window == 0 || key > pos - p.window);
+                        if (!see) x[half][n][i] = -INFINITY, seen[half][n] &= ~(1u << i);
+                    }
+                }
+                grown |= fmaxf(x[half][n][0], x[half][n][2]) > st.m[n][0] + kPeak ||
+                         fmaxf(x[half][n][1], x[half][n][3]) > st.m[n][1] + kPeak;
+            }
+        }
+        if (__any_sync(~0u, grown)) {                // rows whose maximum has outgrown m (the first keys seen: from -inf)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float mx = fmaxf(fmaxf(x[0][n][c], x[0][n][c + 2]), fmaxf(x[1][n][c], x[1][n][c + 2]));
+                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+                    const float to = fmaxf(mx - kStart, st.m[n][c]);
+                    const Rescale by(to == st.m[n][c] ? 0.f : st.m[n][c] - to);
+                    const float f = by.of_o();
+                    st.m[n][c] = to;
+                    st.l[n][c] = by.of_l(st.l[n][c]);
+#pragma unroll
+                    for (int k = 0; k < 2 * G; ++k) st.o[k][n][c] *= f, st.o[k][n][c + 2] *= f;
+                }
+        }
+        uint32_t pb[2][N][2];                        // P^T: B fragments
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                // A row that has seen nothing has m = -inf; its scores are -inf as well.
+                const float m0 = EDGE && st.m[n][0] == -INFINITY ? 0.f : st.m[n][0], m1 = EDGE && st.m[n][1] == -INFINITY ? 0.f : st.m[n][1];
+                float (&y)[4] = x[half][n];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = ex2(y[i] - (i & 1 ? m1 : m0));
+                st.l[n][0] += y[0] + y[2];
+                st.l[n][1] += y[1] + y[3];
+                pb[half][n][0] = transpose8(f32x2_to_f16x2(y[0], y[1]));
+                pb[half][n][1] = transpose8(f32x2_to_f16x2(y[2], y[3]));
+            }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            // Scales of keys 2t, 2t + 1 and 2t + 8, 2t + 9; zero past the sequence's end.
+            uint32_t w[4];
+            if constexpr (D == 128) {
+                ptx::lds_v2<0>(vst + at.scales[half], w[0], w[1]);
+                ptx::lds_v2<8 * G>(vst + at.scales[half], w[2], w[3]);
+            } else {
+                w[0] = w[1] = ptx::lds_u32(vst + at.scales[half]);
+                w[2] = w[3] = ptx::lds_u32_off<8 * G>(vst + at.scales[half]);
+            }
+            uint32_t bad[4];
+            bool apart = false;                      // a scale that is no number, at a key that not all rows see
+            if constexpr (EDGE) {
+                const int key = key0 + half * 16 + 2 * t;
+                const bool in[4] = {key < len, key + 1 < len, key + 8 < len, key + 9 < len};
+                uint32_t any = 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (D == 128) {
+                        if (!in[i]) w[i] = 0u;
+                    } else {
+                        w[i] &= (in[i & 2] ? 0xFFFFu : 0u) | (in[(i & 2) + 1] ? 0xFFFF0000u : 0u);
+                    }
+                    bad[i] = bad_scales(w[i]);
+                    any |= bad[i];
+                    w[i] &= ~bad[i];
+                }
+                apart = __any_sync(~0u, any != 0u);
+            }
+#pragma unroll
+            for (int c = 0; c < G; c += 2) {
+                uint32_t r[4];
+                ldsm_x4_trans((vat + half * 8 * D) ^ (c << 4), r);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = c + i, k = D == 128 ? 4 + j : 2 + j;
+                    // The upper bytes of an fp16 pair; the lower ones take the scale's sign bits, 0.
+                    const uint32_t pick = (uint32_t)((8 | j) | j << 4 | (8 | k) << 8 | k << 12);
+                    const uint32_t s0 = ptx::prmt(w[0], w[1], pick), s1 = ptx::prmt(w[2], w[3], pick);
+                    const uint32_t t0 = hmul2(s0, 0xBC80BC80u), t1 = hmul2(s1, 0xBC80BC80u);       // times -1.125
+                    const uint32_t a = r[2 * i], b = r[2 * i + 1];
+                    const uint32_t lo[4] = {values4<0>(a, s0, t0), values4<1>(a, s0, t0), values4<0>(b, s1, t1), values4<1>(b, s1, t1)};
+                    const uint32_t hi[4] = {values4<2>(a, s0, t0), values4<3>(a, s0, t0), values4<2>(b, s1, t1), values4<3>(b, s1, t1)};
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        ptx::mma_16816_f16(st.o[2 * j][n], lo[0], lo[1], lo[2], lo[3], pb[half][n][0], pb[half][n][1]);
+                        ptx::mma_16816_f16(st.o[2 * j + 1][n], hi[0], hi[1], hi[2], hi[3], pb[half][n][0], pb[half][n][1]);
+                    }
+                    if constexpr (EDGE) {
+                        if (apart) {                 // rows that see such a key take NaN in its group
+                            const uint32_t both = (uint32_t)(j | j << 4 | k << 8 | k << 12);
+                            const uint32_t b0 = ptx::prmt(bad[0], bad[1], both), b1 = ptx::prmt(bad[2], bad[3], both);
+#pragma unroll
+                            for (int n = 0; n < N; ++n) {
+                                const uint32_t see = seen[half][n];
+                                const uint32_t f0 = (see & 1u ? 0xFFFFu : 0u) | (see & 2u ? 0xFFFF0000u : 0u);
+                                const uint32_t f1 = (see & 4u ? 0xFFFFu : 0u) | (see & 8u ? 0xFFFF0000u : 0u);
+                                uint32_t hit = (transpose8(f0) & b0) | (transpose8(f1) & b1);          // of row g
+                                hit |= __shfl_xor_sync(~0u, hit, 1);
+                                hit |= __shfl_xor_sync(~0u, hit, 2);
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    if (__shfl_sync(~0u, hit, 8 * t + 4 * q) == 0u) continue;
+#pragma unroll
+                                    for (int e = q; e < 4; e += 2)
+                                        st.o[2 * j][n][e] = st.o[2 * j + 1][n][e] = __int_as_float(0x7FFFFFFF);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    template <int D>
+    static bool make_maps(const AttentionArgs &p, Maps *m) {
+        const uint32_t rows = (uint32_t)std::min(p.P, kTile);
+        const uint64_t dims[4] = {(uint64_t)D / 2, (uint64_t)p.P, (uint64_t)p.Hk, (uint64_t)p.pages};
+        const uint64_t strides[3] = {(uint64_t)D / 2, (uint64_t)p.head_stride, (uint64_t)p.page_stride};
+        const uint32_t box[4] = {(uint32_t)D / 2, rows, 1, 1};
+        // A page's scales of a head are one run of bytes, copied as words (a box has 256 elements at most).
+        const uint64_t sdims[4] = {(uint64_t)p.P * D / kGroup4 / 4, (uint64_t)p.Hk, (uint64_t)p.pages, 1};
+        const uint64_t sstrides[3] = {(uint64_t)p.scale_head_stride, (uint64_t)p.scale_page_stride, (uint64_t)p.scale_page_stride};
+        const uint32_t sbox[4] = {rows * D / kGroup4 / 4, 1, 1, 1};
+        const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+        return encode_tiled(&m->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.k_cache, dims, strides, box, sw) &&
+               encode_tiled(&m->v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.v_cache, dims, strides, box, sw) &&
+               encode_tiled(&m->k_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.k_scale, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+               encode_tiled(&m->v_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.v_scale, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
+};
+
+}  // namespace
+
+cudaError_t launch_attention4(const AttentionArgs &p, cudaStream_t stream) { return launch_few_rows<Four>(p, stream); }
+uint32_t attention4_timeouts(bool reset) { return few_rows_timeouts(reset); }
+
+}  // namespace lowbit

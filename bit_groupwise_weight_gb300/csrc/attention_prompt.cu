@@ -1,9 +1,11 @@
-// attention_prompt.cu -- attention over the 8-bit paged cache for many new tokens
+// attention_prompt.cu -- attention over a paged cache of 8 or 4 bits for many new tokens
 // (prompts), on the tcgen05 tensor cores with accumulators in tensor memory.
 //
 // Mathematics: as attention.cu (codes multiplied as fp16 numbers, page exponents
 // applied in fp32, V's exponent inside the softmax exponent).  As m may lag behind the
 // maximum (attention.cuh), the rescaling of O, a round trip through tensor memory, is rare.
+// A 4-bit cache's codes are turned into their values / 64, exact in fp16 (attention4.cu), so that
+// there are no exponents then; 64 is in the row's factor of the scores and in the last division.
 //
 // Work split.  A CTA takes 256 rows (new tokens x heads of a group) of one sequence
 // and kv head, as two 128-row tiles whose softmax and products alternate: while one
@@ -31,6 +33,7 @@
 #include <algorithm>
 
 #include "attention.cuh"
+#include "int4.cuh"
 
 namespace lowbit {
 namespace {
@@ -57,14 +60,18 @@ constexpr int kLongSteps = 32;                   // of sequences whose tiles are
 
 __device__ unsigned int g_prompt_timeouts;
 
-template <int D>
+template <int D, bool FOUR>
 struct Smem {
-    static constexpr int kQ = 128 * D * 2, kTile = kKeys * D * 2, kRawBytes = kUnit * D;
+    // A raw unit: codes, then a 4-bit cache's scales.
+    static constexpr int kQ = 128 * D * 2, kTile = kKeys * D * 2, kRawCodes = kUnit * D / (FOUR ? 2 : 1);
+    static constexpr int kRawBytes = kRawCodes + (FOUR ? kUnit / 16 * 128 : 0);
+    // A copy's place in shared memory is a multiple of 128 bytes: so far apart are the scales of pages in a unit.
+    static __device__ __forceinline__ int slot(int box) { return max(box * (D / kGroup4), 128); }
     alignas(1024) uint8_t q[2][kQ];
     alignas(1024) uint8_t k[kBuf][kTile];
     alignas(1024) uint8_t v[kBuf][kTile];
     alignas(1024) uint8_t raw[kRaw][kRawBytes];
-    float4 exps[kExps][kKeys / 16];              // of each 16 keys: 2^ke, ve, 2^-ve (0 below kDeep), whether one of the 64 is below
+    float4 exps[kExps][kKeys / 16];              // (8 bits) of each 16 keys: 2^ke, ve, 2^-ve (0 below kDeep), whether one of the 64 is below
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kBuf], v_full[kBuf], kv_empty[kBuf];
     uint64_t s_full[2][2], p_full[2][2], o_full, e_full[kExps];
     uint32_t tmem;
@@ -283,12 +290,24 @@ __device__ __forceinline__ float *part_of(const AttentionArgs &p, const PromptGr
     return p.workspace + g.workspace + (int64_t)slot * (kRows * (D + 2));
 }
 
-template <int D>
+struct Maps { CUtensorMap k, v, k_scale, v_scale; };      // the scales' of a 4-bit cache only
+
+// A word of eight 4-bit codes as eight values / 64: in the order 0, 4, 1, 5, 2, 6, 3, 7 (attention4.cu).
+__device__ __forceinline__ uint4 turn4(uint32_t w, __half2 s, __half2 t) {
+    auto values = [&](uint32_t in) {
+        const uint32_t one = ptx::lop3_and_or(in, 0x00F000F0u, 0x3C003C00u);
+        const __half2 y = __hfma2(*reinterpret_cast<const __half2 *>(&one), s, t);
+        return *reinterpret_cast<const uint32_t *>(&y);
+    };
+    return make_uint4(values(w << 4), values(w), values(w >> 4), values(w >> 8));
+}
+
+template <int D, bool FOUR>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttentionArgs p,
-                  const PromptGrid grid) {
+    prompt_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const PromptGrid grid) {
+    constexpr float kValueUnit = FOUR ? 64.f : 1.f;            // what a cached value counts in the products
     extern __shared__ uint8_t raw_smem[];
-    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw_smem + ((1024 - (ptx::smem_u32(raw_smem) & 1023)) & 1023));
+    Smem<D, FOUR> &sm = *reinterpret_cast<Smem<D, FOUR> *>(raw_smem + ((1024 - (ptx::smem_u32(raw_smem) & 1023)) & 1023));
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;      // the warp number, uniform
     auto at = [](const uint64_t &bar) { return ptx::smem_u32(&bar); };
     if (tid == 0) {
@@ -305,8 +324,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(at(sm.o_full), 2);
         sm.poisoned = 0;
         ptx::fence_mbar_init();
-        ptx::prefetch_tensormap(&kmap);
-        ptx::prefetch_tensormap(&vmap);
+        ptx::prefetch_tensormap(&maps.k);
+        ptx::prefetch_tensormap(&maps.v);
+        if constexpr (FOUR) {
+            ptx::prefetch_tensormap(&maps.k_scale);
+            ptx::prefetch_tensormap(&maps.v_scale);
+        }
     }
     __syncthreads();
     ptx::pdl_launch_dependents();
@@ -380,14 +403,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int up = query_shift(__uint_as_float(top << 16));
             const float f = __uint_as_float(__float_as_uint(exp2_int(up)) | (p.scale_log2 < 0.f ? 0x80000000u : 0u));
-            qs = exp2_int(-up) * fabsf(p.scale_log2);
+            qs = exp2_int(-up) * fabsf(p.scale_log2) * kValueUnit;
             auto turn = [&](uint32_t v) {
                 const float2 y = ptx::fmul2(make_float2(bf16_lo(v), bf16_hi(v)), make_float2(f, f));
                 return f32x2_to_f16x2(y.x, y.y);
             };
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
-                sts_v4(own + (c >> 3) * 16384u + (((c & 7) ^ (lane & 7)) << 4), turn(x[c].x), turn(x[c].y), turn(x[c].z), turn(x[c].w));
+                if constexpr (FOUR) {                                  // in the order of a word's codes
+                    const uint4 y = make_uint4(turn(ptx::prmt(x[c].x, x[c].z, 0x5410u)), turn(ptx::prmt(x[c].x, x[c].z, 0x7632u)),
+                                               turn(ptx::prmt(x[c].y, x[c].w, 0x5410u)), turn(ptx::prmt(x[c].y, x[c].w, 0x7632u)));
+                    sts_v4(own + (c >> 3) * 16384u + (((c & 7) ^ (lane & 7)) << 4), y.x, y.y, y.z, y.w);
+                } else {
+                    sts_v4(own + (c >> 3) * 16384u + (((c & 7) ^ (lane & 7)) << 4), turn(x[c].x), turn(x[c].y), turn(x[c].z), turn(x[c].w));
+                }
             ptx::fence_proxy_async_smem();
         }
         bool ok = true;
@@ -395,16 +424,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tmem = meet(), sc = tmem + t * 128 + quarter, oc = tmem + 256 + t * D + quarter;
         for (int hs = 0; hs < 2 * w.n; ++hs) {                          // half-steps of 64 keys
             const int j = hs >> 1, h = hs & 1, key0 = (w.lo + j) * kKeys + h * kHalf;
-            if (h == 0 && ok) ok = ptx::mbar_wait(at(sm.e_full[j % kExps]), (j / kExps) & 1, &g_prompt_timeouts);
+            if (!FOUR && h == 0 && ok) ok = ptx::mbar_wait(at(sm.e_full[j % kExps]), (j / kExps) & 1, &g_prompt_timeouts);
             if (ok) ok = ptx::mbar_wait(at(sm.s_full[t][h]), j & 1, &g_prompt_timeouts);
             ptx::tc_fence_after();
-            const float4 *ex = sm.exps[j % kExps] + h * (kHalf / 16);
+            const float4 *exps = sm.exps[j % kExps] + h * (kHalf / 16);
+            auto ex = [&](int g) { return FOUR ? make_float4(1.f, 0.f, 1.f, 0.f) : exps[g]; };
             float v[kHalf];
             tmem_ld32(sc + h * kHalf, v);
             tmem_ld32(sc + h * kHalf + 32, v + 32);
             ptx::tmem_ld_wait();
             // A factor of 0 would make masked scores NaN.
-            auto factor = [&](int g) { return fmaxf(qs * ex[g].x, 1.2e-38f); };
+            auto factor = [&](int g) { return fmaxf(qs * ex(g).x, 1.2e-38f); };
             // The row's maximum, by 16 keys (all of one page).
             auto largest = [&] {
                 float mx = -INFINITY;
@@ -413,20 +443,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float *x = v + g * 16;
                     const float a = max3(max3(x[0], x[1], x[2]), x[3], x[4]), b = max3(max3(x[5], x[6], x[7]), x[8], x[9]);
                     const float c = max3(max3(x[10], x[11], x[12]), x[13], x[14]);
-                    mx = fmaxf(mx, fmaf(max3(max3(a, b, c), x[15], x[15]), factor(g), ex[g].y));
+                    mx = fmaxf(mx, fmaf(max3(max3(a, b, c), x[15], x[15]), factor(g), ex(g).y));
                 }
                 return mx;
             };
             float deep = 0.f;                                          // of l: the keys with ve below kDeep
-            if (partial(key0, kHalf) || ex[0].w != 0.f) {
+            if (partial(key0, kHalf) || ex(0).w != 0.f) {
                 const int hi = pos - key0, lo = low - key0;            // of the keys, those in (lo, hi] are seen
 #pragma unroll
                 for (int k = 0; k < kHalf; ++k)
                     if (k > hi || k <= lo) v[k] = -INFINITY;
-                if (ex[0].w != 0.f) {
+                if (ex(0).w != 0.f) {
                     const float mx = largest(), to = mx > m + kPeak ? mx - kStart : m, ref = to == -INFINITY ? 0.f : to;
 #pragma unroll
-                    for (int k = 0; k < kHalf; ++k) deep += ex[k / 16].y < kDeep ? ex2(fmaf(v[k], factor(k / 16), -ref)) : 0.f;
+                    for (int k = 0; k < kHalf; ++k) deep += ex(k / 16).y < kDeep ? ex2(fmaf(v[k], factor(k / 16), -ref)) : 0.f;
                 }
             }
             float f[kHalf / 16];
@@ -463,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t hp[16];
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const float4 e = ex[2 * c + g];
+                    const float4 e = ex(2 * c + g);
                     const float2 ff = make_float2(f[2 * c + g], f[2 * c + g]), d = make_float2(e.y - ref, e.y - ref);
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -500,6 +530,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int key = max(key0, low + 1); key <= min(key0 + kKeys - 1, pos); ++key) {
                     const int page = p.page_table[(int64_t)w.b * p.table_stride + key / P];
                     if ((unsigned)page >= (unsigned)p.pages) continue;
+                    if constexpr (FOUR) {                              // a scale that is no number: its 32 values
+                        const uint8_t *scale = p.v_scale + page * p.scale_page_stride + w.h * p.scale_head_stride + (int64_t)(key % P) * (D / kGroup4);
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i)
+                            if ((scale[i] & 0x7C) == 0x7C) nan[i] = ~0u;
+                        continue;
+                    }
                     const uint8_t *code = p.v_cache + page * p.page_stride + w.h * p.head_stride + (int64_t)(key % P) * D;
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i)
@@ -512,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // that stores cover whole rows; parts for the join go out value by value, a layout in
         // which the lanes' rows are neighbours.
         float4 *part = w.parts > 1 ? reinterpret_cast<float4 *>(part_of<D>(p, grid, w.slot + w.part)) + r : nullptr;
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const float inv = (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * kValueUnit;
         const int lr = r & 127;
         const uint32_t stage = ptx::smem_u32(sm.q[t]) + lr * (D * 2);
 #pragma unroll
@@ -524,6 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = 0.f;
+            }
+            if constexpr (FOUR) {                                      // back from the order of a word's codes
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    const float y[8] = {v[k], v[k + 2], v[k + 4], v[k + 6], v[k + 1], v[k + 3], v[k + 5], v[k + 7]};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k + i] = y[i];
+                }
             }
             if (nan[c] != 0u) {
 #pragma unroll
@@ -572,10 +617,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // addresses but the key's are the thread's own.  A chunk makes the 16-byte pieces
         // 2 (c % 4) and + 1 of half c / 4 of the key's row; halves alternate which piece goes
         // first: eight lanes then fill all banks.
-        constexpr int kChunks = kUnit * D / 16 / (kConvertWarps * 32), kStep = 128 * 16 / D;
-        const int ct = tid - kSoftmaxWarps * 32, c = ct % (D / 16), key_in = ct / (D / 16), half = c >> 2, sw = key_in & 7;
+        // A 4-bit cache's chunk holds 32 codes, all of one scale, and makes the pieces 4 (c % 2) to + 3 of
+        // half c / 2; halves begin two pieces apart.
+        constexpr int kOf = FOUR ? 32 : 16;                              // codes of a chunk
+        constexpr int kChunks = kUnit * D / kOf / (kConvertWarps * 32), kStep = 128 * kOf / D;
+        const int ct = tid - kSoftmaxWarps * 32, c = ct % (D / kOf), key_in = ct / (D / kOf), half = c / (64 / kOf), sw = key_in & 7;
         const uint32_t row_off = half * 16384 + key_in * 128;
         const uint32_t first = row_off + (((2 * (c & 3) + half) ^ sw) << 4), second = row_off + (((2 * (c & 3) + (half ^ 1)) ^ sw) << 4);
+        int scale_at[FOUR ? kChunks : 1];
+        if constexpr (FOUR) {
+            const int box = min(P, kUnit);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int key = key_in + i * kStep;
+                scale_at[i] = Smem<D, FOUR>::kRawCodes + key / box * Smem<D, FOUR>::slot(box) + key % box * (D / kGroup4) + c;
+            }
+        }
         bool ok = true;
         int unit = 0;
         for (int j = 0; j < w.n; ++j) {
@@ -593,14 +650,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int st = unit % kRaw;
                     if (ok) ok = ptx::mbar_wait(at(sm.raw_full[st]), (unit / kRaw) & 1, &g_prompt_timeouts);
                     uint4 x[kChunks];
+                    uint32_t scale[FOUR ? kChunks : 1];
 #pragma unroll
                     for (int i = 0; i < kChunks; ++i) x[i] = *reinterpret_cast<const uint4 *>(sm.raw[st] + (ct + i * 128) * 16);
+                    if constexpr (FOUR) {
+#pragma unroll
+                        for (int i = 0; i < kChunks; ++i) scale[i] = sm.raw[st][scale_at[i]];
+                    }
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(at(sm.raw_empty[st]));
                     if (mask && which) {
                         // Codes past the end, and NaN that not all rows may see, are cleared.
 #pragma unroll
                         for (int i = 0; i < kChunks; ++i) {
+                            if constexpr (FOUR) {
+                                if (key0 + u * kUnit + key_in + i * kStep >= w.len) scale[i] = 0u;
+                                if ((scale[i] & 0x7Cu) == 0x7Cu) scale[i] = 0u, sm.poisoned = 1;
+                                continue;
+                            }
                             uint32_t *in = reinterpret_cast<uint32_t *>(&x[i]), any = 0u;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -614,6 +681,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < kChunks; ++i) {
+                        if constexpr (FOUR) {
+                            const __half2 s = __half2half2(__ushort_as_half((unsigned short)(scale[i] << 8)));
+                            const __half2 t = __hmul2(s, __float2half2_rn(-1.125f));
+                            const uint4 y[4] = {turn4(x[i].x, s, t), turn4(x[i].y, s, t), turn4(x[i].z, s, t), turn4(x[i].w, s, t)};
+                            const uint32_t key_at = dst + (u * kUnit + i * kStep) * 128 + row_off;
+                            const bool flip = half != 0;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint4 z = flip ? y[k ^ 2] : y[k];
+                                sts_v4(key_at + (((4 * (c & 1) + (flip ? k ^ 2 : k)) ^ sw) << 4), z.x, z.y, z.z, z.w);
+                            }
+                            continue;
+                        }
                         uint32_t o[8];
                         e4m3x4_to_f16x2(x[i].x, o[0], o[1]);
                         e4m3x4_to_f16x2(x[i].y, o[2], o[3]);
@@ -666,16 +746,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int part = lane % parts, key = u * kUnit + part * box;
                 const int id = __shfl_sync(~0u, page, (j & 3) * 8 + ((key / 16) & 7));
                 const bool mine = lane < parts && id >= 0;
-                const uint32_t bytes = __popc(__ballot_sync(~0u, mine)) * (uint32_t)(box * D);
+                const uint32_t bytes = __popc(__ballot_sync(~0u, mine)) * (uint32_t)(box * (FOUR ? D / 2 + D / kGroup4 : D));
                 const uint32_t bar = at(sm.raw_full[st]);
                 if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
                 __syncwarp();
-                if (mine)
-                    ptx::tma_load_4d(ptx::smem_u32(sm.raw[st]) + part * box * D, i < kKeys / kUnit ? &kmap : &vmap, 0,
-                                     ((w.lo + j) * kKeys + key) & (P - 1), w.h, id, bar);
+                if (mine) {
+                    const int row = ((w.lo + j) * kKeys + key) & (P - 1);
+                    ptx::tma_load_4d(ptx::smem_u32(sm.raw[st]) + part * box * (Smem<D, FOUR>::kRawCodes / kUnit),
+                                     i < kKeys / kUnit ? &maps.k : &maps.v, 0, row, w.h, id, bar);
+                    if constexpr (FOUR)
+                        ptx::tma_load_4d(ptx::smem_u32(sm.raw[st]) + Smem<D, FOUR>::kRawCodes + part * Smem<D, FOUR>::slot(box),
+                                         i < kKeys / kUnit ? &maps.k_scale : &maps.v_scale, row * (D / kGroup4) / 4, w.h, id, 0, bar);
+                }
                 __syncwarp();
             }
-            if (j == 0 || (j & 3) == 2) look_exps();
+            if (!FOUR && (j == 0 || (j & 3) == 2)) look_exps();
+            if (FOUR) {
+                if ((j & 3) == 0) look(j + 4);
+                continue;
+            }
             if ((j & 3) == 0) {
                 ke = min(max(nke, kExpMin), kExpMax), ve = min(max(nve, kExpMin), kExpMax);
                 look(j + 4);
@@ -695,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = warp - kIssuer;
         const uint32_t qk = (1u << 4) | ((uint32_t)(kHalf >> 3) << 17) | (8u << 24);             // fp16 x fp16 -> fp32, M = 128
         const uint32_t pv = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);    // B along N
-        constexpr uint64_t kTileStep = Smem<D>::kTile >> 4;
+        constexpr uint64_t kTileStep = Smem<D, FOUR>::kTile >> 4;
         const uint64_t qd = ptx::sw128_desc(ptx::smem_u32(sm.q)) + (uint64_t)t * kTileStep;
         const uint64_t kd0 = ptx::sw128_desc(ptx::smem_u32(sm.k)), vd0 = sw128_mn_desc(ptx::smem_u32(sm.v), 16384);
         const uint32_t tmem = meet(), sd = tmem + t * 128, od = tmem + 256 + t * D;
@@ -760,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the splits: block (unit, y) takes 32 rows of a unit, a lane each; warp i takes
 // every eighth group of four values.
-template <int D>
+template <int D, bool FOUR>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const AttentionArgs p, const PromptGrid grid) {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
@@ -791,7 +880,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const AttentionArgs p,
         l = old.of_l(l) + more.of_l(ml.y);
         m = mx;
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const float inv = (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * (FOUR ? 64.f : 1.f);
     uint16_t *out = p.out + token * p.o_token + head * p.o_head;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k)
@@ -800,22 +889,31 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const AttentionArgs p,
     if (warp == 0 && p.lse != nullptr) p.lse[token * p.lse_token + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
 }
 
-template <int D>
+template <int D, bool FOUR>
 cudaError_t launch(const AttentionArgs &p, const PromptGrid &g, cudaStream_t stream) {
-    const uint32_t box[4] = {(uint32_t)D, (uint32_t)std::min(p.P, kUnit), 1, 1};
-    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.P, (uint64_t)p.Hk, (uint64_t)p.pages};
-    const uint64_t strides[3] = {(uint64_t)D, (uint64_t)p.head_stride, (uint64_t)p.page_stride};
-    CUtensorMap kmap, vmap;
-    if (!encode_tiled(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.k_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-        !encode_tiled(&vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.v_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+    constexpr uint32_t kRow = D / (FOUR ? 2 : 1);                       // bytes of a key's codes
+    const uint32_t rows = (uint32_t)std::min(p.P, kUnit), box[4] = {kRow, rows, 1, 1};
+    const uint64_t dims[4] = {(uint64_t)kRow, (uint64_t)p.P, (uint64_t)p.Hk, (uint64_t)p.pages};
+    const uint64_t strides[3] = {(uint64_t)kRow, (uint64_t)p.head_stride, (uint64_t)p.page_stride};
+    Maps maps{};
+    if (!encode_tiled(&maps.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.k_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_tiled(&maps.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.v_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
-    const int smem = (int)sizeof(Smem<D>) + 1024;
-    cudaError_t e = raise_smem_limit((const void *)prompt_kernel<D>, current_device(), smem);
+    if constexpr (FOUR) {                                               // a page's scales of a head are one run of bytes
+        const uint64_t sdims[4] = {(uint64_t)p.P * D / kGroup4 / 4, (uint64_t)p.Hk, (uint64_t)p.pages, 1};
+        const uint64_t sstrides[3] = {(uint64_t)p.scale_head_stride, (uint64_t)p.scale_page_stride, (uint64_t)p.scale_page_stride};
+        const uint32_t sbox[4] = {rows * D / kGroup4 / 4, 1, 1, 1};
+        if (!encode_tiled(&maps.k_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.k_scale, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !encode_tiled(&maps.v_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.v_scale, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+    }
+    const int smem = (int)sizeof(Smem<D, FOUR>) + 1024;
+    cudaError_t e = raise_smem_limit((const void *)prompt_kernel<D, FOUR>, current_device(), smem);
     if (e != cudaSuccess) return e;
     const unsigned units = (unsigned)(g.tiles * p.Hk);
-    e = launch_pdl(prompt_kernel<D>, dim3(units * (unsigned)g.splits), dim3(kThreads), smem, stream, kmap, vmap, p, g);
+    e = launch_pdl(prompt_kernel<D, FOUR>, dim3(units * (unsigned)g.splits), dim3(kThreads), smem, stream, maps, p, g);
     if (e != cudaSuccess || g.splits == 1) return e;
-    return launch_pdl(prompt_join_kernel<D>, dim3(units, kRows / 32), dim3(256), 0, stream, p, g);
+    return launch_pdl(prompt_join_kernel<D, FOUR>, dim3(units, kRows / 32), dim3(256), 0, stream, p, g);
 }
 
 }  // namespace
@@ -843,7 +941,8 @@ size_t prompt_workspace_bytes(const PromptGrid &g, int Hk, int D) {
 }
 
 cudaError_t launch_prompt(const AttentionArgs &p, const PromptGrid &g, cudaStream_t stream) {
-    return p.D == 128 ? launch<128>(p, g, stream) : launch<64>(p, g, stream);
+    if (p.k_scale != nullptr) return p.D == 128 ? launch<128, true>(p, g, stream) : launch<64, true>(p, g, stream);
+    return p.D == 128 ? launch<128, false>(p, g, stream) : launch<64, false>(p, g, stream);
 }
 
 uint32_t prompt_timeouts(bool reset) {
