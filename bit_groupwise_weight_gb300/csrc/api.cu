@@ -196,6 +196,7 @@ lowbit_status values_args(const Cache *c, uint16_t *k_out, uint16_t *v_out, lowb
     if (c == nullptr) return LOWBIT_EINVAL;
     lowbit_status st = check_heads(c);
     if (st != LOWBIT_OK || c->pages == 0) return st;
+    if ((int64_t)c->pages * c->kv_heads > INT32_MAX) return LOWBIT_EINVAL;
     if ((st = check_layout(c)) != LOWBIT_OK) return st;
     if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return LOWBIT_EINVAL;
     if ((st = check_device()) != LOWBIT_OK) return st;

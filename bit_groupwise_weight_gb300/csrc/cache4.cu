@@ -6,12 +6,11 @@
 // codes of 4 bits with a scale for each 32 values (int4.cuh).  No token's codes depend on
 // another's, unlike the 8-bit cache's, whose exponent is a page's.
 //
-// Work split.  A CTA takes a few tokens and, when there are few of them, a part of their rows
-// (the heads of q, k and v); a row is held by D / 8 neighbouring lanes, 8 values each, so that
-// norms and scales are shuffles.  A thread keeps to one row at a time and goes through the
-// tokens, four loads ahead of the work.  Cosines and sines are computed once a CTA for all its
-// rows.  Where the vectors allow it a value's mate of the rotation comes by a shuffle, else (odd
-// sizes, unaligned rows) by way of shared memory.
+// Work split.  A warp takes one token, or a part of its rows (the heads of q, k and v) when
+// there are few tokens; a row is held by D / 8 neighbouring lanes, 8 values each, so that norms and
+// scales are shuffles, and so are a value's mates in the rotation.  A lane holds the same values of
+// every row: its cosines and sines stay in registers for all of them.  Four rows are loaded
+// ahead of the work.  Odd sizes and unaligned rows find their mates by way of shared memory.
 #include <algorithm>
 
 #include "append.cuh"
@@ -24,34 +23,34 @@ namespace {
 
 using namespace append;
 
-constexpr int kThreads = 256, kMostTokens = 8, kAhead = 4;
-constexpr int kCtasToFill = 152 * 4;             // fewer CTAs than this: fewer tokens each, then rows divided
+constexpr int kThreads = 256, kWarps = kThreads / 32, kAhead = 4;
+constexpr int kWarpsToFill = 152 * 32;           // fewer warps than this: the rows of a token are divided
 
 struct Token {
-    int live;                            // whether it is of a sequence, and not past max_q
+    bool live;                           // whether it is of a sequence, and not past max_q
     int pos;                             // its place in the sequence
     int page, slot;                      // where its codes go; page -1: nowhere
 };
 
-// Where token `at` of q, k and v stands: by bisection of cu_q.
+// Where token `at` of q, k and v stands.  A whole warp looks: 32 places of cu_q at a time.
 __device__ __forceinline__ Token token_of(const AppendArgs &p, int at) {
-    Token t{0, 0, -1, 0};
-    int b, i, all;
+    Token t{false, 0, -1, 0};
+    int b = 0, i = at, all = p.n;
     if (p.cu_q == nullptr) {
-        b = at / p.n, i = at - b * p.n, all = p.n;
+        if (p.B > 1) b = at / p.n, i = at - b * p.n;
     } else {
-        int lo = 0, hi = p.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.cu_q[mid] <= at) lo = mid;
-            else hi = mid - 1;
+        int n = p.B;                     // the last sequence that begins at `at` or before, among n from b on
+        while (n > 1) {
+            const int step = (n + 31) / 32, mine = (int)(threadIdx.x & 31) * step;
+            const uint32_t begun = __ballot_sync(~0u, mine < n && (mine == 0 || p.cu_q[b + mine] <= at));
+            const int last = (31 - __clz(begun)) * step;
+            b += last, n = min(step, n - last);
         }
-        b = lo;
         const int start = min(max(p.cu_q[b], 0), p.T);
         i = at - start, all = min(p.cu_q[b + 1], p.T) - start;
         if (i < 0 || i >= min(all, p.max_q)) return t;
     }
-    t.live = 1;
+    t.live = true;
     t.pos = max(p.lens[b], 0) - all + i;
     const int page = t.pos >> p.pshift;
     if (t.pos >= 0 && page < p.width) {
@@ -61,202 +60,220 @@ __device__ __forceinline__ Token token_of(const AppendArgs &p, int at) {
     return t;
 }
 
+// Eight values of a group of 32 (held by four lanes) into their codes; the group's scale to its place.
+__device__ __forceinline__ void store_codes(const float (&x)[8], uint8_t *codes, uint8_t *scale) {
+    const uint32_t four = 0xFu << (threadIdx.x & 28);
+    uint32_t top = 0u;                   // the largest magnitude, as bits
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(four, top, 1));
+    top = max(top, __shfl_xor_sync(four, top, 2));
+    bool nan = false;
+    if (top >= 0x7F800000u) {            // not all of it finite
+        nan = top > 0x7F800000u;
+        top = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+            top = max(top, a < 0x7F800000u ? a : 0u);
+        }
+        top = max(top, __shfl_xor_sync(four, top, 1));
+        top = max(top, __shfl_xor_sync(four, top, 2));
+    }
+    const float s = scale4(__uint_as_float(top));
+    *reinterpret_cast<uint32_t *>(codes) = codes4(x, s);
+    if ((threadIdx.x & 3) == 0) *scale = (uint8_t)(nan ? 0x7Fu : scale4_byte(s));
+}
+
 template <int D, Form FORM>
-__global__ void __launch_bounds__(kThreads, 4) kv_append4_kernel(const AppendArgs p) {
-    constexpr int kRow = D / 8, kRows = kThreads / kRow;                  // lanes of a row, rows of a CTA at once
-    extern __shared__ __align__(16) float table[];                       // [tokens][R / 2] cosines, then sines
+__global__ void __launch_bounds__(kThreads, 3) kv_append4_kernel(const AppendArgs p) {
+    constexpr int kRow = D / 8, kRows = 32 / kRow;                       // lanes of a row, rows of a warp
+    __shared__ __align__(16) float turns[kWarps][2][D / 2];              // cosines and sines of the warp's token
     __shared__ __align__(16) float weights[2][D];                        // of the norms of q and k
-    __shared__ Token tokens[kMostTokens];
-    __shared__ float whole[FORM == kAny ? kRows : 1][FORM == kAny ? D : 1];
+    __shared__ float whole[FORM == kAny ? kThreads / kRow : 1][FORM == kAny ? D : 1];
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const int tid = threadIdx.x, half = p.R >> 1, first = blockIdx.x * p.table_tokens, nt = min(p.table_tokens, p.T - first);
-    const bool normed = p.q_norm != nullptr || p.k_norm != nullptr;
-    if (tid < nt) tokens[tid] = token_of(p, first + tid);
-    if (normed)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lane_in = lane % kRow, d0 = lane_in * 8, half = p.R >> 1;
+    const int unit = blockIdx.x * kWarps + warp, at = min(unit / p.units, p.T - 1), part = unit - unit / p.units * p.units;
+    const int rows = p.Hq + 2 * p.Hk, turns_of_rows = (rows + kRows - 1) / kRows;
+    const int last = (int)((uint32_t)turns_of_rows * (uint32_t)(part + 1) / (uint32_t)p.units);
+    int turn = (int)((uint32_t)turns_of_rows * (uint32_t)part / (uint32_t)p.units);
+    const bool mine = unit / p.units < p.T;
+    if (p.q_norm != nullptr || p.k_norm != nullptr)
         for (int i = tid; i < 2 * D; i += kThreads) {
             const void *w = i < D ? p.q_norm : p.k_norm;
             weights[i / D][i % D] = w == nullptr ? 1.f : norm_weight(w, p.norm_dtype, i % D);
         }
+    auto row_of = [&](int r) {
+        return r < p.Hq ? p.q + at * p.q_token + r * p.q_head
+                        : (r < p.Hq + p.Hk ? p.k + at * p.k_token + (r - p.Hq) * p.k_head : p.v + at * p.v_token + (r - p.Hq - p.Hk) * p.v_head);
+    };
+    uint4 v[kAhead];
+    auto load = [&](uint4 &to, int t) {
+        const int r = t * kRows + lane / kRow;
+        if (mine && t < last && r < rows) to = load8<FORM>(row_of(r) + d0);
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load(v[u], turn + u);
+    const Token tok = token_of(p, at);
+    for (int j = lane; j < half; j += 32) turn_of(p, position_of(p, at, tok.pos, j), j, turns[warp][0][j], turns[warp][1][j]);
     __syncthreads();
-    for (int i = tid; i < nt * half; i += kThreads) {
-        const int t = i / half, j = i - t * half;
-        turn_of(p, position_of(p, first + t, tokens[t].pos, j), j, table[i], table[p.table_tokens * half + i]);
-    }
-    __syncthreads();
+    if (!mine || !tok.live) return;
 
-    const int lane_in = tid % kRow, d0 = lane_in * 8;
+    // What the lane's values are multiplied by in the rotation: kHalves x cos + mate sin (the lower half's
+    // sines turned around), kNeighbours four pairs.
     const uint32_t mask = row_mask<kRow>();
-    const bool upper = d0 >= half;
-    const int mate_at = upper ? d0 - half : d0 + half;                   // where kHalves' mates are
-    for (int r = blockIdx.y * kRows + tid / kRow; r < p.Hq + 2 * p.Hk; r += gridDim.y * kRows) {
+    const bool upper = d0 >= half, turned = FORM != kAny && d0 < p.R;
+    const int mate_lane = FORM == kHalves && turned ? (upper ? d0 - half : d0 + half) >> 3 : lane_in;
+    float cs[8], sn[8];
+    if (turned) {
+        const int j0 = FORM == kHalves ? (upper ? d0 - half : d0) : d0 >> 1;
+#pragma unroll
+        for (int k = 0; k < (FORM == kHalves ? 8 : 4); ++k) {
+            cs[k] = turns[warp][0][j0 + k], sn[k] = turns[warp][1][j0 + k];
+            if (FORM == kHalves && !upper) sn[k] = -sn[k];
+        }
+    }
+    float wt[8];
+    int weighed = -1;                                                    // whose weights wt holds
+    const int64_t codes = tok.page * p.page_stride + tok.slot * (D / 2) + lane_in * 4;
+    const int64_t scales = tok.page * p.scale_page_stride + tok.slot * (D / kGroup4) + lane_in / 4;
+    uint16_t *const out = p.q_out + at * p.o_token + d0;
+    auto work = [&](const uint4 &in, int r) {
         const int kind = r < p.Hq ? 0 : (r < p.Hq + p.Hk ? 1 : 2);       // of q, k or v
-        const int head = kind == 0 ? r : (kind == 1 ? r - p.Hq : r - p.Hq - p.Hk);
-        const int64_t pitch = kind == 0 ? p.q_token : (kind == 1 ? p.k_token : p.v_token);
-        const uint16_t *row = (kind == 0 ? p.q + head * p.q_head : (kind == 1 ? p.k + head * p.k_head : p.v + head * p.v_head)) +
-                              first * pitch + d0;
-        const bool norm = kind == 0 ? p.q_norm != nullptr : (kind == 1 && p.k_norm != nullptr);
-        const float *wt = weights[kind == 1];
-        for (int t0 = 0; t0 < nt; t0 += kAhead) {
-            uint4 v[kAhead];
+        float x[8];
+        widen(in, x);
+        if (kind != 2) {
+            if (kind == 0 ? p.q_norm != nullptr : p.k_norm != nullptr) {
+                if (weighed != kind) {
+                    weighed = kind;
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (t0 + u < nt) v[u] = load8<FORM>(row + (t0 + u) * pitch);
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int t = t0 + u;
-                if (t >= nt) break;
-                const Token tok = tokens[t];
-                if (!tok.live || (kind != 0 && tok.page < 0)) continue;  // the same for the row's lanes
-                float x[8];
-                widen(v[u], x);
-                if (kind != 2) {
-                    float by = 1.f;
-                    if (norm) {
-                        by = row_norm<kRow>(x, p.eps);
-                        weigh(x, by, wt + d0);
-                    }
-                    const float *cs = table + t * half, *sn = table + (p.table_tokens + t) * half;
-                    if constexpr (FORM == kHalves) {
-                        const int from = d0 < p.R ? mate_at >> 3 : lane_in;
-                        const uint32_t flip = upper ? 0u : 0x80008000u;
-                        float y[8];
-                        widen(make_uint4(__shfl_sync(mask, v[u].x, from, kRow) ^ flip, __shfl_sync(mask, v[u].y, from, kRow) ^ flip,
-                                         __shfl_sync(mask, v[u].z, from, kRow) ^ flip, __shfl_sync(mask, v[u].w, from, kRow) ^ flip), y);
-                        if (d0 < p.R) {
-                            if (norm) weigh(y, by, wt + mate_at);
-                            const int j0 = upper ? mate_at : d0;
-#pragma unroll
-                            for (int i = 0; i < 8; i += 4) {
-                                const float4 c = *reinterpret_cast<const float4 *>(cs + j0 + i), s = *reinterpret_cast<const float4 *>(sn + j0 + i);
-                                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) x[i + k] = __fadd_rn(__fmul_rn(x[i + k], cc[k]), __fmul_rn(y[i + k], ss[k]));
-                            }
-                        }
-                    } else if constexpr (FORM == kNeighbours) {
-                        if (d0 < p.R) {
-                            const float4 c = *reinterpret_cast<const float4 *>(cs + (d0 >> 1)), s = *reinterpret_cast<const float4 *>(sn + (d0 >> 1));
-                            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float a = x[2 * k], b = x[2 * k + 1];
-                                x[2 * k] = __fsub_rn(__fmul_rn(a, cc[k]), __fmul_rn(b, ss[k]));
-                                x[2 * k + 1] = __fadd_rn(__fmul_rn(a, ss[k]), __fmul_rn(b, cc[k]));
-                            }
-                        }
-                    } else {
-                        float *all = whole[tid / kRow];
-                        __syncwarp(mask);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) all[d0 + i] = x[i];
-                        __syncwarp(mask);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int d = d0 + i;
-                            if (d >= p.R) continue;
-                            const bool second = p.interleaved ? d & 1 : d >= half;
-                            const int m = p.interleaved ? d ^ 1 : (second ? d - half : d + half), j = p.interleaved ? d >> 1 : (second ? m : d);
-                            const float a = __fmul_rn(x[i], cs[j]), b = __fmul_rn(all[m], sn[j]);
-                            x[i] = second ? __fadd_rn(b, a) : __fsub_rn(a, b);
-                        }
-                    }
+                    for (int k = 0; k < 8; ++k) wt[k] = weights[kind][d0 + k];
                 }
-                if (kind == 0) {
-                    uint16_t *to = p.q_out + (int64_t)(first + t) * p.o_token + head * p.o_head + d0;
-                    const uint32_t w[4] = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
-                                           f32x2_to_bf16x2(x[6], x[7])};
-                    if constexpr (FORM != kAny) {
-                        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-                    } else {
+                const float by = row_norm<kRow>(x, p.eps);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) to[i] = (uint16_t)(w[i >> 1] >> (i & 1 ? 16 : 0));
-                    }
-                    continue;
-                }
-                // The group's largest magnitude: as bits, over the four lanes that hold it.
-                const uint32_t four = 0xFu << (tid & 28);
-                uint32_t top = 0u;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-                top = max(top, __shfl_xor_sync(four, top, 1));
-                top = max(top, __shfl_xor_sync(four, top, 2));
-                bool nan = false;
-                if (top >= 0x7F800000u) {                                // not all of it finite
-                    nan = top > 0x7F800000u;
-                    top = 0u;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t a = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-                        top = max(top, a < 0x7F800000u ? a : 0u);
-                    }
-                    top = max(top, __shfl_xor_sync(four, top, 1));
-                    top = max(top, __shfl_xor_sync(four, top, 2));
-                }
-                const float s = scale4(__uint_as_float(top));
-                uint8_t *codes = (kind == 1 ? p.k_cache : p.v_cache) + tok.page * p.page_stride + head * p.head_stride + tok.slot * (D / 2);
-                uint8_t *scales = (kind == 1 ? p.k_scale : p.v_scale) + tok.page * p.scale_page_stride + head * p.scale_head_stride + tok.slot * (D / kGroup4);
-                *reinterpret_cast<uint32_t *>(codes + lane_in * 4) = codes4(x, s);
-                if ((tid & 3) == 0) scales[lane_in / 4] = (uint8_t)(nan ? 0x7Fu : scale4_byte(s));
+                for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(__fmul_rn(x[k], by), wt[k]);
             }
+            if constexpr (FORM == kHalves) {
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(mask, x[k], mate_lane, kRow);
+                if (turned) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = __fadd_rn(__fmul_rn(x[k], cs[k]), __fmul_rn(y[k], sn[k]));
+                }
+            } else if constexpr (FORM == kNeighbours) {
+                if (turned) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float a = x[2 * k], b = x[2 * k + 1];
+                        x[2 * k] = __fsub_rn(__fmul_rn(a, cs[k]), __fmul_rn(b, sn[k]));
+                        x[2 * k + 1] = __fadd_rn(__fmul_rn(a, sn[k]), __fmul_rn(b, cs[k]));
+                    }
+                }
+            } else {
+                float *all = whole[tid / kRow];
+                __syncwarp(mask);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) all[d0 + i] = x[i];
+                __syncwarp(mask);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int d = d0 + i;
+                    if (d >= p.R) continue;
+                    const bool second = p.interleaved ? d & 1 : d >= half;
+                    const int m = p.interleaved ? d ^ 1 : (second ? d - half : d + half), j = p.interleaved ? d >> 1 : (second ? m : d);
+                    const float a = __fmul_rn(x[i], turns[warp][0][j]), b = __fmul_rn(all[m], turns[warp][1][j]);
+                    x[i] = second ? __fadd_rn(b, a) : __fsub_rn(a, b);
+                }
+            }
+        }
+        if (kind == 0) {
+            uint16_t *to = out + r * p.o_head;
+            const uint32_t w[4] = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
+                                   f32x2_to_bf16x2(x[6], x[7])};
+            if constexpr (FORM != kAny) {
+                *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) to[i] = (uint16_t)(w[i >> 1] >> (i & 1 ? 16 : 0));
+            }
+        } else if (tok.page >= 0) {
+            const int head = kind == 1 ? r - p.Hq : r - p.Hq - p.Hk;
+            store_codes(x, (kind == 1 ? p.k_cache : p.v_cache) + codes + head * p.head_stride,
+                        (kind == 1 ? p.k_scale : p.v_scale) + scales + head * p.scale_head_stride);
+        }
+    };
+    for (; turn < last; turn += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = (turn + u) * kRows + lane / kRow;
+            const uint4 in = v[u];
+            load(v[u], turn + u + kAhead);
+            if (turn + u < last && r < rows) work(in, r);
         }
     }
 }
 
 template <int D>
 cudaError_t launch(const AppendArgs &p, cudaStream_t stream) {
-    constexpr int kRows = kThreads / (D / 8);
+    constexpr int kRows = 32 / (D / 8);
     const bool vec = p.qvec && p.kvec && p.vvec && p.ovec;
     const auto kernel = vec && p.interleaved && p.R % 8 == 0 ? kv_append4_kernel<D, kNeighbours>
                         : vec && !p.interleaved && p.R % 16 == 0 ? kv_append4_kernel<D, kHalves>
                                                                  : kv_append4_kernel<D, kAny>;
-    AppendArgs a = p;
-    const int passes = (p.Hq + 2 * p.Hk + kRows - 1) / kRows;
-    a.table_tokens = kMostTokens;
-    while (a.table_tokens > 1 && p.T < (int64_t)a.table_tokens * kCtasToFill) a.table_tokens /= 2;
-    const int64_t gx = (p.T + a.table_tokens - 1) / a.table_tokens;
-    const int gy = gx >= kCtasToFill ? 1 : (int)std::min<int64_t>(passes, (kCtasToFill + gx - 1) / gx);
-    return launch_pdl(kernel, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), (size_t)a.table_tokens * p.R * sizeof(float),
-                      stream, (const AppendArgs)a);
+    AppendArgs a = p;                    // units: warps of a token
+    a.units = (int)std::min<int64_t>((p.Hq + 2 * (int64_t)p.Hk + kRows - 1) / kRows, (kWarpsToFill + (int64_t)p.T - 1) / p.T);
+    const int64_t ctas = ((int64_t)p.T * a.units + kWarps - 1) / kWarps;
+    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, (const AppendArgs)a);
 }
 
-// Eight values a thread.  Bound: HBM, mostly the 16-bit values that are written.
+// Eight values of K and of V a thread; a page's head is 2^place of such.  Bound: HBM, mostly the 16-bit
+// values that are written.
 template <int D, bool FOUR>
-__global__ void __launch_bounds__(256) cache_values_kernel(const ValuesArgs p) {
+__global__ void __launch_bounds__(256) cache_values_kernel(const ValuesArgs p, int place_bits) {
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const int64_t n = (int64_t)p.pages * p.Hk * p.P * (D / 8);
+    const int64_t n = ((int64_t)p.pages * p.Hk) << place_bits;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int d8 = (int)(i % (D / 8));
-        const int64_t row = i / (D / 8), place = row / p.P;              // place: page and head
-        const int slot = (int)(row - place * p.P), head = (int)(place % p.Hk);
-        const int64_t page = place / p.Hk;
+        const uint32_t place = (uint32_t)(i >> place_bits), in = (uint32_t)i & ((1u << place_bits) - 1u);
+        const uint32_t page = place / (uint32_t)p.Hk, head = place - page * (uint32_t)p.Hk;
+        uint32_t w[2][2], scale[2];
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const uint8_t *codes = (which ? p.v : p.k) + page * p.page_stride + head * p.head_stride;
-            float x[8];
             if constexpr (FOUR) {
-                const uint8_t *scales = (which ? p.v_scale : p.k_scale) + page * p.scale_page_stride + head * p.scale_head_stride;
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + slot * (D / 2) + d8 * 4);
-                const float s = __half2float(__ushort_as_half((uint16_t)(scales[slot * (D / kGroup4) + d8 / 4] << 8)));
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = (float)((int)(w >> (4 * k) & 15u) - 8) * s;
+                w[which][0] = *reinterpret_cast<const uint32_t *>(codes + in * 4);
+                scale[which] = ((which ? p.v_scale : p.k_scale) + page * p.scale_page_stride + head * p.scale_head_stride)[in / 4];
             } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(codes + slot * D + d8 * 8);
-                const int e = (which ? p.v_exp : p.k_exp)[place];
-                const float s = exp2_int(min(max(e, kExpMin), kExpMax));
-                uint32_t h[4];
-                e4m3x4_to_f16x2(w.x, h[0], h[1]);
-                e4m3x4_to_f16x2(w.y, h[2], h[3]);
+                const uint2 v = *reinterpret_cast<const uint2 *>(codes + in * 8);
+                w[which][0] = v.x, w[which][1] = v.y;
+                scale[which] = (uint32_t)(which ? p.v_exp : p.k_exp)[place];
+            }
+        }
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float2 x[4];
+            if constexpr (FOUR) {
+                const float s = __half2float(__ushort_as_half((uint16_t)(scale[which] << 8)));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
-                    x[2 * k] = y.x * s, x[2 * k + 1] = y.y * s;
+                    const uint32_t v = w[which][0] >> (8 * k);           // 2^23 + code - (2^23 + 8)
+                    x[k] = ptx::fadd2(make_float2(__uint_as_float(0x4B000000u | (v & 15u)), __uint_as_float(0x4B000000u | (v >> 4 & 15u))),
+                                      make_float2(-8388616.f, -8388616.f));
+                    x[k] = ptx::fmul2(x[k], make_float2(s, s));
                 }
+            } else {
+                const float s = exp2_int(min(max((int)scale[which], kExpMin), kExpMax));
+                uint32_t h[4];
+                e4m3x4_to_f16x2(w[which][0], h[0], h[1]);
+                e4m3x4_to_f16x2(w[which][1], h[2], h[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = ptx::fmul2(__half22float2(*reinterpret_cast<const __half2 *>(&h[k])), make_float2(s, s));
             }
             *reinterpret_cast<uint4 *>((which ? p.v_out : p.k_out) + i * 8) =
-                make_uint4(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
-                           f32x2_to_bf16x2(x[6], x[7]));
+                make_uint4(f32x2_to_bf16x2(x[0].x, x[0].y), f32x2_to_bf16x2(x[1].x, x[1].y), f32x2_to_bf16x2(x[2].x, x[2].y),
+                           f32x2_to_bf16x2(x[3].x, x[3].y));
         }
     }
 }
@@ -275,8 +292,10 @@ cudaError_t launch_cache_values(const ValuesArgs &p, cudaStream_t stream) {
     const bool four = p.k_scale != nullptr;
     const auto kernel = p.D == 128 ? (four ? cache_values_kernel<128, true> : cache_values_kernel<128, false>)
                                    : (four ? cache_values_kernel<64, true> : cache_values_kernel<64, false>);
-    const int64_t n = (int64_t)p.pages * p.Hk * p.P * (p.D / 8);
-    return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 152 * 8 * 8)), dim3(256), 0, stream, p);
+    int bits = 0;
+    while (1 << bits < p.P * (p.D / 8)) ++bits;
+    const int64_t n = (int64_t)p.pages * p.Hk << bits;
+    return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 152 * 8 * 16)), dim3(256), 0, stream, p, bits);
 }
 
 }  // namespace lowbit

@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace lowbit {
 
@@ -37,12 +38,16 @@ __device__ __forceinline__ uint32_t scale4_byte(float s) { return (__float_as_ui
 // corrected by its remainder (1 / s rounded alone would put ties next to where they are).
 __device__ __forceinline__ uint32_t codes4(const float (&x)[8], float s) {
     const float inv = __frcp_rn(s), top = 7.f * s;
+    const float2 s2 = make_float2(-s, -s), inv2 = make_float2(inv, inv), to_int = make_float2(12582920.f, 12582920.f);
     uint32_t w = 0u;
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-        const float a = fminf(fmaxf(x[i], -top), top), t = a * inv;
-        const float q = fmaf(fmaf(-t, s, a), inv, t);
-        w = w * 16u + (__float_as_uint(q + 12582920.f) & 15u);            // 1.5 * 2^23 + 8: rounds to whole numbers
+    for (int i = 6; i >= 0; i -= 2) {
+        const float2 a = make_float2(fminf(fmaxf(x[i], -top), top), fminf(fmaxf(x[i + 1], -top), top)), t = ptx::fmul2(a, inv2);
+        float2 q;
+        ptx::ffma2(q, t, s2, a);
+        ptx::ffma2(q, q, inv2, t);
+        q = ptx::fadd2(q, to_int);                                        // 1.5 * 2^23 + 8: rounds to whole numbers
+        w = w * 256u + (__float_as_uint(q.y) & 15u) * 16u + (__float_as_uint(q.x) & 15u);
     }
     return w;
 }
