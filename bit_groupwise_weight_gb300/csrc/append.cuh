@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace lowbit {
 namespace append {
@@ -28,23 +29,19 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p) {
                       p[6] | (uint32_t)p[7] << 16);
 }
 
-// The lanes that hold this lane's row, LANES neighbours.
-template <int LANES>
-__device__ __forceinline__ uint32_t row_mask() {
-    return ((1u << LANES) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
-}
-
 // 1 / sqrt(mean of squares + eps) of a row held by LANES lanes, 8 values each.  Every operation
 // is rounded by itself, the squares are added in pairs: a key's codes are then the same in any
-// implementation, also next to a border between two.
+// implementation, also next to a border between two.  The lanes of `mask` call, whole rows of them.
 template <int LANES>
-__device__ __forceinline__ float row_norm(const float (&x)[8], float eps) {
+__device__ __forceinline__ float row_norm(const float (&x)[8], float eps, uint32_t mask) {
     float s[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = __fmul_rn(x[i], x[i]);
+    for (int i = 0; i < 8; i += 2) {
+        const float2 a = make_float2(x[i], x[i + 1]), b = ptx::fmul2(a, a);
+        s[i] = b.x, s[i + 1] = b.y;
+    }
     float t = __fadd_rn(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])),
                         __fadd_rn(__fadd_rn(s[4], s[5]), __fadd_rn(s[6], s[7])));
-    const uint32_t mask = row_mask<LANES>();
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) t = __fadd_rn(t, __shfl_xor_sync(mask, t, o));
     return __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(t, 1.f / (8 * LANES)), eps)));

@@ -74,8 +74,9 @@ struct Rows {
 };
 
 // Values d0 .. d0+7 of a row, rotated.  cs, sn: the token's cosines and sines, one a
-// pair.  Products and sums are rounded one by one (not contracted): the page's
-// exponent then follows from the same fp32 values in any implementation.  With PRE, x comes
+// pair.  Products and sums are rounded one by one, so that the page's exponent follows from
+// the same fp32 values in any implementation, but for kHalves without PRE: there they are taken
+// two at a time, and the compiler makes one rounding of a product and the sum.  With PRE, x comes
 // normed, and its mates are: times `norm`, times their weights `wt`.
 template <Form FORM, bool PRE>
 __device__ __forceinline__ void rotate(const AppendArgs &p, const uint16_t *row, int d0, const uint4 &mate, const float *cs,
@@ -94,7 +95,12 @@ __device__ __forceinline__ void rotate(const AppendArgs &p, const uint16_t *row,
             const float4 c = *reinterpret_cast<const float4 *>(cs + j0 + i), s = *reinterpret_cast<const float4 *>(sn + j0 + i);
             const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) {     // x cos -+ y sin, two at a time
+            for (int k = 0; k < 4; k += 2) {     // x cos -+ y sin
+                if constexpr (PRE) {
+                    x[i + k] = __fadd_rn(__fmul_rn(x[i + k], cc[k]), __fmul_rn(y[i + k], ss[k]));
+                    x[i + k + 1] = __fadd_rn(__fmul_rn(x[i + k + 1], cc[k + 1]), __fmul_rn(y[i + k + 1], ss[k + 1]));
+                    continue;
+                }
                 const float2 a = ptx::fmul2(make_float2(x[i + k], x[i + k + 1]), make_float2(cc[k], cc[k + 1]));
                 const float2 b = ptx::fmul2(make_float2(y[i + k], y[i + k + 1]), make_float2(ss[k], ss[k + 1]));
                 const float2 r = ptx::fadd2(a, b);
@@ -216,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
         const float *wt = weights[kind == kQuery ? 0 : 1];
         float norm = 1.f;
         if constexpr (PRE) {
-            if ((kind == kQuery ? p.q_norm : p.k_norm) != nullptr) norm = row_norm<kRow>(x, p.eps);
+            if ((kind == kQuery ? p.q_norm : p.k_norm) != nullptr) norm = row_norm<kRow>(x, p.eps, ((1u << kRow) - 1u) << (tid & 31 & ~(kRow - 1)));
             weigh(x, norm, wt + d0);
         }
         rotate<FORM, PRE>(p, row, d0, r.mate[FORM == kHalves ? v : 0], table + t * half, table + (p.table_tokens + t) * half, x,

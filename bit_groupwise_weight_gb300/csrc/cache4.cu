@@ -12,6 +12,7 @@
 // every row: its cosines and sines stay in registers for all of them.  Four rows are loaded
 // ahead of the work.  Odd sizes and unaligned rows find their mates by way of shared memory.
 #include <algorithm>
+#include <type_traits>
 
 #include "append.cuh"
 #include "fp8.cuh"
@@ -60,32 +61,39 @@ __device__ __forceinline__ Token token_of(const AppendArgs &p, int at) {
     return t;
 }
 
-// Eight values of a group of 32 (held by four lanes) into their codes; the group's scale to its place.
-__device__ __forceinline__ void store_codes(const float (&x)[8], uint8_t *codes, uint8_t *scale) {
-    const uint32_t four = 0xFu << (threadIdx.x & 28);
-    uint32_t top = 0u;                   // the largest magnitude, as bits
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(four, top, 1));
-    top = max(top, __shfl_xor_sync(four, top, 2));
-    bool nan = false;
-    if (top >= 0x7F800000u) {            // not all of it finite
-        nan = top > 0x7F800000u;
-        top = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t a = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-            top = max(top, a < 0x7F800000u ? a : 0u);
-        }
-        top = max(top, __shfl_xor_sync(four, top, 1));
-        top = max(top, __shfl_xor_sync(four, top, 2));
-    }
-    const float s = scale4(__uint_as_float(top));
-    *reinterpret_cast<uint32_t *>(codes) = codes4(x, s);
-    if ((threadIdx.x & 3) == 0) *scale = (uint8_t)(nan ? 0x7Fu : scale4_byte(s));
+// The largest magnitude of three, NaN if one is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+    return d;
 }
 
-template <int D, Form FORM>
+// Eight values of a group of 32 (held by four lanes) into their codes, and the group's scale; the
+// whole warp calls, and what is not `stored` is not written.
+__device__ __forceinline__ void store_codes(const float (&x)[8], bool stored, uint8_t *codes, uint8_t *scale) {
+    float top = max3(max3(max3(0.f, x[0], x[1]), x[2], x[3]), max3(max3(0.f, x[4], x[5]), x[6], x[7]), 0.f);
+    top = max3(top, __shfl_xor_sync(~0u, top, 1), 0.f);
+    top = max3(top, __shfl_xor_sync(~0u, top, 2), 0.f);
+    const bool nan = top != top;
+    if (__any_sync(~0u, !(top < INFINITY))) {        // not all of it finite
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fabsf(x[i]) < INFINITY ? fmaxf(top, fabsf(x[i])) : top;
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+    }
+    const float s = scale4(top);
+    const uint32_t w = codes4(x, s);
+    if (stored) {
+        *reinterpret_cast<uint32_t *>(codes) = w;
+        if ((threadIdx.x & 3) == 0) *scale = (uint8_t)(nan ? 0x7Fu : scale4_byte(s));
+    }
+}
+
+enum Kind { kQuery, kKey, kValue };
+
+// FULL: the whole head is rotated.
+template <int D, Form FORM, bool FULL>
 __global__ void __launch_bounds__(kThreads, 3) kv_append4_kernel(const AppendArgs p) {
     constexpr int kRow = D / 8, kRows = 32 / kRow;                       // lanes of a row, rows of a warp
     __shared__ __align__(16) float turns[kWarps][2][D / 2];              // cosines and sines of the warp's token
@@ -93,137 +101,153 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append4_kernel(const AppendArg
     __shared__ float whole[FORM == kAny ? kThreads / kRow : 1][FORM == kAny ? D : 1];
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lane_in = lane % kRow, d0 = lane_in * 8, half = p.R >> 1;
-    const int unit = blockIdx.x * kWarps + warp, at = min(unit / p.units, p.T - 1), part = unit - unit / p.units * p.units;
-    const int rows = p.Hq + 2 * p.Hk, turns_of_rows = (rows + kRows - 1) / kRows;
-    const int last = (int)((uint32_t)turns_of_rows * (uint32_t)(part + 1) / (uint32_t)p.units);
-    int turn = (int)((uint32_t)turns_of_rows * (uint32_t)part / (uint32_t)p.units);
-    const bool mine = unit / p.units < p.T;
-    if (p.q_norm != nullptr || p.k_norm != nullptr)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lane_in = lane % kRow, row_in = lane / kRow, d0 = lane_in * 8;
+    const int half = p.R >> 1, unit = blockIdx.x * kWarps + warp, at = unit / p.units, part = unit - at * p.units;
+    if (p.q_norm != nullptr || p.k_norm != nullptr) {
         for (int i = tid; i < 2 * D; i += kThreads) {
             const void *w = i < D ? p.q_norm : p.k_norm;
             weights[i / D][i % D] = w == nullptr ? 1.f : norm_weight(w, p.norm_dtype, i % D);
         }
-    auto row_of = [&](int r) {
-        return r < p.Hq ? p.q + at * p.q_token + r * p.q_head
-                        : (r < p.Hq + p.Hk ? p.k + at * p.k_token + (r - p.Hq) * p.k_head : p.v + at * p.v_token + (r - p.Hq - p.Hk) * p.v_head);
-    };
-    uint4 v[kAhead];
-    auto load = [&](uint4 &to, int t) {
-        const int r = t * kRows + lane / kRow;
-        if (mine && t < last && r < rows) to = load8<FORM>(row_of(r) + d0);
-    };
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) load(v[u], turn + u);
+        __syncthreads();
+    }
+    if (at >= p.T) return;
     const Token tok = token_of(p, at);
+    if (!tok.live) return;
     for (int j = lane; j < half; j += 32) turn_of(p, position_of(p, at, tok.pos, j), j, turns[warp][0][j], turns[warp][1][j]);
-    __syncthreads();
-    if (!mine || !tok.live) return;
+    __syncwarp();
 
     // What the lane's values are multiplied by in the rotation: kHalves x cos + mate sin (the lower half's
-    // sines turned around), kNeighbours four pairs.
-    const uint32_t mask = row_mask<kRow>();
-    const bool upper = d0 >= half, turned = FORM != kAny && d0 < p.R;
+    // sines turned around), kNeighbours four pairs.  Not turned: by 1 and 0.
+    const bool upper = d0 >= half, turned = FULL || d0 < p.R;
     const int mate_lane = FORM == kHalves && turned ? (upper ? d0 - half : d0 + half) >> 3 : lane_in;
-    float cs[8], sn[8];
-    if (turned) {
+    constexpr int kAngles = FORM == kHalves ? 8 : (FORM == kNeighbours ? 4 : 1);
+    float cs[kAngles], sn[kAngles];
+    if constexpr (FORM != kAny) {
         const int j0 = FORM == kHalves ? (upper ? d0 - half : d0) : d0 >> 1;
 #pragma unroll
-        for (int k = 0; k < (FORM == kHalves ? 8 : 4); ++k) {
-            cs[k] = turns[warp][0][j0 + k], sn[k] = turns[warp][1][j0 + k];
+        for (int k = 0; k < kAngles; ++k) {
+            cs[k] = turned ? turns[warp][0][j0 + k] : 1.f, sn[k] = turned ? turns[warp][1][j0 + k] : 0.f;
             if (FORM == kHalves && !upper) sn[k] = -sn[k];
         }
     }
-    float wt[8];
-    int weighed = -1;                                                    // whose weights wt holds
-    const int64_t codes = tok.page * p.page_stride + tok.slot * (D / 2) + lane_in * 4;
-    const int64_t scales = tok.page * p.scale_page_stride + tok.slot * (D / kGroup4) + lane_in / 4;
-    uint16_t *const out = p.q_out + at * p.o_token + d0;
-    auto work = [&](const uint4 &in, int r) {
-        const int kind = r < p.Hq ? 0 : (r < p.Hq + p.Hk ? 1 : 2);       // of q, k or v
-        float x[8];
-        widen(in, x);
-        if (kind != 2) {
-            if (kind == 0 ? p.q_norm != nullptr : p.k_norm != nullptr) {
-                if (weighed != kind) {
-                    weighed = kind;
+    // The warp's share of the rows, in sets of kRows of one kind.
+    const int q_sets = (p.Hq + kRows - 1) / kRows, k_sets = (p.Hk + kRows - 1) / kRows, sets = q_sets + 2 * k_sets;
+    const int begin = (int)((uint32_t)sets * (uint32_t)part / (uint32_t)p.units);
+    const int end = (int)((uint32_t)sets * (uint32_t)(part + 1) / (uint32_t)p.units);
+    auto rows = [&]<int KIND>(std::integral_constant<int, KIND>) {
+        const int before = KIND == kQuery ? 0 : (KIND == kKey ? q_sets : q_sets + k_sets), count = KIND == kQuery ? p.Hq : p.Hk;
+        const int first = max(begin - before, 0), last = min(end - before, KIND == kQuery ? q_sets : k_sets);
+        if (first >= last || (KIND != kQuery && tok.page < 0)) return;
+        const int64_t pitch = (KIND == kQuery ? p.q_head : (KIND == kKey ? p.k_head : p.v_head)) * kRows;
+        const int r0 = first * kRows + row_in;
+        const uint16_t *from = (KIND == kQuery ? p.q + at * p.q_token + r0 * p.q_head
+                                               : (KIND == kKey ? p.k + at * p.k_token + r0 * p.k_head : p.v + at * p.v_token + r0 * p.v_head)) + d0;
+        uint16_t *to = p.q_out + at * p.o_token + r0 * p.o_head + d0;
+        uint8_t *codes = (KIND == kKey ? p.k_cache : p.v_cache) + tok.page * p.page_stride + r0 * p.head_stride + tok.slot * (D / 2) + lane_in * 4;
+        uint8_t *scale = (KIND == kKey ? p.k_scale : p.v_scale) + tok.page * p.scale_page_stride + r0 * p.scale_head_stride +
+                         tok.slot * (D / kGroup4) + lane_in / 4;
+        const bool norm = KIND == kQuery ? p.q_norm != nullptr : (KIND == kKey && p.k_norm != nullptr);
+        float wt[KIND == kValue ? 1 : 8];
+        if constexpr (KIND != kValue) {
+            if (norm) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) wt[k] = weights[kind][d0 + k];
-                }
-                const float by = row_norm<kRow>(x, p.eps);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(__fmul_rn(x[k], by), wt[k]);
+                for (int k = 0; k < 8; ++k) wt[k] = weights[KIND][d0 + k];
             }
-            if constexpr (FORM == kHalves) {
-                float y[8];
+        }
+        uint4 v[kAhead];
+        auto load = [&](uint4 &next, int set) {
+            if (set < last && set * kRows + row_in < count) next = load8<FORM>(from);
+            from += pitch;
+        };
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(mask, x[k], mate_lane, kRow);
-                if (turned) {
+        for (int u = 0; u < kAhead; ++u) load(v[u], first + u);
+        for (int s0 = first; s0 < last; s0 += kAhead) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = __fadd_rn(__fmul_rn(x[k], cs[k]), __fmul_rn(y[k], sn[k]));
-                }
-            } else if constexpr (FORM == kNeighbours) {
-                if (turned) {
+            for (int u = 0; u < kAhead; ++u) {
+                const int set = s0 + u;
+                const bool live = set * kRows + row_in < count;          // the last set may have fewer rows
+                if (set >= last) break;
+                float x[8];
+                widen(v[u], x);
+                load(v[u], set + kAhead);
+                if constexpr (KIND != kValue) {
+                    if (norm) {
+                        const float by = row_norm<kRow>(x, p.eps, ~0u);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float a = x[2 * k], b = x[2 * k + 1];
-                        x[2 * k] = __fsub_rn(__fmul_rn(a, cs[k]), __fmul_rn(b, sn[k]));
-                        x[2 * k + 1] = __fadd_rn(__fmul_rn(a, sn[k]), __fmul_rn(b, cs[k]));
+                        for (int k = 0; k < 8; k += 2) {
+                            const float2 y = ptx::fmul2(ptx::fmul2(make_float2(x[k], x[k + 1]), make_float2(by, by)), make_float2(wt[k], wt[k + 1]));
+                            x[k] = y.x, x[k + 1] = y.y;
+                        }
+                    }
+                    if constexpr (FORM == kHalves) {
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2) {
+                            const float2 y = make_float2(__shfl_sync(~0u, x[k], mate_lane, kRow), __shfl_sync(~0u, x[k + 1], mate_lane, kRow));
+                            const float2 a = ptx::fmul2(make_float2(x[k], x[k + 1]), make_float2(cs[k], cs[k + 1]));
+                            const float2 b = ptx::fmul2(y, make_float2(sn[k], sn[k + 1]));
+                            // (Sums two at a time would be contracted with the products.)
+                            x[k] = turned ? __fadd_rn(a.x, b.x) : x[k], x[k + 1] = turned ? __fadd_rn(a.y, b.y) : x[k + 1];
+                        }
+                    } else if constexpr (FORM == kNeighbours) {
+                        if (turned) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float a = x[2 * k], b = x[2 * k + 1];
+                                x[2 * k] = __fsub_rn(__fmul_rn(a, cs[k]), __fmul_rn(b, sn[k]));
+                                x[2 * k + 1] = __fadd_rn(__fmul_rn(a, sn[k]), __fmul_rn(b, cs[k]));
+                            }
+                        }
+                    } else {
+                        float *all = whole[tid / kRow];
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) all[d0 + i] = x[i];
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int d = d0 + i;
+                            if (d >= p.R) continue;
+                            const bool second = p.interleaved ? d & 1 : d >= half;
+                            const int m = p.interleaved ? d ^ 1 : (second ? d - half : d + half), j = p.interleaved ? d >> 1 : (second ? m : d);
+                            const float a = __fmul_rn(x[i], turns[warp][0][j]), b = __fmul_rn(all[m], turns[warp][1][j]);
+                            x[i] = second ? __fadd_rn(b, a) : __fsub_rn(a, b);
+                        }
                     }
                 }
-            } else {
-                float *all = whole[tid / kRow];
-                __syncwarp(mask);
+                if constexpr (KIND == kQuery) {
+                    const uint32_t w[4] = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
+                                           f32x2_to_bf16x2(x[6], x[7])};
+                    if (!live) {
+                    } else if constexpr (FORM != kAny) {
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) all[d0 + i] = x[i];
-                __syncwarp(mask);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int d = d0 + i;
-                    if (d >= p.R) continue;
-                    const bool second = p.interleaved ? d & 1 : d >= half;
-                    const int m = p.interleaved ? d ^ 1 : (second ? d - half : d + half), j = p.interleaved ? d >> 1 : (second ? m : d);
-                    const float a = __fmul_rn(x[i], turns[warp][0][j]), b = __fmul_rn(all[m], turns[warp][1][j]);
-                    x[i] = second ? __fadd_rn(b, a) : __fsub_rn(a, b);
+                        for (int i = 0; i < 8; ++i) to[i] = (uint16_t)(w[i >> 1] >> (i & 1 ? 16 : 0));
+                    }
+                    to += kRows * p.o_head;
+                } else {
+                    store_codes(x, live, codes, scale);
+                    codes += kRows * p.head_stride, scale += kRows * p.scale_head_stride;
                 }
             }
         }
-        if (kind == 0) {
-            uint16_t *to = out + r * p.o_head;
-            const uint32_t w[4] = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
-                                   f32x2_to_bf16x2(x[6], x[7])};
-            if constexpr (FORM != kAny) {
-                *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) to[i] = (uint16_t)(w[i >> 1] >> (i & 1 ? 16 : 0));
-            }
-        } else if (tok.page >= 0) {
-            const int head = kind == 1 ? r - p.Hq : r - p.Hq - p.Hk;
-            store_codes(x, (kind == 1 ? p.k_cache : p.v_cache) + codes + head * p.head_stride,
-                        (kind == 1 ? p.k_scale : p.v_scale) + scales + head * p.scale_head_stride);
-        }
     };
-    for (; turn < last; turn += kAhead) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int r = (turn + u) * kRows + lane / kRow;
-            const uint4 in = v[u];
-            load(v[u], turn + u + kAhead);
-            if (turn + u < last && r < rows) work(in, r);
-        }
-    }
+    rows(std::integral_constant<int, kQuery>{});
+    rows(std::integral_constant<int, kKey>{});
+    rows(std::integral_constant<int, kValue>{});
 }
 
 template <int D>
 cudaError_t launch(const AppendArgs &p, cudaStream_t stream) {
     constexpr int kRows = 32 / (D / 8);
     const bool vec = p.qvec && p.kvec && p.vvec && p.ovec;
-    const auto kernel = vec && p.interleaved && p.R % 8 == 0 ? kv_append4_kernel<D, kNeighbours>
-                        : vec && !p.interleaved && p.R % 16 == 0 ? kv_append4_kernel<D, kHalves>
-                                                                 : kv_append4_kernel<D, kAny>;
+    const bool full = p.R == D;
+    const auto kernel = vec && p.interleaved && p.R % 8 == 0 ? (full ? kv_append4_kernel<D, kNeighbours, true> : kv_append4_kernel<D, kNeighbours, false>)
+                        : vec && !p.interleaved && p.R % 16 == 0 ? (full ? kv_append4_kernel<D, kHalves, true> : kv_append4_kernel<D, kHalves, false>)
+                                                                 : kv_append4_kernel<D, kAny, false>;
     AppendArgs a = p;                    // units: warps of a token
-    a.units = (int)std::min<int64_t>((p.Hq + 2 * (int64_t)p.Hk + kRows - 1) / kRows, (kWarpsToFill + (int64_t)p.T - 1) / p.T);
+    const int64_t sets = (p.Hq + kRows - 1) / kRows + 2 * (int64_t)((p.Hk + kRows - 1) / kRows);
+    a.units = (int)std::min<int64_t>(sets, (kWarpsToFill + (int64_t)p.T - 1) / p.T);
     const int64_t ctas = ((int64_t)p.T * a.units + kWarps - 1) / kWarps;
     return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, (const AppendArgs)a);
 }
