@@ -9,8 +9,10 @@
 // Work split.  A warp takes one token, or a part of its rows (the heads of q, k and v) when
 // there are few tokens; a row is held by D / 8 neighbouring lanes, 8 values each, so that norms and
 // scales are shuffles, and so are a value's mates in the rotation.  A lane holds the same values of
-// every row: its cosines and sines stay in registers for all of them.  Four rows are loaded
-// ahead of the work.  Odd sizes and unaligned rows find their mates by way of shared memory.
+// every row: its cosines and sines stay in registers for all of them.  Rows come by asynchronous
+// copies into a ring in shared memory, each lane's own bytes, as far ahead as the ring is long, the
+// first ones before the token's place is known.  Odd sizes and unaligned rows are read directly
+// and find their mates by way of shared memory.
 #include <algorithm>
 #include <type_traits>
 
@@ -25,13 +27,17 @@ namespace {
 using namespace append;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kAhead = 4;
-constexpr int kWarpsToFill = 152 * 32;           // fewer warps than this: the rows of a token are divided
+constexpr int kWarpsToFill = 152 * 32;       // fewer warps than this: the rows of a token are divided
 
 struct Token {
     bool live;                           // whether it is of a sequence, and not past max_q
     int pos;                             // its place in the sequence
     int page, slot;                      // where its codes go; page -1: nowhere
 };
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 // Where token `at` of q, k and v stands.  A whole warp looks: 32 places of cu_q at a time.
 __device__ __forceinline__ Token token_of(const AppendArgs &p, int at) {
@@ -94,11 +100,12 @@ enum Kind { kQuery, kKey, kValue };
 
 // FULL: the whole head is rotated.
 template <int D, Form FORM, bool FULL>
-__global__ void __launch_bounds__(kThreads, 3) kv_append4_kernel(const AppendArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) kv_append4_kernel(const AppendArgs p) {
     constexpr int kRow = D / 8, kRows = 32 / kRow;                       // lanes of a row, rows of a warp
     __shared__ __align__(16) float turns[kWarps][2][D / 2];              // cosines and sines of the warp's token
     __shared__ __align__(16) float weights[2][D];                        // of the norms of q and k
     __shared__ float whole[FORM == kAny ? kThreads / kRow : 1][FORM == kAny ? D : 1];
+    __shared__ uint4 ring[FORM == kAny ? 1 : kWarps][FORM == kAny ? 1 : kAhead][32];
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lane_in = lane % kRow, row_in = lane / kRow, d0 = lane_in * 8;
@@ -111,8 +118,56 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append4_kernel(const AppendArg
         __syncthreads();
     }
     if (at >= p.T) return;
+    // The warp's share of the rows, in sets of kRows of one kind.
+    const int q_sets = (p.Hq + kRows - 1) / kRows, k_sets = (p.Hk + kRows - 1) / kRows, sets = q_sets + 2 * k_sets;
+    const int begin = (int)((uint32_t)sets * (uint32_t)part / (uint32_t)p.units);
+    const int end = (int)((uint32_t)sets * (uint32_t)(part + 1) / (uint32_t)p.units);
+    // The next row to come: where it is, how far the following one of its kind, how many rows are left of it.
+    const uint16_t *coming;
+    int64_t pitch;
+    int left, coming_set = begin;
+    auto find = [&] {
+        const int kind = coming_set < q_sets ? kQuery : (coming_set < q_sets + k_sets ? kKey : kValue);
+        const int r = (coming_set - (kind == kQuery ? 0 : (kind == kKey ? q_sets : q_sets + k_sets))) * kRows + row_in;
+        const int64_t head = kind == kQuery ? p.q_head : (kind == kKey ? p.k_head : p.v_head);
+        coming = (kind == kQuery ? p.q + at * p.q_token : (kind == kKey ? p.k + at * p.k_token : p.v + at * p.v_token)) + r * head + d0;
+        pitch = head * kRows, left = (kind == kQuery ? p.Hq : p.Hk) - r;
+    };
+    auto advance = [&] {
+        coming += pitch, left -= kRows;
+        if (++coming_set == q_sets || coming_set == q_sets + k_sets) find();
+    };
+    uint32_t slot = 0, taken = 0;                                        // of the ring, for what comes and what is next
+    auto fetch = [&] {
+        if constexpr (FORM != kAny) {
+            if (coming_set < end) {
+                if (left > 0) cp_async16(ptx::smem_u32(&ring[warp][slot][lane]), coming);
+                advance();
+            }
+            slot = (slot + 1) % kAhead;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    auto next = [&] {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (FORM == kAny) {
+            if (left > 0) v = load8<FORM>(coming);
+            advance();
+        } else {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            v = ring[warp][taken][lane];
+            taken = (taken + 1) % kAhead;
+        }
+        return v;
+    };
+    find();
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch();
     const Token tok = token_of(p, at);
-    if (!tok.live) return;
+    if (!tok.live) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
     for (int j = lane; j < half; j += 32) turn_of(p, position_of(p, at, tok.pos, j), j, turns[warp][0][j], turns[warp][1][j]);
     __syncwarp();
 
@@ -130,18 +185,11 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append4_kernel(const AppendArg
             if (FORM == kHalves && !upper) sn[k] = -sn[k];
         }
     }
-    // The warp's share of the rows, in sets of kRows of one kind.
-    const int q_sets = (p.Hq + kRows - 1) / kRows, k_sets = (p.Hk + kRows - 1) / kRows, sets = q_sets + 2 * k_sets;
-    const int begin = (int)((uint32_t)sets * (uint32_t)part / (uint32_t)p.units);
-    const int end = (int)((uint32_t)sets * (uint32_t)(part + 1) / (uint32_t)p.units);
     auto rows = [&]<int KIND>(std::integral_constant<int, KIND>) {
         const int before = KIND == kQuery ? 0 : (KIND == kKey ? q_sets : q_sets + k_sets), count = KIND == kQuery ? p.Hq : p.Hk;
         const int first = max(begin - before, 0), last = min(end - before, KIND == kQuery ? q_sets : k_sets);
-        if (first >= last || (KIND != kQuery && tok.page < 0)) return;
-        const int64_t pitch = (KIND == kQuery ? p.q_head : (KIND == kKey ? p.k_head : p.v_head)) * kRows;
+        if (first >= last) return;
         const int r0 = first * kRows + row_in;
-        const uint16_t *from = (KIND == kQuery ? p.q + at * p.q_token + r0 * p.q_head
-                                               : (KIND == kKey ? p.k + at * p.k_token + r0 * p.k_head : p.v + at * p.v_token + r0 * p.v_head)) + d0;
         uint16_t *to = p.q_out + at * p.o_token + r0 * p.o_head + d0;
         uint8_t *codes = (KIND == kKey ? p.k_cache : p.v_cache) + tok.page * p.page_stride + r0 * p.head_stride + tok.slot * (D / 2) + lane_in * 4;
         uint8_t *scale = (KIND == kKey ? p.k_scale : p.v_scale) + tok.page * p.scale_page_stride + r0 * p.scale_head_stride +
@@ -154,81 +202,69 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append4_kernel(const AppendArg
                 for (int k = 0; k < 8; ++k) wt[k] = weights[KIND][d0 + k];
             }
         }
-        uint4 v[kAhead];
-        auto load = [&](uint4 &next, int set) {
-            if (set < last && set * kRows + row_in < count) next = load8<FORM>(from);
-            from += pitch;
-        };
+        for (int set = first; set < last; ++set) {
+            const bool live = set * kRows + row_in < count && (KIND == kQuery || tok.page >= 0);   // the last set may have fewer rows
+            float x[8];
+            widen(next(), x);
+            fetch();
+            if constexpr (KIND != kValue) {
+                if (norm) {
+                    const float by = row_norm<kRow>(x, p.eps, ~0u);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) load(v[u], first + u);
-        for (int s0 = first; s0 < last; s0 += kAhead) {
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int set = s0 + u;
-                const bool live = set * kRows + row_in < count;          // the last set may have fewer rows
-                if (set >= last) break;
-                float x[8];
-                widen(v[u], x);
-                load(v[u], set + kAhead);
-                if constexpr (KIND != kValue) {
-                    if (norm) {
-                        const float by = row_norm<kRow>(x, p.eps, ~0u);
-#pragma unroll
-                        for (int k = 0; k < 8; k += 2) {
-                            const float2 y = ptx::fmul2(ptx::fmul2(make_float2(x[k], x[k + 1]), make_float2(by, by)), make_float2(wt[k], wt[k + 1]));
-                            x[k] = y.x, x[k + 1] = y.y;
-                        }
-                    }
-                    if constexpr (FORM == kHalves) {
-#pragma unroll
-                        for (int k = 0; k < 8; k += 2) {
-                            const float2 y = make_float2(__shfl_sync(~0u, x[k], mate_lane, kRow), __shfl_sync(~0u, x[k + 1], mate_lane, kRow));
-                            const float2 a = ptx::fmul2(make_float2(x[k], x[k + 1]), make_float2(cs[k], cs[k + 1]));
-                            const float2 b = ptx::fmul2(y, make_float2(sn[k], sn[k + 1]));
-                            // (Sums two at a time would be contracted with the products.)
-                            x[k] = turned ? __fadd_rn(a.x, b.x) : x[k], x[k + 1] = turned ? __fadd_rn(a.y, b.y) : x[k + 1];
-                        }
-                    } else if constexpr (FORM == kNeighbours) {
-                        if (turned) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float a = x[2 * k], b = x[2 * k + 1];
-                                x[2 * k] = __fsub_rn(__fmul_rn(a, cs[k]), __fmul_rn(b, sn[k]));
-                                x[2 * k + 1] = __fadd_rn(__fmul_rn(a, sn[k]), __fmul_rn(b, cs[k]));
-                            }
-                        }
-                    } else {
-                        float *all = whole[tid / kRow];
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) all[d0 + i] = x[i];
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int d = d0 + i;
-                            if (d >= p.R) continue;
-                            const bool second = p.interleaved ? d & 1 : d >= half;
-                            const int m = p.interleaved ? d ^ 1 : (second ? d - half : d + half), j = p.interleaved ? d >> 1 : (second ? m : d);
-                            const float a = __fmul_rn(x[i], turns[warp][0][j]), b = __fmul_rn(all[m], turns[warp][1][j]);
-                            x[i] = second ? __fadd_rn(b, a) : __fsub_rn(a, b);
-                        }
+                    for (int k = 0; k < 8; k += 2) {
+                        const float2 y = ptx::fmul2(ptx::fmul2(make_float2(x[k], x[k + 1]), make_float2(by, by)), make_float2(wt[k], wt[k + 1]));
+                        x[k] = y.x, x[k + 1] = y.y;
                     }
                 }
-                if constexpr (KIND == kQuery) {
-                    const uint32_t w[4] = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
-                                           f32x2_to_bf16x2(x[6], x[7])};
-                    if (!live) {
-                    } else if constexpr (FORM != kAny) {
-                        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-                    } else {
+                if constexpr (FORM == kHalves) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) to[i] = (uint16_t)(w[i >> 1] >> (i & 1 ? 16 : 0));
+                    for (int k = 0; k < 8; k += 2) {
+                        const float2 y = make_float2(__shfl_sync(~0u, x[k], mate_lane, kRow), __shfl_sync(~0u, x[k + 1], mate_lane, kRow));
+                        const float2 a = ptx::fmul2(make_float2(x[k], x[k + 1]), make_float2(cs[k], cs[k + 1]));
+                        const float2 b = ptx::fmul2(y, make_float2(sn[k], sn[k + 1]));
+                        // (Sums two at a time would be contracted with the products.)
+                        x[k] = turned ? __fadd_rn(a.x, b.x) : x[k], x[k + 1] = turned ? __fadd_rn(a.y, b.y) : x[k + 1];
                     }
-                    to += kRows * p.o_head;
+                } else if constexpr (FORM == kNeighbours) {
+                    if (turned) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float a = x[2 * k], b = x[2 * k + 1];
+                            x[2 * k] = __fsub_rn(__fmul_rn(a, cs[k]), __fmul_rn(b, sn[k]));
+                            x[2 * k + 1] = __fadd_rn(__fmul_rn(a, sn[k]), __fmul_rn(b, cs[k]));
+                        }
+                    }
                 } else {
-                    store_codes(x, live, codes, scale);
-                    codes += kRows * p.head_stride, scale += kRows * p.scale_head_stride;
+                    float *all = whole[tid / kRow];
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) all[d0 + i] = x[i];
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int d = d0 + i;
+                        if (d >= p.R) continue;
+                        const bool second = p.interleaved ? d & 1 : d >= half;
+                        const int m = p.interleaved ? d ^ 1 : (second ? d - half : d + half), j = p.interleaved ? d >> 1 : (second ? m : d);
+                        const float a = __fmul_rn(x[i], turns[warp][0][j]), b = __fmul_rn(all[m], turns[warp][1][j]);
+                        x[i] = second ? __fadd_rn(b, a) : __fsub_rn(a, b);
+                    }
                 }
+            }
+            if constexpr (KIND == kQuery) {
+                const uint32_t w[4] = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
+                                       f32x2_to_bf16x2(x[6], x[7])};
+                if (!live) {
+                } else if constexpr (FORM != kAny) {
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) to[i] = (uint16_t)(w[i >> 1] >> (i & 1 ? 16 : 0));
+                }
+                to += kRows * p.o_head;
+            } else {
+                store_codes(x, live, codes, scale);
+                codes += kRows * p.head_stride, scale += kRows * p.scale_head_stride;
             }
         }
     };
