@@ -39,6 +39,16 @@ __device__ __forceinline__ uint32_t values4(uint32_t w, uint32_t s, uint32_t t) 
     const uint32_t in = I == 0 ? w << 4 : w >> (4 * I - 4);
     return hfma2(ptx::lop3_and_or(in, 0x00F000F0u, 0x3C003C00u), s, t);
 }
+// D = A B + C with C in other registers than D.
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                         float c0, float c1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+// An infinite factor (of a row of values near 2^127) would make NaN of sums that are 0.
+__device__ __forceinline__ float within(float x) { return fminf(fmaxf(x, -3.4028234663852886e38f), 3.4028234663852886e38f); }
 // Bytes that hold an infinite or no number (e5m2), as 0xFF each.
 __device__ __forceinline__ uint32_t bad_scales(uint32_t v) {
     return ((((v & 0x7C7C7C7Cu) + 0x04040404u) & 0x80808080u) >> 7) * 0xFFu;
@@ -52,6 +62,8 @@ struct Four {
     static constexpr int per_sm(int D, int ROWS) { return D == 128 && ROWS == 16 ? 2 : 3; }
     static constexpr int stages(int D, int ROWS) { return D == 64 ? 6 : (ROWS == 16 ? 5 : 3); }
     static constexpr float kUnit = 64.f;
+    // m of a row that has seen nothing: any score outgrows it, and, unlike with -inf, scores less m are numbers.
+    static constexpr float kNone = -3e38f;
     template <int D>
     static constexpr int kKeyBytes = D + D / 16;                          // codes and scales of K and V
 
@@ -149,7 +161,7 @@ struct Four {
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
             const int up = query_shift(amax);
-            const float odd = exp2_int(up), even = exp2_int(up + 4), scale = exp2_int(-up) * p.scale_log2;
+            const float odd = exp2_int(up), even = exp2_int(up + 4), scale = within(exp2_int(-up) * p.scale_log2 * 0x1p20f);
             float sum[G];
 #pragma unroll
             for (int j = 0; j < G; ++j) {
@@ -177,7 +189,7 @@ struct Four {
                 for (int j = 0; j < G; ++j) a.start[j][n][c] = __shfl_sync(~0u, sum[j], 8 * t + 4 * c);
                 a.qs[n][c] = __shfl_sync(~0u, scale, 8 * t + 4 * c);
                 a.pos[n][c] = __shfl_sync(~0u, position, 8 * t + 4 * c);
-                a.m[n][c] = -INFINITY, a.l[n][c] = 0.f;
+                a.m[n][c] = kNone, a.l[n][c] = 0.f;
             }
 #pragma unroll
             for (int c = 0; c < KS; ++c) a.o[c][n][0] = a.o[c][n][1] = a.o[c][n][2] = a.o[c][n][3] = 0.f;
@@ -222,9 +234,9 @@ struct Four {
                     const uint32_t a = r[2 * i], b = r[2 * i + 1], a8 = a >> 8, b8 = b >> 8;
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
-                        float acc[4] = {st.start[j][n][0], st.start[j][n][1], st.start[j][n][0], st.start[j][n][1]};
-                        ptx::mma_16816_f16(acc, a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u, b & 0x00F000F0u,
-                                           st.q[2 * j][n][0], st.q[2 * j][n][1]);
+                        float acc[4];
+                        mma_from(acc, a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u, b & 0x00F000F0u, st.q[2 * j][n][0],
+                                 st.q[2 * j][n][1], st.start[j][n][0], st.start[j][n][1]);
                         ptx::mma_16816_f16(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u,
                                            st.q[2 * j + 1][n][0], st.q[2 * j + 1][n][1]);
 #pragma unroll
@@ -238,25 +250,42 @@ struct Four {
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 seen[half][n] = 0xFu;
+                if constexpr (EDGE) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {        // (key g, row 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
-                    x[half][n][i] = x[half][n][i] * 0x1p20f * st.qs[n][i & 1];
-                    if constexpr (EDGE) {
+                    for (int i = 0; i < 4; ++i) {    // (key g, row 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
                         const int key = key0 + half * 16 + g + 8 * (i >> 1), pos = st.pos[n][i & 1];
-                        const bool see = key <= pos && (p.window == 0 || key > pos - p.window);
-                        if (!see) x[half][n][i] = -INFINITY, seen[half][n] &= ~(1u << i);
+                        if (!(key <= pos && (p.window == 0 || key > pos - p.window))) seen[half][n] &= ~(1u << i);
                     }
                 }
-                grown |= fmaxf(x[half][n][0], x[half][n][2]) > st.m[n][0] + kPeak ||
-                         fmaxf(x[half][n][1], x[half][n][3]) > st.m[n][1] + kPeak;
             }
         }
-        if (__any_sync(~0u, grown)) {                // rows whose maximum has outgrown m (the first keys seen: from -inf)
+        // Exponents of the weights: scores over m.
+        float y[2][N][4];
+        auto exponents = [&] {
+            float top = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[half][n][i] = fmaf(x[half][n][i], st.qs[n][i & 1], -st.m[n][i & 1]);
+                        if (EDGE && !(seen[half][n] >> i & 1u)) y[half][n][i] = -INFINITY;
+                        top = fmaxf(top, y[half][n][i]);
+                    }
+            return top;
+        };
+        if (__any_sync(~0u, exponents() > kPeak)) {  // rows whose maximum has outgrown m (the first keys seen: from kNone)
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(fmaxf(x[0][n][c], x[0][n][c + 2]), fmaxf(x[1][n][c], x[1][n][c + 2]));
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int i = c; i < 4; i += 2)
+                            if (!EDGE || (seen[half][n] >> i & 1u)) mx = fmaxf(mx, x[half][n][i] * st.qs[n][c]);
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
@@ -268,21 +297,20 @@ struct Four {
 #pragma unroll
                     for (int k = 0; k < 2 * G; ++k) st.o[k][n][c] *= f, st.o[k][n][c + 2] *= f;
                 }
+            exponents();
         }
         uint32_t pb[2][N][2];                        // P^T: B fragments
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                // A row that has seen nothing has m = -inf; its scores are -inf as well.
-                const float m0 = EDGE && st.m[n][0] == -INFINITY ? 0.f : st.m[n][0], m1 = EDGE && st.m[n][1] == -INFINITY ? 0.f : st.m[n][1];
-                float (&y)[4] = x[half][n];
+                float (&w)[4] = y[half][n];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = ex2(y[i] - (i & 1 ? m1 : m0));
-                st.l[n][0] += y[0] + y[2];
-                st.l[n][1] += y[1] + y[3];
-                pb[half][n][0] = transpose8(f32x2_to_f16x2(y[0], y[1]));
-                pb[half][n][1] = transpose8(f32x2_to_f16x2(y[2], y[3]));
+                for (int i = 0; i < 4; ++i) w[i] = ex2(w[i]);
+                st.l[n][0] += w[0] + w[2];
+                st.l[n][1] += w[1] + w[3];
+                pb[half][n][0] = transpose8(f32x2_to_f16x2(w[0], w[1]));
+                pb[half][n][1] = transpose8(f32x2_to_f16x2(w[2], w[3]));
             }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {

@@ -1,6 +1,6 @@
 // cache4.cu -- rotary positions and the write into the 4-bit paged cache, in one kernel
 // (lowbit_kv_append4), and the values that a cache of either kind holds (lowbit_cache_values,
-// lowbit_cache4_values).
+// lowbit_cache4_values).  Its part for queries serves the 8-bit write too (launch_append_queries).
 //
 // Mathematics: norms (optional) and rotation as in cache.cu (append.cuh), then k and v into
 // codes of 4 bits with a scale for each 32 values (int4.cuh).  No token's codes depend on
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append4_kernel(const AppendArg
     }
     if (at >= p.T) return;
     // The warp's share of the rows, in sets of kRows of one kind.
-    const int q_sets = (p.Hq + kRows - 1) / kRows, k_sets = (p.Hk + kRows - 1) / kRows, sets = q_sets + 2 * k_sets;
+    const int q_sets = (p.Hq + kRows - 1) / kRows, k_sets = p.q_only ? 0 : (p.Hk + kRows - 1) / kRows, sets = q_sets + 2 * k_sets;
     const int begin = (int)((uint32_t)sets * (uint32_t)part / (uint32_t)p.units);
     const int end = (int)((uint32_t)sets * (uint32_t)(part + 1) / (uint32_t)p.units);
     // The next row to come: where it is, how far the following one of its kind, how many rows are left of it.
@@ -282,7 +282,7 @@ cudaError_t launch(const AppendArgs &p, cudaStream_t stream) {
                         : vec && !p.interleaved && p.R % 16 == 0 ? (full ? kv_append4_kernel<D, kHalves, true> : kv_append4_kernel<D, kHalves, false>)
                                                                  : kv_append4_kernel<D, kAny, false>;
     AppendArgs a = p;                    // units: warps of a token
-    const int64_t sets = (p.Hq + kRows - 1) / kRows + 2 * (int64_t)((p.Hk + kRows - 1) / kRows);
+    const int64_t sets = (p.Hq + kRows - 1) / kRows + (p.q_only ? 0 : 2 * (int64_t)((p.Hk + kRows - 1) / kRows));
     a.units = (int)std::min<int64_t>(sets, (kWarpsToFill + (int64_t)p.T - 1) / p.T);
     const int64_t ctas = ((int64_t)p.T * a.units + kWarps - 1) / kWarps;
     return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, (const AppendArgs)a);
@@ -339,6 +339,12 @@ __global__ void __launch_bounds__(256) cache_values_kernel(const ValuesArgs p, i
 }
 
 }  // namespace
+
+cudaError_t launch_append_queries(const AppendArgs &args, cudaStream_t stream) {
+    AppendArgs p = args;
+    p.q_only = true;
+    return launch_kv_append4(p, stream);
+}
 
 cudaError_t launch_kv_append4(const AppendArgs &args, cudaStream_t stream) {
     AppendArgs p = args;

@@ -196,9 +196,11 @@ struct AppendArgs {
     // The 4-bit cache's scales (cache4.cu).
     uint8_t *k_scale, *v_scale;
     int64_t scale_page_stride, scale_head_stride;
+    bool q_only;                                                        // cache4.cu: no keys and values
 };
 cudaError_t launch_kv_append(const AppendArgs &args, cudaStream_t stream);
 cudaError_t launch_kv_append4(const AppendArgs &args, cudaStream_t stream);   // into the 4-bit cache (cache4.cu)
+cudaError_t launch_append_queries(const AppendArgs &args, cudaStream_t stream);  // the rows of q alone (cache4.cu)
 // The values that a cache holds, bf16 [pages, Hk, P, D] (cache4.cu); exps of the 8-bit one, or scales of the 4-bit one.
 struct ValuesArgs {
     const uint8_t *k, *v;
