@@ -5,6 +5,7 @@
 // allocates device memory or synchronises.
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -212,7 +213,7 @@ size_t attention_workspace(int32_t heads, const Cache *c, const lowbit_sequences
     if (check_sizes(c, s, heads) != LOWBIT_OK || empty(s)) return 0;
     const bool uniform = s->cu_q == nullptr;
     return lowbit::attention_workspace_bytes(s->tokens, s->batch, uniform ? s->tokens / s->batch : s->max_q, uniform,
-                                             heads, c->kv_heads, c->head_dim, (int64_t)s->width * c->page);
+                                             heads, c->kv_heads, c->head_dim, (int64_t)s->width * c->page, std::is_same_v<Cache, lowbit_cache4>);
 }
 
 // What an attention over a cache of either kind is launched with, checked.

@@ -77,6 +77,7 @@ struct Eight {
     // CTAs of an SM (what registers allow) and stages: about 150 KB of loads in flight.
     static constexpr int per_sm(int D, int ROWS) { return D == 128 && ROWS == 16 ? 2 : 3; }
     static constexpr int stages(int D, int ROWS) { return D == 64 ? 6 : (ROWS == 16 ? 5 : 3); }
+    static constexpr int kCtas = kSms * 3;                                // at most
     static constexpr float kUnit = 1.f;                                   // what a value of V counts in the product
     template <int D>
     static constexpr int kKeyBytes = 2 * D;                               // of K and V
@@ -355,9 +356,8 @@ Kernels kernels_for(int max_q, bool uniform, int G) {
     return {!uniform, true, uniform ? 0 : kFewRows};
 }
 
-size_t few_workspace_bytes(int max_q, int G, int D) {
-    const int rows = (int64_t)max_q * G <= 8 ? 8 : 16;
-    return (size_t)kCtas * (sizeof(u64) + sizeof(Join) + 2 * rows * (D + 2) * sizeof(float));
+size_t few_workspace_bytes(int max_q, int G, int D, bool four) {
+    return four ? attention4_workspace_bytes(max_q, G, D) : few_rows_workspace<Eight>(max_q, G, D);
 }
 
 }  // namespace
@@ -367,9 +367,9 @@ uint32_t attention_timeouts(bool reset) {
     return few_rows_timeouts(reset) + attention4_timeouts(reset) + prompt;
 }
 
-size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D, int64_t max_len) {
+size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D, int64_t max_len, bool four) {
     const Kernels k = kernels_for(max_q, uniform, Hq / Hk);
-    size_t bytes = k.few ? few_workspace_bytes(max_q, Hq / Hk, D) : 0;
+    size_t bytes = k.few ? few_workspace_bytes(max_q, Hq / Hk, D, four) : 0;
     if (k.many) bytes += prompt_workspace_bytes(prompt_grid(T, B, max_q, uniform, Hq, Hk, max_len), Hk, D);
     return std::max<size_t>(bytes, 16);
 }
@@ -389,7 +389,7 @@ cudaError_t launch_attention(const AttentionArgs &args, cudaStream_t stream) {
     p.call = calls.fetch_add(1, std::memory_order_relaxed) | 1ull << 63;
     if (k.many) {
         PromptGrid g = prompt_grid(p.T, p.B, p.max_q, uniform, p.Hq, p.Hk, (int64_t)p.width * p.P);
-        g.workspace = k.few ? (int64_t)(few_workspace_bytes(p.max_q, p.G, p.D) / sizeof(float)) : 0;
+        g.workspace = k.few ? (int64_t)(few_workspace_bytes(p.max_q, p.G, p.D, p.k_scale != nullptr) / sizeof(float)) : 0;
         const cudaError_t e = launch_prompt(p, g, stream);
         if (e != cudaSuccess || !k.few) return e;
     }

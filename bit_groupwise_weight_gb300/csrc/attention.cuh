@@ -21,6 +21,7 @@ uint32_t prompt_timeouts(bool reset);
 // Few query rows a sequence over a 4-bit cache (attention4.cu).
 cudaError_t launch_attention4(const AttentionArgs &p, cudaStream_t stream);
 uint32_t attention4_timeouts(bool reset);
+size_t attention4_workspace_bytes(int max_q, int G, int D);
 
 namespace attn {
 

@@ -6,8 +6,9 @@
 //     q . k = sum over groups of s (q . c - 8 sum q),
 // and the products run on the codes c alone, groups apart: masking two nibbles out of a word of
 // eight leaves a pair of fp16 subnormals c 2^-24 (c 2^-20 for the second nibble of a byte, whose q
-// is held 2^4 smaller instead), exact, one instruction for two codes.  The accumulators start at
-// -8 sum q; scales are applied to the groups' sums in fp32.
+// is held 2^4 smaller instead), exact, one instruction for two codes.  Scales are applied to the groups'
+// sums in fp32.  The offsets, s times -8 sum q, are a product of their own for all groups at once: scales are
+// fp16 numbers, and a sum is three of them (33 bits).
 // In the product with V the groups run along the rows of the result and the scales along the sum:
 // there codes become values first.  A nibble in the mantissa of 1.0 is 1 + c / 64, and
 //     (1 + c / 64) s - 1.125 s = (c - 8) s / 64,
@@ -39,13 +40,12 @@ __device__ __forceinline__ uint32_t values4(uint32_t w, uint32_t s, uint32_t t) 
     const uint32_t in = I == 0 ? w << 4 : w >> (4 * I - 4);
     return hfma2(ptx::lop3_and_or(in, 0x00F000F0u, 0x3C003C00u), s, t);
 }
-// D = A B + C with C in other registers than D.
-__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
-                                         float c0, float c1) {
+// D = A B.
+__device__ __forceinline__ void mma_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // An infinite factor (of a row of values near 2^127) would make NaN of sums that are 0.
 __device__ __forceinline__ float within(float x) { return fminf(fmaxf(x, -3.4028234663852886e38f), 3.4028234663852886e38f); }
@@ -57,10 +57,11 @@ __device__ __forceinline__ uint32_t bad_scales(uint32_t v) {
 // The 4-bit cache.
 struct Four {
     static constexpr int kTile = 128, kTileBits = 7, kWarpKeys = 32;
-    static constexpr int kItemCost = 4;
+    static constexpr int kItemCost = 3;
     static constexpr int kMinChunk = 4;
-    static constexpr int per_sm(int D, int ROWS) { return D == 128 && ROWS == 16 ? 2 : 3; }
-    static constexpr int stages(int D, int ROWS) { return D == 64 ? 6 : (ROWS == 16 ? 5 : 3); }
+    static constexpr int per_sm(int D, int ROWS) { return ROWS == 16 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 4); }
+    static constexpr int stages(int D, int ROWS) { return D == 64 ? (ROWS == 16 ? 6 : 4) : (ROWS == 16 ? 5 : 3); }
+    static constexpr int kCtas = kSms * 4;                                // at most
     static constexpr float kUnit = 64.f;
     // m of a row that has seen nothing: any score outgrows it, and, unlike with -inf, scores less m are numbers.
     static constexpr float kNone = -3e38f;
@@ -94,15 +95,17 @@ struct Four {
                                                 uint32_t bar) {
         constexpr int kCodes = D / 2;
         const int x = row * (D / kGroup4) / 4, slot = part * slot_of_box<D>(box);
-        ptx::tma_load_4d(ptx::smem_u32(s.k) + part * box * kCodes, &m.k, 0, row, head, page, bar);
+        ptx::tma_load_4d(ptx::smem_u32(s.k) + part * box * kCodes, &m.k, 0, row * kCodes / 128, head, page, bar);
         ptx::tma_load_4d(ptx::smem_u32(s.k_scale) + slot, &m.k_scale, x, head, page, 0, bar);
-        ptx::tma_load_4d(ptx::smem_u32(s.v) + part * box * kCodes, &m.v, 0, row, head, page, bar);
+        ptx::tma_load_4d(ptx::smem_u32(s.v) + part * box * kCodes, &m.v, 0, row * kCodes / 128, head, page, bar);
         ptx::tma_load_4d(ptx::smem_u32(s.v_scale) + slot, &m.v_scale, x, head, page, 0, bar);
     }
     static __device__ __forceinline__ void put_beside(StageBeside &, const Beside &, int, int) {}
 
-    // A lane's ldmatrix address in the first 16 keys of its warp's 32, without the chunk of 16 bytes (32
-    // codes, a group): chunk c is at (address ^ c << 4), the second 16 keys 8 D bytes on.
+    // A stage's codes are lines of 128 bytes, two keys (of 128 values) or four: whole lines are what copies are
+    // quick with (lines of 64 bytes: 40.5 us for 131001 keys).  A lane's ldmatrix address in the first 16 keys of its warp's 32,
+    // without the chunk of 16 bytes (32 codes, a group): the swizzle flips bits of a chunk's number in its line by the
+    // line's, so chunk c is at (address ^ c << 4); the second 16 keys are 8 lines on, or 4.
     template <int D>
     struct Lane {
         uint32_t off, scales[2];                     // scales: of the first key of each 16
@@ -114,9 +117,16 @@ struct Four {
                 scales[i] = first / box * slot + first % box * (D / kGroup4);
             }
             const int lane = threadIdx.x & 31, key = warp * kWarpKeys + ((lane >> 3) & 1) * 8 + (lane & 7);
-            off = key * (D / 2) + (((lane >> 4) ^ (D == 128 ? (key >> 1) & 3 : (key >> 2) & 1)) << 4);
+            const uint32_t in = key * (D / 2) + ((lane >> 4) << 4);
+            off = in ^ (in >> 7 & 7) << 4;
         }
     };
+
+    // Of the first 16 keys (half 0) or the second.
+    template <int D>
+    static __device__ __forceinline__ uint32_t second(uint32_t at, int half) {
+        return half == 0 ? at : (D == 128 ? at : at ^ 64u) + 8 * D;
+    }
 
     // A consumer warp's state of an item.  Lane (g, t) = (lane / 4, lane % 4); column pair
     // n: query rows 8n + 2t and 8n + 2t + 1.
@@ -124,7 +134,7 @@ struct Four {
     struct State {
         static constexpr int KS = D / 16, N = ROWS / 8, G = D / kGroup4;
         uint32_t q[KS][N][2];                        // B fragments of q^T: values 8t + (0, 4), (1, 5); (2, 6), (3, 7) of a group
-        float start[G][N][2];                        // -8 sum q of the group, as the accumulators hold it
+        uint32_t offset[N][2];                       // B fragment of -8 sum q of the groups, in three parts
         float qs[N][2];                              // factor of the row's scores
         int pos[N][2];
         float o[KS][N][4];                           // O^T
@@ -177,16 +187,26 @@ struct Four {
                     const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&a.q[2 * j + 1][n][c]));
                     half[c] = (x.x + x.y) + (y.x + y.y);
                 }
-                sum[j] = fmaf(half[1], 16.f, half[0]) * (-8.f * 0x1p-24f);
+                sum[j] = fmaf(half[1], 16.f, half[0]) * (-8.f * 0x1p-8f);          // below 2^15
                 sum[j] += __shfl_xor_sync(~0u, sum[j], 1);
                 sum[j] += __shfl_xor_sync(~0u, sum[j], 2);
             }
+            // Rows of the fragment: lanes t = 0 and 1 the groups' upper 11 bits, 2 and 3 the next 11; then, 0 and 1, the last.
+            float rest[2] = {G == 4 && (t & 1) ? sum[G - 2] : sum[0], G == 4 && (t & 1) ? sum[G - 1] : sum[1]};
+            uint32_t parts[3];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                parts[k] = f32x2_to_f16x2(rest[0], rest[1]);
+                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&parts[k]));
+                rest[0] -= x.x, rest[1] -= x.y;
+            }
+            const bool counts = G == 4 || (t & 1) == 0;                        // two groups fill half of the lanes
+            a.offset[n][0] = counts ? (t < 2 ? parts[0] : parts[1]) : 0u;
+            a.offset[n][1] = counts && t < 2 ? parts[2] : 0u;
             // This lane's columns are rows 2t and 2t + 1.
             const int position = live ? first + i : -1;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int j = 0; j < G; ++j) a.start[j][n][c] = __shfl_sync(~0u, sum[j], 8 * t + 4 * c);
                 a.qs[n][c] = __shfl_sync(~0u, scale, 8 * t + 4 * c);
                 a.pos[n][c] = __shfl_sync(~0u, position, 8 * t + 4 * c);
                 a.m[n][c] = kNone, a.l[n][c] = 0.f;
@@ -198,7 +218,7 @@ struct Four {
 
     // The scales of a key's groups as fp32.
     template <int D>
-    static __device__ __forceinline__ void key_scales(uint32_t at, float (&s)[D / kGroup4]) {
+    static __device__ __forceinline__ uint32_t key_scales(uint32_t at, float (&s)[D / kGroup4]) {
         const uint32_t u = D == 128 ? ptx::lds_u32(at) : (uint32_t)ptx::lds_u16(at);
 #pragma unroll
         for (int j = 0; j < D / kGroup4; j += 2) {
@@ -206,6 +226,7 @@ struct Four {
             const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
             s[j] = x.x, s[j + 1] = x.y;
         }
+        return u;
     }
 
     // A warp's 32 keys of a stage, in two halves of 16.  EDGE: some row does not see some key of them.
@@ -216,18 +237,26 @@ struct Four {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const uint32_t kat = ptx::smem_u32(stage.k) + at.off, vat = ptx::smem_u32(stage.v) + at.off;
         const uint32_t kst = ptx::smem_u32(stage.k_scale) + g * G, vst = ptx::smem_u32(stage.v_scale) + 2 * t * G;
+        const uint32_t mine = D == 128 && (t & 1) ? 0x3424u : 0x1404u;           // this lane's two groups as an fp16 pair
         float x[2][N][4];
         uint32_t seen[2][N];                         // bit i: value i of the pair is seen
         bool grown = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float s0[G], s1[G];                      // of keys g and g + 8
-            key_scales<D>(kst + at.scales[half], s0);
-            key_scales<D>(kst + at.scales[half] + 8 * G, s1);
+            const uint32_t u0 = key_scales<D>(kst + at.scales[half], s0), u1 = key_scales<D>(kst + at.scales[half] + 8 * G, s1);
+            // The groups' offsets: scales times -8 sum q.
+            const uint32_t f0 = ptx::prmt(u0, 0u, mine), f1 = ptx::prmt(u1, 0u, mine);
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                mma_new(x[half][n], f0, f1, f0, f1, st.offset[n][0], st.offset[n][1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[half][n][k] *= 0x1p-16f;
+            }
 #pragma unroll
             for (int c = 0; c < G; c += 2) {
                 uint32_t r[4];
-                ldsm_x4((kat + half * 8 * D) ^ (c << 4), r);     // (keys 0-7, chunk c), (8-15, c), (0-7, c+1), (8-15, c+1)
+                ldsm_x4(second<D>(kat, half) ^ (c << 4), r);     // (keys 0-7, chunk c), (8-15, c), (0-7, c+1), (8-15, c+1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int j = c + i;
@@ -235,14 +264,14 @@ struct Four {
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
                         float acc[4];
-                        mma_from(acc, a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u, b & 0x00F000F0u, st.q[2 * j][n][0],
-                                 st.q[2 * j][n][1], st.start[j][n][0], st.start[j][n][1]);
+                        mma_new(acc, a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u, b & 0x00F000F0u, st.q[2 * j][n][0],
+                                st.q[2 * j][n][1]);
                         ptx::mma_16816_f16(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u,
                                            st.q[2 * j + 1][n][0], st.q[2 * j + 1][n][1]);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float s = k < 2 ? s0[j] : s1[j];
-                            x[half][n][k] = j == 0 ? acc[k] * s : fmaf(acc[k], s, x[half][n][k]);
+                            x[half][n][k] = fmaf(acc[k], s, x[half][n][k]);
                         }
                     }
                 }
@@ -345,7 +374,7 @@ struct Four {
 #pragma unroll
             for (int c = 0; c < G; c += 2) {
                 uint32_t r[4];
-                ldsm_x4_trans((vat + half * 8 * D) ^ (c << 4), r);
+                ldsm_x4_trans(second<D>(vat, half) ^ (c << 4), r);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int j = c + i, k = D == 128 ? 4 + j : 2 + j;
@@ -391,14 +420,14 @@ struct Four {
     template <int D>
     static bool make_maps(const AttentionArgs &p, Maps *m) {
         const uint32_t rows = (uint32_t)std::min(p.P, kTile);
-        const uint64_t dims[4] = {(uint64_t)D / 2, (uint64_t)p.P, (uint64_t)p.Hk, (uint64_t)p.pages};
-        const uint64_t strides[3] = {(uint64_t)D / 2, (uint64_t)p.head_stride, (uint64_t)p.page_stride};
-        const uint32_t box[4] = {(uint32_t)D / 2, rows, 1, 1};
+        const uint64_t dims[4] = {128, (uint64_t)p.P * D / 2 / 128, (uint64_t)p.Hk, (uint64_t)p.pages};
+        const uint64_t strides[3] = {128, (uint64_t)p.head_stride, (uint64_t)p.page_stride};
+        const uint32_t box[4] = {128, rows * D / 2 / 128, 1, 1};
         // A page's scales of a head are one run of bytes, copied as words (a box has 256 elements at most).
         const uint64_t sdims[4] = {(uint64_t)p.P * D / kGroup4 / 4, (uint64_t)p.Hk, (uint64_t)p.pages, 1};
         const uint64_t sstrides[3] = {(uint64_t)p.scale_head_stride, (uint64_t)p.scale_page_stride, (uint64_t)p.scale_page_stride};
         const uint32_t sbox[4] = {rows * D / kGroup4 / 4, 1, 1, 1};
-        const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+        const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
         return encode_tiled(&m->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.k_cache, dims, strides, box, sw) &&
                encode_tiled(&m->v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.v_cache, dims, strides, box, sw) &&
                encode_tiled(&m->k_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.k_scale, sdims, sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE) &&
@@ -409,6 +438,7 @@ struct Four {
 }  // namespace
 
 cudaError_t launch_attention4(const AttentionArgs &p, cudaStream_t stream) { return launch_few_rows<Four>(p, stream); }
+size_t attention4_workspace_bytes(int max_q, int G, int D) { return few_rows_workspace<Four>(max_q, G, D); }
 uint32_t attention4_timeouts(bool reset) { return few_rows_timeouts(reset); }
 
 }  // namespace lowbit

@@ -17,7 +17,6 @@ using namespace attn;
 typedef unsigned long long u64;
 constexpr int kWarps = 4;                        // consumer warps, each with a quarter of a stage's keys
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kCtas = kSms * 3;                  // at most
 
 __device__ unsigned int g_attn_timeouts;
 
@@ -138,10 +137,11 @@ constexpr int kManyParts = 12;
 // to a later CTA (it leaves one at most), and for the part of the item that it joins
 // itself.  A slot: ROWS x D sums, then ROWS (m, l) pairs.
 __device__ __forceinline__ u64 *flag_of(const AttentionArgs &p, int cta) { return reinterpret_cast<u64 *>(p.workspace) + cta; }
-__device__ __forceinline__ Join *join_of(const AttentionArgs &p, int cta) { return reinterpret_cast<Join *>(p.workspace + kCtas * 2) + cta; }
-template <int D, int ROWS>
+template <class F>
+__device__ __forceinline__ Join *join_of(const AttentionArgs &p, int cta) { return reinterpret_cast<Join *>(p.workspace + F::kCtas * 2) + cta; }
+template <class F, int D, int ROWS>
 __device__ __forceinline__ float *slot_of(const AttentionArgs &p, int slot) {
-    return p.workspace + kCtas * (2 + (int)sizeof(Join) / 4) + (int64_t)slot * (ROWS * (D + 2));
+    return p.workspace + F::kCtas * (2 + (int)sizeof(Join) / 4) + (int64_t)slot * (ROWS * (D + 2));
 }
 __device__ __forceinline__ u64 load_acquire(const u64 *at) {
     u64 v;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(D, ROWS))
     ptx::pdl_wait();
     const Plan plan = make_plan<F, ROWS>(p, blockIdx.x, gridDim.x);
     if (plan.begin >= plan.end) {
-        if (p.defer && tid == 0) join_of(p, blockIdx.x)->begun = -1;
+        if (p.defer && tid == 0) join_of<F>(p, blockIdx.x)->begun = -1;
         return;
     }
     __syncthreads();
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(D, ROWS))
 
         // The warps' parts of the item are joined in shared memory, 8 rows at a time.
         const bool continued = t0 > 0, unfinished = t0 + cnt < s.nt;
-        float *slot = slot_of<D, ROWS>(p, 2 * (int)blockIdx.x + (unfinished ? 0 : 1));
+        float *slot = slot_of<F, D, ROWS>(p, 2 * (int)blockIdx.x + (unfinished ? 0 : 1));
         if (continued && !unfinished) join = Join{(int)(first_tile / plan.chunk), s.start, nrows, row0, pl.h, 0};
 #pragma unroll
         for (int n = 0; n < N; ++n) {
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(D, ROWS))
             if (tid == 0) store_release(flag_of(p, blockIdx.x), p.call);
         }
     }
-    if (p.defer && tid == 0) *join_of(p, blockIdx.x) = join;
+    if (p.defer && tid == 0) *join_of<F>(p, blockIdx.x) = join;
     if (p.defer || join.begun < 0) return;
 
     // The parts of the CTAs before this one have to be there.
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(D, ROWS))
     }
 #pragma unroll(8 / kPer)
     for (int c = join.begun; c <= (int)blockIdx.x; ++c) {
-        const float *part = slot_of<D, ROWS>(p, 2 * c + (c == (int)blockIdx.x));
+        const float *part = slot_of<F, D, ROWS>(p, 2 * c + (c == (int)blockIdx.x));
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + ROWS * D + 2 * r[q]));
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const int c = blockIdx.x, r = blockIdx.y;
-    const Join join = *join_of(p, c);
+    const Join join = *join_of<F>(p, c);
     if (join.begun < 0 || join.row0 + r >= join.nrows) return;
     const int grp = threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
     float m = -INFINITY, l = 0.f;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
     };
 #pragma unroll 4
     for (int i = join.begun + grp; i <= c; i += kGroups) {
-        const float *slot = slot_of<D, ROWS>(p, 2 * i + (i == c));
+        const float *slot = slot_of<F, D, ROWS>(p, 2 * i + (i == c));
         const float2 ml = *reinterpret_cast<const float2 *>(slot + ROWS * D + 2 * r);
         add(ml.x, ml.y, *reinterpret_cast<const float4 *>(slot + r * D + d));
     }
@@ -447,6 +447,12 @@ cudaError_t launch_few_rows(const AttentionArgs &p, cudaStream_t stream) {
     const bool half = (int64_t)p.max_q * p.G <= 8;
     if (p.D == 128) return half ? launch_few<F, 128, 8>(p, stream) : launch_few<F, 128, 16>(p, stream);
     return half ? launch_few<F, 64, 8>(p, stream) : launch_few<F, 64, 16>(p, stream);
+}
+
+template <class F>
+size_t few_rows_workspace(int max_q, int G, int D) {
+    const int rows = (int64_t)max_q * G <= 8 ? 8 : 16;
+    return (size_t)F::kCtas * (sizeof(u64) + sizeof(Join) + 2 * rows * (D + 2) * sizeof(float));
 }
 
 inline uint32_t few_rows_timeouts(bool reset) {

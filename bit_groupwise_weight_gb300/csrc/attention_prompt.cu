@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mine) {
                     const int row = ((w.lo + j) * kKeys + key) & (P - 1);
                     ptx::tma_load_4d(ptx::smem_u32(sm.raw[st]) + part * box * (Smem<D, FOUR>::kRawCodes / kUnit),
-                                     i < kKeys / kUnit ? &maps.k : &maps.v, 0, row, w.h, id, bar);
+                                     i < kKeys / kUnit ? &maps.k : &maps.v, 0, FOUR ? row / 16 : row, w.h, id, bar);
                     if constexpr (FOUR)
                         ptx::tma_load_4d(ptx::smem_u32(sm.raw[st]) + Smem<D, FOUR>::kRawCodes + part * Smem<D, FOUR>::slot(box),
                                          i < kKeys / kUnit ? &maps.k_scale : &maps.v_scale, row * (D / kGroup4) / 4, w.h, id, 0, bar);
@@ -891,13 +891,16 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const AttentionArgs p,
 
 template <int D, bool FOUR>
 cudaError_t launch(const AttentionArgs &p, const PromptGrid &g, cudaStream_t stream) {
-    constexpr uint32_t kRow = D / (FOUR ? 2 : 1);                       // bytes of a key's codes
-    const uint32_t rows = (uint32_t)std::min(p.P, kUnit), box[4] = {kRow, rows, 1, 1};
-    const uint64_t dims[4] = {(uint64_t)kRow, (uint64_t)p.P, (uint64_t)p.Hk, (uint64_t)p.pages};
-    const uint64_t strides[3] = {(uint64_t)kRow, (uint64_t)p.head_stride, (uint64_t)p.page_stride};
+    // A head's page is one run of bytes: lines of a key (8 bits), or of 16 (4 bits, as words: the box's limit is 256 elements).
+    const uint32_t rows = (uint32_t)std::min(p.P, kUnit);
+    constexpr uint32_t kLine = FOUR ? 16 * D / 2 : D, kKeysOf = FOUR ? 16 : 1;
+    const CUtensorMapDataType type = FOUR ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const uint32_t box[4] = {FOUR ? kLine / 4 : kLine, rows / kKeysOf, 1, 1};
+    const uint64_t dims[4] = {box[0], (uint64_t)p.P / kKeysOf, (uint64_t)p.Hk, (uint64_t)p.pages};
+    const uint64_t strides[3] = {(uint64_t)kLine, (uint64_t)p.head_stride, (uint64_t)p.page_stride};
     Maps maps{};
-    if (!encode_tiled(&maps.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.k_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-        !encode_tiled(&maps.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.v_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+    if (!encode_tiled(&maps.k, type, 4, p.k_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_tiled(&maps.v, type, 4, p.v_cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     if constexpr (FOUR) {                                               // a page's scales of a head are one run of bytes
         const uint64_t sdims[4] = {(uint64_t)p.P * D / kGroup4 / 4, (uint64_t)p.Hk, (uint64_t)p.pages, 1};

@@ -231,7 +231,7 @@ struct AttentionArgs {
     bool defer;                          // parts are joined by a second launch
     int few_rows;                        // more query rows than this: a sequence for the prompt kernel
 };
-size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D, int64_t max_len);
+size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D, int64_t max_len, bool four);
 cudaError_t launch_attention(const AttentionArgs &args, cudaStream_t stream);
 uint32_t attention_timeouts(bool reset);
 // A token for each row of logits (sample.cu).  Per-row settings may be null:
