@@ -78,6 +78,7 @@ struct Eight {
     static constexpr int per_sm(int D, int ROWS) { return D == 128 && ROWS == 16 ? 2 : 3; }
     static constexpr int stages(int D, int ROWS) { return D == 64 ? 6 : (ROWS == 16 ? 5 : 3); }
     static constexpr int kCtas = kSms * 3;                                // at most
+    static constexpr bool kHold = false;                                   // the list in shared memory during tiles
     static constexpr float kUnit = 1.f;                                   // what a value of V counts in the product
     template <int D>
     static constexpr int kKeyBytes = 2 * D;                               // of K and V

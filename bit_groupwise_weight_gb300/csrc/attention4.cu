@@ -62,6 +62,7 @@ struct Four {
     static constexpr int per_sm(int D, int ROWS) { return ROWS == 16 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 4); }
     static constexpr int stages(int D, int ROWS) { return D == 64 ? (ROWS == 16 ? 6 : 4) : (ROWS == 16 ? 5 : 3); }
     static constexpr int kCtas = kSms * 4;                                // at most
+    static constexpr bool kHold = true;                                   // the list in shared memory during tiles
     static constexpr float kUnit = 64.f;
     // m of a row that has seen nothing: any score outgrows it, and, unlike with -inf, scores less m are numbers.
     static constexpr float kNone = -3e38f;

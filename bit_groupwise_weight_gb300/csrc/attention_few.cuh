@@ -115,18 +115,29 @@ __device__ __forceinline__ Plan make_plan(const AttentionArgs &p, int cta, int c
 // ---------------------------------------------------------------------------
 // Shared memory of a CTA.
 
+// What the second launch needs to know of an item: written by the CTA that ends it, from
+// CTA `begun` on (below 0: none).
+struct Join { int begun, start, nrows, row0, h, pad; };
+// What a consumer warp keeps of the list while it goes through tiles.
+struct Held {
+    Plan plan;
+    Place pl;
+    Seq s;
+    long long idx, first_tile;
+    Join join;
+    int t0, cnt, nrows, row0;
+};
+
 template <class F, int D, int ROWS>
 struct Smem {
     typename F::template Stage<D> stage[F::stages(D, ROWS)];
     float o[kWarps][8][D + 4];                   // the warps' sums at an item's end, 8 rows at a time
     float m[kWarps][8], l[kWarps][8];
+    Held held[F::kHold ? kWarps : 1];
     typename F::StageBeside beside[F::stages(D, ROWS)];
     alignas(8) uint64_t full[F::stages(D, ROWS)], empty[F::stages(D, ROWS)];
 };
 
-// What the second launch needs to know of an item: written by the CTA that ends it, from
-// CTA `begun` on (below 0: none).
-struct Join { int begun, start, nrows, row0, h, pad; };
 // More CTAs than this for each item that the page table allows: a second launch joins the parts.
 // (By the last CTA always, 131001 keys take 55.6 us instead of 49.6; with 4 or 48 instead of 12 no
 // measured case changes by more than 1.2 us.  The lengths may be far below the table's width, and
@@ -179,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(D, ROWS))
     }
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const Plan plan = make_plan<F, ROWS>(p, blockIdx.x, gridDim.x);
+    Plan plan = make_plan<F, ROWS>(p, blockIdx.x, gridDim.x);
     if (plan.begin >= plan.end) {
         if (p.defer && tid == 0) join_of<F>(p, blockIdx.x)->begun = -1;
         return;
@@ -265,28 +276,42 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(D, ROWS))
     Join join{-1, 0, 0, 0, 0, 0};                                        // the item that this CTA ends and others began
     typename F::template State<D, ROWS> a;
     for (long long idx = plan.begin; idx < plan.end;) {
-        const Seq s = locate<F, ROWS>(p, idx, pl);
+        Seq s = locate<F, ROWS>(p, idx, pl);
         const int units = (int)min((long long)(s.nt - pl.t), plan.end - idx);
-        const int t0 = max(pl.t, 0), cnt = pl.t + units - t0;            // this CTA's tiles of the item
-        const long long first_tile = idx - pl.t;                         // place of the item's first tile
+        int t0 = max(pl.t, 0), cnt = pl.t + units - t0;                  // this CTA's tiles of the item
+        long long first_tile = idx - pl.t;                               // place of the item's first tile
         idx += units;
         if (cnt <= 0) continue;
-        const int nrows = s.n * p.G, row0 = pl.rt * ROWS, first = s.len - s.n;
+        int nrows = s.n * p.G, row0 = pl.rt * ROWS;
+        const int first = s.len - s.n;
 
         F::template queries<D, ROWS>(p, a, s, pl.h, row0);
         const int pos_lo = first + row0 / p.G, pos_hi = first + (min(row0 + ROWS, nrows) - 1) / p.G;
 
+        // The tiles' loop needs its registers: what only the items need waits in shared memory.
+        if constexpr (F::kHold) {
+            if (lane == 0) sm.held[warp] = Held{plan, pl, s, idx, first_tile, join, t0, cnt, nrows, row0};
+            __syncwarp();
+        }
+        const int len = s.len;
         int key0 = (s.lo + t0) * F::kTile + warp * F::kWarpKeys;
-        for (int tile = 0; tile < cnt; ++tile, key0 += F::kTile) {
+        for (int tile = cnt; tile > 0; --tile, key0 += F::kTile) {
             if (ok) ok = ptx::mbar_wait(ptx::smem_u32(&sm.full[st]), round, &g_attn_timeouts);
             const int last = key0 + F::kWarpKeys - 1;
             if (last <= pos_lo && (p.window == 0 || key0 > pos_hi - p.window))
-                F::template slice<D, ROWS, false>(p, a, at, sm.stage[st], sm.beside[st], key0, s.len);
+                F::template slice<D, ROWS, false>(p, a, at, sm.stage[st], sm.beside[st], key0, len);
             else if (key0 <= pos_hi && (p.window == 0 || last > pos_lo - p.window))
-                F::template slice<D, ROWS, true>(p, a, at, sm.stage[st], sm.beside[st], key0, s.len);
+                F::template slice<D, ROWS, true>(p, a, at, sm.stage[st], sm.beside[st], key0, len);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sm.empty[st]));
             if (++st == S) st = 0, round ^= 1;
+        }
+        if constexpr (F::kHold) {
+            asm volatile("" ::: "memory");
+            const Held &w = sm.held[warp];
+            plan = w.plan, pl = w.pl, s = w.s, idx = w.idx, first_tile = w.first_tile, join = w.join;
+            t0 = w.t0, cnt = w.cnt, nrows = w.nrows, row0 = w.row0;
+            __syncwarp();
         }
 
         // The warps' parts of the item are joined in shared memory, 8 rows at a time.
