@@ -73,7 +73,7 @@ def build_binding(verbose: bool = False) -> None:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{p}" for p in (INCLUDE, root / "include", root / "include/torch/csrc/api/include",
                                 sysconfig.get_paths()["include"], cuda / "include")),
-           str(CSRC / "binding.cpp"), "-o", str(tmp), f"-L{root / 'lib'}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           str(CSRC / "binding.cpp"), "-o", str(tmp), f"-L{root / 'lib'}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
            "-ltorch_python", f"-Wl,-rpath,{root / 'lib'}"]
     if verbose:
         print(" ".join(cmd), flush=True)
