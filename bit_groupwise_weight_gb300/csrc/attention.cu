@@ -349,12 +349,19 @@ struct Eight {
 //   1 x 8000 keys of 128:        14, 17, 20, 22, 26, 31 and 32, 33, 33, 35, 35;
 //   1 x 300 keys of 128:         10, 11, 11, 11, 12, 12 and 13, 13, 13, 13, 13.
 // 64 lies between: full batches of 128 values would cross at 45, of 64 values at 90, single
-// sequences at 150.
-constexpr int kFewRows = 64;
+// sequences at 150.  Over a 4-bit cache, where few rows cost more and the prompt kernel does not, for 16, 32, 48, 64, 96
+// and 128 rows:
+//   8 x 6000 keys of 128 values: 33, 53, 73, 93, 133, 172 and 53, 54, 55, 56, 58, 59;
+//   8 x 6000 keys of 64:         19, 27, 35, 43, 60, 76 and 49, 50, 51, 51, 52, 52;
+//   1 x 8000 keys of 128:        16, 19, 24, 26, 32, 39 and 30, 32, 33, 34, 35, 36;
+//   1 x 300 keys of 128:         11, 11, 12, 12, 12, 13 and 12, 13, 13, 13, 13, 13;
+// so that full batches (of sequences times kv heads) of 128 values cross at 32.
+constexpr int kFewRows = 64, kFewRowsFull4 = 32, kFullBatch = 64;
 struct Kernels { bool few, many; int few_rows; };
-Kernels kernels_for(int max_q, bool uniform, int G) {
-    if ((int64_t)max_q * G <= kFewRows) return {true, false, kFewRows};
-    return {!uniform, true, uniform ? 0 : kFewRows};
+Kernels kernels_for(int max_q, bool uniform, int B, int Hq, int Hk, int D, bool four) {
+    const int few_rows = four && D == 128 && (int64_t)B * Hk >= kFullBatch ? kFewRowsFull4 : kFewRows;
+    if ((int64_t)max_q * (Hq / Hk) <= few_rows) return {true, false, few_rows};
+    return {!uniform, true, uniform ? 0 : few_rows};
 }
 
 size_t few_workspace_bytes(int max_q, int G, int D, bool four) {
@@ -369,7 +376,7 @@ uint32_t attention_timeouts(bool reset) {
 }
 
 size_t attention_workspace_bytes(int64_t T, int B, int max_q, bool uniform, int Hq, int Hk, int D, int64_t max_len, bool four) {
-    const Kernels k = kernels_for(max_q, uniform, Hq / Hk);
+    const Kernels k = kernels_for(max_q, uniform, B, Hq, Hk, D, four);
     size_t bytes = k.few ? few_workspace_bytes(max_q, Hq / Hk, D, four) : 0;
     if (k.many) bytes += prompt_workspace_bytes(prompt_grid(T, B, max_q, uniform, Hq, Hk, max_len), Hk, D);
     return std::max<size_t>(bytes, 16);
@@ -383,7 +390,7 @@ cudaError_t launch_attention(const AttentionArgs &args, cudaStream_t stream) {
     if (uniform) p.max_q = p.n;
     p.pshift = 0;
     while ((1 << p.pshift) < p.P) ++p.pshift;
-    const Kernels k = kernels_for(p.max_q, uniform, p.G);
+    const Kernels k = kernels_for(p.max_q, uniform, p.B, p.Hq, p.Hk, p.D, p.k_scale != nullptr);
     p.few_rows = k.few_rows;
     // A number that no other call's flags hold, and no other content of the workspace is likely to.
     static std::atomic<u64> calls{(u64)std::chrono::steady_clock::now().time_since_epoch().count() * 0x9E3779B97F4A7C15ull};

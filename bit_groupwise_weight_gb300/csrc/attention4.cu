@@ -57,8 +57,12 @@ __device__ __forceinline__ uint32_t bad_scales(uint32_t v) {
 // The 4-bit cache.
 struct Four {
     static constexpr int kTile = 128, kTileBits = 7, kWarpKeys = 32;
+    // As for the 8-bit cache (attention.cu), in tiles twice as long: an item's cost of 2 and 4 instead of 3 gives
+    // 37.7 and 36.4 us for 64 sequences of up to 16001 keys (34.4), 36.7 and 37.8 for one of 131001 (37.6); a
+    // least range of 4 and 6 instead of 3 7.2 and 6.1 us for 257 keys (6.2), 8.4 and 10.4 for 1000 (7.9), 20.9
+    // and 22.3 for 8 sequences of 5 tokens (20.9), 9.4 and 10.4 for 4000 (9.9).
     static constexpr int kItemCost = 3;
-    static constexpr int kMinChunk = 4;
+    static constexpr int kMinChunk = 3;
     static constexpr int per_sm(int D, int ROWS) { return ROWS == 16 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 4); }
     static constexpr int stages(int D, int ROWS) { return D == 64 ? (ROWS == 16 ? 6 : 4) : (ROWS == 16 ? 5 : 3); }
     static constexpr int kCtas = kSms * 4;                                // at most
