@@ -684,13 +684,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (FOUR) {
                             const __half2 s = __half2half2(__ushort_as_half((unsigned short)(scale[i] << 8)));
                             const __half2 t = __hmul2(s, __float2half2_rn(-1.125f));
-                            const uint4 y[4] = {turn4(x[i].x, s, t), turn4(x[i].y, s, t), turn4(x[i].z, s, t), turn4(x[i].w, s, t)};
                             const uint32_t key_at = dst + (u * kUnit + i * kStep) * 128 + row_off;
-                            const bool flip = half != 0;
+                            const uint32_t at = ((4 * (c & 1) + (half != 0 ? 2 : 0)) ^ sw) << 4;      // the first piece's
+                            const uint32_t w[4] = {half ? x[i].z : x[i].x, half ? x[i].w : x[i].y, half ? x[i].x : x[i].z, half ? x[i].y : x[i].w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const uint4 z = flip ? y[k ^ 2] : y[k];
-                                sts_v4(key_at + (((4 * (c & 1) + (flip ? k ^ 2 : k)) ^ sw) << 4), z.x, z.y, z.z, z.w);
+                                const uint4 y = turn4(w[k], s, t);
+                                sts_v4(key_at + (at ^ k << 4), y.x, y.y, y.z, y.w);
                             }
                             continue;
                         }
