@@ -1,12 +1,12 @@
-"""A small decoder that answers with low-bit weights and an 8-bit key-value cache.
+"""A small decoder that answers with low-bit weights and an 8-bit or 4-bit key-value cache.
 
 The layers' products are the library's low-bit linears, what stands between them its
-decoder operators: kv_append (rotation, cache write), attention, sample.  A batch of
+decoder operators: kv_append (norms of the heads, rotation, cache write), attention, sample.  A batch of
 prompts of different lengths goes through in one ragged call; each further token is
 one replay of a captured CUDA graph, in which the lengths and the sampled tokens stay on
 the device.  Weights are random: the point is the calls, not the text.
 
-    python examples/decode.py [--layers 4] [--batch 4] [--steps 64]
+    python examples/decode.py [--layers 4] [--batch 4] [--steps 64] [--cache-bits 8] [--head-norms]
 """
 from __future__ import annotations
 
@@ -23,7 +23,7 @@ import bit_groupwise_weight_gb300 as lb  # noqa: E402
 
 
 class Layer(torch.nn.Module):
-    def __init__(self, width, heads, kv_heads, dim, hidden, bits, group, pages, page):
+    def __init__(self, width, heads, kv_heads, dim, hidden, bits, group, pages, page, cache_bits=8, head_norms=False):
         super().__init__()
         def linear(n, k):
             return torch.nn.Linear(k, n, bias=False, device="cuda", dtype=torch.bfloat16)
@@ -33,12 +33,13 @@ class Layer(torch.nn.Module):
         self.o = lb.LowbitLinear.from_linear(linear(width, heads * dim), bits, group)
         self.gate_up = lb.LowbitGateUp.from_linears(linear(hidden, width), linear(hidden, width), bits, group)
         self.down = lb.LowbitLinear.from_linear(linear(width, hidden), bits, group)
-        self.cache = lb.empty_cache(pages, kv_heads, dim, page)
+        self.cache = lb.empty_cache(pages, kv_heads, dim, page, bits=cache_bits)
+        self.q_norm = self.k_norm = torch.ones(dim, device="cuda", dtype=torch.bfloat16) if head_norms else None
 
     def forward(self, x, table, lens, cu_q, max_q, turns):
         qkv = self.qkv(F.rms_norm(x, x.shape[-1:], self.norm1)).view(-1, self.heads + 2 * self.kv_heads, self.dim)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
-        q = lb.kv_append(q, k, v, *self.cache, table, lens, cu_q, max_q, turns=turns)
+        q = lb.kv_append(q, k, v, *self.cache, table, lens, cu_q, max_q, turns=turns, q_norm=self.q_norm, k_norm=self.k_norm)
         x = x + self.o(lb.attention(q, *self.cache, table, lens, cu_q, max_q).flatten(1))
         return x + self.down(self.gate_up(F.rms_norm(x, x.shape[-1:], self.norm2)))
 
@@ -47,7 +48,7 @@ class Decoder(torch.nn.Module):
     """`batch` sequences of up to `length` tokens, each with pages of its own."""
 
     def __init__(self, layers=4, width=1024, heads=16, kv_heads=4, dim=64, hidden=2816, vocab=32000, bits=4, group=64, batch=4,
-                 length=1024, page=64, seed=0):
+                 length=1024, page=64, seed=0, cache_bits=8, head_norms=False):
         super().__init__()
         torch.manual_seed(seed)
         per = -(-length // page)
@@ -57,7 +58,8 @@ class Decoder(torch.nn.Module):
         self.turns = lb.rotary_turns(dim, base=500000.0, device="cuda")
         self.embed = torch.randn(vocab, width, device="cuda").to(torch.bfloat16)
         self.norm = torch.ones(width, device="cuda", dtype=torch.bfloat16)
-        self.layers = torch.nn.ModuleList(Layer(width, heads, kv_heads, dim, hidden, bits, group, batch * per, page)
+        self.layers = torch.nn.ModuleList(Layer(width, heads, kv_heads, dim, hidden, bits, group, batch * per, page,
+                                                cache_bits, head_norms)
                                           for _ in range(layers))
         self.head = lb.LowbitLinear.from_linear(
             torch.nn.Linear(width, vocab, bias=False, device="cuda", dtype=torch.bfloat16), bits, group)
@@ -106,9 +108,11 @@ def main():
     a.add_argument("--layers", type=int, default=4)
     a.add_argument("--batch", type=int, default=4)
     a.add_argument("--steps", type=int, default=64)
+    a.add_argument("--cache-bits", type=int, default=8, choices=(4, 8))
+    a.add_argument("--head-norms", action="store_true")
     a = a.parse_args()
     settings = dict(temperature=0.8, top_k=50, top_p=0.95, min_p=0.02)
-    model = Decoder(layers=a.layers, batch=a.batch)
+    model = Decoder(layers=a.layers, batch=a.batch, cache_bits=a.cache_bits, head_norms=a.head_norms)
     gen = torch.Generator(device="cuda").manual_seed(1)
     prompts = [[(37 * i + 11 * b) % 32000 for i in range(5 + 40 * b % 700)] for b in range(a.batch)]
     u = torch.rand(a.batch, generator=gen, device="cuda")
