@@ -52,7 +52,10 @@ __device__ __forceinline__ void weigh(float (&x)[8], float norm, const float *wt
     const float4 a = *reinterpret_cast<const float4 *>(wt), b = *reinterpret_cast<const float4 *>(wt + 4);
     const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], norm), w[i]);
+    for (int i = 0; i < 8; i += 2) {
+        const float2 y = ptx::fmul2(ptx::fmul2(make_float2(x[i], x[i + 1]), make_float2(norm, norm)), make_float2(w[i], w[i + 1]));
+        x[i] = y.x, x[i + 1] = y.y;
+    }
 }
 
 // Norm weight d of q or k.

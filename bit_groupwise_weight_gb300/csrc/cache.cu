@@ -45,6 +45,7 @@ template <int THREADS>
 constexpr int kPerSm = 512 / THREADS;                         // CTAs of an SM
 
 enum Kind { kKey, kValue, kQuery };
+constexpr int kCtasToFill = 152 * 4;
 
 struct Seq { int start, n, len; };
 
@@ -180,13 +181,16 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
     const bool write = page >= 0 && page < p.pages;
     const int older = write ? lo - slot * P : 0;          // slots that hold older tokens
 
-    const int tid = threadIdx.x, half = p.R >> 1, head = blockIdx.y;
+    // Without rows of q (PRE, G = 0) a CTA takes the keys or the values (blockIdx.z) of several heads, with one table.
+    const bool apart = PRE && p.G == 0;
+    const int tid = threadIdx.x, half = p.R >> 1;
+    int head = apart ? (int)blockIdx.y * p.heads_each : (int)blockIdx.y;
     const int d0 = (tid % kRow) * 8, t_in = tid / kRow;
     const int j0 = FORM == kHalves ? (d0 >= half ? d0 - half : d0 + half) : 0;       // where the mates are
     const bool mated = FORM == kHalves && d0 < p.R;
     const int chunks = (hi - lo + kChunk - 1) / kChunk;
     int8_t *k_exp = p.k_exp + (int64_t)page * p.Hk + head, *v_exp = p.v_exp + (int64_t)page * p.Hk + head;
-    const int was[2] = {older ? *k_exp : kExpMin, older ? *v_exp : kExpMin};
+    const int was_k = older ? *k_exp : kExpMin, was_v = older ? *v_exp : kExpMin;
     int phase = 0;
     if constexpr (PRE) {
         for (int i = tid; i < 2 * D; i += THREADS) {
@@ -269,6 +273,7 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
 #pragma unroll
                 for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[v][i]));
         }
+        const int was = apart ? (older ? *(kind == kKey ? k_exp : v_exp) : kExpMin) : (kind == kKey ? was_k : was_v);
         m = reduce(m);
         if (m == INFINITY) {                              // infinities count for nothing either
             m = 0.f;
@@ -281,11 +286,11 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
             }
             m = reduce(m);
         }
-        const int e = max(page_exponent(m), was[kind]);
+        const int e = max(page_exponent(m), was);
         if (tid == 0) *(kind == kKey ? k_exp : v_exp) = (int8_t)e;
         uint8_t *cache = (kind == kKey ? p.k_cache : p.v_cache) + (int64_t)page * p.page_stride + (int64_t)head * p.head_stride;
-        if (older != 0 && e != was[kind]) {
-            const float scale = exp2_int(max(was[kind] - e, -126));
+        if (older != 0 && e != was) {
+            const float scale = exp2_int(max(was - e, -126));
             for (int i = tid; i < older * kRow; i += THREADS) {          // 8 codes at a time
                 uint2 *at = reinterpret_cast<uint2 *>(cache + (int64_t)i * 8);
                 const uint2 v = *at;
@@ -329,13 +334,14 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
         const uint16_t *q = p.q + tok0 * p.q_token + (int64_t)head * p.G * p.q_head;
         uint16_t *o = p.q_out + tok0 * p.o_token + (int64_t)head * p.G * p.o_head + d0;
         const bool keys = write && chunks == 1;
+        if (apart) break;
         if (keys) load(r[0], k_row(t0), p.k_token * kStep, nt, true);
         make_table(t0, nt);
         if (keys) {
             load(r[1], v_row(t0), p.v_token * kStep, nt, false);
             write_rows(std::integral_constant<int, kKey>{}, r[0]);
         }
-        if (!PRE || p.G > 0) load(r[0], q, p.q_token * kStep, nt, true);
+        load(r[0], q, p.q_token * kStep, nt, true);
         if (keys) write_rows(std::integral_constant<int, kValue>{}, r[1]);
         // A row's vectors lie in one warp and are all loaded before any is stored, so q may
         // be rotated in place.
@@ -367,6 +373,28 @@ __global__ void __launch_bounds__(THREADS, kPerSm<THREADS>) kv_append_kernel(con
             if (h + 1 < p.G) turn(r[1], h + 1);
         }
     }
+    if constexpr (PRE) {
+        if (apart) {
+            if (!write) return;
+            const int nt = hi - lo, last = min(head + p.heads_each, p.Hk);
+            auto each = [&]<int kind>(std::integral_constant<int, kind> which) {
+                const int64_t pitch = kind == kKey ? p.k_token : p.v_token, next = kind == kKey ? p.k_head : p.v_head;
+                if (chunks == 1) {
+                    load(r[0], kind == kKey ? k_row(lo) : v_row(lo), pitch * kStep, nt, kind == kKey);
+                    if (kind == kKey) make_table(lo, nt);
+                }
+                while (head < last) {
+                    if (chunks == 1 && head + 1 < last) load(r[1], (kind == kKey ? k_row(lo) : v_row(lo)) + next, pitch * kStep, nt, kind == kKey);
+                    write_rows(which, r[0]);
+                    r[0] = r[1];
+                    ++head, ++k_exp, ++v_exp, k0 += p.k_head, v0 += p.v_head;
+                }
+            };
+            if (blockIdx.z == 0) each(std::integral_constant<int, kKey>{});
+            else each(std::integral_constant<int, kValue>{});
+            return;
+        }
+    }
     if (write && chunks > 1) {
         write_rows(std::integral_constant<int, kKey>{}, r[0]);
         write_rows(std::integral_constant<int, kValue>{}, r[0]);
@@ -383,6 +411,11 @@ cudaError_t launch(AppendArgs &p, int n, int64_t gx, cudaStream_t stream) {
     p.table_tokens = std::min(std::min(n, p.P), kChunk);
     static_assert(kChunk * D * sizeof(float) <= 48 * 1024, "the table fits what a kernel may use without asking");
     const size_t smem = (size_t)p.table_tokens * (size_t)p.R * sizeof(float);
+    if (PRE && p.G == 0) {                                // CTAs to fill the GPU a few times, of as many heads as leaves
+        p.heads_each = (int)std::min<int64_t>(p.Hk, std::max<int64_t>(1, gx * p.Hk * 2 / kCtasToFill));
+        return launch_pdl(kernel, dim3((unsigned)gx, (unsigned)((p.Hk + p.heads_each - 1) / p.heads_each), 2), dim3(THREADS), smem,
+                          stream, (const AppendArgs)p);
+    }
     return launch_pdl(kernel, dim3((unsigned)gx, (unsigned)p.Hk), dim3(THREADS), smem, stream, (const AppendArgs)p);
 }
 

@@ -197,6 +197,7 @@ struct AppendArgs {
     uint8_t *k_scale, *v_scale;
     int64_t scale_page_stride, scale_head_stride;
     bool q_only;                                                        // cache4.cu: no keys and values
+    int heads_each;                                                     // cache.cu without rows of q: heads of a CTA
 };
 cudaError_t launch_kv_append(const AppendArgs &args, cudaStream_t stream);
 cudaError_t launch_kv_append4(const AppendArgs &args, cudaStream_t stream);   // into the 4-bit cache (cache4.cu)
