@@ -29,6 +29,17 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p) {
                       p[6] | (uint32_t)p[7] << 16);
 }
 
+// 1 / sqrt(v), root and reciprocal rounded to nearest each (but for 15 of 2^26 values tried, which are the float
+// beside).  Within the range that rows have in earnest by a
+// Newton step each from the approximate inverse root, its remainder exact in a fused operation (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990): a dozen instructions, where the
+// two functions take some sixty.
+__device__ __forceinline__ float inverse_root(float v) {
+    if (!(v > 0x1p-100f && v < 0x1p100f)) return __frcp_rn(__fsqrt_rn(v));
+    const float y = rsqrtf(v), s0 = v * y, s = fmaf(fmaf(-s0, s0, v), 0.5f * y, s0);
+    return fmaf(fmaf(-s, y, 1.f), y, y);
+}
+
 // 1 / sqrt(mean of squares + eps) of a row held by LANES lanes, 8 values each.  Every operation
 // is rounded by itself, the squares are added in pairs: a key's codes are then the same in any
 // implementation, also next to a border between two.  The lanes of `mask` call, whole rows of them.
@@ -44,7 +55,7 @@ __device__ __forceinline__ float row_norm(const float (&x)[8], float eps, uint32
                         __fadd_rn(__fadd_rn(s[4], s[5]), __fadd_rn(s[6], s[7])));
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) t = __fadd_rn(t, __shfl_xor_sync(mask, t, o));
-    return __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(t, 1.f / (8 * LANES)), eps)));
+    return inverse_root(__fadd_rn(__fmul_rn(t, 1.f / (8 * LANES)), eps));
 }
 
 // x times `norm`, times the weights from wt (16-byte aligned) on.

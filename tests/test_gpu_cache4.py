@@ -582,3 +582,21 @@ def test_empty_calls(bits):
         args[n] = args[n][:0]
     assert lb.kv_append(**args).shape == (0, 4, 64)
     assert not any(args[n].view(torch.uint8).any() for n in ("k_cache", "v_cache", "k_exp", "v_exp"))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norms_to_the_bit(dim, eps):
+    """Norms alone, as fp32 operations one by one: squares added in pairs, root and reciprocal rounded to nearest."""
+    T = 20000
+    gen = torch.Generator(device="cuda").manual_seed(87)
+    x = torch.randn(T, 4, dim, generator=gen, device="cuda") * torch.exp(torch.randn(T, 4, 1, generator=gen, device="cuda") * 8)
+    x, w = x.to(torch.bfloat16), torch.randn(dim, generator=gen, device="cuda")
+    cache, pages = lb.empty_cache(-(-T // 64), 1, dim, 64, bits=4), torch.arange(-(-T // 64), dtype=torch.int32, device="cuda")[None]
+    q, k, v = x.split([2, 1, 1], 1)
+    out = lb.kv_append(q, k, v, *cache, pages, torch.tensor([T], dtype=torch.int32, device="cuda"), q_norm=w, eps=eps)
+    s = q.float() * q.float()
+    while s.shape[-1] > 1:
+        s = s[..., 0::2] + s[..., 1::2]
+    want = q.float() * torch.reciprocal(torch.sqrt(s * (1.0 / dim) + eps)) * w
+    assert torch.equal(out, want.to(torch.bfloat16))
