@@ -323,8 +323,8 @@ struct Four {
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-                    const float to = fmaxf(mx - kStart, st.m[n][c]);
-                    const Rescale by(to == st.m[n][c] ? 0.f : st.m[n][c] - to);
+                    const float to = mx > st.m[n][c] + kPeak ? mx - kStart : st.m[n][c];    // of this row alone
+                    const Rescale by(st.m[n][c] - to);
                     const float f = by.of_o();
                     st.m[n][c] = to;
                     st.l[n][c] = by.of_l(st.l[n][c]);

@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append4_kernel(const AppendArg
     if (at >= p.T) return;
     // The warp's share of the rows, in sets of kRows of one kind.
     const int q_sets = (p.Hq + kRows - 1) / kRows, k_sets = p.q_only ? 0 : (p.Hk + kRows - 1) / kRows, sets = q_sets + 2 * k_sets;
-    const int begin = (int)((uint32_t)sets * (uint32_t)part / (uint32_t)p.units);
-    const int end = (int)((uint32_t)sets * (uint32_t)(part + 1) / (uint32_t)p.units);
+    const int begin = (int)((int64_t)sets * part / p.units);
+    const int end = (int)((int64_t)sets * (part + 1) / p.units);
     // The next row to come: where it is, how far the following one of its kind, how many rows are left of it.
     const uint16_t *coming;
     int64_t pitch;

@@ -214,7 +214,8 @@ LOWBIT_API lowbit_status lowbit_linear_swiglu(const uint16_t *x, const uint8_t *
 
 /* ---------------------------------------------------------------------------
  * Between the linear layers of a decoder: rotary positions and the write into an
- * 8-bit key-value cache, attention over that cache, and sampling.
+ * 8-bit key-value cache, attention over that cache, and sampling.  (The cache in 4 bits,
+ * and what may stand before the rotation, follow: lowbit_cache4, lowbit_kv_prologue.)
  *
  * The cache holds keys and values in pages of `page` tokens, as e4m3 codes with
  * one exponent for each page and key-value head: value = code * 2^exp.  (A power
@@ -324,8 +325,8 @@ LOWBIT_API lowbit_status lowbit_kv_append_ex(const lowbit_kv_append_args *args, 
  * amax <= 7.5 s, amax the largest finite magnitude of the group, code - 8 the nearest
  * whole number to value / s (ties to even, within -7 .. 7).  Infinities, and values
  * past 7 * 57344, are stored as 7 s; a group that holds a NaN gets a NaN scale.
- * Scales are read as they are, and have to be not negative; one that is infinite or no number makes its 32
- * values NaN. */
+ * Scales are read as they are: they have to be finite and not negative, or NaN, which makes
+ * all 32 values NaN. */
 typedef struct {
     uint8_t *k, *v;              /* [pages, kv_heads, page, head_dim / 2], 16-byte aligned           */
     uint8_t *k_scale, *v_scale;  /* [pages, kv_heads, page, head_dim / 32] e5m2, 16-byte aligned      */

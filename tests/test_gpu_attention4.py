@@ -348,3 +348,15 @@ def test_both_sides_of_the_binding_make_the_same_call(monkeypatch):
     assert torch.equal(a, c) and torch.equal(lse[0], lse[1])
     with pytest.raises(lb.LowbitError):
         lb.attention(q, *cache, table, lens, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("n", [1, 3, 64])
+def test_a_row_does_not_depend_on_the_others(n):
+    """Other rows of the same sequence and heads with far larger scores, to the bit."""
+    b = ref4.make_batch(47, [700], [n], 1, 128, 64)
+    q = queries(48, n, 8, 128)
+    few, _ = run(b, q)
+    loud = q.clone()
+    loud[:, ::2] *= 30
+    got, _ = run(b, loud)
+    assert np.array_equal(got[:, 1::2], few[:, 1::2]) and not np.array_equal(got[:, ::2], few[:, ::2])
