@@ -18,6 +18,16 @@
 // Operands: the four bytes that a lane gets from ldmatrix are eight codes of one key (K), or, transposed,
 // four codes of two neighbouring keys (V): the order of the values within a group is the codes' own,
 // q is laid out to match, and a lane's four rows of the result are four neighbouring values.
+//
+// A stage is 128 keys, a warp's share 32 of them in two halves: softmax bookkeeping and the loop's own cost are
+// paid once for both.
+// Bound: instructions.  16 keys of K and V and 128 values take a warp some 230, half of them on the ALU (masks,
+// shifts), issued at 0.57 a cycle and scheduler: one of 131001 keys takes 37.6 us, 3.8 TB/s, 0.57 of a copy's rate (20.9
+// us would be the bytes'); the number of stages does not matter (2: the same), registers do: what only the list needs is
+// in shared memory while a warp goes through its tiles (40.3 us without).  q's fragments there too, and four CTAs an SM
+// with 96 registers, were no faster.  64 sequences of up to 16001 keys 34.4 us; 96 windows of 1000 keys of 64 values in
+// pages of 16 19.1; 8 sequences of 5 tokens, 28 heads over 4, 20.9: what an item costs beside its tiles, as for the 8-bit
+// cache.  One sequence of 257 keys 6.2 us.
 #include "attention_few.cuh"
 #include "int4.cuh"
 
@@ -245,7 +255,6 @@ struct Four {
         const uint32_t mine = D == 128 && (t & 1) ? 0x3424u : 0x1404u;           // this lane's two groups as an fp16 pair
         float x[2][N][4];
         uint32_t seen[2][N];                         // bit i: value i of the pair is seen
-        bool grown = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float s0[G], s1[G];                      // of keys g and g + 8

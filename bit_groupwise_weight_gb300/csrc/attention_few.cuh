@@ -2,7 +2,7 @@
 // the list of tiles and how it is cut, the kernel's frame, and the join of parts.  What
 // depends on how a cache holds its values is a format's own (attention.cu: 8 bits,
 // attention4.cu: 4 bits): stages, copies, query fragments, and the products over a
-// warp's slice of a stage.
+// warp's slice of a stage.  attention.cu describes the work's split.
 #pragma once
 
 #include <algorithm>

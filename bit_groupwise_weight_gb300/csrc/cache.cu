@@ -20,6 +20,9 @@
 // second launch).  The cosines and sines of the page's tokens are computed once for the
 // head's rows (sharing them over a cluster of the heads' CTAs was slower: 101 against
 // 88 us for 16002 tokens).  Rows are loaded one set ahead of the one in work.
+// With norms or positions of the caller's own, prompts go another way: the rows of q through cache4.cu's kernel,
+// and here a CTA takes the keys or the values of a page, of several heads with one table (15500 tokens with norms 50 + 54
+// us; all in one kernel 169, a CTA a head for keys and values 128).
 //
 // Bound: HBM (T D (4 Hq + 6 Hk) bytes) for prompts, launch latency for decode.  16002 tokens
 // of 32 + 8 heads of 128 take 84.5 us, 4.1 TB/s (0.61 of a copy's rate: the CTAs of an SM hold

@@ -13,6 +13,12 @@
 // copies into a ring in shared memory, each lane's own bytes, as far ahead as the ring is long, the
 // first ones before the token's place is known.  Odd sizes and unaligned rows are read directly
 // and find their mates by way of shared memory.
+//
+// Bound: instructions (0.8 issued a cycle and scheduler; some 190 for two rows of q of 128 values with norm and rotation).
+// 15500 tokens of 32 + 8 heads of 128 with norms take 76 us, 4.1 TB/s; 5003 of 28 + 4 heads with positions of three axes
+// 19; one token 3.3, a launch's shortest.  Steps on the way: tokens' tables in shared memory read for every row 141 us; rows of
+// different kinds in one loop, with shuffles of half warps, 116; loads ahead in registers 97; a ring of eight rows instead
+// of four 1 us more.
 #include <algorithm>
 #include <type_traits>
 
