@@ -360,3 +360,79 @@ def test_a_row_does_not_depend_on_the_others(n):
     loud[:, ::2] *= 30
     got, _ = run(b, loud)
     assert np.array_equal(got[:, 1::2], few[:, 1::2]) and not np.array_equal(got[:, ::2], few[:, ::2])
+
+
+def test_full_batch_of_few_and_many_rows():
+    """Sequences times kv heads enough that 32 rows, and not 64, divide the two kernels; sequences on both sides of it."""
+    news = [1, 8, 9, 16, 17, 2, 40, 0] * 2
+    lens = [n + 37 * i for i, n in enumerate(news)]
+    b = ref4.make_batch(49, lens, news, 4, 128, 32)
+    check(b, queries(50, sum(news), 16, 128))
+    b = ref4.make_batch(51, [60 + i for i in range(16)], [8] * 16, 4, 128, 64)
+    check(b, queries(52, 128, 16, 128))
+
+
+@pytest.mark.parametrize("n", [1, 30])
+def test_table_far_wider_than_the_lengths(n):
+    """What is planned by the table's width, more CTAs and a second launch, changes no result beyond rounding."""
+    b = ref4.make_batch(53, [66, 300], [n, n], 2, 128, 64)
+    b.table = np.concatenate([b.table, np.full((2, 2000), -1, np.int32)], 1)
+    check(b, queries(54, 2 * n, 8, 128))
+
+
+def test_lengths_below_nothing_and_past_the_table():
+    b = ref4.make_batch(55, [64, 64], [3, 3], 1, 64, 16)
+    cache, table, _, _ = b.device()
+    q = queries(56, 6, 4, 64).cuda()
+    lse = torch.zeros(6, 4, device="cuda")
+    out = lb.attention(q, *cache, table, torch.tensor([-7, 64], dtype=torch.int32, device="cuda"), lse=lse)
+    assert not out[:3].any() and torch.isneginf(lse[:3]).all() and out[3:].any()
+    # past the table: counted as the table's 64 tokens
+    past = lb.attention(q, *cache, table, torch.tensor([2 ** 31 - 1, 64], dtype=torch.int32, device="cuda"))
+    whole = lb.attention(q, *cache, table, torch.tensor([64, 64], dtype=torch.int32, device="cuda"))
+    assert torch.equal(past, whole)
+
+
+def test_two_calls_at_once():
+    """Decode, prompts and cache writes on two streams at the same time, each with its own outputs."""
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    work = []
+    for i, (lens, n) in enumerate((([5000, 700], 1), ([900, 300], 90))):
+        b = ref4.make_batch(57 + i, lens, [n, n], 2, 128, 64)
+        cache, table, lens, _ = b.device()
+        q = queries(59 + i, 2 * n, 8, 128).cuda()
+        kv = queries(61 + i, 2 * n, 4, 128).cuda()
+        work.append((q, kv, cache, table, lens, lb.attention(q, *cache, table, lens)))
+    torch.cuda.synchronize()
+    results = [[], []]
+    for _ in range(20):
+        for side, (q, kv, cache, table, lens, _), got in zip(sides, work, results):
+            with torch.cuda.stream(side):
+                got.append(lb.attention(q, *cache, table, lens))
+                fresh = lb.empty_cache(cache[0].shape[0], 2, 128, 64, bits=4)
+                lb.kv_append(q, kv[:, :2], kv[:, 2:], *fresh, table, lens)
+                got.append(fresh[0])
+    torch.cuda.synchronize()
+    for got, (*_, want) in zip(results, work):
+        assert all(torch.equal(x, want) for x in got[::2]) and all(torch.equal(x, got[1]) for x in got[3::2])
+
+
+def test_two_graphs_with_one_workspace():
+    """Replayed in turn, also after calls outside of them."""
+    b = ref4.make_batch(63, [3000, 80], [2, 2], 2, 128, 64)
+    cache, table, lens, _ = b.device()
+    qs = [queries(64 + i, 4, 8, 128).cuda() for i in range(2)]
+    ws = torch.empty(lb.attention_workspace(qs[0], *cache, table, lens), dtype=torch.uint8, device="cuda")
+    want = [lb.attention(q, *cache, table, lens, workspace=ws) for q in qs]
+    graphs, outs = [], []
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(lb.attention(q, *cache, table, lens, workspace=ws))
+        graphs.append(g)
+    for _ in range(5):
+        for g, o, w in zip(graphs, outs, want):
+            o.zero_()
+            g.replay()
+            assert torch.equal(o, w)
+        assert torch.equal(lb.attention(qs[0], *cache, table, lens, workspace=ws), want[0])
