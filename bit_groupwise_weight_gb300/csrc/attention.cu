@@ -137,12 +137,15 @@ struct Eight {
         float m[N][2], l[N][2];
     };
 
+    template <int D, int ROWS>
+    struct Queries {};
     // Where a lane's sums o[k] stand: values value_of(k, g) and the next one.
     static __device__ __forceinline__ int value_of(int k, int g) { return 16 * k + 2 * g; }
 
     // Query fragments of an item's rows: fp16, each row times a power of two.
     template <int D, int ROWS>
-    static __device__ __forceinline__ void queries(const AttentionArgs &p, State<D, ROWS> &a, const Seq &s, int h, int row0) {
+    static __device__ __forceinline__ void queries(const AttentionArgs &p, State<D, ROWS> &a, const Seq &s, int h, int row0,
+                                                   Queries<D, ROWS> &) {
         constexpr int KS = D / 16, N = ROWS / 8;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, nrows = s.n * p.G, first = s.len - s.n;
                 #pragma unroll
@@ -349,14 +352,13 @@ struct Eight {
 //   1 x 8000 keys of 128:        14, 17, 20, 22, 26, 31 and 32, 33, 33, 35, 35;
 //   1 x 300 keys of 128:         10, 11, 11, 11, 12, 12 and 13, 13, 13, 13, 13.
 // 64 lies between: full batches of 128 values would cross at 45, of 64 values at 90, single
-// sequences at 150.  Over a 4-bit cache, where few rows cost more and the prompt kernel does not, for 16, 32, 48, 64, 96
-// and 128 rows:
-//   8 x 6000 keys of 128 values: 33, 53, 73, 93, 133, 172 and 53, 54, 55, 56, 58, 59;
-//   8 x 6000 keys of 64:         19, 27, 35, 43, 60, 76 and 49, 50, 51, 51, 52, 52;
-//   1 x 8000 keys of 128:        16, 19, 24, 26, 32, 39 and 30, 32, 33, 34, 35, 36;
-//   1 x 300 keys of 128:         11, 11, 12, 12, 12, 13 and 12, 13, 13, 13, 13, 13;
-// so that full batches (of sequences times kv heads) of 128 values cross at 32.
-constexpr int kFewRows = 64, kFewRowsFull4 = 32, kFullBatch = 64;
+// sequences at 150.  Over a 4-bit cache, for 16, 32, 48, 64, 96 and 128 rows:
+//   8 x 6000 keys of 128 values: 26, 39, 52, 67, 94, 121 and 53, 54, 55, 56, 58, 59;
+//   8 x 6000 keys of 64:         19, 27, 36, 44, 60, 77 and 49, 50, 51, 51, 52, 52;
+//   1 x 8000 keys of 128:        14, 17, 20, 21, 25, 29 and 30, 32, 33, 34, 35, 36;
+//   1 x 300 keys of 128:         9, 10, 10, 10, 10, 11 and 12, 13, 13, 13, 13, 13;
+// so that full batches (of sequences times kv heads) of 128 values take 48.
+constexpr int kFewRows = 64, kFewRowsFull4 = 48, kFullBatch = 64;
 struct Kernels { bool few, many; int few_rows; };
 Kernels kernels_for(int max_q, bool uniform, int B, int Hq, int Hk, int D, bool four) {
     const int few_rows = four && D == 128 && (int64_t)B * Hk >= kFullBatch ? kFewRowsFull4 : kFewRows;

@@ -25,8 +25,8 @@
 // shifts), issued at 0.57 a cycle and scheduler: one of 131001 keys takes 37.6 us, 3.8 TB/s, 0.57 of a copy's rate (20.9
 // us would be the bytes'); the number of stages does not matter (2: the same), registers do: what only the list needs is
 // in shared memory while a warp goes through its tiles (40.3 us without).  q's fragments there too, and four CTAs an SM
-// with 96 registers, were no faster.  64 sequences of up to 16001 keys 34.4 us; 96 windows of 1000 keys of 64 values in
-// pages of 16 19.1; 8 sequences of 5 tokens, 28 heads over 4, 20.9: what an item costs beside its tiles, as for the 8-bit
+// with 96 registers, were no faster (with 16 rows the first is).  64 sequences of up to 16001 keys 34.4 us; 96 windows of 1000 keys of 64 values in
+// pages of 16 19.1; 8 sequences of 5 tokens, 28 heads over 4, 18.1: what an item costs beside its tiles, as for the 8-bit
 // cache.  One sequence of 257 keys 6.2 us.
 #include "attention_few.cuh"
 #include "int4.cuh"
@@ -148,19 +148,36 @@ struct Four {
     template <int D, int ROWS>
     struct State {
         static constexpr int KS = D / 16, N = ROWS / 8, G = D / kGroup4;
-        uint32_t q[KS][N][2];                        // B fragments of q^T: values 8t + (0, 4), (1, 5); (2, 6), (3, 7) of a group
+        // B fragments of q^T: values 8t + (0, 4), (1, 5); (2, 6), (3, 7) of a group.  Of 16 rows the warps
+        // of a CTA share them in shared memory: the registers are worth more (8 sequences of 5 tokens 20.9 -> 18.1 us, 4 of 16
+        // 33.1 -> 26.2; 8 rows gain nothing).
+        static constexpr bool kShared = N == 2;
+        uint32_t q[kShared ? 1 : KS][N][2];
+        uint32_t shared;
+        __device__ __forceinline__ void fragments(int j, uint32_t (&f)[N][4]) const {
+            if constexpr (kShared) {
+                #pragma unroll
+                for (int n = 0; n < N; ++n) ptx::lds_v4<0>(shared + (n * G + j) * 512, f[n][0], f[n][1], f[n][2], f[n][3]);
+            } else {
+#pragma unroll
+                for (int n = 0; n < N; ++n) f[n][0] = q[2 * j][n][0], f[n][1] = q[2 * j][n][1], f[n][2] = q[2 * j + 1][n][0], f[n][3] = q[2 * j + 1][n][1];
+            }
+        }
         uint32_t offset[N][2];                       // B fragment of -8 sum q of the groups, in three parts
         float qs[N][2];                              // factor of the row's scores
         int pos[N][2];
         float o[KS][N][4];                           // O^T
         float m[N][2], l[N][2];
     };
+    template <int D, int ROWS>
+    struct Queries { uint4 q[State<D, ROWS>::kShared ? ROWS / 8 * (D / kGroup4) : 1][State<D, ROWS>::kShared ? 32 : 1]; };
     static __device__ __forceinline__ int value_of(int k, int g) { return 32 * (k >> 1) + 4 * g + 2 * (k & 1); }
 
     // Query fragments: fp16, each row times a power of two, 2^4 more than for the 8-bit cache where the
     // codes are 2^-24 of themselves.
     template <int D, int ROWS>
-    static __device__ __forceinline__ void queries(const AttentionArgs &p, State<D, ROWS> &a, const Seq &s, int h, int row0) {
+    static __device__ __forceinline__ void queries(const AttentionArgs &p, State<D, ROWS> &a, const Seq &s, int h, int row0,
+                                                   Queries<D, ROWS> &queries) {
         constexpr int KS = D / 16, N = ROWS / 8, G = D / kGroup4;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, nrows = s.n * p.G, first = s.len - s.n;
 #pragma unroll
@@ -191,15 +208,18 @@ struct Four {
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 const uint2 lo = v[j][0], hi = v[j][1];                     // values 0 .. 3 and 4 .. 7 of the lane's eight
-                a.q[2 * j][n][0] = f32x2_to_f16x2(bf16_lo(lo.x) * even, bf16_lo(hi.x) * even);
-                a.q[2 * j][n][1] = f32x2_to_f16x2(bf16_hi(lo.x) * odd, bf16_hi(hi.x) * odd);
-                a.q[2 * j + 1][n][0] = f32x2_to_f16x2(bf16_lo(lo.y) * even, bf16_lo(hi.y) * even);
-                a.q[2 * j + 1][n][1] = f32x2_to_f16x2(bf16_hi(lo.y) * odd, bf16_hi(hi.y) * odd);
+                const uint32_t q[4] = {f32x2_to_f16x2(bf16_lo(lo.x) * even, bf16_lo(hi.x) * even), f32x2_to_f16x2(bf16_hi(lo.x) * odd, bf16_hi(hi.x) * odd),
+                                       f32x2_to_f16x2(bf16_lo(lo.y) * even, bf16_lo(hi.y) * even), f32x2_to_f16x2(bf16_hi(lo.y) * odd, bf16_hi(hi.y) * odd)};
+                if constexpr (State<D, ROWS>::kShared) {
+                    if (threadIdx.x < 32) queries.q[n * G + j][lane] = make_uint4(q[0], q[1], q[2], q[3]);
+                } else {
+                    a.q[2 * j][n][0] = q[0], a.q[2 * j][n][1] = q[1], a.q[2 * j + 1][n][0] = q[2], a.q[2 * j + 1][n][1] = q[3];
+                }
                 float half[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a.q[2 * j][n][c]));
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&a.q[2 * j + 1][n][c]));
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&q[c]));
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&q[2 + c]));
                     half[c] = (x.x + x.y) + (y.x + y.y);
                 }
                 sum[j] = fmaf(half[1], 16.f, half[0]) * (-8.f * 0x1p-8f);          // below 2^15
@@ -229,19 +249,19 @@ struct Four {
 #pragma unroll
             for (int c = 0; c < KS; ++c) a.o[c][n][0] = a.o[c][n][1] = a.o[c][n][2] = a.o[c][n][3] = 0.f;
         }
+        if constexpr (State<D, ROWS>::kShared) {     // (the last item's are no longer read: its warps have been joined)
+            a.shared = ptx::smem_u32(&queries.q[0][lane]);
+            ptx::named_sync(1, kWarps * 32);
+        }
     }
 
-    // The scales of a key's groups as fp32.
+    // The scales of a key's groups, a byte each.
     template <int D>
-    static __device__ __forceinline__ uint32_t key_scales(uint32_t at, float (&s)[D / kGroup4]) {
-        const uint32_t u = D == 128 ? ptx::lds_u32(at) : (uint32_t)ptx::lds_u16(at);
-#pragma unroll
-        for (int j = 0; j < D / kGroup4; j += 2) {
-            const uint32_t h = ptx::prmt(u, 0u, j == 0 ? 0x1404u : 0x3424u);
-            const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            s[j] = x.x, s[j + 1] = x.y;
-        }
-        return u;
+    static __device__ __forceinline__ uint32_t key_scales(uint32_t at) { return D == 128 ? ptx::lds_u32(at) : (uint32_t)ptx::lds_u16(at); }
+    // Those of groups c and c + 1 as fp32.
+    static __device__ __forceinline__ float2 scale_pair(uint32_t u, int c) {
+        const uint32_t h = ptx::prmt(u, 0u, c == 0 ? 0x1404u : 0x3424u);
+        return __half22float2(*reinterpret_cast<const __half2 *>(&h));
     }
 
     // A warp's 32 keys of a stage, in two halves of 16.  EDGE: some row does not see some key of them.
@@ -255,49 +275,49 @@ struct Four {
         const uint32_t mine = D == 128 && (t & 1) ? 0x3424u : 0x1404u;           // this lane's two groups as an fp16 pair
         float x[2][N][4];
         uint32_t seen[2][N];                         // bit i: value i of the pair is seen
+        uint32_t u[2][2];                            // the scales of keys g and g + 8 of both halves
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            float s0[G], s1[G];                      // of keys g and g + 8
-            const uint32_t u0 = key_scales<D>(kst + at.scales[half], s0), u1 = key_scales<D>(kst + at.scales[half] + 8 * G, s1);
+            u[half][0] = key_scales<D>(kst + at.scales[half]), u[half][1] = key_scales<D>(kst + at.scales[half] + 8 * G);
             // The groups' offsets: scales times -8 sum q.
-            const uint32_t f0 = ptx::prmt(u0, 0u, mine), f1 = ptx::prmt(u1, 0u, mine);
+            const uint32_t f0 = ptx::prmt(u[half][0], 0u, mine), f1 = ptx::prmt(u[half][1], 0u, mine);
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 mma_new(x[half][n], f0, f1, f0, f1, st.offset[n][0], st.offset[n][1]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x[half][n][k] *= 0x1p-16f;
-            }
-#pragma unroll
-            for (int c = 0; c < G; c += 2) {
-                uint32_t r[4];
-                ldsm_x4(second<D>(kat, half) ^ (c << 4), r);     // (keys 0-7, chunk c), (8-15, c), (0-7, c+1), (8-15, c+1)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = c + i;
-                    const uint32_t a = r[2 * i], b = r[2 * i + 1], a8 = a >> 8, b8 = b >> 8;
-#pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        float acc[4];
-                        mma_new(acc, a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u, b & 0x00F000F0u, st.q[2 * j][n][0],
-                                st.q[2 * j][n][1]);
-                        ptx::mma_16816_f16(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u,
-                                           st.q[2 * j + 1][n][0], st.q[2 * j + 1][n][1]);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float s = k < 2 ? s0[j] : s1[j];
-                            x[half][n][k] = fmaf(acc[k], s, x[half][n][k]);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
                 seen[half][n] = 0xFu;
                 if constexpr (EDGE) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {    // (key g, row 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
                         const int key = key0 + half * 16 + g + 8 * (i >> 1), pos = st.pos[n][i & 1];
                         if (!(key <= pos && (p.window == 0 || key > pos - p.window))) seen[half][n] &= ~(1u << i);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < G; c += 2) {
+            uint32_t r[2][4];
+            ldsm_x4(second<D>(kat, 0) ^ (c << 4), r[0]);         // (keys 0-7, chunk c), (8-15, c), (0-7, c+1), (8-15, c+1)
+            ldsm_x4(second<D>(kat, 1) ^ (c << 4), r[1]);
+            const float2 s[2][2] = {{scale_pair(u[0][0], c), scale_pair(u[0][1], c)}, {scale_pair(u[1][0], c), scale_pair(u[1][1], c)}};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = c + i;
+                uint32_t q[N][4];
+                st.fragments(j, q);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t a = r[half][2 * i], b = r[half][2 * i + 1], a8 = a >> 8, b8 = b >> 8;
+                    const float s0 = i == 0 ? s[half][0].x : s[half][0].y, s1 = i == 0 ? s[half][1].x : s[half][1].y;
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        float acc[4];
+                        mma_new(acc, a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u, b & 0x00F000F0u, q[n][0], q[n][1]);
+                        ptx::mma_16816_f16(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, q[n][2], q[n][3]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[half][n][k] = fmaf(acc[k], k < 2 ? s0 : s1, x[half][n][k]);
                     }
                 }
             }

@@ -134,6 +134,7 @@ struct Smem {
     float o[kWarps][8][D + 4];                   // the warps' sums at an item's end, 8 rows at a time
     float m[kWarps][8], l[kWarps][8];
     Held held[F::kHold ? kWarps : 1];
+    typename F::template Queries<D, ROWS> queries;
     typename F::StageBeside beside[F::stages(D, ROWS)];
     alignas(8) uint64_t full[F::stages(D, ROWS)], empty[F::stages(D, ROWS)];
 };
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, F::per_sm(D, ROWS))
         int nrows = s.n * p.G, row0 = pl.rt * ROWS;
         const int first = s.len - s.n;
 
-        F::template queries<D, ROWS>(p, a, s, pl.h, row0);
+        F::template queries<D, ROWS>(p, a, s, pl.h, row0, sm.queries);
         const int pos_lo = first + row0 / p.G, pos_hi = first + (min(row0 + ROWS, nrows) - 1) / p.G;
 
         // The tiles' loop needs its registers: what only the items need waits in shared memory.
