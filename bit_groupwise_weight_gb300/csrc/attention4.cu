@@ -22,12 +22,12 @@
 // A stage is 128 keys, a warp's share 32 of them in two halves: softmax bookkeeping and the loop's own cost are
 // paid once for both.
 // Bound: instructions.  16 keys of K and V and 128 values take a warp some 230, half of them on the ALU (masks,
-// shifts), issued at 0.57 a cycle and scheduler: one of 131001 keys takes 37.6 us, 3.8 TB/s, 0.57 of a copy's rate (20.9
+// shifts), issued at 0.57 a cycle and scheduler: one of 131001 keys takes 38 us, 3.8 TB/s, 0.56 of a copy's rate (21.3
 // us would be the bytes'); the number of stages does not matter (2: the same), registers do: what only the list needs is
 // in shared memory while a warp goes through its tiles (40.3 us without).  q's fragments there too, and four CTAs an SM
-// with 96 registers, were no faster (with 16 rows the first is).  64 sequences of up to 16001 keys 34.4 us; 96 windows of 1000 keys of 64 values in
+// with 96 registers, were no faster (with 16 rows the first is).  64 sequences of up to 16001 keys 34.9 us; 96 windows of 1000 keys of 64 values in
 // pages of 16 19.1; 8 sequences of 5 tokens, 28 heads over 4, 18.1: what an item costs beside its tiles, as for the 8-bit
-// cache.  One sequence of 257 keys 6.2 us.
+// cache.  One sequence of 257 keys 6.4 us.
 #include "attention_few.cuh"
 #include "int4.cuh"
 
