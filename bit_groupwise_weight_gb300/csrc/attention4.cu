@@ -117,8 +117,8 @@ struct Four {
     }
     static __device__ __forceinline__ void put_beside(StageBeside &, const Beside &, int, int) {}
 
-    // A stage's codes are lines of 128 bytes, two keys (of 128 values) or four: whole lines are what copies are
-    // quick with (lines of 64 bytes: 40.5 us for 131001 keys).  A lane's ldmatrix address in the first 16 keys of its warp's 32,
+    // A stage's codes are lines of 128 bytes, two keys (of 128 values) or four (lines of 64 bytes took 40.5 us
+    // for 131001 keys where these took 40.3: copies were not the bound).  A lane's ldmatrix address in the first 16 keys of its warp's 32,
     // without the chunk of 16 bytes (32 codes, a group): the swizzle flips bits of a chunk's number in its line by the
     // line's, so chunk c is at (address ^ c << 4); the second 16 keys are 8 lines on, or 4.
     template <int D>
