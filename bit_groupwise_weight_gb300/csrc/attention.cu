@@ -229,7 +229,7 @@ struct Eight {
                     if (!see) x[n][i] = -INFINITY, seen[n] &= ~(1u << i);
                 }
             }
-            grown |= fmaxf(x[n][0], x[n][2]) > st.m[n][0] + kPeak || fmaxf(x[n][1], x[n][3]) > st.m[n][1] + kPeak;
+            grown |= fmaxf(x[n][0], x[n][2]) - st.m[n][0] > kPeak || fmaxf(x[n][1], x[n][3]) - st.m[n][1] > kPeak;
         }
         if (__any_sync(~0u, grown)) {                // rows whose maximum has outgrown m (the first keys seen: from -inf)
 #pragma unroll

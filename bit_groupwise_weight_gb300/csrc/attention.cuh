@@ -45,6 +45,11 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
 // m moves more often: a prompt of 4096 tokens takes 140 or 150 us instead of 125, 8 sequences of 5
 // guessed tokens 19.2 or 19.9 instead of 18.7.)
 constexpr float kStart = 7.f, kPeak = 15.f;
+// Scores less m by one fused operation are differences of the exact products, m comes from a rounded one.  Up to this
+// size of m the two are half a unit apart at most, past it any number of them, and what is below kPeak in one
+// way overflows, or counts for nothing, in the other: there products are rounded first.  (kPeak is compared with the
+// difference as the exponential takes it: m + kPeak may be rounded to 16 more than m.)
+constexpr float kFar = 4194304.f;
 // The weights' sum l does not have ve in it, and what counts in it may count for nothing in the
 // product (a page of zeros).  For ve below kDeep, where the weight may be under fp32's range, it
 // takes 2^(s - m) by itself; and l is rescaled in two halves of the exponent, which may be past -126.

@@ -28,6 +28,8 @@
 // with 96 registers, were no faster (with 16 rows the first is).  64 sequences of up to 16001 keys 34.9 us; 96 windows of 1000 keys of 64 values in
 // pages of 16 19.1; 8 sequences of 5 tokens, 28 heads over 4, 18.1: what an item costs beside its tiles, as for the 8-bit
 // cache.  One sequence of 257 keys 6.4 us.
+#include <type_traits>
+
 #include "attention_few.cuh"
 #include "int4.cuh"
 
@@ -80,6 +82,7 @@ struct Four {
     static constexpr float kUnit = 64.f;
     // m of a row that has seen nothing: any score outgrows it, and, unlike with -inf, scores less m are numbers.
     static constexpr float kNone = -3e38f;
+    static __device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m != kNone; }
     template <int D>
     static constexpr int kKeyBytes = D + D / 16;                          // codes and scales of K and V
 
@@ -168,6 +171,7 @@ struct Four {
         int pos[N][2];
         float o[KS][N][4];                           // O^T
         float m[N][2], l[N][2];
+        float limit;                                 // of scores over m: kPeak, or all are looked at (some |m| past kFar)
     };
     template <int D, int ROWS>
     struct Queries { uint4 q[State<D, ROWS>::kShared ? ROWS / 8 * (D / kGroup4) : 1][State<D, ROWS>::kShared ? 32 : 1]; };
@@ -180,6 +184,7 @@ struct Four {
                                                    Queries<D, ROWS> &queries) {
         constexpr int KS = D / 16, N = ROWS / 8, G = D / kGroup4;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, nrows = s.n * p.G, first = s.len - s.n;
+        a.limit = kPeak;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int r = row0 + 8 * n + g;
@@ -324,7 +329,7 @@ struct Four {
         }
         // Exponents of the weights: scores over m.
         float y[2][N][4];
-        auto exponents = [&] {
+        auto exponents = [&](auto moved) {
             float top = -INFINITY;
 #pragma unroll
             for (int n = 0; n < N; ++n)
@@ -332,13 +337,15 @@ struct Four {
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        y[half][n][i] = fmaf(x[half][n][i], st.qs[n][i & 1], -st.m[n][i & 1]);
+                        const float by = st.qs[n][i & 1], m = st.m[n][i & 1];
+                        y[half][n][i] = moved && is_far(m) ? __fsub_rn(__fmul_rn(x[half][n][i], by), m) : fmaf(x[half][n][i], by, -m);
                         if (EDGE && !(seen[half][n] >> i & 1u)) y[half][n][i] = -INFINITY;
                         top = fmaxf(top, y[half][n][i]);
                     }
             return top;
         };
-        if (__any_sync(~0u, exponents() > kPeak)) {  // rows whose maximum has outgrown m (the first keys seen: from kNone)
+        if (__any_sync(~0u, exponents(std::false_type{}) > st.limit)) {   // rows whose maximum has outgrown m (the first keys seen: from kNone)
+            bool any = false;
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -352,15 +359,17 @@ struct Four {
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-                    const float to = mx > st.m[n][c] + kPeak ? mx - kStart : st.m[n][c];    // of this row alone
+                    const float to = mx - st.m[n][c] > kPeak ? mx - kStart : st.m[n][c];    // of this row alone
                     const Rescale by(st.m[n][c] - to);
                     const float f = by.of_o();
                     st.m[n][c] = to;
                     st.l[n][c] = by.of_l(st.l[n][c]);
+                    any |= is_far(to);
 #pragma unroll
                     for (int k = 0; k < 2 * G; ++k) st.o[k][n][c] *= f, st.o[k][n][c + 2] *= f;
                 }
-            exponents();
+            st.limit = __any_sync(~0u, any) ? -INFINITY : kPeak;
+            exponents(std::true_type{});
         }
         uint32_t pb[2][N][2];                        // P^T: B fragments
 #pragma unroll

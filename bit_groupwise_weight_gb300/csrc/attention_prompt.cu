@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::fence_proxy_async_smem();
         }
         bool ok = true;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, limit = kPeak;
         const uint32_t tmem = meet(), sc = tmem + t * 128 + quarter, oc = tmem + 256 + t * D + quarter;
         for (int hs = 0; hs < 2 * w.n; ++hs) {                          // half-steps of 64 keys
             const int j = hs >> 1, h = hs & 1, key0 = (w.lo + j) * kKeys + h * kHalf;
@@ -454,18 +454,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < kHalf; ++k)
                     if (k > hi || k <= lo) v[k] = -INFINITY;
                 if (ex(0).w != 0.f) {
-                    const float mx = largest(), to = mx > m + kPeak ? mx - kStart : m, ref = to == -INFINITY ? 0.f : to;
+                    const float mx = largest(), to = mx - m > kPeak ? mx - kStart : m, ref = to == -INFINITY ? 0.f : to;
+                    const bool far = fabsf(ref) >= kFar;
 #pragma unroll
-                    for (int k = 0; k < kHalf; ++k) deep += ex(k / 16).y < kDeep ? ex2(fmaf(v[k], factor(k / 16), -ref)) : 0.f;
+                    for (int k = 0; k < kHalf; ++k) {
+                        const float f = factor(k / 16);
+                        deep += ex(k / 16).y < kDeep ? ex2(far ? __fsub_rn(__fmul_rn(v[k], f), ref) : fmaf(v[k], f, -ref)) : 0.f;
+                    }
                 }
             }
             float f[kHalf / 16];
 #pragma unroll
             for (int g = 0; g < kHalf / 16; ++g) f[g] = factor(g);
-            // m follows the maximum when it has been outgrown.
+            // m follows the maximum when it has been outgrown; rows far from zero (limit: -inf) always come here.
             const float mx = largest();
-            const bool move = mx > m + kPeak;
-            if (__any_sync(~0u, move)) {
+            float base = m;
+            if (__any_sync(~0u, mx - m > limit)) {
+                const bool move = mx - m > kPeak;
                 const Rescale by(move ? m - (mx - kStart) : 0.f);
                 const float a = by.of_o();
                 if (move) m = mx - kStart;
@@ -484,9 +489,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tmem_st16(oc + c * 16, o);
                     }
                 }
+                base = m, limit = kPeak;
+                if (m != -INFINITY && fabsf(m) >= kFar) {              // products are rounded before m is taken off
+                    base = 0.f, limit = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < kHalf; ++k) v[k] = __fsub_rn(__fsub_rn(fmaf(v[k], f[k / 16], ex(k / 16).y), m), ex(k / 16).y);
+#pragma unroll
+                    for (int g = 0; g < kHalf / 16; ++g) f[g] = 1.f;
+                }
             }
             l += deep;
-            const float ref = m == -INFINITY ? 0.f : m;
+            const float ref = base == -INFINITY ? 0.f : base;
             // Weights, their sum, and fp16 pairs in the place of the scores.
 #pragma unroll
             for (int c = 0; c < 2; ++c) {

@@ -1,0 +1,136 @@
+"""Attention over both kinds of cache where scores leave the sizes that models have: far from
+zero (next to which fp32 holds no fractions), at fp32's ends, rows of q near the largest number."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import cache4_ref as ref4
+import decoder_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import bit_groupwise_weight_gb300 as lb  # noqa: E402
+from bit_groupwise_weight_gb300 import build as lbuild  # noqa: E402
+
+lbuild.build()
+
+HEADS = 4                                                 # over one kv head: 1 new token is 4 rows, 80 are 320
+FEW_AND_MANY = "n", [1, 80]
+
+
+def batch(bits, seed, n, dim, keys, power):
+    """Two sequences whose keys are rows of `keys` (whole numbers of up to 7) times 2^power, chosen at random, all
+    kinds of them among the first.  Returns the batch and each sequence's choice."""
+    lens = [300, 131]
+    make = (ref4 if bits == 4 else ref).make_batch
+    b = make(seed, lens, [n, n], 1, dim, 32)
+    rng = np.random.default_rng([seed, 1])
+    kinds = [np.concatenate([np.arange(len(keys)), rng.integers(0, len(keys), m - len(keys))]) for m in lens]
+    if bits == 8:
+        b.k_exp[:], b.v_exp[:] = power, -6                                    # (v's exponent is added to the scores)
+    for s, m in enumerate(lens):
+        at = np.arange(m)
+        page, slot = b.table[s, at // 32], at % 32
+        if bits == 4:
+            b.k[page, 0, slot] = keys[kinds[s]] + 8
+            b.k_scale[page, 0, slot] = (power + 15) << 2                      # 2^power as e5m2
+        else:
+            b.k[page, 0, slot] = ref.e4m3_round(keys[kinds[s]].astype(float))
+    return b, kinds
+
+
+def run(b, q, scale):
+    cache, table, lens, cu = b.device()
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device="cuda")
+    out = lb.attention(q.cuda(), *cache, table, lens, cu_q=cu, max_q=max(b.news), scale=scale, lse=lse)
+    assert lb.wait_timeouts() == 0
+    return ref.f64(out), ref.f64(lse)
+
+
+def seen_values(bits, b, s):
+    """(v fp64 [len, dim], how many keys each of the sequence's new rows sees)."""
+    v = ref4.cached(b, s, 0, "v")[0] if bits == 4 else ref.cached(b, s, 0, "v")
+    return v, b.lens[s] - b.news[s] + np.arange(b.news[s]) + 1
+
+
+def check(bits, b, kinds, q, keys, power, scale):
+    """Kinds of keys whose scores are so far apart that the best one has all of the weight: the mean of its values.
+    Equal keys have equal scores and so equal weights, rounded to fp16 (2^-11 of themselves) for the product and not for
+    their sum; sums and products are fp32's (2^-16 of the magnitudes covers 300 of them), out is rounded to bf16; scores
+    are some ten roundings of sums of up to 16 |q| 2^power a value over 4 bits (2^-20 of that), the logarithm is off by
+    2 units and lse by one.
+    Of the few rows for which two kinds come near each other only sizes are looked at."""
+    out, lse = run(b, q, scale)
+    x, checked = ref.f64(q), 0
+    for s, n in enumerate(b.news):
+        v, sees = seen_values(bits, b, s)
+        for i in range(n):
+            row, mine = b.starts[s] + i, kinds[s][:sees[i]]
+            for h in range(HEADS):
+                scores = keys.astype(float) @ x[row, h] * 2.0 ** power * scale
+                mag = np.abs(x[row, h]).sum() * 16 * 2.0 ** power * abs(scale)
+                order = np.argsort(-scores)
+                best = mine == order[0]
+                assert np.all(np.abs(out[row, h]) <= np.abs(v).max() * (1 + 2.0 ** -8)), (row, h)
+                assert abs(lse[row, h] - scores[order[0]]) <= 2.0 ** -19 * mag + 10, (row, h, lse[row, h], scores[order[0]])
+                if len(keys) > 1 and scores[order[0]] - scores[order[1]] < max(2.0 ** -14 * mag, 200):
+                    continue
+                checked += 1
+                want, mean = v[:sees[i]][best].mean(0), np.abs(v[:sees[i]][best]).mean(0)
+                assert np.all(np.abs(out[row, h] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -11 * mean + 2.0 ** -16 * np.abs(v).max()), (row, h)
+                want = scores[order[0]] + np.log(best.sum())
+                assert abs(lse[row, h] - want) <= 2.0 ** -20 * mag + 2.0 ** -21 * abs(want) + 2.0 ** -18, (row, h, lse[row, h], want)
+    assert checked >= 0.8 * out.shape[0] * HEADS
+
+
+def make_keys(seed, count, dim):
+    return np.random.default_rng([seed, 2]).integers(-7, 8, (count, dim))
+
+
+def make_q(seed, n, dim, size):
+    """Rows whose largest magnitude is in [size, 2 size)."""
+    x = np.random.default_rng([seed, 3]).uniform(-1, 1, (2 * n, HEADS, dim))
+    x *= 1.5 * size / np.abs(x).max(-1, keepdims=True)
+    return ref.bf16(x)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize(*FEW_AND_MANY)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("far", [20, 23, 24, 26, 27, 30, 60, 118])
+def test_scores_far_from_zero(bits, n, dim, far):
+    """A score's fraction is lost in fp32: its product, rounded and not, must not be taken for different scores."""
+    keys, q = make_keys(far, 3, dim), make_q(far, n, dim, 2.0 ** (far // 2))
+    b, kinds = batch(bits, far, n, dim, keys, 0)
+    for sign in (1, -1):
+        check(bits, b, kinds, q, keys, 0, sign * 2.0 ** (far - far // 2) / 100)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize(*FEW_AND_MANY)
+@pytest.mark.parametrize("unit", [1, 2, 4, 8, 16, 32])
+def test_scores_some_units_apart_far_from_zero(bits, n, unit):
+    """Scores of 2^23 units and 0 to 21 more, a unit being what fp32 holds there: weights of a unit are e^unit, and
+    what comes out lies between the values that went in."""
+    rng = np.random.default_rng([unit, 5])
+    keys = np.zeros((64, 64), int)
+    keys[:, 0] = 4
+    keys[:, [33, 40, 50]] = rng.integers(0, 8, (64, 3))
+    b, kinds = batch(bits, 70 + unit, n, 64, keys, 0)
+    q = torch.zeros(2 * n, HEADS, 64)
+    q[..., 0], q[..., [33, 40, 50]] = 2.0 ** 21 * unit, float(unit)
+    out, lse = run(b, q.to(torch.bfloat16), float(np.log(2.0)))
+    for s in range(2):
+        v, sees = seen_values(bits, b, s)
+        for i in range(n):
+            row = b.starts[s] + i
+            low, high = v[:sees[i]].min(0), v[:sees[i]].max(0)
+            slack = 2.0 ** -8 * np.abs(v).max()
+            assert np.all((low - slack <= out[row]) & (out[row] <= high + slack)), row
+            want = 2.0 ** 23 * unit * np.log(2.0)
+            assert np.all(np.abs(lse[row] - want) <= 2.0 ** -18 * want + 30), (row, lse[row], want)
