@@ -208,7 +208,7 @@ struct Four {
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
             const int up = query_shift(amax);
-            const float odd = exp2_int(up), even = exp2_int(up + 4), scale = within(exp2_int(-up) * p.scale_log2 * 0x1p20f);
+            const float odd = exp2_int(up), even = exp2_int(up + 4), scale = within(exp2_int(4 - up) * p.scale_log2);
             float sum[G];
 #pragma unroll
             for (int j = 0; j < G; ++j) {
@@ -263,10 +263,11 @@ struct Four {
     // The scales of a key's groups, a byte each.
     template <int D>
     static __device__ __forceinline__ uint32_t key_scales(uint32_t at) { return D == 128 ? ptx::lds_u32(at) : (uint32_t)ptx::lds_u16(at); }
-    // Those of groups c and c + 1 as fp32.
+    // Those of groups c and c + 1 as fp32, times 2^16: what the codes are 2^-24 (2^-20) and q 2^4 (1) times themselves, and the
+    // offsets 2^-8 and the 2^4 of q, leave 2^-4 for the row's factor, a number for every row of q (2^20 was none from 2^121 on).
     static __device__ __forceinline__ float2 scale_pair(uint32_t u, int c) {
         const uint32_t h = ptx::prmt(u, 0u, c == 0 ? 0x1404u : 0x3424u);
-        return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        return ptx::fmul2(__half22float2(*reinterpret_cast<const __half2 *>(&h)), make_float2(0x1p16f, 0x1p16f));
     }
 
     // A warp's 32 keys of a stage, in two halves of 16.  EDGE: some row does not see some key of them.
@@ -289,8 +290,6 @@ struct Four {
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 mma_new(x[half][n], f0, f1, f0, f1, st.offset[n][0], st.offset[n][1]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[half][n][k] *= 0x1p-16f;
                 seen[half][n] = 0xFu;
                 if constexpr (EDGE) {
 #pragma unroll

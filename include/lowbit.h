@@ -386,7 +386,8 @@ LOWBIT_API lowbit_status lowbit_attention(const lowbit_attention_args *args, con
 LOWBIT_API size_t lowbit_attention_workspace(int32_t heads, const lowbit_cache *cache, const lowbit_sequences *seqs);
 
 /* lowbit_attention over a 4-bit cache, with the same arguments, sizes and guarantees.
- * Scores are taken from the codes and scaled in fp32; the weights are rounded to fp16 for
+ * Scores are taken from the codes and scaled in fp32, for any row of q whose largest |q|
+ * times |scale| is a finite fp32 number; the weights are rounded to fp16 for
  * the product with v, to 2^-11 of themselves, or to 2^-32 of the row's largest where that
  * is more. */
 LOWBIT_API lowbit_status lowbit_attention4(const lowbit_attention_args *args, const lowbit_cache4 *cache,

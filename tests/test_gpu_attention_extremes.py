@@ -134,3 +134,15 @@ def test_scores_some_units_apart_far_from_zero(bits, n, unit):
             assert np.all((low - slack <= out[row]) & (out[row] <= high + slack)), row
             want = 2.0 ** 23 * unit * np.log(2.0)
             assert np.all(np.abs(lse[row] - want) <= 2.0 ** -18 * want + 30), (row, lse[row], want)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize(*FEW_AND_MANY)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [119, 121, 123, 125, 127])
+def test_rows_of_q_near_the_largest_number(bits, n, dim, size):
+    """What turns codes into scores stays a number for every row of q: with small keys the scores are."""
+    keys, q = make_keys(size, 3, dim), make_q(size, n, dim, 2.0 ** (size if size < 127 else 126.9))
+    b, kinds = batch(bits, size, n, dim, keys, -14)
+    for scale in (dim ** -0.5, -dim ** -0.5, 1.0):
+        check(bits, b, kinds, q, keys, -14, scale)
