@@ -80,8 +80,8 @@ struct Four {
     static constexpr int kCtas = kSms * 4;                                // at most
     static constexpr bool kHold = true;                                   // the list in shared memory during tiles
     static constexpr float kUnit = 64.f;
-    // m of a row that has seen nothing: any score outgrows it, and, unlike with -inf, scores less m are numbers.
-    static constexpr float kNone = -3e38f;
+    // m of a row that has seen nothing: any score outgrows it, and, unlike with -inf, scores less m are no NaN.
+    static constexpr float kNone = -3.4028234663852886e38f;
     static __device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m != kNone; }
     template <int D>
     static constexpr int kKeyBytes = D + D / 16;                          // codes and scales of K and V

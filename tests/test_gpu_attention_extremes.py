@@ -146,3 +146,16 @@ def test_rows_of_q_near_the_largest_number(bits, n, dim, size):
     b, kinds = batch(bits, size, n, dim, keys, -14)
     for scale in (dim ** -0.5, -dim ** -0.5, 1.0):
         check(bits, b, kinds, q, keys, -14, scale)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize(*FEW_AND_MANY)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_at_the_ends_of_fp32(bits, n, sign):
+    """Times log2 e within a tenth of the largest number, on either side of 0."""
+    keys = np.zeros((1, 64), int)
+    keys[0, 5] = 7
+    b, kinds = batch(bits, 90, n, 64, keys, 10)
+    q = torch.zeros(2 * n, HEADS, 64)
+    q[..., 5] = sign * 3.2e38 / np.log2(np.e) / 7 / 2.0 ** 10 * 8
+    check(bits, b, kinds, q.to(torch.bfloat16), keys, 10, 0.125)
