@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int up = query_shift(__uint_as_float(top << 16));
             const float f = __uint_as_float(__float_as_uint(exp2_int(up)) | (p.scale_log2 < 0.f ? 0x80000000u : 0u));
             qs = exp2_int(-up) * fabsf(p.scale_log2) * kValueUnit;
+            if constexpr (FOUR) qs = fminf(qs, 3.4028234663852886e38f);    // an infinite factor would make NaN of sums that are 0
             auto turn = [&](uint32_t v) {
                 const float2 y = ptx::fmul2(make_float2(bf16_lo(v), bf16_hi(v)), make_float2(f, f));
                 return f32x2_to_f16x2(y.x, y.y);

@@ -159,3 +159,17 @@ def test_scores_at_the_ends_of_fp32(bits, n, sign):
     q = torch.zeros(2 * n, HEADS, 64)
     q[..., 5] = sign * 3.2e38 / np.log2(np.e) / 7 / 2.0 ** 10 * 8
     check(bits, b, kinds, q.to(torch.bfloat16), keys, 10, 0.125)
+
+
+@pytest.mark.parametrize(*FEW_AND_MANY)
+@pytest.mark.parametrize("scale", [64.0, -1e6, 9e29])
+def test_zero_keys_have_zero_scores_whatever_the_row_of_q(n, scale):
+    keys = np.zeros((1, 64), int)
+    b, kinds = batch(4, 91, n, 64, keys, 0)
+    out, lse = run(b, make_q(91, n, 64, 2.0 ** 126.9), scale)
+    for s in range(2):
+        v, sees = seen_values(4, b, s)
+        for i in range(n):
+            row, want, mean = b.starts[s] + i, v[:sees[i]].mean(0), np.abs(v[:sees[i]]).mean(0)
+            assert np.all(np.abs(out[row] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -11 * mean + 2.0 ** -16 * np.abs(v).max())
+            assert np.all(np.abs(lse[row] - np.log(sees[i])) <= 2.0 ** -20)
