@@ -29,20 +29,23 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p) {
                       p[6] | (uint32_t)p[7] << 16);
 }
 
-// 1 / sqrt(v), root and reciprocal rounded to nearest each (but for 15 of 2^26 values tried, which are the float
-// beside).  Within the range that rows have in earnest by a
-// Newton step each from the approximate inverse root, its remainder exact in a fused operation (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990): a dozen instructions, where the
-// two functions take some sixty.
+// 1 / sqrt(v), root and reciprocal rounded to nearest each.  Within the range that rows have in earnest by Newton
+// steps from the approximate inverse root, their remainders exact in a fused operation (P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990), one for the root and two for the reciprocal: some
+// fifteen instructions, where the two functions take some sixty.  A reciprocal step does not round right for a mantissa of ones,
+// which the root of v next below a power of 4 has.  (Compared with the two functions for every float that is not negative;
+// with one step for the reciprocal 400 of 1.7e9 were the float beside.)
 __device__ __forceinline__ float inverse_root(float v) {
-    if (!(v > 0x1p-100f && v < 0x1p100f)) return __frcp_rn(__fsqrt_rn(v));
-    const float y = rsqrtf(v), s0 = v * y, s = fmaf(fmaf(-s0, s0, v), 0.5f * y, s0);
-    return fmaf(fmaf(-s, y, 1.f), y, y);
+    const uint32_t u = __float_as_uint(v);
+    if (u - 0x0D800000u >= 0x64000000u || (u & 0xFFFFFEu) == 0x7FFFFEu) return __frcp_rn(__fsqrt_rn(v));     // 2^-100 .. 2^100
+    const float y = rsqrtf(v), s0 = v * y, s = fmaf(fmaf(-s0, s0, v), 0.5f * y, s0), r = fmaf(fmaf(-s, y, 1.f), y, y);
+    return fmaf(fmaf(-s, r, 1.f), r, r);
 }
 
 // 1 / sqrt(mean of squares + eps) of a row held by LANES lanes, 8 values each.  Every operation
-// is rounded by itself, the squares are added in pairs: a key's codes are then the same in any
-// implementation, also next to a border between two.  The lanes of `mask` call, whole rows of them.
+// is rounded by itself, the squares are added in pairs: the codes of a key that is not turned are then
+// the same in any implementation, also next to a border between two (cosines and sines are not
+// rounded to nearest).  The lanes of `mask` call, whole rows of them.
 template <int LANES>
 __device__ __forceinline__ float row_norm(const float (&x)[8], float eps, uint32_t mask) {
     float s[8];

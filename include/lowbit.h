@@ -291,8 +291,9 @@ LOWBIT_API lowbit_status lowbit_kv_append(const lowbit_kv_append_args *args, con
 /* What may stand before the rotation and the write, in the same pass:
  *   norms      each head's q and k over its root mean square, times weights:
  *              y = (x r) w, r = 1 / sqrt(mean x^2 + eps), in fp32, every operation rounded
- *              by itself and the squares added in pairs (neighbours, then neighbouring
- *              sums), so that codes next to a border come out the same in any implementation.
+ *              to nearest by itself and the squares added in pairs (neighbours, then neighbouring
+ *              sums), so that without a rotation codes next to a border come out the same in any
+ *              implementation.  (Cosines and sines of a rotation are off by up to 2 units.)
  *              q_norm, k_norm [head_dim] of norm_dtype, naturally aligned, each may be NULL.
  *   positions  token t's pairs turn by positions[t * positions_token + axis[j]] instead of
  *              its place in its sequence (which still says where it is written): several
