@@ -9,9 +9,12 @@
 // returned as an integer.
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -64,13 +67,21 @@ bool rows(const Tensor *t, int dev, int64_t T, int64_t H, int64_t D, Rows *r) {
     return true;
 }
 
-// A new contiguous tensor.  (Through the dispatcher it costs a microsecond more.)
-Tensor fresh(at::IntArrayRef sizes, ScalarType type, c10::Device device) {
-    return Tensor(at::detail::empty_cuda(sizes, type, device, std::nullopt));
+// Whether torch has something to say about new tensors beside `like`: a mode or a subclass that sees what is
+// called, or deterministic algorithms, which fill them.
+bool watched(const Tensor &like) {
+    return at::globalContext().deterministicAlgorithms() || c10::impl::TorchDispatchModeTLS::any_modes_set() ||
+           like.key_set().has(c10::DispatchKey::Python);
+}
+// A new contiguous tensor beside `like`.  (Through the dispatcher it costs a microsecond more.)
+Tensor fresh(at::IntArrayRef sizes, ScalarType type, const Tensor &like) {
+    if (watched(like)) return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
+    return Tensor(at::detail::empty_cuda(sizes, type, like.device(), std::nullopt));
 }
 // at::empty_like of rows [T, H, D].
 Tensor fresh_rows(const Tensor &q) {
-    if (q.stride(2) == 1 && q.stride(1) >= q.size(2) && q.stride(0) >= q.stride(1)) return fresh(q.sizes(), ScalarType::BFloat16, q.device());
+    if (!watched(q) && q.stride(2) == 1 && q.stride(1) >= q.size(2) && q.stride(0) >= q.stride(1))
+        return fresh(q.sizes(), ScalarType::BFloat16, q);
     return at::empty_like(q);
 }
 
@@ -258,10 +269,12 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Tensor out = a[11] == Py_None ? fresh_rows(*q) : (tensor(a[11]) != nullptr ? *tensor(a[11]) : Tensor());
     if (!out.defined() || !rows(&out, dev, T, H, D, &ro)) return refuse();
     c10::DataPtr own;                            // like a tensor of the current stream that goes after the launch
+    Tensor seen;                                 // or one
     if (a[13] == Py_None) {
         const size_t bytes = c.four ? fn.workspace4((int32_t)H, &c.c4, &s) : fn.workspace((int32_t)H, &c.c8, &s);
-        own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
-        args.workspace = own.get(), args.workspace_bytes = bytes;
+        if (watched(*q)) seen = fresh({(int64_t)bytes}, ScalarType::Byte, *q);
+        else own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+        args.workspace = seen.defined() ? seen.data_ptr() : own.get(), args.workspace_bytes = bytes;
     } else {
         const Tensor *w = tensor(a[13]);
         if (!is(w, ScalarType::Byte, dev, 1) || !w->is_contiguous()) return refuse();
@@ -286,7 +299,7 @@ PyObject *cache_values(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Tensor out[2];
     for (int i = 0; i < 2; ++i) {
         if (a[4 + i] == Py_None) {
-            out[i] = fresh({k->size(0), k->size(1), k->size(2), D}, ScalarType::BFloat16, k->device());
+            out[i] = fresh({k->size(0), k->size(1), k->size(2), D}, ScalarType::BFloat16, *k);
             continue;
         }
         const Tensor *t = tensor(a[4 + i]);
@@ -334,7 +347,7 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (THPVariable_Check(a[3]) ? !vector(a[3], ScalarType::Int, dev, B, &args.top_k) : !integer(a[3], &args.top_k_all)) return refuse();
     if (a[7] != Py_None && !vector(a[7], ScalarType::Float, dev, B, &args.logprob)) return refuse();
     const c10::cuda::OptionalCUDAGuard guard(x->device());
-    const Tensor out = a[6] == Py_None ? fresh({B}, ScalarType::Long, x->device()) : (tensor(a[6]) != nullptr ? *tensor(a[6]) : Tensor());
+    const Tensor out = a[6] == Py_None ? fresh({B}, ScalarType::Long, *x) : (tensor(a[6]) != nullptr ? *tensor(a[6]) : Tensor());
     if (!out.defined() || !is(&out, ScalarType::Long, dev, 1) || out.size(0) != B || (B > 1 && out.stride(0) != 1)) return refuse();
     args.token = static_cast<int64_t *>(out.data_ptr());
     args.logits = x->data_ptr(), args.row_stride = x->stride(0), args.rows = (int32_t)B, args.vocab = (int32_t)V;
