@@ -90,9 +90,10 @@ __device__ __forceinline__ int position_of(const AppendArgs &p, int64_t token, i
 __device__ __forceinline__ void turn_of(const AppendArgs &p, int position, int j, float &cs, float &sn) {
     // As a signed fraction of a turn, the nearest way round.
     const int32_t ph = (int32_t)(((uint64_t)(int64_t)position * (uint64_t)p.turns[j]) >> 32);
-    sincosf((float)ph * 1.4629180792671596e-9f, &sn, &cs);        // 2 pi / 2^32
-    cs = __fmul_rn(cs, p.factor);
-    sn = __fmul_rn(sn, p.factor);
+    float c, s;                          // (cs and sn may be places in shared memory)
+    sincosf((float)ph * 1.4629180792671596e-9f, &s, &c);          // 2 pi / 2^32
+    cs = __fmul_rn(c, p.factor);
+    sn = __fmul_rn(s, p.factor);
 }
 
 }  // namespace append
