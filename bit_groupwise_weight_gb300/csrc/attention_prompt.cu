@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::fence_proxy_async_smem();
         }
         bool ok = true;
-        float m = -INFINITY, l = 0.f, limit = kPeak;
+        float m = -INFINITY, l = 0.f;
+        float ref = 0.f, limit = -INFINITY;      // of m: what is taken off the scores, what they outgrow it by
         const uint32_t tmem = meet(), sc = tmem + t * 128 + quarter, oc = tmem + 256 + t * D + quarter;
         for (int hs = 0; hs < 2 * w.n; ++hs) {                          // half-steps of 64 keys
             const int j = hs >> 1, h = hs & 1, key0 = (w.lo + j) * kKeys + h * kHalf;
@@ -455,22 +456,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < kHalf; ++k)
                     if (k > hi || k <= lo) v[k] = -INFINITY;
                 if (ex(0).w != 0.f) {
-                    const float mx = largest(), to = mx - m > kPeak ? mx - kStart : m, ref = to == -INFINITY ? 0.f : to;
-                    const bool far = fabsf(ref) >= kFar;
+                    const float mx = largest(), to = mx - m > kPeak ? mx - kStart : m, off = to == -INFINITY ? 0.f : to;
 #pragma unroll
                     for (int k = 0; k < kHalf; ++k) {
                         const float f = factor(k / 16);
-                        deep += ex(k / 16).y < kDeep ? ex2(far ? __fsub_rn(__fmul_rn(v[k], f), ref) : fmaf(v[k], f, -ref)) : 0.f;
+                        deep += ex(k / 16).y < kDeep ? ex2(fabsf(off) >= kFar ? __fsub_rn(__fmul_rn(v[k], f), off) : fmaf(v[k], f, -off)) : 0.f;
                     }
                 }
             }
-            float f[kHalf / 16];
+            constexpr int kF = FOUR ? 1 : kHalf / 16;                  // factors of 16 keys each
+            float f[kF];
 #pragma unroll
-            for (int g = 0; g < kHalf / 16; ++g) f[g] = factor(g);
+            for (int g = 0; g < kF; ++g) f[g] = factor(g);
             // m follows the maximum when it has been outgrown; rows far from zero (limit: -inf) always come here.
             const float mx = largest();
-            float base = m;
-            if (__any_sync(~0u, mx - m > limit)) {
+            if (__any_sync(~0u, mx > limit)) {
                 const bool move = mx - m > kPeak;
                 const Rescale by(move ? m - (mx - kStart) : 0.f);
                 const float a = by.of_o();
@@ -490,17 +490,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tmem_st16(oc + c * 16, o);
                     }
                 }
-                base = m, limit = kPeak;
-                if (m != -INFINITY && fabsf(m) >= kFar) {              // products are rounded before m is taken off
-                    base = 0.f, limit = -INFINITY;
+                ref = m == -INFINITY ? 0.f : m, limit = m + kPeak;
+                if (fabsf(ref) >= kFar) {                              // products are rounded before m is taken off
+                    limit = -INFINITY;
+                    if constexpr (!FOUR) ref = 0.f;
 #pragma unroll
-                    for (int k = 0; k < kHalf; ++k) v[k] = __fsub_rn(__fsub_rn(fmaf(v[k], f[k / 16], ex(k / 16).y), m), ex(k / 16).y);
+                    for (int k = 0; k < kHalf; ++k)
+                        v[k] = FOUR ? v[k] * f[0] : __fsub_rn(__fsub_rn(fmaf(v[k], f[k / 16 % kF], ex(k / 16).y), m), ex(k / 16).y);
 #pragma unroll
-                    for (int g = 0; g < kHalf / 16; ++g) f[g] = 1.f;
+                    for (int g = 0; g < kF; ++g) f[g] = 1.f;
                 }
             }
             l += deep;
-            const float ref = base == -INFINITY ? 0.f : base;
             // Weights, their sum, and fp16 pairs in the place of the scores.
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const float4 e = ex(2 * c + g);
-                    const float2 ff = make_float2(f[2 * c + g], f[2 * c + g]), d = make_float2(e.y - ref, e.y - ref);
+                    const float2 ff = make_float2(f[(2 * c + g) % kF], f[(2 * c + g) % kF]), d = make_float2(e.y - ref, e.y - ref);
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
