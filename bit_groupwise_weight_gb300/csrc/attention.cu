@@ -357,7 +357,8 @@ struct Eight {
 //   8 x 6000 keys of 64:         19, 27, 36, 44, 60, 77 and 49, 50, 51, 51, 52, 52;
 //   1 x 8000 keys of 128:        14, 17, 20, 21, 25, 29 and 30, 32, 33, 34, 35, 36;
 //   1 x 300 keys of 128:         9, 10, 10, 10, 10, 11 and 12, 13, 13, 13, 13, 13;
-// so that full batches (of sequences times kv heads) of 128 values take 48.
+// so that full batches (of sequences times kv heads) of 128 values take 48.  Between one and eight sequences, and for
+// full batches of short ones, nothing was measured: single sequences behind long caches would cross past 128.
 constexpr int kFewRows = 64, kFewRowsFull4 = 48, kFullBatch = 64;
 struct Kernels { bool few, many; int few_rows; };
 Kernels kernels_for(int max_q, bool uniform, int B, int Hq, int Hk, int D, bool four) {

@@ -21,13 +21,14 @@
 //
 // A stage is 128 keys, a warp's share 32 of them in two halves: softmax bookkeeping and the loop's own cost are
 // paid once for both.
-// Bound: instructions.  16 keys of K and V and 128 values take a warp some 230, half of them on the ALU (masks,
-// shifts), issued at 0.57 a cycle and scheduler: one of 131001 keys takes 38 us, 3.8 TB/s, 0.56 of a copy's rate (21.3
-// us would be the bytes'); the number of stages does not matter (2: the same), registers do: what only the list needs is
-// in shared memory while a warp goes through its tiles (40.3 us without).  q's fragments there too, and four CTAs an SM
-// with 96 registers, were no faster (with 16 rows the first is).  64 sequences of up to 16001 keys 34.9 us; 96 windows of 1000 keys of 64 values in
-// pages of 16 19.1; 8 sequences of 5 tokens, 28 heads over 4, 18.1: what an item costs beside its tiles, as for the 8-bit
-// cache.  One sequence of 257 keys 6.4 us.
+// Bound: no unit is full.  One sequence of 131001 keys takes 38 us, 3.8 TB/s, 0.56 of a copy's rate (21.3 us would be the
+// bytes'), with 0.57 instructions issued a cycle and scheduler and the ALU (masks, shifts) at 0.52: each of the three consumer
+// warps of a scheduler goes through one chain of dependent steps a slice (stage, K's products, scales, maximum, weights,
+// transposition, V's products), and begins none of the next slice before.  The number of stages does not matter (2: the
+// same), registers do: what only the list needs is in shared memory while a warp goes through its tiles (40.3 us without).
+// q's fragments there too, and four CTAs an SM with 96 registers, were no faster (with 16 rows the first is).  64 sequences of
+// up to 16001 keys 35.8 us; 96 windows of 1000 keys of 64 values in pages of 16 19.7; 8 sequences of 5 tokens, 28 heads over 4,
+// 18.6: what an item costs beside its tiles, as for the 8-bit cache.  One sequence of 257 keys 6.3 us.
 #include <type_traits>
 
 #include "attention_few.cuh"
@@ -69,7 +70,8 @@ __device__ __forceinline__ uint32_t bad_scales(uint32_t v) {
 // The 4-bit cache.
 struct Four {
     static constexpr int kTile = 128, kTileBits = 7, kWarpKeys = 32;
-    // As for the 8-bit cache (attention.cu), in tiles twice as long: an item's cost of 2 and 4 instead of 3 gives
+    // As for the 8-bit cache (attention.cu), in tiles twice as long (before 16 rows had q in shared memory, which takes the
+    // 20.9 below to 18.6): an item's cost of 2 and 4 instead of 3 gives
     // 37.7 and 36.4 us for 64 sequences of up to 16001 keys (34.4), 36.7 and 37.8 for one of 131001 (37.6); a
     // least range of 4 and 6 instead of 3 7.2 and 6.1 us for 257 keys (6.2), 8.4 and 10.4 for 1000 (7.9), 20.9
     // and 22.3 for 8 sequences of 5 tokens (20.9), 9.4 and 10.4 for 4000 (9.9).

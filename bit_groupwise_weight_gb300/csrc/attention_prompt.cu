@@ -29,7 +29,9 @@
 // but leave the weights waiting: 152 us against 132), 512 for V, 1024 to bring in, turn and
 // store the codes.  A step takes 3100; a CTA beside its steps about 15000 (its queries and
 // first keys 8000, its last product and result 6000).  4096 tokens, 32 heads of 128 over 8:
-// 125 us, 1.1 PFLOP/s (0.58 of the rate of a library product).
+// 126 us, 1.1 PFLOP/s (0.57 of the rate of a library product); over 4 bits 124.  (What keeps scores past 2^22 right costs
+// 0.8 and 1.5 us of them: code that does not run, but stands between the maximum and the weights.  In a loop of its own, or as
+// weights of its own, it cost 2 to 6.)
 #include <algorithm>
 
 #include "attention.cuh"

@@ -21,8 +21,10 @@
 // head's rows (sharing them over a cluster of the heads' CTAs was slower: 101 against
 // 88 us for 16002 tokens).  Rows are loaded one set ahead of the one in work.
 // With norms or positions of the caller's own, prompts go another way: the rows of q through cache4.cu's kernel,
-// and here a CTA takes the keys or the values of a page, of several heads with one table (15500 tokens with norms 50 + 54
-// us; all in one kernel 169, a CTA a head for keys and values 128).
+// and here a CTA takes the keys or the values of a page, of several heads with one table (15502 tokens with norms 103
+// us, with positions 94; all in one kernel 169, a CTA a head for keys and values 128).  Pages of more tokens than a CTA holds at
+// once (64 of 128 values) are read twice, with a table for each head and set of rows: with pages of 128 and 256 tokens
+// it is 169 and 171 us.
 //
 // Bound: HBM (T D (4 Hq + 6 Hk) bytes) for prompts, launch latency for decode.  16002 tokens
 // of 32 + 8 heads of 128 take 84.5 us, 4.1 TB/s (0.61 of a copy's rate: the CTAs of an SM hold

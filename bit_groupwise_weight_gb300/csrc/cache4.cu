@@ -15,8 +15,8 @@
 // and find their mates by way of shared memory.
 //
 // Bound: instructions (0.8 issued a cycle and scheduler; some 190 for two rows of q of 128 values with norm and rotation).
-// 15500 tokens of 32 + 8 heads of 128 with norms take 76 us, 4.1 TB/s; 5003 of 28 + 4 heads with positions of three axes
-// 19; one token 3.3, a launch's shortest.  Steps on the way: tokens' tables in shared memory read for every row 141 us; rows of
+// 15502 tokens of 32 + 8 heads of 128 with norms take 78 us, 4.3 TB/s; 5003 of 28 + 4 heads with positions of three axes
+// 21; one token 3.5, a launch's shortest.  Steps on the way: tokens' tables in shared memory read for every row 141 us; rows of
 // different kinds in one loop, with shuffles of half warps, 116; loads ahead in registers 97; a ring of eight rows instead
 // of four 1 us more.
 #include <algorithm>
@@ -33,7 +33,10 @@ namespace {
 using namespace append;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kAhead = 4;
-constexpr int kWarpsToFill = 152 * 32;       // fewer warps than this: the rows of a token are divided
+// Fewer warps than this: the rows of a token are divided.  A warp a token from 4864 on: 4800 and 4864 tokens take 28.9 and
+// 28.5 us (32 + 8 heads of 128, norms; 28 + 4, three axes: 19.4 and 17.5), 4900 and 5500, a few CTAs past the 608 that the SMs hold,
+// 33.4 and 34.3 (20.4 and 22.0), 8000 43.8 (27.5).
+constexpr int kWarpsToFill = 152 * 32;
 
 struct Token {
     bool live;                           // whether it is of a sequence, and not past max_q
@@ -295,7 +298,7 @@ cudaError_t launch(const AppendArgs &p, cudaStream_t stream) {
 }
 
 // Eight values of K and of V a thread; a page's head is 2^place_bits of such.  Bound: HBM, mostly the 16-bit
-// values that are written: 250 pages of 64 tokens, 8 heads of 128, 10.8 us, 2000 99, 6.0 TB/s, 0.90 of a copy's rate.
+// values that are written: 250 pages of 64 tokens, 8 heads of 128, 12.8 us, 2000 99, 6.7 TB/s, a copy's rate.
 template <int D, bool FOUR>
 __global__ void __launch_bounds__(256) cache_values_kernel(const ValuesArgs p, int place_bits) {
     ptx::pdl_launch_dependents();

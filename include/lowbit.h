@@ -356,7 +356,8 @@ LOWBIT_API lowbit_status lowbit_cache4_values(const lowbit_cache4 *cache, uint16
  * at position pos, over the keys t <= pos (and t > pos - window when window > 0)
  *     out = sum_t softmax_t(scale q.k_t) v_t,   lse = ln sum_t e^(scale q.k_t),
  * with k and v the cached values (code * 2^exp), head h reading key-value head
- * h / (heads / kv_heads).  Scores, softmax and sums in fp32; for the product with
+ * h / (heads / kv_heads).  Scores, softmax and sums in fp32 (a weight e^s is off by what fp32
+ * rounds of s, over 8 bits with v's exponent added to it); for the product with
  * the codes of v the weights are rounded to fp16, to 2^-11 of themselves, or to 2^-32
  * of the row's largest e^(..) 2^exp (weight times page scale of v) where that is more;
  * out rounded once to bf16.  A row that sees no key gives out 0 and lse -infinity.  What the cache holds
