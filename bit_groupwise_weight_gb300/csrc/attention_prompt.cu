@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // m follows the maximum when it has been outgrown; rows far from zero (limit: -inf) always come here.
             const float mx = largest();
             if (__any_sync(~0u, mx > limit)) {
-                const bool move = mx - m > kPeak;
+                const bool move = mx > limit && mx - m > kPeak;        // what this row alone asks for
                 const Rescale by(move ? m - (mx - kStart) : 0.f);
                 const float a = by.of_o();
                 if (move) m = mx - kStart;

@@ -23,10 +23,10 @@ HEADS = 4                                                 # over one kv head: 1 
 FEW_AND_MANY = "n", [1, 80]
 
 
-def batch(bits, seed, n, dim, keys, power):
+def batch(bits, seed, n, dim, keys, power, lens=(300, 131)):
     """Two sequences whose keys are rows of `keys` (whole numbers of up to 7) times 2^power, chosen at random, all
     kinds of them among the first.  Returns the batch and each sequence's choice."""
-    lens = [300, 131]
+    lens = list(lens)
     make = (ref4 if bits == 4 else ref).make_batch
     b = make(seed, lens, [n, n], 1, dim, 32)
     rng = np.random.default_rng([seed, 1])
@@ -61,7 +61,7 @@ def seen_values(bits, b, s):
 def check(bits, b, kinds, q, keys, power, scale):
     """Kinds of keys whose scores are so far apart that the best one has all of the weight: the mean of its values.
     Equal keys have equal scores and so equal weights, rounded to fp16 (2^-11 of themselves) for the product and not for
-    their sum; sums and products are fp32's (2^-16 of the magnitudes covers 300 of them), out is rounded to bf16; scores
+    their sum; sums and products are fp32's (2^-16 of the magnitudes covers 300 of them in a row; more are divided), out is rounded to bf16; scores
     are some ten roundings of sums of up to 16 |q| 2^power a value over 4 bits (2^-20 of that), the logarithm is off by
     2 units and lse by one.
     Of the few rows for which two kinds come near each other only sizes are looked at."""
@@ -173,3 +173,28 @@ def test_zero_keys_have_zero_scores_whatever_the_row_of_q(n, scale):
             row, want, mean = b.starts[s] + i, v[:sees[i]].mean(0), np.abs(v[:sees[i]]).mean(0)
             assert np.all(np.abs(out[row] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -11 * mean + 2.0 ** -16 * np.abs(v).max())
             assert np.all(np.abs(lse[row] - np.log(sees[i])) <= 2.0 ** -20)
+
+
+@pytest.mark.parametrize("n", [1, 3, 64, 150])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("by", [2.0 ** 24, -2.0 ** 40, 2.0 ** 90])
+def test_rows_beside_others_far_from_zero_are_the_same(n, dim, by):
+    """To the bit, over 4 bits: rows of the same tiles, warps and sequences."""
+    b = ref4.make_batch(98, [700], [n], 1, dim, 64)
+    q = ref.bf16(np.random.default_rng([99, n]).standard_normal((n, 8, dim)))
+    alone, alone_lse = run(b, q, dim ** -0.5)
+    loud = q.clone()
+    loud[:, ::2] *= by
+    got, lse = run(b, loud, dim ** -0.5)
+    assert np.array_equal(got[:, 1::2], alone[:, 1::2]) and np.array_equal(lse[:, 1::2], alone_lse[:, 1::2])
+    assert np.isfinite(got).all() and np.isfinite(lse).all() and not np.array_equal(got[:, ::2], alone[:, ::2])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize(*FEW_AND_MANY)
+@pytest.mark.parametrize("far", [25, 60])
+def test_scores_far_from_zero_in_parts(bits, n, far):
+    """Keys divided between CTAs, whose parts are joined."""
+    keys, q = make_keys(far, 3, 128), make_q(far, n, 128, 2.0 ** (far // 2))
+    b, kinds = batch(bits, far, n, 128, keys, 0, lens=(9000, 2500))
+    check(bits, b, kinds, q, keys, 0, 2.0 ** (far - far // 2) / 100)
